@@ -23,6 +23,17 @@ Gradients of the chunked forward (any gate and beta mode):
 
     g = dr_chunk_bwd(q, k, v, log_alpha, beta, S0, dO, dS_final, gate="scalar")
     g["dq"], g["dk"], g["dv"], g["dlog_alpha"], g["dbeta"], g["dS0"]
+
+Linear attention with a decay per head (no erase term), its gradients and one token:
+
+    o, S = dr_linear_attn_fwd(q, k, v, log_alpha, S0, decay="token")
+    g = dr_linear_attn_bwd(q, k, v, log_alpha, S0, dO, dS_final, decay="token")
+    o = dr_linear_attn_step(S, q, k, v, log_alpha, decay="head")
+
+Layer norm of rows, such as those outputs, and its gradients:
+
+    y, mean, rstd = dr_layernorm_fwd(o, weight, bias)
+    g = dr_layernorm_bwd(o, weight, mean, rstd, dy)
 """
 from __future__ import annotations
 
@@ -33,11 +44,12 @@ from typing import Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdeltarule.so")
 
-DR_ABI_VERSION = 10
+DR_ABI_VERSION = 11
 DR_OK, DR_ERR_NULL, DR_ERR_SHAPE, DR_ERR_UNSUPPORTED, DR_ERR_ALIGN, DR_ERR_WORKSPACE, DR_ERR_HIP = range(7)
 DR_F32, DR_BF16 = 0, 1
 GATES = {"none": 0, "scalar": 1, "channel": 2}
 BETAS = {"scalar": 0, "channel": 1}
+DECAYS = {"none": 0, "head": 1, "token": 2}
 DR_IN_QK_L2NORM, DR_IN_BETA_LOGIT = 1, 2
 EXPORTS = ("dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd", "dr_chunk_fwd_kv", "dr_decode_step",
            "dr_decode_step_kv", "dr_chunk_fwd_precond_workspace_bytes", "dr_chunk_fwd_precond",
@@ -45,7 +57,9 @@ EXPORTS = ("dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd", "dr_chunk_fwd_kv", "d
            "dr_profile_begin", "dr_profile_end", "dr_chunk_bwd_workspace_bytes", "dr_chunk_bwd",
            "dr_chunk_bwd_kv", "dr_chunk_fwd_noalloc", "dr_chunk_fwd_kv_workspace_bytes",
            "dr_chunk_bwd_kv_workspace_bytes", "dr_chunk_bwd_precond_workspace_bytes", "dr_chunk_bwd_precond",
-           "dr_chunk_bwd_workspace_bytes_min")
+           "dr_chunk_bwd_workspace_bytes_min", "dr_linear_attn_fwd_workspace_bytes", "dr_linear_attn_fwd",
+           "dr_linear_attn_bwd_workspace_bytes", "dr_linear_attn_bwd", "dr_linear_attn_step", "dr_layernorm_fwd",
+           "dr_layernorm_bwd_workspace_bytes", "dr_layernorm_bwd")
 DR_NOALLOC_SCRATCH_BYTES = 256 << 20
 
 
@@ -67,13 +81,40 @@ class ProfileReport(ctypes.Structure):
     _fields_ = [("chunk_calls", ctypes.c_int), ("decode_calls", ctypes.c_int), ("prep_ms", ctypes.c_double),
                 ("scan_ms", ctypes.c_double), ("decode_ms", ctypes.c_double), ("bwd_calls", ctypes.c_int),
                 ("bwd_prep_ms", ctypes.c_double), ("bwd_fscan_ms", ctypes.c_double),
-                ("bwd_rscan_ms", ctypes.c_double), ("bwd_post_ms", ctypes.c_double)]
+                ("bwd_rscan_ms", ctypes.c_double), ("bwd_post_ms", ctypes.c_double),
+                ("linear_attn_fwd_ms", ctypes.c_double), ("linear_attn_bwd_ms", ctypes.c_double),
+                ("linear_attn_step_ms", ctypes.c_double), ("layernorm_fwd_ms", ctypes.c_double),
+                ("layernorm_bwd_ms", ctypes.c_double)]
 
 
 class DecodeDesc(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int), ("H", ctypes.c_int), ("Dk", ctypes.c_int), ("Dv", ctypes.c_int),
                 ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("gate", ctypes.c_int),
                 ("beta", ctypes.c_int), ("input_flags", ctypes.c_uint)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("t", ctypes.c_longlong)]
+
+
+class LinAttnDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("L", ctypes.c_int),
+                ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("decay", ctypes.c_int), ("q", Strides), ("k", Strides), ("v", Strides), ("o", Strides),
+                ("dq", Strides), ("dk", Strides), ("dv", Strides)]
+
+
+class LinAttnStepDesc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("Dk", ctypes.c_int),
+                ("Dv", ctypes.c_int), ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("decay", ctypes.c_int)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("D", ctypes.c_int),
+                ("per_head", ctypes.c_int), ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("dy_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("x", Strides), ("y", Strides),
+                ("dy", Strides)]
 
 
 _lib = None
@@ -126,6 +167,19 @@ def lib() -> ctypes.CDLL:
         L.dr_chunk_bwd_precond_workspace_bytes.restype = ctypes.c_size_t
         L.dr_chunk_bwd_precond.argtypes = [ctypes.POINTER(ChunkDesc)] + [vp] * 17 + [ctypes.c_size_t, vp]
         L.dr_chunk_bwd_precond.restype = ctypes.c_int
+        for name, desc, nptr in (("dr_linear_attn_fwd", LinAttnDesc, 7), ("dr_linear_attn_bwd", LinAttnDesc, 12)):
+            getattr(L, name).argtypes = [ctypes.POINTER(desc)] + [vp] * (nptr + 1) + [ctypes.c_size_t, vp]
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name + "_workspace_bytes").argtypes = [ctypes.POINTER(desc)]
+            getattr(L, name + "_workspace_bytes").restype = ctypes.c_size_t
+        L.dr_linear_attn_step.argtypes = [ctypes.POINTER(LinAttnStepDesc)] + [vp] * 7
+        L.dr_linear_attn_step.restype = ctypes.c_int
+        L.dr_layernorm_fwd.argtypes = [ctypes.POINTER(LayerNormDesc)] + [vp] * 7
+        L.dr_layernorm_fwd.restype = ctypes.c_int
+        L.dr_layernorm_bwd_workspace_bytes.argtypes = [ctypes.POINTER(LayerNormDesc)]
+        L.dr_layernorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.dr_layernorm_bwd.argtypes = [ctypes.POINTER(LayerNormDesc)] + [vp] * 9 + [ctypes.c_size_t, vp]
+        L.dr_layernorm_bwd.restype = ctypes.c_int
         L.dr_status_str.argtypes = [ctypes.c_int]
         L.dr_status_str.restype = ctypes.c_char_p
         L.dr_last_error.argtypes = []
@@ -531,3 +585,298 @@ def _decode(S, q, k, v, log_alpha, beta, beta_v, gate, beta_mode, out_dtype, o, 
         _check(lib().dr_decode_step_kv(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                                        _ptr(beta), _ptr(beta_v), _ptr(S), _ptr(o), _stream(stream)))
     return o
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay per head; layer norm
+# ---------------------------------------------------------------------------
+
+def _strides(t) -> Strides:
+    """The strides of a [B,H,L,D] view in elements (0 where a dimension is 1)."""
+    return Strides(*(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])))
+
+
+def _need_rows(t, name, device, dtype=None, shape=None):
+    """A device tensor whose last dimension is contiguous; other strides are free."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _need_on(t, name, device, dtype, shape):
+    _need(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class _on:
+    """Runs on `device`, on `stream` (default: the device's current stream), so
+    that what is allocated inside belongs to that stream."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _workspace(workspace, nbytes, device):
+    torch = _torch()
+    if workspace is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes else (None, 0)
+    _need(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _decay_arg(log_alpha, decay, H, token_shape, device):
+    torch = _torch()
+    if decay not in DECAYS:
+        raise ValueError(f"decay must be one of {sorted(DECAYS)}, got {decay!r}")
+    if decay == "none":
+        if log_alpha is not None:
+            raise ValueError("decay 'none' takes no log_alpha")
+    else:
+        _need_on(log_alpha, "log_alpha", device, torch.float32, (H,) if decay == "head" else token_shape)
+
+
+def linattn_desc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, decay: str) -> LinAttnDesc:
+    """A descriptor for dense tensors; the strides can be set afterwards."""
+    qk, vo = Strides(Hk * L * Dk, L * Dk, Dk), Strides(H * L * Dv, L * Dv, Dv)
+    return LinAttnDesc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, DECAYS[decay], qk, qk, vo, vo, qk, qk, vo)
+
+
+def dr_linear_attn_fwd_workspace_bytes(desc: LinAttnDesc) -> int:
+    return int(lib().dr_linear_attn_fwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_linear_attn_bwd_workspace_bytes(desc: LinAttnDesc) -> int:
+    return int(lib().dr_linear_attn_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def _linattn_inputs(q, k, v, log_alpha, S0, decay):
+    torch = _torch()
+    if not (isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor)) or q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, heads, L, channels] tensors")
+    B, Hk, L, Dk = q.shape
+    H, Dv = v.shape[1], v.shape[-1]
+    _need_rows(q, "q", None)
+    _need_rows(k, "k", q.device, q.dtype, (B, Hk, L, Dk))
+    _need_rows(v, "v", q.device, q.dtype, (B, H, L, Dv))
+    _decay_arg(log_alpha, decay, H, (B, H, L), q.device)
+    if S0 is not None:
+        _need_on(S0, "S0", q.device, torch.float32, (B, H, Dk, Dv))
+    return B, H, Hk, L, Dk, Dv
+
+
+def dr_linear_attn_fwd(q, k, v, log_alpha=None, S0=None, *, decay: str, out_dtype=None, o=None, S_final=None,
+                       want_state: bool = True, workspace=None, stream=None):
+    """Linear attention with a decay per head, S_t = alpha_t S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t, over [B, heads, L, D] device tensors; returns (o, S_final).
+
+    q, k: [B,Hk,L,Dk]; v: [B,H,L,Dv] (bf16 or fp32, same dtype), H a multiple of
+    Hk; any strides whose channels are contiguous and whose rows start at
+    multiples of 16 bytes (views of [B,L,H,D] projections).  decay "head":
+    log_alpha [H] fp32, one constant per head; "token": [B,H,L] fp32; "none".
+    S0: [B,H,Dk,Dv] fp32 or None.  o defaults to out_dtype (fp32) in v's order
+    of dimensions; S_final may be S0 itself; with want_state=False and no
+    S_final none is written and None is returned for it.
+    """
+    torch = _torch()
+    B, H, Hk, L, Dk, Dv = _linattn_inputs(q, k, v, log_alpha, S0, decay)
+    dev = q.device
+    with _on(dev, stream) as st:
+        if o is None:
+            o = torch.empty_like(v, dtype=torch.float32 if out_dtype is None else out_dtype)
+        else:
+            _need_rows(o, "o", dev, out_dtype, (B, H, L, Dv))
+        if S_final is not None:
+            _need_on(S_final, "S_final", dev, torch.float32, (B, H, Dk, Dv))
+        elif want_state:
+            S_final = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+        desc = LinAttnDesc(B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay],
+                           _strides(q), _strides(k), _strides(v), _strides(o))
+        workspace, wbytes = _workspace(workspace, dr_linear_attn_fwd_workspace_bytes(desc), dev)
+        _check(lib().dr_linear_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
+                                        _ptr(o), _ptr(S_final), _ptr(workspace), wbytes, st))
+    return o, S_final
+
+
+def dr_linear_attn_bwd(q, k, v, log_alpha, S0, dO, dS_final=None, *, decay: str, grad_dtype=None,
+                       want_dS0: bool = True, workspace=None, stream=None):
+    """Gradients of dr_linear_attn_fwd for the loss whose gradients with respect
+    to o and S_final are dO [B,H,L,Dv] (q's dtype) and dS_final [B,H,Dk,Dv]
+    (fp32; None: zero).  Returns a dict of device tensors: dq, dk, dv in
+    grad_dtype (fp32) and in the order of their inputs' dimensions, dlog_alpha
+    (log_alpha's shape, fp32; None for decay "none") and dS0 (fp32; None with
+    want_dS0=False)."""
+    torch = _torch()
+    B, H, Hk, L, Dk, Dv = _linattn_inputs(q, k, v, log_alpha, S0, decay)
+    dev = q.device
+    _need_rows(dO, "dO", dev, q.dtype, (B, H, L, Dv))
+    if dS_final is not None:
+        _need_on(dS_final, "dS_final", dev, torch.float32, (B, H, Dk, Dv))
+    to = torch.float32 if grad_dtype is None else grad_dtype
+    with _on(dev, stream) as st:
+        out = {"dq": torch.empty_like(q, dtype=to), "dk": torch.empty_like(k, dtype=to),
+               "dv": torch.empty_like(v, dtype=to),
+               "dlog_alpha": None if log_alpha is None else torch.empty_like(log_alpha),
+               "dS0": torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if want_dS0 else None}
+        desc = LinAttnDesc(B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(to), DECAYS[decay], _strides(q),
+                           _strides(k), _strides(v), _strides(dO), _strides(out["dq"]), _strides(out["dk"]),
+                           _strides(out["dv"]))
+        workspace, wbytes = _workspace(workspace, dr_linear_attn_bwd_workspace_bytes(desc), dev)
+        _check(lib().dr_linear_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
+                                        _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+                                        _ptr(out["dlog_alpha"]), _ptr(out["dS0"]), _ptr(workspace), wbytes, st))
+    return out
+
+
+def dr_linear_attn_step(S, q, k, v, log_alpha=None, *, decay: str, out_dtype=None, o=None, stream=None):
+    """One token of the linear attention for N x H states (updated in place);
+    returns o [N,H,Dv].
+
+    S: [N,H,Dk,Dv] fp32; q, k: [N,Hk,Dk]; v: [N,H,Dv]; log_alpha: [H] (decay
+    "head"), [N,H] ("token") or None ("none").
+    """
+    torch = _torch()
+    N, H, Dk, Dv = S.shape
+    _need(S, "S", torch.float32)
+    dev, Hk = S.device, q.shape[1]
+    _need_on(q, "q", dev, None, (N, Hk, Dk))
+    _need_on(k, "k", dev, q.dtype, (N, Hk, Dk))
+    _need_on(v, "v", dev, q.dtype, (N, H, Dv))
+    _decay_arg(log_alpha, decay, H, (N, H), dev)
+    with _on(dev, stream) as st:
+        if o is None:
+            o = torch.empty((N, H, Dv), dtype=torch.float32 if out_dtype is None else out_dtype, device=dev)
+        else:
+            _need_on(o, "o", dev, out_dtype, (N, H, Dv))
+        desc = LinAttnStepDesc(N, H, Hk, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay])
+        _check(lib().dr_linear_attn_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S),
+                                         _ptr(o), st))
+    return o
+
+
+def _norm_rows(t, weight_dims):
+    """x of two to four dimensions as [B, H, L, D]: [N, D], and with a weight
+    for each head [N, H, D] or [B, H, L, D]; with one weight also [B, H, L, D]
+    and [B, L, D]."""
+    if t.dim() == 4:
+        return t
+    if t.dim() == 2 and weight_dims == 1:
+        return t[None, None]
+    if t.dim() == 3:
+        return t[:, :, None] if weight_dims == 2 else t[:, None]
+    raise ValueError("x must be [N, D], [B, L, D], [N, H, D] or [B, H, L, D], with a weight [D] or [H, D]")
+
+
+def _norm_args(x, per_head, weight, bias, names=("weight", "bias")):
+    """The [B, H, L, D] view of x and whether the weights are one per head."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dims = {t.dim() for t in (weight, bias) if t is not None}
+    if len(dims) > 1:
+        raise ValueError("weight and bias must have the same shape")
+    per_head = per_head if per_head is not None else dims == {2}
+    x4 = _norm_rows(x, 2 if per_head else 1)
+    _need_rows(x, "x", None)
+    shape = (x4.shape[1], x4.shape[3]) if per_head else (x4.shape[3],)
+    for t, name in zip((weight, bias), names):
+        if t is not None:
+            _need_on(t, name, x.device, torch.float32, shape)
+    return x4, per_head, shape
+
+
+def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=None, y=None, mean=None, rstd=None,
+                     stream=None):
+    """Layer norm over the last dimension of x: (x - mean) rstd weight + bias;
+    returns (y, mean, rstd).
+
+    x: [N,D], [B,L,D] or [B,H,L,D] (bf16 or fp32) with weight and bias [D] fp32;
+    or, with one weight per head [H,D], [N,H,D] or [B,H,L,D].  Channels are
+    contiguous, other strides free.  y defaults to out_dtype (x's dtype) in x's
+    order of dimensions; mean and rstd are fp32, contiguous, of x's leading shape.
+    """
+    torch = _torch()
+    x4, per_head, _ = _norm_args(x, None, weight, bias)
+    B, H, L, D = x4.shape
+    dev, lead = x.device, tuple(x.shape[:-1])
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x, dtype=x.dtype if out_dtype is None else out_dtype)
+        else:
+            _need_rows(y, "y", dev, out_dtype, tuple(x.shape))
+        stats = []
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is None:
+                t = torch.empty(lead, dtype=torch.float32, device=dev)
+            else:
+                _need_on(t, name, dev, torch.float32, lead)
+            stats.append(t)
+        y4 = _norm_rows(y, 2 if per_head else 1)
+        desc = LayerNormDesc(B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32, eps,
+                             _strides(x4), _strides(y4))
+        _check(lib().dr_layernorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(stats[0]),
+                                      _ptr(stats[1]), st))
+    return y, stats[0], stats[1]
+
+
+def dr_layernorm_bwd_workspace_bytes(desc: LayerNormDesc) -> int:
+    return int(lib().dr_layernorm_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_layernorm_bwd(x, weight, mean, rstd, dy, *, per_head=None, grad_dtype=None, dx=None, want_sums: bool = True,
+                     workspace=None, stream=None):
+    """Gradients of dr_layernorm_fwd: dx in grad_dtype (x's dtype) and in x's
+    order of dimensions, dweight and dbias fp32 (None with want_sums=False), in
+    a dict.  x, weight, mean and rstd are the forward's; dy (bf16 or fp32) has
+    x's shape.  Without a weight, per_head=True makes the sums one per head."""
+    torch = _torch()
+    if weight is not None and per_head is not None and per_head != (weight.dim() == 2):
+        raise ValueError("per_head does not fit the weight's shape")
+    x4, per_head, wshape = _norm_args(x, per_head, weight, None)
+    B, H, L, D = x4.shape
+    dev, lead = x.device, tuple(x.shape[:-1])
+    _need_on(mean, "mean", dev, torch.float32, lead)
+    _need_on(rstd, "rstd", dev, torch.float32, lead)
+    _need_rows(dy, "dy", dev, None, tuple(x.shape))
+    with _on(dev, stream) as st:
+        if dx is None:
+            dx = torch.empty_like(x, dtype=x.dtype if grad_dtype is None else grad_dtype)
+        else:
+            _need_rows(dx, "dx", dev, grad_dtype, tuple(x.shape))
+        dims = 2 if per_head else 1
+        desc = LayerNormDesc(B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
+                             _dtype_code(dy.dtype), 0.0, _strides(x4), _strides(_norm_rows(dx, dims)),
+                             _strides(_norm_rows(dy, dims)))
+        out = {"dx": dx, "dweight": None, "dbias": None}
+        wbytes = 0
+        if want_sums:
+            out["dweight"] = torch.empty(wshape, dtype=torch.float32, device=dev)
+            out["dbias"] = torch.empty(wshape, dtype=torch.float32, device=dev)
+            workspace, wbytes = _workspace(workspace, dr_layernorm_bwd_workspace_bytes(desc), dev)
+        _check(lib().dr_layernorm_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
+                                      _ptr(dx), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), wbytes,
+                                      st))
+    return out

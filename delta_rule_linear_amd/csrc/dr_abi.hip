@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "deltarule.h"
+#include "dr_host.h"
 #include "dr_internal.h"
 
 // The allocation-free forward's workspace: one array per GPU, from the
@@ -26,53 +27,13 @@ namespace {
 
 thread_local char g_err[512] = "";
 
-dr_status fail(dr_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-dr_status fail(dr_status s, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return s;
-}
+using dr::align256;
+using dr::aligned16;
+using dr::check_disjoint;
+using dr::fail;
+using dr::Span;
+using dr::valid_dtype;
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// A tensor argument as a byte range (p may be NULL: an absent tensor).
-struct Span {
-    const void* p;
-    size_t bytes;
-    const char* name;
-};
-
-bool overlap(const Span& a, const Span& b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const char* x = (const char*)a.p;
-    const char* y = (const char*)b.p;
-    return x < y + b.bytes && y < x + a.bytes;
-}
-
-// Every output in `outs` must be disjoint from every input in `ins` and from
-// the other outputs, except that output alias_out may be input alias_in
-// exactly (the same address and size: the in-place state carry); any other
-// overlap is an error.
-dr_status check_disjoint(const Span* outs, int nout, const Span* ins, int nin, const void* alias_out = nullptr,
-                         const void* alias_in = nullptr) {
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j) {
-            if (!overlap(outs[i], ins[j])) continue;
-            if (alias_out && outs[i].p == alias_out && ins[j].p == alias_in && outs[i].p == ins[j].p &&
-                outs[i].bytes == ins[j].bytes)
-                continue;
-            return fail(DR_ERR_UNSUPPORTED, "%s overlaps %s", outs[i].name, ins[j].name);
-        }
-        for (int j = i + 1; j < nout; ++j)
-            if (overlap(outs[i], outs[j]))
-                return fail(DR_ERR_UNSUPPORTED, "%s overlaps %s", outs[i].name, outs[j].name);
-    }
-    return DR_OK;
-}
-
-bool valid_dtype(int x) { return x == DR_F32 || x == DR_BF16; }
 bool valid_gate(int x) { return x == DR_GATE_NONE || x == DR_GATE_SCALAR || x == DR_GATE_CHANNEL; }
 bool valid_beta(int x) { return x == DR_BETA_SCALAR || x == DR_BETA_CHANNEL; }
 
@@ -96,8 +57,6 @@ dr_status check_modes(int Dk, int Dv, int in_dtype, int out_dtype, int gate, int
 struct WsLayout {
     size_t T, Pm, G, Q, Ks, Kl, V, total;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // precond: write-side key scales, which run on the channel-gate path;
 // kvtok: separate scalar strengths, which run on the channel-beta path
@@ -228,6 +187,40 @@ void prof_record(hipEvent_t start, hipEvent_t stop, int slot) {
 }
 }  // namespace dr
 
+namespace dr {
+dr_status fail(dr_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+static bool overlap(const Span& a, const Span& b) {
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const char* x = (const char*)a.p;
+    const char* y = (const char*)b.p;
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
+dr_status check_disjoint(const Span* outs, int nout, const Span* ins, int nin, const void* alias_out,
+                         const void* alias_in) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j) {
+            if (!overlap(outs[i], ins[j])) continue;
+            if (alias_out && outs[i].p == alias_out && ins[j].p == alias_in && outs[i].p == ins[j].p &&
+                outs[i].bytes == ins[j].bytes)
+                continue;
+            return fail(DR_ERR_UNSUPPORTED, "%s overlaps %s", outs[i].name, ins[j].name);
+        }
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(outs[i], outs[j]))
+                return fail(DR_ERR_UNSUPPORTED, "%s overlaps %s", outs[i].name, outs[j].name);
+    }
+    return DR_OK;
+}
+}  // namespace dr
+
 extern "C" {
 
 dr_status dr_profile_begin(void) {
@@ -270,6 +263,11 @@ dr_status dr_profile_end(dr_profile_report* report) {
     report->bwd_fscan_ms = ms[dr::kProfBwdFscan];
     report->bwd_rscan_ms = ms[dr::kProfBwdRscan];
     report->bwd_post_ms = ms[dr::kProfBwdPost];
+    report->linear_attn_fwd_ms = ms[dr::kProfLaFwd];
+    report->linear_attn_bwd_ms = ms[dr::kProfLaBwd];
+    report->linear_attn_step_ms = ms[dr::kProfLaStep];
+    report->layernorm_fwd_ms = ms[dr::kProfLnFwd];
+    report->layernorm_bwd_ms = ms[dr::kProfLnBwd];
     return DR_OK;
 }
 

@@ -1,0 +1,251 @@
+// dr_linattn.hip -- linear attention with a decay per head: the chunked kernel
+// for bf16 inputs (dr_linattn_kernel.h), the joining of segment states, the
+// gate's gradient, the sum of gradients over heads that share q and k, and the
+// one-token step.
+
+#include "dr_linattn_kernel.h"
+
+namespace dr {
+
+hipError_t launch_la16(const LaArgs& a, int dx, int waves, int terms, bool state_only, int slot, hipStream_t st) {
+    if (state_only)
+        return dx == 64 ? la_launch_w<__bf16, 64, 3, true>(a, waves, slot, st)
+                        : la_launch_w<__bf16, 128, 3, true>(a, waves, slot, st);
+    if (terms == 2)
+        return dx == 64 ? la_launch_w<__bf16, 64, 2, false>(a, waves, slot, st)
+                        : la_launch_w<__bf16, 128, 2, false>(a, waves, slot, st);
+    return dx == 64 ? la_launch_w<__bf16, 64, 3, false>(a, waves, slot, st)
+                    : la_launch_w<__bf16, 128, 3, false>(a, waves, slot, st);
+}
+
+// ------------------------------------------------------ joining the segments
+struct LaJoin2 {
+    LaJoinArgs j[2];
+};
+
+// One thread walks four elements of a sequence's state over the segments; the
+// loads of all segments are independent of the walk.
+__global__ __launch_bounds__(256) void la_join_kernel(LaJoin2 p) {
+    const LaJoinArgs& a = p.j[blockIdx.y];
+    const int n4 = a.elems / 4;
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (size_t)a.nseq * n4) return;
+    const size_t seq = i / n4, e = i % n4;
+    f32x4 cur = {0.f, 0.f, 0.f, 0.f};
+    if (a.start) cur = reinterpret_cast<const f32x4*>(a.start)[seq * n4 + e];
+    f32x4* seg = reinterpret_cast<f32x4*>(a.seg) + seq * a.nseg * n4 + e;
+    const float* dec = a.segdec + seq * a.nseg;
+#pragma unroll 4
+    for (int k = 0; k < a.nseg; ++k) {
+        const int s = a.rev ? a.nseg - 1 - k : k;
+        f32x4 local = {0.f, 0.f, 0.f, 0.f};
+        float d = 0.f;
+        if (k + 1 < a.nseg) {
+            local = seg[(size_t)s * n4];
+            d = dec[s];
+        }
+        seg[(size_t)s * n4] = cur;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + local[j];
+    }
+}
+
+hipError_t launch_la_join(const LaJoinArgs* a, int n, int slot, hipStream_t st) {
+    LaJoin2 p{};
+    p.j[0] = a[0];
+    p.j[1] = a[n - 1];
+    const size_t work = (size_t)a[0].nseq * (a[0].elems / 4);
+    return launch_k(slot, la_join_kernel, dim3((unsigned)((work + 255) / 256), n), dim3(256), 0, st, p);
+}
+
+// ------------------------------------------------------ the gate's gradient
+// One workgroup per (sequence, segment): <S, dS> at the segment's end, then the
+// sums over the tokens behind each token.  The differences are small against
+// their terms, so the sums are fp64.
+__global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
+    __shared__ double red[256];
+    const int nseq = a.B * a.H;
+    const int seq = blockIdx.x % nseq, sg = blockIdx.x / nseq;
+    const int tid = threadIdx.x;
+    const float *S = nullptr, *D = nullptr;
+    if (sg + 1 < a.nseg) {
+        S = a.segF + ((size_t)seq * a.nseg + sg + 1) * a.elems;
+        D = a.segR + ((size_t)seq * a.nseg + sg) * a.elems;
+    } else if (a.dS_end) {
+        S = a.S_end + (size_t)seq * a.elems;
+        D = a.dS_end + (size_t)seq * a.elems;
+    }
+    double acc = 0.0;
+    if (S)
+        for (int i = tid; i < a.elems / 4; i += 256) {
+            const f32x4 s = reinterpret_cast<const f32x4*>(S)[i], d = reinterpret_cast<const f32x4*>(D)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc += (double)s[j] * (double)d[j];
+        }
+    red[tid] = acc;
+    __syncthreads();
+    for (int n = 128; n > 0; n >>= 1) {
+        if (tid < n) red[tid] += red[tid + n];
+        __syncthreads();
+    }
+    double carry = red[0];
+    __syncthreads();
+    // 256 tokens at a time, from the segment's last
+    const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
+    const size_t plane = (size_t)nseq * a.L;
+    double total = 0.0;
+    for (int hi = t1; hi > t0; hi -= 256) {
+        const int t = hi - 1 - tid;
+        double d = 0.0;
+        if (t >= t0) {
+            const size_t at = (size_t)seq * a.L + t;
+            for (int i = 0; i < a.tq; ++i) d += (double)a.dq_dots[i * plane + at];
+            for (int i = 0; i < a.tk; ++i) d -= (double)a.dk_dots[i * plane + at];
+        }
+        red[tid] = d;
+        __syncthreads();
+        for (int n = 1; n < 256; n <<= 1) {
+            const double y = tid >= n ? red[tid - n] : 0.0;
+            __syncthreads();
+            red[tid] += y;
+            __syncthreads();
+        }
+        const double v = carry + red[tid];
+        carry += red[255];
+        __syncthreads();
+        if (t >= t0) {
+            if (!a.head) a.dla[(size_t)seq * a.L + t] = (float)v;
+            total += v;
+        }
+    }
+    if (a.head) {
+        red[tid] = total;
+        __syncthreads();
+        for (int n = 128; n > 0; n >>= 1) {
+            if (tid < n) red[tid] += red[tid + n];
+            __syncthreads();
+        }
+        if (tid == 0) reinterpret_cast<double*>(a.dla)[(size_t)seq * a.nseg + sg] = red[0];
+    }
+}
+
+// one workgroup per head: the sum over sequences and segments, in their order
+__global__ __launch_bounds__(64) void la_gate_head_kernel(LaGateArgs a) {
+    const double* part = reinterpret_cast<const double*>(a.dla);
+    const int hd = blockIdx.x;
+    double acc = 0.0;
+    for (size_t i = threadIdx.x; i < (size_t)a.B * a.nseg; i += 64) {
+        const size_t b = i / a.nseg, s = i % a.nseg;
+        acc += part[(b * a.H + hd) * a.nseg + s];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) acc += __shfl_xor(acc, d);
+    if (threadIdx.x == 0) a.dla_head[hd] = (float)acc;
+}
+
+hipError_t launch_la_gate(const LaGateArgs& a, int slot, hipStream_t st) {
+    hipError_t e = launch_k(slot, la_gate_kernel, dim3((unsigned)(a.B * a.H * a.nseg)), dim3(256), 0, st, a);
+    if (e == hipSuccess && a.head) e = launch_k(slot, la_gate_head_kernel, dim3(a.H), dim3(64), 0, st, a);
+    return e;
+}
+
+__global__ __launch_bounds__(256) void la_copy_kernel(float* dst, const float* src, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
+        dst[i] = src ? src[i] : 0.f;
+}
+
+hipError_t launch_la_copy(float* dst, const float* src, size_t n, int slot, hipStream_t st) {
+    const size_t blocks = (n + 255) / 256;
+    return launch_k(slot, la_copy_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, st, dst, src,
+                    n);
+}
+
+// ------------------------------------------------------ shared heads
+__global__ __launch_bounds__(256) void la_group_kernel(LaGroupArgs a) {
+    const int n4 = a.D / 4;
+    const size_t n = (size_t)a.B * a.Hk * a.L * n4;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        const int c = (int)(i % n4);
+        size_t r = i / n4;
+        const int64_t t = r % a.L;
+        r /= a.L;
+        const int64_t hk = r % a.Hk, b = r / a.Hk;
+        const f32x4* in = reinterpret_cast<const f32x4*>(a.in) +
+                          (((size_t)b * a.Hk + hk) * a.group * a.L + t) * n4 + c;
+        f32x4 v = in[0];
+        for (int g = 1; g < a.group; ++g) v = v + in[(size_t)g * a.L * n4];
+        const int64_t at = b * a.ob + hk * a.oh + t * a.ot + 4 * c;
+        if (a.out_bf16) *reinterpret_cast<bf16x4*>((__bf16*)a.out + at) = __builtin_convertvector(v, bf16x4);
+        else *reinterpret_cast<f32x4*>((float*)a.out + at) = v;
+    }
+}
+
+hipError_t launch_la_group(const LaGroupArgs& a, int slot, hipStream_t st) {
+    const size_t n = (size_t)a.B * a.Hk * a.L * (a.D / 4);
+    const size_t blocks = (n + 255) / 256;
+    return launch_k(slot, la_group_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, a);
+}
+
+// ------------------------------------------------------ one token
+// S <- alpha S + k v^T, o = S^T q for N x H states: every state is read once
+// and written once, and nothing else is large.  One workgroup takes 64 columns
+// of a state; a thread holds four columns of every 16th row.
+template <bool F32IN>
+__global__ __launch_bounds__(256) void la_step_kernel(LaStepArgs a) {
+    __shared__ float sq[128], sk[128];
+    __shared__ float red[16][64];
+    const int nslab = (a.Dv + 63) / 64;
+    const int sidx = blockIdx.x / nslab, slab = blockIdx.x % nslab;
+    const int n = sidx / a.H, hd = sidx % a.H;
+    const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
+    const int col = slab * 64 + 4 * cg;
+    const bool ok = col < a.Dv;
+    float* S = a.S + (size_t)sidx * a.Dk * a.Dv + col;
+    f32x4 s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = rg + 16 * i;
+        if (ok && r < a.Dk) s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + (size_t)r * a.Dv));
+    }
+    const size_t qk = ((size_t)n * (a.H / a.group) + hd / a.group) * a.Dk;
+    if (tid < a.Dk) sq[tid] = load1<F32IN>(a.q, qk + tid);
+    else if (tid >= 128 && tid - 128 < a.Dk) sk[tid - 128] = load1<F32IN>(a.k, qk + tid - 128);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ok) load_n<F32IN, 4>(a.v, (size_t)sidx * a.Dv + col, v);
+    const float al = a.la ? expf(a.la[a.la_head ? hd : sidx]) : 1.f;
+    __syncthreads();
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (ok) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = rg + 16 * i;
+            if (r >= a.Dk) continue;
+            const float kr = sk[r], qr = sq[r];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = al * s[i][j] + kr * v[j];
+                o[j] += qr * s[i][j];
+            }
+            __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(S + (size_t)r * a.Dv));
+        }
+    }
+    *reinterpret_cast<f32x4*>(&red[rg][4 * cg]) = o;
+    __syncthreads();
+    const int oc = slab * 64 + tid;
+    if (tid < 64 && oc < a.Dv) {
+        float x = 0.f;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) x += red[g][tid];
+        const size_t at = (size_t)sidx * a.Dv + oc;
+        if (a.out_bf16) static_cast<__bf16*>(a.o)[at] = (__bf16)x;
+        else static_cast<float*>(a.o)[at] = x;
+    }
+}
+
+hipError_t launch_la_step(const LaStepArgs& a, bool f32in, int slot, hipStream_t st) {
+    const dim3 grid((unsigned)((size_t)a.N * a.H * ((a.Dv + 63) / 64)));
+    return f32in ? launch_k(slot, la_step_kernel<true>, grid, dim3(256), 0, st, a)
+                 : launch_k(slot, la_step_kernel<false>, grid, dim3(256), 0, st, a);
+}
+
+}  // namespace dr

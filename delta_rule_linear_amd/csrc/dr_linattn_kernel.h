@@ -1,0 +1,480 @@
+// dr_linattn_kernel.h -- the chunked kernel of linear attention with a decay
+// per head, for bf16 inputs (dr_linattn.hip) and fp32 inputs (dr_linattn32.hip).
+//
+// Mathematics.  With g the running sum of log alpha, S_t = a_t S_{t-1} + k_t v_t^T
+// and o_t = S_t^T q_t give, for a 64-token chunk that starts from state S,
+//   o_i = e^{g_i} S^T q_i + sum_{j <= i} e^{g_i - g_j} (q_i . k_j) v_j
+//   S  <- e^{g_63} S + sum_j e^{g_63 - g_j} k_j v_j^T,
+// and the gradients of q, k and v have the same form with the roles exchanged
+// and, for k and v, the tokens taken backwards (LaPass in dr_linattn.h names
+// them x, y, z).  Backwards, a row's u is the sum of log alpha over the tokens
+// behind it, without its own: the exclusive running sum.
+//
+// Layout.  One workgroup walks the chunks of one segment of one sequence for
+// 32 columns of z per wave.  A wave keeps its Dx x 32 state in accumulator
+// registers of the 32x32 matrix ops.  A lane of an accumulator holds rows
+// 8 b + 4 h + j (b, j < 4; h the half of the wave) of one column; taken as an
+// operand with that row order as the contraction's order, the same registers
+// feed the next product, so neither the state nor the 64 x 64 matrix of
+// products x . y passes through LDS: x and y rows are read from LDS in that
+// order.  Products that contract over tokens read y and z transposed
+// (ds_read_b64_tr_b16 for bf16).
+//
+// Precision.  bf16 inputs are operands as they are.  fp32 quantities that meet
+// them are split into bf16 terms: the decayed z of the state update into three
+// (24 significant bits: the state is as exact as in fp32), the state and the
+// decayed products of the output into NT = 3 where the output is kept in fp32
+// or feeds the gate's gradient, else 2 (16 bits, below the output's own
+// rounding to bf16).  fp32 inputs use the fp32 matrix ops throughout.  Running
+// sums of log alpha are fp64; differences are taken between hi + lo float
+// pairs, so a long or strong decay loses nothing to cancellation.  log alpha
+// below -256 / log2(e) counts as that (its e^ is 0 in fp32 either way), so a
+// decay of exactly zero (log alpha = -inf) resets the state.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "dr_device.h"
+#include "dr_internal.h"
+#include "dr_lds.h"
+#include "dr_linattn.h"
+
+namespace dr {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+// Swizzle of the 16-byte pieces of a row of RB bytes.  Row reads take the same
+// piece of 16 or 32 consecutive rows, transposing reads 64 consecutive bytes of
+// four consecutive rows: the low two bits of the row go to the piece's upper
+// bits (four rows fall on different quarters of the banks), the next two to
+// its lower bits.
+template <int RB>
+__device__ __forceinline__ int la_swz(int r) {
+    if constexpr (RB >= 256) return ((r & 3) << 2) | ((r >> 2) & 3);
+    else if constexpr (RB == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    else return 0;
+}
+
+template <typename T>
+struct LaFrag;   // eight contraction values of one row or column
+template <>
+struct LaFrag<__bf16> {
+    uint4 v;
+};
+template <>
+struct LaFrag<float> {
+    float v[8];
+};
+
+// fp32 values as an operand: NT bf16 terms, or themselves
+template <typename T, int NT>
+struct LaTerms {
+    uint4 t[NT];
+};
+template <int NT>
+struct LaTerms<float, NT> {
+    float v[8];
+};
+
+template <typename T, int NT>
+__device__ __forceinline__ LaTerms<T, NT> la_split(const float (&x)[8]) {
+    LaTerms<T, NT> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = x[e];
+    } else {
+        f32x8 f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = x[e];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bf16x8 h = __builtin_convertvector(f, bf16x8);
+            r.t[n] = __builtin_bit_cast(uint4, h);
+            if (n + 1 < NT) f = f - __builtin_convertvector(h, f32x8);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ f32x16 la_mfma(const uint4& a, const uint4& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+__device__ __forceinline__ f32x16 la_mfma(const float (&a)[8], const float (&b)[8], f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+// c += a b, a or b split into terms (smallest first, so that they are not lost)
+template <int NT>
+__device__ __forceinline__ f32x16 la_mma(const LaTerms<__bf16, NT>& a, const LaFrag<__bf16>& b, f32x16 c) {
+#pragma unroll
+    for (int n = NT - 1; n >= 0; --n) c = la_mfma(a.t[n], b.v, c);
+    return c;
+}
+template <int NT>
+__device__ __forceinline__ f32x16 la_mma(const LaFrag<__bf16>& a, const LaTerms<__bf16, NT>& b, f32x16 c) {
+#pragma unroll
+    for (int n = NT - 1; n >= 0; --n) c = la_mfma(a.v, b.t[n], c);
+    return c;
+}
+template <int NT>
+__device__ __forceinline__ f32x16 la_mma(const LaTerms<float, NT>& a, const LaFrag<float>& b, f32x16 c) {
+    return la_mfma(a.v, b.v, c);
+}
+template <int NT>
+__device__ __forceinline__ f32x16 la_mma(const LaFrag<float>& a, const LaTerms<float, NT>& b, f32x16 c) {
+    return la_mfma(a.v, b.v, c);
+}
+template <typename T>
+__device__ __forceinline__ f32x16 la_mma(const LaFrag<T>& a, const LaFrag<T>& b, f32x16 c) {
+    return la_mfma(a.v, b.v, c);
+}
+
+// Row `row`, contraction values 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.
+template <typename T, int RB>
+__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, int h) {
+    LaFrag<T> f;
+    const lchar* r = tile + row * RB;
+    const int s = la_swz<RB>(row);
+    if constexpr (sizeof(T) == 2) {
+        const uint2 a = lds_ld<uint2>(r + 16 * ((2 * m) ^ s) + 8 * h);
+        const uint2 b = lds_ld<uint2>(r + 16 * ((2 * m + 1) ^ s) + 8 * h);
+        f.v = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+        const f32x4 a = lds_ld<f32x4>(r + 16 * ((4 * m + h) ^ s));
+        const f32x4 b = lds_ld<f32x4>(r + 16 * ((4 * m + 2 + h) ^ s));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.v[j] = a[j];
+            f.v[4 + j] = b[j];
+        }
+    }
+    return f;
+}
+
+// Column c0 + lane % 32, rows 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.
+template <typename T, int RB>
+__device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, int m, int c0, int lane) {
+    LaFrag<T> f;
+    const int h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+        const int i = lane & 15, g = (lane >> 4) & 1;
+        const int piece = (c0 >> 3) + 2 * g + ((i >> 1) & 1), sub = 8 * (i & 1);
+        uint2 w[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int row = 16 * m + 8 * q + 4 * h + (i >> 2);
+            w[q] = lds_tr4(tile + row * RB + 16 * (piece ^ la_swz<RB>(row)) + sub);
+        }
+        f.v = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+    } else {
+        const int col = c0 + (lane & 31);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int row = 16 * m + 8 * (e >> 2) + 4 * h + (e & 3);
+            f.v[e] = lds_ld<float>(tile + row * RB + 16 * ((col >> 2) ^ la_swz<RB>(row)) + 4 * (col & 3));
+        }
+    }
+    return f;
+}
+
+template <typename T>
+__device__ __forceinline__ void la_floats(const LaFrag<T>& f, float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        unpack_bf16x8(f.v, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = f.v[e];
+    }
+}
+
+// 64 x PPR 16-byte pieces of rows 64 c .. 64 c + 63 (in the pass's order) into
+// registers; rows behind the last token and pieces behind the width are zero.
+template <int N, int PPR, int NTHR>
+__device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_t row_bytes, int c, bool rev, int L,
+                                         int pieces, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int idx = tid + i * NTHR;
+        const int row = idx / PPR, p = idx % PPR;
+        const int t = 64 * c + (rev ? 63 - row : row);
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < L && p < pieces) r[i] = *reinterpret_cast<const uint4*>(base + t * row_bytes + 16 * p);
+    }
+}
+template <int N, int PPR, int NTHR>
+__device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int idx = tid + i * NTHR;
+        const int row = idx / PPR, p = idx % PPR;
+        lds_st(tile + row * (PPR * 16) + 16 * (p ^ la_swz<PPR * 16>(row)), r[i]);
+    }
+}
+
+// Running sum of x over the wave's lanes, each lane's own value included.
+__device__ __forceinline__ double la_scan(double x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+constexpr int kLaGateBytes = 4 * 64 * 4 + 16;   // u hi, u lo, e^u, e^{total - u}, e^total
+
+template <typename T, int DX, int NW, bool STATE>
+constexpr int la_lds_bytes() {
+    return (STATE ? 1 : 2) * 64 * DX * (int)sizeof(T) + 64 * 32 * NW * (int)sizeof(T) + kLaGateBytes;
+}
+
+// waves per SIMD that the registers are held to: two for bf16 with up to 64
+// columns or four waves; one for fp32, whose tiles fill the LDS of a CU
+template <typename T, int NW>
+constexpr int la_waves() { return sizeof(T) == 2 && NW > 1 ? 2 : 1; }
+
+template <typename T, int DX, int NW, int NT, bool STATE>
+__global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs a) {
+    constexpr int NTHR = 64 * NW;
+    constexpr int EPP = 16 / (int)sizeof(T);         // elements per piece
+    constexpr int PX = DX / EPP, PZ = 32 * NW / EPP; // pieces per row
+    constexpr int RX = PX * 16, RZ = PZ * 16;        // bytes per row
+    constexpr int NX = 64 * PX / NTHR, NZ = 64 * PZ / NTHR;
+    constexpr int TX = DX / 32;                      // 32-row tiles of the state
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    lchar* const sY = (lchar*)smem;
+    lchar* const sZ = sY + 64 * RX;
+    lchar* const sG = sZ + 64 * RZ;
+    lchar* const sX = sG + kLaGateBytes;             // not with STATE
+
+    // Workgroups go to the eight XCDs in turn; consecutive work (the column
+    // tiles of a sequence, heads that share rows) stays on one of them.
+    const int per = (a.total + 7) / 8;
+    int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if (id >= a.total || (int)(blockIdx.x >> 3) >= per) return;
+    const int ct = id % a.ntile;
+    id /= a.ntile;
+    const int nseq = a.B * a.H;
+    const int seq = id % nseq;
+    id /= nseq;
+    const int sg = id % a.nseg;
+    const LaPass& ps = a.pass[id / a.nseg];
+    const int b = seq / a.H, hd = seq % a.H;
+    const bool rev = ps.rev != 0;
+    // nothing starts from behind the last segment
+    if (STATE && sg == (rev ? 0 : a.nseg - 1)) return;
+
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, h = lane >> 5, l31 = lane & 31;
+    const int zc0 = (ct * NW + wave) * kLaCols;      // the wave's first column
+    const int Dx = ps.Dx, Dz = ps.Dz;
+    const int px = Dx / EPP, pz = (Dz - ct * NW * kLaCols) / EPP;
+    const char* gx = nullptr;
+    if constexpr (!STATE)
+        gx = (const char*)ps.x.p + sizeof(T) * (b * ps.x.b + (hd / ps.x.group) * ps.x.h);
+    const char* gy = (const char*)ps.y.p + sizeof(T) * (b * ps.y.b + (hd / ps.y.group) * ps.y.h);
+    const char* gz = (const char*)ps.z.p + sizeof(T) * (b * ps.z.b + (hd / ps.z.group) * ps.z.h + ct * NW * kLaCols);
+    const int64_t bx = sizeof(T) * ps.x.t, by = sizeof(T) * ps.y.t, bz = sizeof(T) * ps.z.t;
+    const float* la = a.la ? (a.la_head ? a.la + hd : a.la + (size_t)seq * a.L) : nullptr;
+
+    // the state, from its start
+    f32x16 S[TX];
+    const float* start = nullptr;
+    const size_t elems = (size_t)Dx * Dz;
+    if constexpr (!STATE)
+        start = a.nseg > 1 ? ps.seg + ((size_t)seq * a.nseg + sg) * elems : ps.start ? ps.start + seq * elems : nullptr;
+    const int zc = zc0 + l31;
+#pragma unroll
+    for (int t = 0; t < TX; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int d = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
+            float v = 0.f;
+            if (!STATE && start && d < Dx && zc < Dz)
+                v = ps.tr ? start[(size_t)zc * Dx + d] : start[(size_t)d * Dz + zc];
+            S[t][r] = v;
+        }
+
+    const int c_lo = sg * a.cps, c_hi = min(a.NC, c_lo + a.cps);
+    const int nc = c_hi - c_lo;
+    double seg_total = 0.0;   // wave 0: the segment's sum of log2 alpha
+
+    uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
+    auto fetch = [&](int n) {
+        const int c = rev ? c_hi - 1 - n : c_lo + n;
+        if constexpr (!STATE) la_fetch<NX, PX, NTHR>(rx, gx, bx, c, rev, a.L, px, tid);
+        la_fetch<NX, PX, NTHR>(ry, gy, by, c, rev, a.L, px, tid);
+        la_fetch<NZ, PZ, NTHR>(rz, gz, bz, c, rev, a.L, pz, tid);
+    };
+    fetch(0);
+
+    for (int n = 0; n < nc; ++n) {
+        const int c = rev ? c_hi - 1 - n : c_lo + n;
+        if (n) __syncthreads();   // the last chunk's tiles are done with
+        if constexpr (!STATE) la_stage<NX, PX, NTHR>(sX, rx, tid);
+        la_stage<NX, PX, NTHR>(sY, ry, tid);
+        la_stage<NZ, PZ, NTHR>(sZ, rz, tid);
+        if (wave == 0) {
+            const int t = 64 * c + (rev ? 63 - lane : lane);
+            double l2 = 0.0;
+            if (la && t < a.L) {
+                const float x = la[a.la_head ? 0 : t];
+                l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
+            }
+            const double s = la_scan(l2, lane);
+            const double total = __shfl(s, 63);
+            const double u = rev ? s - l2 : s;
+            const float uh = (float)u;
+            lds_st(sG + 4 * lane, uh);
+            lds_st(sG + 256 + 4 * lane, (float)(u - (double)uh));
+            lds_st(sG + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
+            lds_st(sG + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
+            if (lane == 0) lds_st(sG + 1024, __builtin_amdgcn_exp2f((float)total));
+            if constexpr (STATE) seg_total += total;
+        }
+        __syncthreads();
+        if (n + 1 < nc) fetch(n + 1);
+
+        f32x16 O[2], P[3];   // O^T: columns by rows; products y . x of tiles (0,0), (0,1), (1,1)
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = P[0][r] = P[1][r] = P[2][r] = 0.f;
+#pragma unroll
+            for (int m = 0; m < DX / 16; ++m) {
+                const LaFrag<T> x0 = la_row<T, RX>(sX, l31, m, h), x1 = la_row<T, RX>(sX, 32 + l31, m, h);
+                const LaFrag<T> y0 = la_row<T, RX>(sY, l31, m, h), y1 = la_row<T, RX>(sY, 32 + l31, m, h);
+                float s8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s8[e] = S[m >> 1][8 * (m & 1) + e];
+                const LaTerms<T, NT> st = la_split<T, NT>(s8);
+                O[0] = la_mma(st, x0, O[0]);
+                O[1] = la_mma(st, x1, O[1]);
+                P[0] = la_mma(y0, x0, P[0]);
+                P[1] = la_mma(y0, x1, P[1]);
+                P[2] = la_mma(y1, x1, P[2]);
+            }
+        }
+        const float decay = lds_ld<float>(sG + 1024);
+#pragma unroll
+        for (int t = 0; t < TX; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+        float uh[2], ul[2];
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                uh[it] = lds_ld<float>(sG + 4 * (32 * it + l31));
+                ul[it] = lds_ld<float>(sG + 256 + 4 * (32 * it + l31));
+                const float e = lds_ld<float>(sG + 512 + 4 * (32 * it + l31));
+#pragma unroll
+                for (int r = 0; r < 16; ++r) O[it][r] *= e;
+            }
+        }
+        // rows 16 ks .. 16 ks + 15 of y and z: into the output's later rows, then into the state
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const LaFrag<T> z = la_col<T, RZ>(sZ, ks, wave * kLaCols, lane);
+            const int j0 = 16 * ks + 4 * h;   // the lane's rows: j0 + [0, 4) and j0 + 8 + [0, 4)
+            if constexpr (!STATE) {
+                const f32x4 h0 = lds_ld<f32x4>(sG + 4 * j0), h1 = lds_ld<f32x4>(sG + 4 * j0 + 32);
+                const f32x4 w0 = lds_ld<f32x4>(sG + 256 + 4 * j0), w1 = lds_ld<f32x4>(sG + 256 + 4 * j0 + 32);
+#pragma unroll
+                for (int it = ks >> 1; it < 2; ++it) {
+                    const f32x16& pt = P[(ks >> 1) + it];
+                    float p8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float hj = e < 4 ? h0[e & 3] : h1[e & 3], wj = e < 4 ? w0[e & 3] : w1[e & 3];
+                        const float d = (uh[it] - hj) + (ul[it] - wj);
+                        const float v = pt[8 * (ks & 1) + e] * __builtin_amdgcn_exp2f(d);
+                        const bool ok = it > (ks >> 1) || j0 + 8 * (e >> 2) + (e & 3) <= 32 * it + l31;
+                        p8[e] = ok ? v : 0.f;
+                    }
+                    O[it] = la_mma(z, la_split<T, NT>(p8), O[it]);
+                }
+            }
+            const f32x4 k0 = lds_ld<f32x4>(sG + 768 + 4 * j0), k1 = lds_ld<f32x4>(sG + 768 + 4 * j0 + 32);
+            float z8[8];
+            la_floats(z, z8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z8[e] *= e < 4 ? k0[e & 3] : k1[e & 3];
+            const LaTerms<T, 3> zt = la_split<T, 3>(z8);
+#pragma unroll
+            for (int t = 0; t < TX; ++t) S[t] = la_mma(la_col<T, RX>(sY, ks, 32 * t, lane), zt, S[t]);
+        }
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                const int row = 32 * it + l31;
+                const int t = 64 * c + (rev ? 63 - row : row);
+                const bool ok = t < a.L;
+                float dot = 0.f;
+                const int64_t at = b * ps.ob + hd * ps.oh + t * ps.ot;
+                const int64_t wat = b * ps.w.b + (hd / ps.w.group) * ps.w.h + t * ps.w.t;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = zc0 + 8 * q + 4 * h;
+                    if (!ok || col >= Dz) continue;
+                    f32x4 v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = O[it][4 * q + j];
+                    if (ps.w.p) {
+                        float w4[4];
+                        load_n<sizeof(T) == 4, 4>(ps.w.p, (size_t)(wat + col), w4);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dot += v[j] * w4[j];
+                    }
+                    if (ps.out_bf16)
+                        *reinterpret_cast<bf16x4*>((__bf16*)ps.out + at + col) = __builtin_convertvector(v, bf16x4);
+                    else
+                        *reinterpret_cast<f32x4*>((float*)ps.out + at + col) = v;
+                }
+                if (ps.w.p) {
+                    dot += __shfl_xor(dot, 32);
+                    if (ok && h == 0 && zc0 < Dz)
+                        ps.dots[((size_t)(zc0 / kLaCols) * nseq + seq) * a.L + t] = dot;
+                }
+            }
+        }
+    }
+
+    float* end = nullptr;
+    if constexpr (STATE) {
+        end = ps.seg + ((size_t)seq * a.nseg + sg) * elems;
+        if (ct == 0 && tid == 0) ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
+    } else if (ps.end && sg == (rev ? 0 : a.nseg - 1)) {
+        end = ps.end + seq * elems;
+    }
+    if (end && zc < Dz) {
+#pragma unroll
+        for (int t = 0; t < TX; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int d = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (d < Dx) end[ps.tr ? (size_t)zc * Dx + d : (size_t)d * Dz + zc] = S[t][r];
+            }
+    }
+}
+
+template <typename T, int DX, int NW, int NT, bool STATE>
+hipError_t la_launch(const LaArgs& a, int slot, hipStream_t st) {
+    auto kern = la_kernel<T, DX, NW, NT, STATE>;
+    constexpr int lds = la_lds_bytes<T, DX, NW, STATE>();
+    if constexpr (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    const unsigned grid = (unsigned)((a.total + 7) / 8 * 8);
+    return launch_k(slot, kern, dim3(grid), dim3(64 * NW), lds, st, a);
+}
+
+template <typename T, int DX, int NT, bool STATE>
+hipError_t la_launch_w(const LaArgs& a, int waves, int slot, hipStream_t st) {
+    if (waves == 4) return la_launch<T, DX, 4, NT, STATE>(a, slot, st);
+    if (waves == 2) return la_launch<T, DX, 2, NT, STATE>(a, slot, st);
+    return la_launch<T, DX, 1, NT, STATE>(a, slot, st);
+}
+
+}  // namespace dr

@@ -97,7 +97,7 @@
 extern "C" {
 #endif
 
-#define DR_ABI_VERSION 10
+#define DR_ABI_VERSION 11
 
 typedef enum {
     DR_OK = 0,
@@ -434,9 +434,194 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
                                size_t workspace_bytes, void* stream);
 
 /*
+ * Linear attention with a decay for each head, the recurrence without the
+ * erase term:
+ *
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t
+ *
+ * chunked over whole sequences (dr_linear_attn_fwd), its gradients
+ * (dr_linear_attn_bwd) and one token for many states (dr_linear_attn_step).
+ * Every (batch, head) has a d_k x d_v state of its own.
+ *
+ * alpha_t = e^{log_alpha}:
+ *   DR_DECAY_NONE   1
+ *   DR_DECAY_HEAD   one constant per head, log_alpha [H]
+ *   DR_DECAY_TOKEN  one value per token and head, log_alpha [B][H][L]
+ * log_alpha is fp32, expected <= 0 (not checked; larger values grow the state).
+ * -inf (alpha = 0) starts the state anew at that token; its gradient is 0.
+ * Any size of decay is exact to fp32: nothing is divided by a decay.
+ *
+ * Heads.  q and k have Hk heads, Hk a divisor of H: state head h reads q and k
+ * head h / (H / Hk).  Their gradients are summed over the heads that share them.
+ * Dk, Dv: multiples of 8 in [8, 128].
+ *
+ * Strides.  q, k, v, o (and dO) are rows of contiguous channels; the strides
+ * between batches, heads and tokens are free (elements, not negative, whole
+ * multiples of 16 bytes; 0 repeats a row; ignored where the dimension is 1), so
+ * that [B][L][H][D] projections, or slices of a fused one, are passed as they
+ * are.  An output's rows must not overlap each other.  log_alpha and the states
+ * are dense.
+ *
+ * Numerics.  Accumulations and the state are fp32; running sums of log_alpha
+ * are fp64.  bf16 inputs are matrix-core operands as they are; the state and
+ * every fp32 quantity they meet are carried in two or three bf16 terms, so that
+ * fp32 results are fp32-accurate and bf16 results are rounded once.  There is
+ * no limit on magnitudes but that of fp32.  A NaN or Inf in a row reaches every
+ * row of its 64-token chunk and the later ones, also through a zero decay.
+ * Every sum has a fixed order: repeated calls give the same bits.
+ */
+typedef enum { DR_DECAY_NONE = 0, DR_DECAY_HEAD = 1, DR_DECAY_TOKEN = 2 } dr_decay_mode;
+
+/* Elements between consecutive batches, heads and tokens of a row tensor. */
+typedef struct {
+    long long b, h, t;
+} dr_strides;
+
+/* Shapes, modes and strides of the chunked linear attention.
+ *   B, H, L >= 0 as in dr_chunk_desc; Hk >= 1 heads of q and k.
+ *   in_dtype types q, k, v and dO; out_dtype types o, and dq, dk, dv.
+ *   o strides o, or dO in the backward; dq, dk, dv are the gradients' strides
+ *   (ignored by the forward). */
+typedef struct {
+    int B, H, Hk, L, Dk, Dv;
+    dr_dtype in_dtype;
+    dr_dtype out_dtype;
+    dr_decay_mode decay;
+    dr_strides q, k, v, o;
+    dr_strides dq, dk, dv;
+} dr_linattn_desc;
+
+/* One token for N x H states; tensors dense. */
+typedef struct {
+    int N, H, Hk, Dk, Dv;
+    dr_dtype in_dtype;
+    dr_dtype out_dtype;
+    dr_decay_mode decay;
+} dr_linattn_step_desc;
+
+/* Bytes of device workspace dr_linear_attn_fwd needs for `d` (0 if d is invalid
+ * or none is needed): with few sequences a long one is cut into segments, one
+ * fp32 state each. */
+size_t dr_linear_attn_fwd_workspace_bytes(const dr_linattn_desc* d);
+
+/*
+ * dr_linear_attn_fwd -- o_t for t = 0..L-1 and S_L, from S0.
+ *
+ *   q, k       [B][Hk][L][Dk] in_dtype, strided
+ *   v          [B][H][L][Dv]  in_dtype, strided
+ *   log_alpha  [H] (DECAY_HEAD) or [B][H][L] (DECAY_TOKEN) fp32; NULL iff
+ *              decay == DR_DECAY_NONE
+ *   S0         [B][H][Dk][Dv] fp32, or NULL for zeros
+ *   o          [B][H][L][Dv]  out_dtype, strided, written
+ *   S_final    [B][H][Dk][Dv] fp32, written, or NULL to skip; may be S0 itself
+ *   workspace  at least dr_linear_attn_fwd_workspace_bytes(d) bytes
+ * The conventions at the top of this file hold.  Calls in flight at the same
+ * time need workspaces of their own.
+ */
+dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void* k, const void* v,
+                             const float* log_alpha, const float* S0, void* o, float* S_final, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace dr_linear_attn_bwd needs for `d` (0 if d is invalid
+ * or there is no work): the segments' states twice; with a decay one state per
+ * sequence and two floats per token and 32 key channels; with shared heads
+ * fp32 gradients of q and k for every state head. */
+size_t dr_linear_attn_bwd_workspace_bytes(const dr_linattn_desc* d);
+
+/*
+ * dr_linear_attn_bwd -- gradients of dr_linear_attn_fwd's o and S_final with
+ * respect to its inputs, for the loss whose gradients with respect to o and
+ * S_final are dO and dS_final.  Nothing of the forward's is needed but its
+ * inputs.
+ *
+ *   dO          [B][H][L][Dv]  in_dtype, strided as d->o
+ *   dS_final    [B][H][Dk][Dv] fp32, or NULL (zero)
+ *   dq, dk      [B][Hk][L][Dk] out_dtype, strided, written
+ *   dv          [B][H][L][Dv]  out_dtype, strided, written
+ *   dlog_alpha  log_alpha's shape, fp32, written; NULL iff DR_DECAY_NONE
+ *   dS0         [B][H][Dk][Dv] fp32, written, or NULL to skip
+ *   workspace   at least dr_linear_attn_bwd_workspace_bytes(d) bytes
+ * Outputs must not overlap each other or any input (whole byte ranges, from a
+ * tensor's first element to its last).
+ */
+dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void* k, const void* v,
+                             const float* log_alpha, const float* S0, const void* dO, const float* dS_final, void* dq,
+                             void* dk, void* dv, float* dlog_alpha, float* dS0, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * dr_linear_attn_step -- one token for N x H independent states, in place:
+ *
+ *   S[n][h] <- alpha S[n][h] + k v^T,   o[n][h] = S[n][h]^T q
+ *
+ *   q, k       [N][Hk][Dk] in_dtype;  v [N][H][Dv] in_dtype
+ *   log_alpha  [H] (DECAY_HEAD) or [N][H] (DECAY_TOKEN) fp32, NULL iff NONE
+ *   S          [N][H][Dk][Dv] fp32, read and overwritten
+ *   o          [N][H][Dv] out_dtype, written; must not overlap S or the inputs
+ * Equivalent to dr_linear_attn_fwd with L == 1, S0 == S_final == S.
+ */
+dr_status dr_linear_attn_step(const dr_linattn_step_desc* d, const void* q, const void* k, const void* v,
+                              const float* log_alpha, float* S, void* o, void* stream);
+
+/*
+ * Layer norm over the channels of rows, as a layer applies it to the
+ * attention's output (a weight for each head) or to its model-width rows (one
+ * weight), and its backward pass:
+ *
+ *   y  = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps)
+ *   dx = rstd (t - mean(t) - n mean(t n)),  n = (x - mean) rstd, t = dy weight
+ *   dweight = sum of dy n,  dbias = sum of dy  over the rows that share them
+ *
+ * var is the mean of (x - mean)^2.  All arithmetic is fp32, every sum in a
+ * fixed order; y and dx are rounded once.
+ *
+ *   B, H, L >= 0 rows [B][H][L] (at most 2^31 - 1) of D in [1, 16384] values;
+ *   plain [N][D] rows are B = H = 1, L = N.
+ *   per_head   1: weight and bias [H][D], one row per head; 0: [D]
+ *   x_dtype, y_dtype, dy_dtype  of x; of y or dx; of dy (backward)
+ *   x, y, dy   strides of x; of y or dx; of dy (free, not negative, 0 repeats a
+ *              row of an input; any alignment: rows whose strides and D are
+ *              multiples of 8 run on 16-byte accesses)
+ */
+typedef struct {
+    int B, H, L, D;
+    int per_head;
+    dr_dtype x_dtype, y_dtype, dy_dtype;
+    float eps;
+    dr_strides x, y, dy;
+} dr_layernorm_desc;
+
+/*
+ * dr_layernorm_fwd
+ *   x      [B][H][L][D] x_dtype, strided
+ *   weight, bias  [H][D] or [D] fp32, or NULL (ones, zeros)
+ *   y      [B][H][L][D] y_dtype, strided, written; must not overlap an input
+ *   mean, rstd    [B][H][L] fp32, written, or NULL to skip
+ */
+dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const float* weight, const float* bias, void* y,
+                           float* mean, float* rstd, void* stream);
+
+/* Bytes of device workspace dr_layernorm_bwd needs for `d` when dweight or
+ * dbias is wanted (0 if d is invalid or there are no rows). */
+size_t dr_layernorm_bwd_workspace_bytes(const dr_layernorm_desc* d);
+
+/*
+ * dr_layernorm_bwd
+ *   mean, rstd  [B][H][L] fp32, as the forward wrote them
+ *   dy          [B][H][L][D] dy_dtype, strided
+ *   dx          [B][H][L][D] y_dtype, strided as d->y, written
+ *   dweight, dbias  [H][D] or [D] fp32, written, or NULL to skip
+ *   workspace   at least dr_layernorm_bwd_workspace_bytes(d) bytes; may be NULL
+ *               when both dweight and dbias are
+ */
+dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const float* weight, const float* mean,
+                           const float* rstd, const void* dy, void* dx, float* dweight, float* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Per-kernel timing, for benchmarks and profiling (not part of the method).
- * Between dr_profile_begin and dr_profile_end every chunked-forward, backward
- * and decode call launches each of its kernels with a start and a stop event
+ * Between dr_profile_begin and dr_profile_end every chunked-forward, backward,
+ * decode, linear-attention and layer-norm call launches each of its kernels with a start and a stop event
  * of its own, set from the kernel dispatch's timestamps (no marker packets
  * between the kernels); dr_profile_end waits for those events and reports the
  * summed kernel durations.  Calls made while profiling must come from one
@@ -457,6 +642,11 @@ typedef struct dr_profile_report {
     double bwd_fscan_ms;  /* backward: forward state scan (chunk start states) */
     double bwd_rscan_ms;  /* backward: reverse scan of the state gradient */
     double bwd_post_ms;   /* backward: per-chunk gradients of q, k, beta, log alpha */
+    double linear_attn_fwd_ms;   /* every kernel of dr_linear_attn_fwd calls */
+    double linear_attn_bwd_ms;   /* of dr_linear_attn_bwd calls */
+    double linear_attn_step_ms;  /* of dr_linear_attn_step calls */
+    double layernorm_fwd_ms;     /* of dr_layernorm_fwd calls */
+    double layernorm_bwd_ms;     /* of dr_layernorm_bwd calls */
 } dr_profile_report;
 
 dr_status dr_profile_begin(void);
