@@ -48,7 +48,7 @@ struct LaPass {
 };
 
 struct LaArgs {
-    LaPass pass[2];      // one or two passes in one launch (the same Dx class)
+    LaPass pass[3];      // one to three passes in one launch (of one Dx class and tiling)
     int npass;
     const float* la;     // log alpha: [H] (la_head), [B][H][L], or NULL
     int la_head;

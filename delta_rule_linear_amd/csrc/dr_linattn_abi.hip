@@ -50,6 +50,9 @@ dr_status check_strides(const Rows& r, bool vec) {
         if (s[i] < 0) return fail(DR_ERR_SHAPE, "%s has a negative stride (%lld)", r.name, (long long)s[i]);
         if (vec && s[i] % unit)
             return fail(DR_ERR_ALIGN, "%s: stride %lld is not a multiple of 16 bytes", r.name, (long long)s[i]);
+        if (vec && i == 2 && s[i] > ((int64_t)1 << 23))
+            return fail(DR_ERR_UNSUPPORTED, "%s: tokens %lld elements apart, at most 2^23 are supported", r.name,
+                        (long long)s[i]);
         if (s[i] > ((int64_t)1 << 48)) return fail(DR_ERR_SHAPE, "%s: stride %lld too large", r.name, (long long)s[i]);
     }
     return DR_OK;
@@ -135,7 +138,7 @@ int64_t seqs(const dr_linattn_desc& d) { return (int64_t)d.B * d.H; }
 LaLayout la_layout(const dr_linattn_desc& d, bool bwd) {
     LaLayout w{};
     const size_t nseq = (size_t)seqs(d), elems = (size_t)d.Dk * d.Dv;
-    w.split = la_split_of(d.L, (int64_t)nseq * (bwd ? 2 * tiles_of(d.Dk) + tiles_of(d.Dv) : tiles_of(d.Dv)));
+    w.split = la_split_of(d.L, (int64_t)nseq * (bwd ? std::max(tiles_of(d.Dk), tiles_of(d.Dv)) : tiles_of(d.Dv)));
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -190,7 +193,7 @@ dr_status hip_status(hipError_t e, const char* what) {
     return e == hipSuccess ? DR_OK : fail(DR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-// One launch of a pass, or of two of the same shape.
+// One launch of passes that run in the same kernel on the same tiling.
 hipError_t run_passes(dr::LaArgs a, const dr::LaPass* p, int n, bool f32in, int terms, bool state_only, int slot,
                       hipStream_t st) {
     const int dx = p[0].Dx <= 64 ? 64 : 128, waves = waves_of(p[0].Dz);
@@ -388,7 +391,8 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
     }
 
     // dq and dk (contraction over d_v), then dv (over d_k)
-    dr::LaPass p[2] = {}, pv{};
+    dr::LaPass p[3] = {};
+    dr::LaPass& pv = p[2];
     p[0].x = tdo;
     p[0].y = tv;
     p[0].z = tk;
@@ -422,9 +426,6 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
             p[i].out_bf16 = od == DR_BF16;
         }
     }
-    const int terms = gate || group > 1 || od == DR_F32 ? 3 : 2;
-    s = hip_status(run_passes(a, p, 2, f32in, terms, false, slot, st), "dq and dk launch");
-    if (s != DR_OK) return s;
     pv.x = tk;
     pv.y = tq;
     pv.z = tdo;
@@ -441,8 +442,14 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
     pv.out_bf16 = od == DR_BF16;
     pv.Dx = d->Dk;
     pv.Dz = d->Dv;
-    s = hip_status(run_passes(a, &pv, 1, f32in, od == DR_F32 ? 3 : 2, false, slot, st), "dv launch");
+    const int terms = gate || group > 1 || od == DR_F32 ? 3 : 2;
+    const bool one = (d->Dk <= 64) == (d->Dv <= 64) && waves_of(d->Dk) == waves_of(d->Dv);
+    s = hip_status(run_passes(a, p, one ? 3 : 2, f32in, terms, false, slot, st), "gradient launch");
     if (s != DR_OK) return s;
+    if (!one) {
+        s = hip_status(run_passes(a, &pv, 1, f32in, od == DR_F32 ? 3 : 2, false, slot, st), "dv launch");
+        if (s != DR_OK) return s;
+    }
 
     if (gate) {
         dr::LaGateArgs g{};

@@ -190,19 +190,46 @@ __device__ __forceinline__ void la_floats(const LaFrag<T>& f, float (&x)[8]) {
     }
 }
 
-// 64 x PPR 16-byte pieces of rows 64 c .. 64 c + 63 (in the pass's order) into
-// registers; rows behind the last token and pieces behind the width are zero.
+// A value that the compiler takes as new here, so that what follows from it is
+// computed in the loop and not held in registers across it.
+__device__ __forceinline__ int la_fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// 64 x PPR 16-byte pieces of a chunk's rows (in the pass's order) into
+// registers.  A thread takes the same piece of rows row0 + i STEP; `base` (the
+// chunk's first token, the same for all lanes) moves by STEP rows at a time and
+// `off` is the thread's own part, so that the addresses are a scalar base and
+// one 32-bit offset.  Rows behind the last token and (ok) pieces behind the
+// width are zero.
 template <int N, int PPR, int NTHR>
-__device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_t row_bytes, int c, bool rev, int L,
-                                         int pieces, int tid) {
+__device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_t row_bytes, unsigned off, bool rev,
+                                         int rows, bool ok, int tid) {
+    constexpr int STEP = NTHR / PPR;
+    const int row0 = tid / PPR;
+    if (rows >= 64) {
+        if (ok) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int idx = tid + i * NTHR;
-        const int row = idx / PPR, p = idx % PPR;
-        const int t = 64 * c + (rev ? 63 - row : row);
-        r[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < L && p < pieces) r[i] = *reinterpret_cast<const uint4*>(base + t * row_bytes + 16 * p);
+            for (int i = 0; i < N; ++i)
+                r[i] = *reinterpret_cast<const uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * row_bytes + off);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int row = row0 + i * STEP;
+            r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (ok && (rev ? 63 - row : row) < rows)
+                r[i] = *reinterpret_cast<const uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * row_bytes + off);
+        }
     }
+}
+// The thread's part of la_fetch's addresses.
+template <int PPR, int NTHR>
+__device__ __forceinline__ unsigned la_offset(int64_t row_bytes, bool rev, int tid) {
+    constexpr int STEP = NTHR / PPR;
+    const int row0 = tid / PPR;
+    return (unsigned)(rev ? STEP - 1 - row0 : row0) * (unsigned)row_bytes + 16 * (tid % PPR);
 }
 template <int N, int PPR, int NTHR>
 __device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int tid) {
@@ -214,25 +241,39 @@ __device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int t
     }
 }
 
-// Running sum of x over the wave's lanes, each lane's own value included.
-__device__ __forceinline__ double la_scan(double x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    return x;
+// One step of a running sum on DPP moves: x plus the value that CTRL brings
+// (zero where it brings none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double la_scan_step(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xF, false);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xF, false);
+    return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Running sum of x over the wave's lanes, each lane's own value included:
+// shifts by 1, 2, 4 and 8 within rows of 16 lanes, then a row's sum to the
+// next row (rows 1 and 3) and the lower half's to the upper half.
+__device__ __forceinline__ double la_scan(double x) {
+    x = la_scan_step<0x111, 0xF>(x);
+    x = la_scan_step<0x112, 0xF>(x);
+    x = la_scan_step<0x114, 0xF>(x);
+    x = la_scan_step<0x118, 0xF>(x);
+    x = la_scan_step<0x142, 0xA>(x);
+    return la_scan_step<0x143, 0xC>(x);
 }
 
-constexpr int kLaGateBytes = 4 * 64 * 4 + 16;   // u hi, u lo, e^u, e^{total - u}, e^total
+// The decays of a chunk in LDS: u as hi + lo floats, e^u, e^{total - u}, and
+// e^total; two buffers, the next chunk's made while this one's are read.
+constexpr int kLaGateBytes = 4 * 64 * 4 + 16;
 
-template <typename T, int DX, int NW, bool STATE>
+template <typename T, int DX, int NW, int NT, bool STATE>
 constexpr int la_lds_bytes() {
-    return (STATE ? 1 : 2) * 64 * DX * (int)sizeof(T) + 64 * 32 * NW * (int)sizeof(T) + kLaGateBytes;
+    constexpr int y = 64 * DX * (int)sizeof(T), z = 64 * 32 * NW * (int)sizeof(T);
+    return (STATE ? y + z : 2 * y + z + 64 * 64 * (int)sizeof(T) * (sizeof(T) == 2 ? NT : 1)) + 2 * kLaGateBytes;
 }
 
-// waves per SIMD that the registers are held to: two for bf16 with up to 64
-// columns or four waves; one for fp32, whose tiles fill the LDS of a CU
+// waves per SIMD that the registers are held to: two for bf16, one for fp32,
+// whose tiles fill the LDS of a CU
 template <typename T, int NW>
 constexpr int la_waves() { return sizeof(T) == 2 && NW > 1 ? 2 : 1; }
 
@@ -242,13 +283,15 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     constexpr int EPP = 16 / (int)sizeof(T);         // elements per piece
     constexpr int PX = DX / EPP, PZ = 32 * NW / EPP; // pieces per row
     constexpr int RX = PX * 16, RZ = PZ * 16;        // bytes per row
+    constexpr int RP = 64 * (int)sizeof(T);          // of the products x . y (each term)
     constexpr int NX = 64 * PX / NTHR, NZ = 64 * PZ / NTHR;
     constexpr int TX = DX / 32;                      // 32-row tiles of the state
     extern __shared__ __attribute__((aligned(16))) char smem[];
     lchar* const sY = (lchar*)smem;
     lchar* const sZ = sY + 64 * RX;
     lchar* const sG = sZ + 64 * RZ;
-    lchar* const sX = sG + kLaGateBytes;             // not with STATE
+    lchar* const sX = sG + 2 * kLaGateBytes;         // not with STATE
+    lchar* const sP = sX + 64 * RX;
 
     // Workgroups go to the eight XCDs in turn; consecutive work (the column
     // tiles of a sequence, heads that share rows) stays on one of them.
@@ -267,7 +310,9 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     // nothing starts from behind the last segment
     if (STATE && sg == (rev ? 0 : a.nseg - 1)) return;
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, h = lane >> 5, l31 = lane & 31;
+    const int tid = threadIdx.x, lane0 = tid & 63;
+    int lane = lane0, h = lane >> 5, l31 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int zc0 = (ct * NW + wave) * kLaCols;      // the wave's first column
     const int Dx = ps.Dx, Dz = ps.Dz;
     const int px = Dx / EPP, pz = (Dz - ct * NW * kLaCols) / EPP;
@@ -299,103 +344,155 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 
     const int c_lo = sg * a.cps, c_hi = min(a.NC, c_lo + a.cps);
     const int nc = c_hi - c_lo;
-    double seg_total = 0.0;   // wave 0: the segment's sum of log2 alpha
+    const bool gate_wave = wave == NW - 1;
+    double seg_total = 0.0;   // the gate wave's: the segment's sum of log2 alpha
 
     uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
+    auto chunk = [&](int n) { return rev ? c_hi - 1 - n : c_lo + n; };
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        if constexpr (!STATE) rx[i] = make_uint4(0u, 0u, 0u, 0u);
+        ry[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) rz[i] = make_uint4(0u, 0u, 0u, 0u);
+    const bool okx = tid % PX < px, okz = tid % PZ < pz;
+    const unsigned fx = STATE ? 0 : la_offset<PX, NTHR>(bx, rev, tid), fy = la_offset<PX, NTHR>(by, rev, tid),
+                   fz = la_offset<PZ, NTHR>(bz, rev, tid);
     auto fetch = [&](int n) {
-        const int c = rev ? c_hi - 1 - n : c_lo + n;
-        if constexpr (!STATE) la_fetch<NX, PX, NTHR>(rx, gx, bx, c, rev, a.L, px, tid);
-        la_fetch<NX, PX, NTHR>(ry, gy, by, c, rev, a.L, px, tid);
-        la_fetch<NZ, PZ, NTHR>(rz, gz, bz, c, rev, a.L, pz, tid);
+        const int c = chunk(n), rows = a.L - 64 * c;
+        if constexpr (!STATE) la_fetch<NX, PX, NTHR>(rx, gx + 64 * c * bx, bx, fx, rev, rows, okx, tid);
+        la_fetch<NX, PX, NTHR>(ry, gy + 64 * c * by, by, fy, rev, rows, okx, tid);
+        la_fetch<NZ, PZ, NTHR>(rz, gz + 64 * c * bz, bz, fz, rev, rows, okz, tid);
+    };
+    auto log_alpha = [&](int n) {
+        const int t = 64 * chunk(n) + (rev ? 63 - lane : lane);
+        return la && t < a.L ? la[a.la_head ? 0 : t] : 0.f;
+    };
+    auto decays = [&](int n, float x) {
+        lchar* g = sG + (n & 1) * kLaGateBytes;
+        const double l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
+        const double s = la_scan(l2);
+        const double total = __shfl(s, 63);
+        const double u = rev ? s - l2 : s;
+        const float uh = (float)u;
+        lds_st(g + 4 * lane, uh);
+        lds_st(g + 256 + 4 * lane, (float)(u - (double)uh));
+        lds_st(g + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
+        lds_st(g + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
+        if (lane == 0) lds_st(g + 1024, __builtin_amdgcn_exp2f((float)total));
+        if constexpr (STATE) seg_total += total;
     };
     fetch(0);
+    if (gate_wave) decays(0, log_alpha(0));
 
     for (int n = 0; n < nc; ++n) {
-        const int c = rev ? c_hi - 1 - n : c_lo + n;
-        if (n) __syncthreads();   // the last chunk's tiles are done with
+        const int c = chunk(n);
+        const lchar* g = sG + (n & 1) * kLaGateBytes;
+        if (n) lds_barrier();   // the last chunk's tiles are done with
         if constexpr (!STATE) la_stage<NX, PX, NTHR>(sX, rx, tid);
         la_stage<NX, PX, NTHR>(sY, ry, tid);
         la_stage<NZ, PZ, NTHR>(sZ, rz, tid);
-        if (wave == 0) {
-            const int t = 64 * c + (rev ? 63 - lane : lane);
-            double l2 = 0.0;
-            if (la && t < a.L) {
-                const float x = la[a.la_head ? 0 : t];
-                l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
-            }
-            const double s = la_scan(l2, lane);
-            const double total = __shfl(s, 63);
-            const double u = rev ? s - l2 : s;
-            const float uh = (float)u;
-            lds_st(sG + 4 * lane, uh);
-            lds_st(sG + 256 + 4 * lane, (float)(u - (double)uh));
-            lds_st(sG + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
-            lds_st(sG + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
-            if (lane == 0) lds_st(sG + 1024, __builtin_amdgcn_exp2f((float)total));
-            if constexpr (STATE) seg_total += total;
+        lds_barrier();
+        lane = la_fresh(lane0);
+        h = lane >> 5;
+        l31 = lane & 31;
+        float next_la = 0.f;
+        if (n + 1 < nc) {
+            fetch(n + 1);
+            if (gate_wave) next_la = log_alpha(n + 1);
         }
-        __syncthreads();
-        if (n + 1 < nc) fetch(n + 1);
 
-        f32x16 O[2], P[3];   // O^T: columns by rows; products y . x of tiles (0,0), (0,1), (1,1)
+        f32x16 O[2];   // O^T: the wave's columns by rows
         if constexpr (!STATE) {
+            // the products x . y of 32 x 32 tiles (i, j) = (0,0), (1,0), (1,1), times their decays, into LDS
+            for (int k = wave; k < 3; k += NW) {
+                const int it = (k + 1) >> 1, jt = k >> 1;
+                f32x16 P;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = P[0][r] = P[1][r] = P[2][r] = 0.f;
+                for (int r = 0; r < 16; ++r) P[r] = 0.f;
+#pragma unroll
+                for (int m = 0; m < DX / 16; ++m)
+                    P = la_mma(la_row<T, RX>(sY, 32 * jt + l31, m, h), la_row<T, RX>(sX, 32 * it + l31, m, h), P);
+                const int i = 32 * it + l31;
+                const float ui = lds_ld<float>(g + 4 * i), wi = lds_ld<float>(g + 256 + 4 * i);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int j = 32 * jt + 8 * q + 4 * h;
+                    const f32x4 uj = lds_ld<f32x4>(g + 4 * j), wj = lds_ld<f32x4>(g + 256 + 4 * j);
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = (ui - uj[e]) + (wi - wj[e]);
+                        const float x = P[4 * q + e] * __builtin_amdgcn_exp2f(d);
+                        v[e] = j + e <= i ? x : 0.f;
+                    }
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int term = 0; term < NT; ++term) {
+                            const bf16x4 t4 = __builtin_convertvector(v, bf16x4);
+                            lds_st(sP + term * 64 * RP + i * RP + 16 * ((j >> 3) ^ la_swz<RP>(i)) + 8 * h, t4);
+                            if (term + 1 < NT) v = v - __builtin_convertvector(t4, f32x4);
+                        }
+                    } else {
+                        lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<RP>(i)), v);
+                    }
+                }
+            }
+            // what the state at the chunk's start gives the rows
+#pragma unroll
+            for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = 0.f;
+            LaFrag<T> x0 = la_row<T, RX>(sX, l31, 0, h), x1 = la_row<T, RX>(sX, 32 + l31, 0, h);
 #pragma unroll
             for (int m = 0; m < DX / 16; ++m) {
-                const LaFrag<T> x0 = la_row<T, RX>(sX, l31, m, h), x1 = la_row<T, RX>(sX, 32 + l31, m, h);
-                const LaFrag<T> y0 = la_row<T, RX>(sY, l31, m, h), y1 = la_row<T, RX>(sY, 32 + l31, m, h);
+                const LaFrag<T> c0 = x0, c1 = x1;
+                if (m + 1 < DX / 16) {
+                    x0 = la_row<T, RX>(sX, l31, m + 1, h);
+                    x1 = la_row<T, RX>(sX, 32 + l31, m + 1, h);
+                }
                 float s8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s8[e] = S[m >> 1][8 * (m & 1) + e];
                 const LaTerms<T, NT> st = la_split<T, NT>(s8);
-                O[0] = la_mma(st, x0, O[0]);
-                O[1] = la_mma(st, x1, O[1]);
-                P[0] = la_mma(y0, x0, P[0]);
-                P[1] = la_mma(y0, x1, P[1]);
-                P[2] = la_mma(y1, x1, P[2]);
+                O[0] = la_mma(st, c0, O[0]);
+                O[1] = la_mma(st, c1, O[1]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
-        const float decay = lds_ld<float>(sG + 1024);
-#pragma unroll
-        for (int t = 0; t < TX; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
-        float uh[2], ul[2];
-        if constexpr (!STATE) {
 #pragma unroll
             for (int it = 0; it < 2; ++it) {
-                uh[it] = lds_ld<float>(sG + 4 * (32 * it + l31));
-                ul[it] = lds_ld<float>(sG + 256 + 4 * (32 * it + l31));
-                const float e = lds_ld<float>(sG + 512 + 4 * (32 * it + l31));
+                const float e = lds_ld<float>(g + 512 + 4 * (32 * it + l31));
 #pragma unroll
                 for (int r = 0; r < 16; ++r) O[it][r] *= e;
             }
         }
+        const float decay = lds_ld<float>(g + 1024);
+#pragma unroll
+        for (int t = 0; t < TX; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+        if constexpr (!STATE) lds_barrier();   // the products are in LDS
         // rows 16 ks .. 16 ks + 15 of y and z: into the output's later rows, then into the state
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const LaFrag<T> z = la_col<T, RZ>(sZ, ks, wave * kLaCols, lane);
             const int j0 = 16 * ks + 4 * h;   // the lane's rows: j0 + [0, 4) and j0 + 8 + [0, 4)
             if constexpr (!STATE) {
-                const f32x4 h0 = lds_ld<f32x4>(sG + 4 * j0), h1 = lds_ld<f32x4>(sG + 4 * j0 + 32);
-                const f32x4 w0 = lds_ld<f32x4>(sG + 256 + 4 * j0), w1 = lds_ld<f32x4>(sG + 256 + 4 * j0 + 32);
 #pragma unroll
                 for (int it = ks >> 1; it < 2; ++it) {
-                    const f32x16& pt = P[(ks >> 1) + it];
-                    float p8[8];
+                    LaTerms<T, NT> pt;
+                    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float hj = e < 4 ? h0[e & 3] : h1[e & 3], wj = e < 4 ? w0[e & 3] : w1[e & 3];
-                        const float d = (uh[it] - hj) + (ul[it] - wj);
-                        const float v = pt[8 * (ks & 1) + e] * __builtin_amdgcn_exp2f(d);
-                        const bool ok = it > (ks >> 1) || j0 + 8 * (e >> 2) + (e & 3) <= 32 * it + l31;
-                        p8[e] = ok ? v : 0.f;
+                        for (int term = 0; term < NT; ++term)
+                            pt.t[term] = la_row<T, RP>(sP + term * 64 * RP, 32 * it + l31, ks, h).v;
+                    } else {
+                        const LaFrag<T> f = la_row<T, RP>(sP, 32 * it + l31, ks, h);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) pt.v[e] = f.v[e];
                     }
-                    O[it] = la_mma(z, la_split<T, NT>(p8), O[it]);
+                    O[it] = la_mma(z, pt, O[it]);
                 }
             }
-            const f32x4 k0 = lds_ld<f32x4>(sG + 768 + 4 * j0), k1 = lds_ld<f32x4>(sG + 768 + 4 * j0 + 32);
+            const f32x4 k0 = lds_ld<f32x4>(g + 768 + 4 * j0), k1 = lds_ld<f32x4>(g + 768 + 4 * j0 + 32);
             float z8[8];
             la_floats(z, z8);
 #pragma unroll
@@ -404,37 +501,39 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 #pragma unroll
             for (int t = 0; t < TX; ++t) S[t] = la_mma(la_col<T, RX>(sY, ks, 32 * t, lane), zt, S[t]);
         }
+        if (gate_wave && n + 1 < nc) decays(n + 1, next_la);
         if constexpr (!STATE) {
+            const int64_t at0 = b * ps.ob + hd * ps.oh + 64 * c * ps.ot;
+            const int64_t wat0 = b * ps.w.b + (hd / ps.w.group) * ps.w.h + 64 * c * ps.w.t;
 #pragma unroll
             for (int it = 0; it < 2; ++it) {
-                const int row = 32 * it + l31;
-                const int t = 64 * c + (rev ? 63 - row : row);
-                const bool ok = t < a.L;
+                const int row = 32 * it + l31, tl = rev ? 63 - row : row;
+                const bool ok = 64 * c + tl < a.L;
                 float dot = 0.f;
-                const int64_t at = b * ps.ob + hd * ps.oh + t * ps.ot;
-                const int64_t wat = b * ps.w.b + (hd / ps.w.group) * ps.w.h + t * ps.w.t;
+                const unsigned at = (unsigned)tl * (unsigned)ps.ot + zc0 + 4 * h;
+                const unsigned wat = (unsigned)tl * (unsigned)ps.w.t + zc0 + 4 * h;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int col = zc0 + 8 * q + 4 * h;
-                    if (!ok || col >= Dz) continue;
+                    if (!ok || zc0 + 8 * q + 4 * h >= Dz) continue;
                     f32x4 v;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = O[it][4 * q + j];
                     if (ps.w.p) {
                         float w4[4];
-                        load_n<sizeof(T) == 4, 4>(ps.w.p, (size_t)(wat + col), w4);
+                        load_n<sizeof(T) == 4, 4>((const T*)ps.w.p + wat0, wat + 8 * q, w4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) dot += v[j] * w4[j];
                     }
                     if (ps.out_bf16)
-                        *reinterpret_cast<bf16x4*>((__bf16*)ps.out + at + col) = __builtin_convertvector(v, bf16x4);
+                        *reinterpret_cast<bf16x4*>((__bf16*)ps.out + at0 + (at + 8 * q)) =
+                            __builtin_convertvector(v, bf16x4);
                     else
-                        *reinterpret_cast<f32x4*>((float*)ps.out + at + col) = v;
+                        *reinterpret_cast<f32x4*>((float*)ps.out + at0 + (at + 8 * q)) = v;
                 }
                 if (ps.w.p) {
                     dot += __shfl_xor(dot, 32);
                     if (ok && h == 0 && zc0 < Dz)
-                        ps.dots[((size_t)(zc0 / kLaCols) * nseq + seq) * a.L + t] = dot;
+                        ps.dots[((size_t)(zc0 / kLaCols) * nseq + seq) * a.L + 64 * c + tl] = dot;
                 }
             }
         }
@@ -443,7 +542,8 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     float* end = nullptr;
     if constexpr (STATE) {
         end = ps.seg + ((size_t)seq * a.nseg + sg) * elems;
-        if (ct == 0 && tid == 0) ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
+        if (ct == 0 && gate_wave && lane == 0)
+            ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
     } else if (ps.end && sg == (rev ? 0 : a.nseg - 1)) {
         end = ps.end + seq * elems;
     }
@@ -461,7 +561,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 template <typename T, int DX, int NW, int NT, bool STATE>
 hipError_t la_launch(const LaArgs& a, int slot, hipStream_t st) {
     auto kern = la_kernel<T, DX, NW, NT, STATE>;
-    constexpr int lds = la_lds_bytes<T, DX, NW, STATE>();
+    constexpr int lds = la_lds_bytes<T, DX, NW, NT, STATE>();
     if constexpr (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;

@@ -457,8 +457,8 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  *
  * Strides.  q, k, v, o (and dO) are rows of contiguous channels; the strides
  * between batches, heads and tokens are free (elements, not negative, whole
- * multiples of 16 bytes; 0 repeats a row; ignored where the dimension is 1), so
- * that [B][L][H][D] projections, or slices of a fused one, are passed as they
+ * multiples of 16 bytes; 0 repeats a row; ignored where the dimension is 1;
+ * tokens at most 2^23 elements apart), so that [B][L][H][D] projections, or slices of a fused one, are passed as they
  * are.  An output's rows must not overlap each other.  log_alpha and the states
  * are dense.
  *
