@@ -42,7 +42,7 @@
 namespace dr {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Swizzle of the 16-byte pieces of a row of RB bytes.  Row reads take the same
 // piece of 16 or 32 consecutive rows, transposing reads 64 consecutive bytes of
@@ -77,21 +77,45 @@ struct LaTerms<float, NT> {
     float v[8];
 };
 
+// The constants of la_rest, kept in scalar registers: bf16 pairs (-1, 0) and
+// (0, -1), as (low, high) halves.
+struct LaNeg {
+    unsigned lo, hi;
+};
+__device__ __forceinline__ LaNeg la_neg() {
+    LaNeg c{0x0000bf80u, 0xbf800000u};
+    asm volatile("" : "+s"(c.lo), "+s"(c.hi));
+    return c;
+}
+__device__ __forceinline__ unsigned la_pack(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 f = {a, b};
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(f, bf16x2));
+}
+// What two values rounded to the bf16 pair p leave: a - p.lo and b - p.hi, as
+// dot products of p with (-1, 0) and (0, -1), one instruction each and exact.
+__device__ __forceinline__ void la_rest(unsigned p, const LaNeg& c, float& a, float& b) {
+    const bf16x2 h = __builtin_bit_cast(bf16x2, p);
+    a = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, c.lo), a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, c.hi), b, false);
+}
+
 template <typename T, int NT>
-__device__ __forceinline__ LaTerms<T, NT> la_split(const float (&x)[8]) {
+__device__ __forceinline__ LaTerms<T, NT> la_split(float (&x)[8], const LaNeg& c) {
     LaTerms<T, NT> r;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.v[e] = x[e];
     } else {
-        f32x8 f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = x[e];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const bf16x8 h = __builtin_convertvector(f, bf16x8);
-            r.t[n] = __builtin_bit_cast(uint4, h);
-            if (n + 1 < NT) f = f - __builtin_convertvector(h, f32x8);
+            unsigned w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = la_pack(x[2 * e], x[2 * e + 1]);
+                if (n + 1 < NT) la_rest(w[e], c, x[2 * e], x[2 * e + 1]);
+            }
+            r.t[n] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     return r;
@@ -132,16 +156,16 @@ __device__ __forceinline__ f32x16 la_mma(const LaFrag<T>& a, const LaFrag<T>& b,
     return la_mfma(a.v, b.v, c);
 }
 
-// Row `row`, contraction values 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.
+// Row `row`, contraction values 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.  bf16
+// tiles that are read so hold the four 8-byte quads of each 16 values in the
+// order 0, 2, 1, 3 (la_stage), so that this is one 16-byte read.
 template <typename T, int RB>
 __device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, int h) {
     LaFrag<T> f;
     const lchar* r = tile + row * RB;
     const int s = la_swz<RB>(row);
     if constexpr (sizeof(T) == 2) {
-        const uint2 a = lds_ld<uint2>(r + 16 * ((2 * m) ^ s) + 8 * h);
-        const uint2 b = lds_ld<uint2>(r + 16 * ((2 * m + 1) ^ s) + 8 * h);
-        f.v = make_uint4(a.x, a.y, b.x, b.y);
+        f.v = lds_ld<uint4>(r + 16 * ((2 * m + h) ^ s));
     } else {
         const f32x4 a = lds_ld<f32x4>(r + 16 * ((4 * m + h) ^ s));
         const f32x4 b = lds_ld<f32x4>(r + 16 * ((4 * m + 2 + h) ^ s));
@@ -154,14 +178,16 @@ __device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, i
     return f;
 }
 
-// Column c0 + lane % 32, rows 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.
-template <typename T, int RB>
+// Column c0 + lane % 32, rows 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.  QUADS:
+// the tile is in la_row's order.
+template <typename T, int RB, bool QUADS>
 __device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, int m, int c0, int lane) {
     LaFrag<T> f;
     const int h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
         const int i = lane & 15, g = (lane >> 4) & 1;
-        const int piece = (c0 >> 3) + 2 * g + ((i >> 1) & 1), sub = 8 * (i & 1);
+        const int piece = (c0 >> 3) + 2 * g + (QUADS ? i & 1 : (i >> 1) & 1);
+        const int sub = 8 * (QUADS ? (i >> 1) & 1 : i & 1);
         uint2 w[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -231,13 +257,18 @@ __device__ __forceinline__ unsigned la_offset(int64_t row_bytes, bool rev, int t
     const int row0 = tid / PPR;
     return (unsigned)(rev ? STEP - 1 - row0 : row0) * (unsigned)row_bytes + 16 * (tid % PPR);
 }
-template <int N, int PPR, int NTHR>
+template <int N, int PPR, int NTHR, bool QUADS>
 __device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int idx = tid + i * NTHR;
-        const int row = idx / PPR, p = idx % PPR;
-        lds_st(tile + row * (PPR * 16) + 16 * (p ^ la_swz<PPR * 16>(row)), r[i]);
+        const int row = tid / PPR + i * (NTHR / PPR), p = tid % PPR;
+        const int s = la_swz<PPR * 16>(row);
+        if constexpr (QUADS) {
+            lds_st(tile + row * (PPR * 16) + 16 * ((p & ~1) ^ s) + 8 * (p & 1), make_uint2(r[i].x, r[i].y));
+            lds_st(tile + row * (PPR * 16) + 16 * ((p | 1) ^ s) + 8 * (p & 1), make_uint2(r[i].z, r[i].w));
+        } else {
+            lds_st(tile + row * (PPR * 16) + 16 * (p ^ s), r[i]);
+        }
     }
 }
 
@@ -314,7 +345,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     int lane = lane0, h = lane >> 5, l31 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int zc0 = (ct * NW + wave) * kLaCols;      // the wave's first column
-    const int Dx = ps.Dx, Dz = ps.Dz;
+    const int Dx = ps.Dx, Dz = ps.Dz, L = a.L;
     const int px = Dx / EPP, pz = (Dz - ct * NW * kLaCols) / EPP;
     const char* gx = nullptr;
     if constexpr (!STATE)
@@ -322,7 +353,8 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     const char* gy = (const char*)ps.y.p + sizeof(T) * (b * ps.y.b + (hd / ps.y.group) * ps.y.h);
     const char* gz = (const char*)ps.z.p + sizeof(T) * (b * ps.z.b + (hd / ps.z.group) * ps.z.h + ct * NW * kLaCols);
     const int64_t bx = sizeof(T) * ps.x.t, by = sizeof(T) * ps.y.t, bz = sizeof(T) * ps.z.t;
-    const float* la = a.la ? (a.la_head ? a.la + hd : a.la + (size_t)seq * a.L) : nullptr;
+    const float* la = a.la ? (a.la_head ? a.la + hd : a.la + (size_t)seq * L) : nullptr;
+    const LaNeg neg = la_neg();
 
     // the state, from its start
     f32x16 S[TX];
@@ -334,13 +366,31 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 #pragma unroll
     for (int t = 0; t < TX; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int d = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-            float v = 0.f;
-            if (!STATE && start && d < Dx && zc < Dz)
-                v = ps.tr ? start[(size_t)zc * Dx + d] : start[(size_t)d * Dz + zc];
-            S[t][r] = v;
+        for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
+    if (!STATE && start && zc < Dz) {
+        if (ps.tr) {
+            const float* s = start + (size_t)zc * Dx + 4 * h;
+#pragma unroll
+            for (int t = 0; t < TX; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (32 * t + 8 * q < Dx) {
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(s + 32 * t + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) S[t][4 * q + j] = v[j];
+                    }
+        } else {
+            const float* s = start + (size_t)(4 * h) * Dz + zc;
+#pragma unroll
+            for (int t = 0; t < TX; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (32 * t + 8 * q < Dx) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) S[t][4 * q + j] = s[(32 * t + 8 * q + j) * Dz];
+                    }
         }
+    }
 
     const int c_lo = sg * a.cps, c_hi = min(a.NC, c_lo + a.cps);
     const int nc = c_hi - c_lo;
@@ -360,14 +410,14 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     const unsigned fx = STATE ? 0 : la_offset<PX, NTHR>(bx, rev, tid), fy = la_offset<PX, NTHR>(by, rev, tid),
                    fz = la_offset<PZ, NTHR>(bz, rev, tid);
     auto fetch = [&](int n) {
-        const int c = chunk(n), rows = a.L - 64 * c;
+        const int c = chunk(n), rows = L - 64 * c;
         if constexpr (!STATE) la_fetch<NX, PX, NTHR>(rx, gx + 64 * c * bx, bx, fx, rev, rows, okx, tid);
         la_fetch<NX, PX, NTHR>(ry, gy + 64 * c * by, by, fy, rev, rows, okx, tid);
         la_fetch<NZ, PZ, NTHR>(rz, gz + 64 * c * bz, bz, fz, rev, rows, okz, tid);
     };
     auto log_alpha = [&](int n) {
-        const int t = 64 * chunk(n) + (rev ? 63 - lane : lane);
-        return la && t < a.L ? la[a.la_head ? 0 : t] : 0.f;
+        const int t = 64 * chunk(n) + (rev ? 63 - lane0 : lane0);
+        return la && t < L ? la[a.la_head ? 0 : t] : 0.f;
     };
     auto decays = [&](int n, float x) {
         lchar* g = sG + (n & 1) * kLaGateBytes;
@@ -376,41 +426,101 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         const double total = __shfl(s, 63);
         const double u = rev ? s - l2 : s;
         const float uh = (float)u;
-        lds_st(g + 4 * lane, uh);
-        lds_st(g + 256 + 4 * lane, (float)(u - (double)uh));
-        lds_st(g + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
-        lds_st(g + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
-        if (lane == 0) lds_st(g + 1024, __builtin_amdgcn_exp2f((float)total));
+        lds_st(g + 4 * lane0, uh);
+        lds_st(g + 256 + 4 * lane0, (float)(u - (double)uh));
+        lds_st(g + 512 + 4 * lane0, __builtin_amdgcn_exp2f(uh));
+        lds_st(g + 768 + 4 * lane0, __builtin_amdgcn_exp2f((float)(total - u)));
+        if (lane0 == 0) lds_st(g + 1024, __builtin_amdgcn_exp2f((float)total));
         if constexpr (STATE) seg_total += total;
+    };
+
+    // the output rows of a chunk, stored while the next one is computed: a wait
+    // for loads waits for every store before them too
+    f32x16 O[2];           // O^T: the wave's columns by rows
+    RawN<sizeof(T) == 4, 4> W[2][4];
+    const bool dots = !STATE && ps.w.p != nullptr, out_bf16 = ps.out_bf16 != 0;
+    char* const gout = STATE ? nullptr : (char*)ps.out + (out_bf16 ? 2 : 4) * (b * ps.ob + hd * ps.oh);
+    const int64_t ot = ps.ot, wt = ps.w.t;
+    const char* gw = dots ? (const char*)ps.w.p + sizeof(T) * (b * ps.w.b + (hd / ps.w.group) * ps.w.h) : nullptr;
+    float* const gd = dots ? ps.dots + ((size_t)(zc0 / kLaCols) * nseq + seq) * L : nullptr;
+    auto fetch_w = [&](int n) {
+        const int c = chunk(n);
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+            const int row = 32 * it + l31, tl = rev ? 63 - row : row;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (64 * c + tl < L && zc0 + 8 * q < Dz)
+                    W[it][q] = ld_rawn<sizeof(T) == 4, 4>(gw + 64 * c * wt * (int64_t)sizeof(T),
+                                                          (unsigned)tl * (unsigned)wt + zc0 + 8 * q + 4 * h);
+        }
+    };
+    auto store = [&](int n) {
+        const int c = chunk(n);
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+            const int row = 32 * it + l31, tl = rev ? 63 - row : row;
+            const bool ok = 64 * c + tl < L;
+            const unsigned at = (unsigned)tl * (unsigned)ot + zc0 + 4 * h;
+            if (out_bf16) {
+                char* base = gout + 64 * c * ot * 2;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (ok && zc0 + 8 * q < Dz)
+                        *reinterpret_cast<uint2*>(base + 2 * (at + 8 * q)) =
+                            make_uint2(la_pack(O[it][4 * q], O[it][4 * q + 1]), la_pack(O[it][4 * q + 2], O[it][4 * q + 3]));
+            } else {
+                char* base = gout + 64 * c * ot * 4;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (ok && zc0 + 8 * q < Dz)
+                        *reinterpret_cast<f32x4*>(base + 4 * (at + 8 * q)) =
+                            f32x4{O[it][4 * q], O[it][4 * q + 1], O[it][4 * q + 2], O[it][4 * q + 3]};
+            }
+            if (dots) {
+                float dot = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float w4[4];
+                    cvt_rawn<sizeof(T) == 4, 4>(W[it][q], w4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (ok && zc0 + 8 * q < Dz) dot += O[it][4 * q + j] * w4[j];
+                }
+                dot += __shfl_xor(dot, 32);
+                if (ok && h == 0 && zc0 < Dz) gd[64 * c + tl] = dot;
+            }
+        }
     };
     fetch(0);
     if (gate_wave) decays(0, log_alpha(0));
 
     for (int n = 0; n < nc; ++n) {
-        const int c = chunk(n);
         const lchar* g = sG + (n & 1) * kLaGateBytes;
         if (n) lds_barrier();   // the last chunk's tiles are done with
-        if constexpr (!STATE) la_stage<NX, PX, NTHR>(sX, rx, tid);
-        la_stage<NX, PX, NTHR>(sY, ry, tid);
-        la_stage<NZ, PZ, NTHR>(sZ, rz, tid);
+        if constexpr (!STATE) la_stage<NX, PX, NTHR, sizeof(T) == 2>(sX, rx, tid);
+        la_stage<NX, PX, NTHR, sizeof(T) == 2>(sY, ry, tid);
+        la_stage<NZ, PZ, NTHR, false>(sZ, rz, tid);
         lds_barrier();
         lane = la_fresh(lane0);
         h = lane >> 5;
         l31 = lane & 31;
         float next_la = 0.f;
+        if constexpr (!STATE)
+            if (n) store(n - 1);
         if (n + 1 < nc) {
             fetch(n + 1);
             if (gate_wave) next_la = log_alpha(n + 1);
         }
+        if constexpr (!STATE)
+            if (dots) fetch_w(n);
 
-        f32x16 O[2];   // O^T: the wave's columns by rows
+        const f32x16 zero = {};
         if constexpr (!STATE) {
             // the products x . y of 32 x 32 tiles (i, j) = (0,0), (1,0), (1,1), times their decays, into LDS
             for (int k = wave; k < 3; k += NW) {
                 const int it = (k + 1) >> 1, jt = k >> 1;
-                f32x16 P;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) P[r] = 0.f;
+                f32x16 P = zero;
 #pragma unroll
                 for (int m = 0; m < DX / 16; ++m)
                     P = la_mma(la_row<T, RX>(sY, 32 * jt + l31, m, h), la_row<T, RX>(sX, 32 * it + l31, m, h), P);
@@ -428,11 +538,18 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                         v[e] = j + e <= i ? x : 0.f;
                     }
                     if constexpr (sizeof(T) == 2) {
+                        // la_row's order of quads: j / 4 = 4 (j / 16) + 2 (q % 2) + h
+                        lchar* at = sP + i * RP + 16 * ((4 * jt + (q & ~1) + h) ^ la_swz<RP>(i)) + 8 * (q & 1);
 #pragma unroll
                         for (int term = 0; term < NT; ++term) {
-                            const bf16x4 t4 = __builtin_convertvector(v, bf16x4);
-                            lds_st(sP + term * 64 * RP + i * RP + 16 * ((j >> 3) ^ la_swz<RP>(i)) + 8 * h, t4);
-                            if (term + 1 < NT) v = v - __builtin_convertvector(t4, f32x4);
+                            const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
+                            lds_st(at + term * 64 * RP, make_uint2(lo, hi));
+                            if (term + 1 < NT) {
+                                float r0 = v[0], r1 = v[1], r2 = v[2], r3 = v[3];
+                                la_rest(lo, neg, r0, r1);
+                                la_rest(hi, neg, r2, r3);
+                                v = f32x4{r0, r1, r2, r3};
+                            }
                         }
                     } else {
                         lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<RP>(i)), v);
@@ -440,8 +557,6 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 }
             }
             // what the state at the chunk's start gives the rows
-#pragma unroll
-            for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = 0.f;
             LaFrag<T> x0 = la_row<T, RX>(sX, l31, 0, h), x1 = la_row<T, RX>(sX, 32 + l31, 0, h);
 #pragma unroll
             for (int m = 0; m < DX / 16; ++m) {
@@ -453,9 +568,9 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 float s8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s8[e] = S[m >> 1][8 * (m & 1) + e];
-                const LaTerms<T, NT> st = la_split<T, NT>(s8);
-                O[0] = la_mma(st, c0, O[0]);
-                O[1] = la_mma(st, c1, O[1]);
+                const LaTerms<T, NT> st = la_split<T, NT>(s8, neg);
+                O[0] = la_mma(st, c0, m ? O[0] : zero);
+                O[1] = la_mma(st, c1, m ? O[1] : zero);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -474,7 +589,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         // rows 16 ks .. 16 ks + 15 of y and z: into the output's later rows, then into the state
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const LaFrag<T> z = la_col<T, RZ>(sZ, ks, wave * kLaCols, lane);
+            const LaFrag<T> z = la_col<T, RZ, false>(sZ, ks, wave * kLaCols, lane);
             const int j0 = 16 * ks + 4 * h;   // the lane's rows: j0 + [0, 4) and j0 + 8 + [0, 4)
             if constexpr (!STATE) {
 #pragma unroll
@@ -497,47 +612,14 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             la_floats(z, z8);
 #pragma unroll
             for (int e = 0; e < 8; ++e) z8[e] *= e < 4 ? k0[e & 3] : k1[e & 3];
-            const LaTerms<T, 3> zt = la_split<T, 3>(z8);
+            const LaTerms<T, 3> zt = la_split<T, 3>(z8, neg);
 #pragma unroll
-            for (int t = 0; t < TX; ++t) S[t] = la_mma(la_col<T, RX>(sY, ks, 32 * t, lane), zt, S[t]);
+            for (int t = 0; t < TX; ++t)
+                S[t] = la_mma(la_col<T, RX, sizeof(T) == 2>(sY, ks, 32 * t, lane), zt, S[t]);
         }
         if (gate_wave && n + 1 < nc) decays(n + 1, next_la);
-        if constexpr (!STATE) {
-            const int64_t at0 = b * ps.ob + hd * ps.oh + 64 * c * ps.ot;
-            const int64_t wat0 = b * ps.w.b + (hd / ps.w.group) * ps.w.h + 64 * c * ps.w.t;
-#pragma unroll
-            for (int it = 0; it < 2; ++it) {
-                const int row = 32 * it + l31, tl = rev ? 63 - row : row;
-                const bool ok = 64 * c + tl < a.L;
-                float dot = 0.f;
-                const unsigned at = (unsigned)tl * (unsigned)ps.ot + zc0 + 4 * h;
-                const unsigned wat = (unsigned)tl * (unsigned)ps.w.t + zc0 + 4 * h;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (!ok || zc0 + 8 * q + 4 * h >= Dz) continue;
-                    f32x4 v;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = O[it][4 * q + j];
-                    if (ps.w.p) {
-                        float w4[4];
-                        load_n<sizeof(T) == 4, 4>((const T*)ps.w.p + wat0, wat + 8 * q, w4);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dot += v[j] * w4[j];
-                    }
-                    if (ps.out_bf16)
-                        *reinterpret_cast<bf16x4*>((__bf16*)ps.out + at0 + (at + 8 * q)) =
-                            __builtin_convertvector(v, bf16x4);
-                    else
-                        *reinterpret_cast<f32x4*>((float*)ps.out + at0 + (at + 8 * q)) = v;
-                }
-                if (ps.w.p) {
-                    dot += __shfl_xor(dot, 32);
-                    if (ok && h == 0 && zc0 < Dz)
-                        ps.dots[((size_t)(zc0 / kLaCols) * nseq + seq) * a.L + 64 * c + tl] = dot;
-                }
-            }
-        }
     }
+    if constexpr (!STATE) store(nc - 1);
 
     float* end = nullptr;
     if constexpr (STATE) {
@@ -548,12 +630,21 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         end = ps.end + seq * elems;
     }
     if (end && zc < Dz) {
+        const bool tr = ps.tr != 0;
+        float* e = tr ? end + (size_t)zc * Dx + 4 * h : end + (size_t)(4 * h) * Dz + zc;
 #pragma unroll
         for (int t = 0; t < TX; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int d = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (d < Dx) end[ps.tr ? (size_t)zc * Dx + d : (size_t)d * Dz + zc] = S[t][r];
+            for (int q = 0; q < 4; ++q) {
+                const int d = 32 * t + 8 * q;
+                if (d >= Dx) continue;
+                if (tr) {
+                    *reinterpret_cast<f32x4*>(e + d) =
+                        f32x4{S[t][4 * q], S[t][4 * q + 1], S[t][4 * q + 2], S[t][4 * q + 3]};
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[(d + j) * Dz] = S[t][4 * q + j];
+                }
             }
     }
 }
