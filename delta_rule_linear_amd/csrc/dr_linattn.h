@@ -9,7 +9,7 @@
 
 namespace dr {
 
-constexpr int kLaCols = 32;   // output columns of one wave
+constexpr int kLaCols = 16;   // output columns of one wave
 
 // One pass of the operator
 //   out_i = sum_{j <= i} e^{u_i - u_j} (x_i . y_j) z_j + e^{u_i} start^T x_i
@@ -44,7 +44,7 @@ struct LaPass {
     // segments' decays [B*H][nseg]
     float* seg;
     float* segdec;
-    float* dots;         // [ceil(Dz / 32)][B*H][L]
+    float* dots;         // [B*H][L]
 };
 
 struct LaArgs {
@@ -54,7 +54,6 @@ struct LaArgs {
     int la_head;
     int B, H, L, NC;     // NC: 64-token chunks of a sequence
     int nseg, cps;       // segments, chunks per segment
-    int ntile;           // column tiles per sequence (of kLaCols * waves columns)
     int total;           // workgroups
 };
 
@@ -70,9 +69,8 @@ struct LaJoinArgs {
 // d log alpha from the rows' dot products: within each segment
 //   dla_t = <S_end, dS_end> + sum_{s >= t} (q_s . dq_s - k_s . dk_s)
 struct LaGateArgs {
-    const float* dq_dots;   // [tq][B*H][L]
-    const float* dk_dots;   // [tk][B*H][L]
-    int tq, tk;
+    const float* dq_dots;   // [B*H][L]
+    const float* dk_dots;
     const float* segF;      // S at the segments' starts, [B*H][nseg][elems]
     const float* segR;      // dS at the segments' ends
     const float* S_end;     // S behind the last token, dS there (NULL: zero)

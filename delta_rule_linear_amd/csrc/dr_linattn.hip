@@ -92,15 +92,13 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
     __syncthreads();
     // 256 tokens at a time, from the segment's last
     const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
-    const size_t plane = (size_t)nseq * a.L;
     double total = 0.0;
     for (int hi = t1; hi > t0; hi -= 256) {
         const int t = hi - 1 - tid;
         double d = 0.0;
         if (t >= t0) {
             const size_t at = (size_t)seq * a.L + t;
-            for (int i = 0; i < a.tq; ++i) d += (double)a.dq_dots[i * plane + at];
-            for (int i = 0; i < a.tk; ++i) d -= (double)a.dk_dots[i * plane + at];
+            d = (double)a.dq_dots[at] - (double)a.dk_dots[at];
         }
         red[tid] = d;
         __syncthreads();

@@ -106,14 +106,13 @@ dr_status check_heads(int H, int Hk, int Dk, int Dv, int in_dtype, int out_dtype
     return DR_OK;
 }
 
-// How the work is split: column tiles of one to four waves (32 columns each)
-// and segments of whole chunks.
+// How the work is split: workgroups of two to eight waves (16 columns each) that
+// hold all columns of a state, and segments of whole chunks.
 struct Split {
     int nseg, cps;
 };
 
-int waves_of(int D) { return D <= 32 ? 1 : D <= 64 ? 2 : 4; }
-int tiles_of(int D) { return (D + 32 * waves_of(D) - 1) / (32 * waves_of(D)); }
+int waves_of(int D) { return D <= 32 ? 2 : D <= 64 ? 4 : 8; }
 
 // Workgroups that fill the GPU: two on each of 256 compute units.
 constexpr int64_t kFill = 512;
@@ -138,7 +137,7 @@ int64_t seqs(const dr_linattn_desc& d) { return (int64_t)d.B * d.H; }
 LaLayout la_layout(const dr_linattn_desc& d, bool bwd) {
     LaLayout w{};
     const size_t nseq = (size_t)seqs(d), elems = (size_t)d.Dk * d.Dv;
-    w.split = la_split_of(d.L, (int64_t)nseq * (bwd ? std::max(tiles_of(d.Dk), tiles_of(d.Dv)) : tiles_of(d.Dv)));
+    w.split = la_split_of(d.L, (int64_t)nseq);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -152,8 +151,7 @@ LaLayout la_layout(const dr_linattn_desc& d, bool bwd) {
         }
     if (bwd && d.decay != DR_DECAY_NONE) {
         w.S_end = take(nseq * elems * sizeof(float));
-        const size_t tiles = (size_t)(d.Dk + 31) / 32;
-        for (int i = 0; i < 2; ++i) w.dots[i] = take(tiles * nseq * d.L * sizeof(float));
+        for (int i = 0; i < 2; ++i) w.dots[i] = take(nseq * d.L * sizeof(float));
         if (d.decay == DR_DECAY_HEAD) w.part = take(nseq * w.split.nseg * sizeof(double));
     }
     if (bwd && d.H > d.Hk)
@@ -199,8 +197,7 @@ hipError_t run_passes(dr::LaArgs a, const dr::LaPass* p, int n, bool f32in, int 
     const int dx = p[0].Dx <= 64 ? 64 : 128, waves = waves_of(p[0].Dz);
     a.npass = n;
     for (int i = 0; i < n; ++i) a.pass[i] = p[i];
-    a.ntile = tiles_of(p[0].Dz);
-    a.total = (int)((int64_t)n * a.B * a.H * a.nseg * a.ntile);
+    a.total = (int)((int64_t)n * a.B * a.H * a.nseg);
     return f32in ? dr::launch_la32(a, dx, waves, state_only, slot, st)
                  : dr::launch_la16(a, dx, waves, terms, state_only, slot, st);
 }
@@ -455,7 +452,6 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
         dr::LaGateArgs g{};
         g.dq_dots = dots[0];
         g.dk_dots = dots[1];
-        g.tq = g.tk = (d->Dk + 31) / 32;
         g.segF = seg[0];
         g.segR = seg[1];
         g.S_end = S_end;

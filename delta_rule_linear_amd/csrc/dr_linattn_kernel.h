@@ -11,14 +11,19 @@
 // behind it, without its own: the exclusive running sum.
 //
 // Layout.  One workgroup walks the chunks of one segment of one sequence for
-// 32 columns of z per wave.  A wave keeps its Dx x 32 state in accumulator
-// registers of the 32x32 matrix ops.  A lane of an accumulator holds rows
-// 8 b + 4 h + j (b, j < 4; h the half of the wave) of one column; taken as an
-// operand with that row order as the contraction's order, the same registers
-// feed the next product, so neither the state nor the 64 x 64 matrix of
-// products x . y passes through LDS: x and y rows are read from LDS in that
-// order.  Products that contract over tokens read y and z transposed
-// (ds_read_b64_tr_b16 for bf16).
+// 16 columns of z per wave.  A wave keeps its Dx x 16 state in accumulator
+// registers of the 16x16 matrix ops.  A lane of two stacked accumulators holds
+// rows 4 g + j and 16 + 4 g + j (j < 4; g the 16-lane group) of one column;
+// taken as an operand with that row order as the contraction's order, the same
+// registers feed the next product, so the state never passes through LDS: x and
+// y rows are staged there in that order.  The 64 x 64 matrix of products x . y
+// is made once per workgroup, a 16 x 16 block or two per wave, and shared
+// through LDS with its decays applied.  Products that contract over tokens read
+// y and z transposed (ds_read_b64_tr_b16 for bf16).  Sixteen columns per wave
+// and eight waves keep the registers at 128, i.e. four waves per SIMD: 32
+// columns and four waves read LDS half as often, but two waves per SIMD left
+// the matrix cores idle (forward, B2 H16 L16384 d128 bf16: 187 us, see DESIGN
+// of the waves' count in la_threads).
 //
 // Precision.  bf16 inputs are operands as they are.  fp32 quantities that meet
 // them are split into bf16 terms: the decayed z of the state update into three
@@ -41,7 +46,6 @@
 
 namespace dr {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Swizzle of the 16-byte pieces of a row of RB bytes.  Row reads take the same
@@ -121,54 +125,39 @@ __device__ __forceinline__ LaTerms<T, NT> la_split(float (&x)[8], const LaNeg& c
     return r;
 }
 
-__device__ __forceinline__ f32x16 la_mfma(const uint4& a, const uint4& b, const f32x16& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+// c += a b over 32 contraction values
+__device__ __forceinline__ f32x4 la_mfma(const uint4& a, const uint4& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
 }
-__device__ __forceinline__ f32x16 la_mfma(const float (&a)[8], const float (&b)[8], f32x16 c) {
+__device__ __forceinline__ f32x4 la_mfma(const float (&a)[8], const float (&b)[8], f32x4 c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
     return c;
 }
-// c += a b, a or b split into terms (smallest first, so that they are not lost)
-template <int NT>
-__device__ __forceinline__ f32x16 la_mma(const LaTerms<__bf16, NT>& a, const LaFrag<__bf16>& b, f32x16 c) {
-#pragma unroll
-    for (int n = NT - 1; n >= 0; --n) c = la_mfma(a.t[n], b.v, c);
-    return c;
+// Term n of a split operand, as a fragment; fp32 operands have one.
+template <typename T, int NT>
+__device__ __forceinline__ auto& la_term(const LaTerms<T, NT>& a, int n) {
+    if constexpr (sizeof(T) == 4) return a.v;
+    else return a.t[n];
 }
-template <int NT>
-__device__ __forceinline__ f32x16 la_mma(const LaFrag<__bf16>& a, const LaTerms<__bf16, NT>& b, f32x16 c) {
-#pragma unroll
-    for (int n = NT - 1; n >= 0; --n) c = la_mfma(a.v, b.t[n], c);
-    return c;
-}
-template <int NT>
-__device__ __forceinline__ f32x16 la_mma(const LaTerms<float, NT>& a, const LaFrag<float>& b, f32x16 c) {
-    return la_mfma(a.v, b.v, c);
-}
-template <int NT>
-__device__ __forceinline__ f32x16 la_mma(const LaFrag<float>& a, const LaTerms<float, NT>& b, f32x16 c) {
-    return la_mfma(a.v, b.v, c);
-}
-template <typename T>
-__device__ __forceinline__ f32x16 la_mma(const LaFrag<T>& a, const LaFrag<T>& b, f32x16 c) {
-    return la_mfma(a.v, b.v, c);
-}
+// Terms that a product runs over (smallest first, so that they are not lost).
+template <typename T, int NT>
+constexpr int la_terms() { return sizeof(T) == 4 ? 1 : NT; }
 
-// Row `row`, contraction values 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.  bf16
-// tiles that are read so hold the four 8-byte quads of each 16 values in the
-// order 0, 2, 1, 3 (la_stage), so that this is one 16-byte read.
+// Row `row`, contraction values 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8.  bf16
+// tiles that are read so hold the eight 8-byte quads of each 32 values in the
+// order 0, 4, 1, 5, 2, 6, 3, 7 (la_stage), so that this is one 16-byte read.
 template <typename T, int RB>
-__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, int h) {
+__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, int g) {
     LaFrag<T> f;
     const lchar* r = tile + row * RB;
     const int s = la_swz<RB>(row);
     if constexpr (sizeof(T) == 2) {
-        f.v = lds_ld<uint4>(r + 16 * ((2 * m + h) ^ s));
+        f.v = lds_ld<uint4>(r + 16 * ((4 * m + g) ^ s));
     } else {
-        const f32x4 a = lds_ld<f32x4>(r + 16 * ((4 * m + h) ^ s));
-        const f32x4 b = lds_ld<f32x4>(r + 16 * ((4 * m + 2 + h) ^ s));
+        const f32x4 a = lds_ld<f32x4>(r + 16 * ((8 * m + g) ^ s));
+        const f32x4 b = lds_ld<f32x4>(r + 16 * ((8 * m + 4 + g) ^ s));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f.v[j] = a[j];
@@ -178,28 +167,27 @@ __device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, i
     return f;
 }
 
-// Column c0 + lane % 32, rows 16 m + 8 (e / 4) + 4 h + (e % 4), e < 8.  QUADS:
+// Column c0 + lane % 16, rows 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8.  QUADS:
 // the tile is in la_row's order.
 template <typename T, int RB, bool QUADS>
 __device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, int m, int c0, int lane) {
     LaFrag<T> f;
-    const int h = lane >> 5;
+    const int g = lane >> 4, i = lane & 15;
     if constexpr (sizeof(T) == 2) {
-        const int i = lane & 15, g = (lane >> 4) & 1;
-        const int piece = (c0 >> 3) + 2 * g + (QUADS ? i & 1 : (i >> 1) & 1);
-        const int sub = 8 * (QUADS ? (i >> 1) & 1 : i & 1);
+        const int piece = QUADS ? 4 * (c0 >> 5) + (i & 3) : (c0 >> 3) + ((i >> 1) & 1);
+        const int sub = QUADS ? 8 * ((c0 >> 4) & 1) : 8 * (i & 1);
         uint2 w[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int row = 16 * m + 8 * q + 4 * h + (i >> 2);
+            const int row = 32 * m + 16 * q + 4 * g + (i >> 2);
             w[q] = lds_tr4(tile + row * RB + 16 * (piece ^ la_swz<RB>(row)) + sub);
         }
         f.v = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
     } else {
-        const int col = c0 + (lane & 31);
+        const int col = c0 + i;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int row = 16 * m + 8 * (e >> 2) + 4 * h + (e & 3);
+            const int row = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
             f.v[e] = lds_ld<float>(tile + row * RB + 16 * ((col >> 2) ^ la_swz<RB>(row)) + 4 * (col & 3));
         }
     }
@@ -234,6 +222,8 @@ __device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_
                                          int rows, bool ok, int tid) {
     constexpr int STEP = NTHR / PPR;
     const int row0 = tid / PPR;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
     if (rows >= 64) {
         if (ok) {
 #pragma unroll
@@ -244,7 +234,6 @@ __device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int row = row0 + i * STEP;
-            r[i] = make_uint4(0u, 0u, 0u, 0u);
             if (ok && (rev ? 63 - row : row) < rows)
                 r[i] = *reinterpret_cast<const uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * row_bytes + off);
         }
@@ -263,12 +252,23 @@ __device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int t
     for (int i = 0; i < N; ++i) {
         const int row = tid / PPR + i * (NTHR / PPR), p = tid % PPR;
         const int s = la_swz<PPR * 16>(row);
+        lchar* at = tile + row * (PPR * 16);
         if constexpr (QUADS) {
-            lds_st(tile + row * (PPR * 16) + 16 * ((p & ~1) ^ s) + 8 * (p & 1), make_uint2(r[i].x, r[i].y));
-            lds_st(tile + row * (PPR * 16) + 16 * ((p | 1) ^ s) + 8 * (p & 1), make_uint2(r[i].z, r[i].w));
+            const int first = (p & ~3) + 2 * (p & 1), sub = 8 * ((p >> 1) & 1);
+            lds_st(at + 16 * (first ^ s) + sub, make_uint2(r[i].x, r[i].y));
+            lds_st(at + 16 * ((first + 1) ^ s) + sub, make_uint2(r[i].z, r[i].w));
         } else {
-            lds_st(tile + row * (PPR * 16) + 16 * (p ^ s), r[i]);
+            lds_st(at + 16 * (p ^ s), r[i]);
         }
+    }
+}
+// What lies where la_stage (not QUADS) puts a thread's pieces.
+template <int N, int PPR, int NTHR>
+__device__ __forceinline__ void la_unstage(const lchar* tile, uint4 (&r)[N], int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = tid / PPR + i * (NTHR / PPR), p = tid % PPR;
+        r[i] = lds_ld<uint4>(tile + row * (PPR * 16) + 16 * (p ^ la_swz<PPR * 16>(row)));
     }
 }
 
@@ -299,38 +299,40 @@ constexpr int kLaGateBytes = 4 * 64 * 4 + 16;
 
 template <typename T, int DX, int NW, int NT, bool STATE>
 constexpr int la_lds_bytes() {
-    constexpr int y = 64 * DX * (int)sizeof(T), z = 64 * 32 * NW * (int)sizeof(T);
-    return (STATE ? y + z : 2 * y + z + 64 * 64 * (int)sizeof(T) * (sizeof(T) == 2 ? NT : 1)) + 2 * kLaGateBytes;
+    constexpr int y = 64 * DX * (int)sizeof(T), z = 64 * kLaCols * NW * (int)sizeof(T);
+    return (STATE ? y + z : 2 * y + z + 64 * 64 * (int)sizeof(T) * la_terms<T, NT>() + NW * 256) + 2 * kLaGateBytes;
 }
 
-// waves per SIMD that the registers are held to: two for bf16, one for fp32,
-// whose tiles fill the LDS of a CU
+// Waves per SIMD that the registers are held to: four for bf16 workgroups of
+// eight waves, two of which share a CU; else two, all that the tiles in LDS
+// leave room for.
 template <typename T, int NW>
-constexpr int la_waves() { return sizeof(T) == 2 && NW > 1 ? 2 : 1; }
+constexpr int la_waves() { return sizeof(T) == 2 && NW == 8 ? 4 : 2; }
 
 template <typename T, int DX, int NW, int NT, bool STATE>
 __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs a) {
     constexpr int NTHR = 64 * NW;
-    constexpr int EPP = 16 / (int)sizeof(T);         // elements per piece
-    constexpr int PX = DX / EPP, PZ = 32 * NW / EPP; // pieces per row
-    constexpr int RX = PX * 16, RZ = PZ * 16;        // bytes per row
-    constexpr int RP = 64 * (int)sizeof(T);          // of the products x . y (each term)
+    constexpr int EPP = 16 / (int)sizeof(T);              // elements per piece
+    constexpr int PX = DX / EPP, PZ = kLaCols * NW / EPP; // pieces per row
+    constexpr int RX = PX * 16, RZ = PZ * 16;             // bytes per row
+    constexpr int RP = 64 * (int)sizeof(T);               // of the products x . y (each term)
     constexpr int NX = 64 * PX / NTHR, NZ = 64 * PZ / NTHR;
-    constexpr int TX = DX / 32;                      // 32-row tiles of the state
+    constexpr int TX = DX / 16;                           // 16-row tiles of the state
+    constexpr int TERMS = la_terms<T, NT>();
+    constexpr bool BF = sizeof(T) == 2;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     lchar* const sY = (lchar*)smem;
     lchar* const sZ = sY + 64 * RX;
     lchar* const sG = sZ + 64 * RZ;
-    lchar* const sX = sG + 2 * kLaGateBytes;         // not with STATE
+    lchar* const sX = sG + 2 * kLaGateBytes;              // not with STATE, nor what follows
     lchar* const sP = sX + 64 * RX;
+    lchar* const sR = sP + TERMS * 64 * RP;               // [NW][64] partial dot products
 
-    // Workgroups go to the eight XCDs in turn; consecutive work (the column
-    // tiles of a sequence, heads that share rows) stays on one of them.
+    // Workgroups go to the eight XCDs in turn; consecutive work (heads that share
+    // rows) stays on one of them.
     const int per = (a.total + 7) / 8;
     int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if (id >= a.total || (int)(blockIdx.x >> 3) >= per) return;
-    const int ct = id % a.ntile;
-    id /= a.ntile;
     const int nseq = a.B * a.H;
     const int seq = id % nseq;
     id /= nseq;
@@ -341,54 +343,50 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     // nothing starts from behind the last segment
     if (STATE && sg == (rev ? 0 : a.nseg - 1)) return;
 
-    const int tid = threadIdx.x, lane0 = tid & 63;
-    int lane = lane0, h = lane >> 5, l31 = lane & 31;
+    int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l15 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int zc0 = (ct * NW + wave) * kLaCols;      // the wave's first column
+    // nothing that follows from the thread's index is held in registers across this
+    auto fresh = [&]() {
+        tid = la_fresh(tid);
+        lane = tid & 63;
+        g = lane >> 4;
+        l15 = lane & 15;
+    };
+    const int zc0 = wave * kLaCols;     // the wave's first column
     const int Dx = ps.Dx, Dz = ps.Dz, L = a.L;
-    const int px = Dx / EPP, pz = (Dz - ct * NW * kLaCols) / EPP;
+    const int px = Dx / EPP, pz = Dz / EPP;
     const char* gx = nullptr;
     if constexpr (!STATE)
         gx = (const char*)ps.x.p + sizeof(T) * (b * ps.x.b + (hd / ps.x.group) * ps.x.h);
     const char* gy = (const char*)ps.y.p + sizeof(T) * (b * ps.y.b + (hd / ps.y.group) * ps.y.h);
-    const char* gz = (const char*)ps.z.p + sizeof(T) * (b * ps.z.b + (hd / ps.z.group) * ps.z.h + ct * NW * kLaCols);
+    const char* gz = (const char*)ps.z.p + sizeof(T) * (b * ps.z.b + (hd / ps.z.group) * ps.z.h);
     const int64_t bx = sizeof(T) * ps.x.t, by = sizeof(T) * ps.y.t, bz = sizeof(T) * ps.z.t;
     const float* la = a.la ? (a.la_head ? a.la + hd : a.la + (size_t)seq * L) : nullptr;
     const LaNeg neg = la_neg();
 
     // the state, from its start
-    f32x16 S[TX];
+    f32x4 S[TX];
     const float* start = nullptr;
     const size_t elems = (size_t)Dx * Dz;
     if constexpr (!STATE)
         start = a.nseg > 1 ? ps.seg + ((size_t)seq * a.nseg + sg) * elems : ps.start ? ps.start + seq * elems : nullptr;
-    const int zc = zc0 + l31;
+    const int zc = zc0 + l15;
 #pragma unroll
-    for (int t = 0; t < TX; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
+    for (int t = 0; t < TX; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (!STATE && start && zc < Dz) {
+        // rows 16 t + 4 g + j: Dx is a multiple of 8, so four rows are inside or outside together
         if (ps.tr) {
-            const float* s = start + (size_t)zc * Dx + 4 * h;
+            const float* s = start + (size_t)zc * Dx + 4 * g;
 #pragma unroll
             for (int t = 0; t < TX; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (32 * t + 8 * q < Dx) {
-                        const f32x4 v = *reinterpret_cast<const f32x4*>(s + 32 * t + 8 * q);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) S[t][4 * q + j] = v[j];
-                    }
+                if (16 * t + 4 * g < Dx) S[t] = *reinterpret_cast<const f32x4*>(s + 16 * t);
         } else {
-            const float* s = start + (size_t)(4 * h) * Dz + zc;
+            const float* s = start + (size_t)(4 * g) * Dz + zc;
 #pragma unroll
             for (int t = 0; t < TX; ++t)
+                if (16 * t + 4 * g < Dx)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (32 * t + 8 * q < Dx) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) S[t][4 * q + j] = s[(32 * t + 8 * q + j) * Dz];
-                    }
+                    for (int j = 0; j < 4; ++j) S[t][j] = s[(16 * t + j) * Dz];
         }
     }
 
@@ -399,253 +397,273 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 
     uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
     auto chunk = [&](int n) { return rev ? c_hi - 1 - n : c_lo + n; };
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-        if constexpr (!STATE) rx[i] = make_uint4(0u, 0u, 0u, 0u);
-        ry[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < NZ; ++i) rz[i] = make_uint4(0u, 0u, 0u, 0u);
-    const bool okx = tid % PX < px, okz = tid % PZ < pz;
-    const unsigned fx = STATE ? 0 : la_offset<PX, NTHR>(bx, rev, tid), fy = la_offset<PX, NTHR>(by, rev, tid),
-                   fz = la_offset<PZ, NTHR>(bz, rev, tid);
     auto fetch = [&](int n) {
         const int c = chunk(n), rows = L - 64 * c;
-        if constexpr (!STATE) la_fetch<NX, PX, NTHR>(rx, gx + 64 * c * bx, bx, fx, rev, rows, okx, tid);
-        la_fetch<NX, PX, NTHR>(ry, gy + 64 * c * by, by, fy, rev, rows, okx, tid);
-        la_fetch<NZ, PZ, NTHR>(rz, gz + 64 * c * bz, bz, fz, rev, rows, okz, tid);
+        const bool okx = tid % PX < px, okz = tid % PZ < pz;
+        if constexpr (!STATE)
+            la_fetch<NX, PX, NTHR>(rx, gx + 64 * c * bx, bx, la_offset<PX, NTHR>(bx, rev, tid), rev, rows, okx, tid);
+        la_fetch<NX, PX, NTHR>(ry, gy + 64 * c * by, by, la_offset<PX, NTHR>(by, rev, tid), rev, rows, okx, tid);
+        la_fetch<NZ, PZ, NTHR>(rz, gz + 64 * c * bz, bz, la_offset<PZ, NTHR>(bz, rev, tid), rev, rows, okz, tid);
     };
     auto log_alpha = [&](int n) {
-        const int t = 64 * chunk(n) + (rev ? 63 - lane0 : lane0);
+        const int t = 64 * chunk(n) + (rev ? 63 - lane : lane);
         return la && t < L ? la[a.la_head ? 0 : t] : 0.f;
     };
     auto decays = [&](int n, float x) {
-        lchar* g = sG + (n & 1) * kLaGateBytes;
+        lchar* gt = sG + (n & 1) * kLaGateBytes;
         const double l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
         const double s = la_scan(l2);
         const double total = __shfl(s, 63);
         const double u = rev ? s - l2 : s;
         const float uh = (float)u;
-        lds_st(g + 4 * lane0, uh);
-        lds_st(g + 256 + 4 * lane0, (float)(u - (double)uh));
-        lds_st(g + 512 + 4 * lane0, __builtin_amdgcn_exp2f(uh));
-        lds_st(g + 768 + 4 * lane0, __builtin_amdgcn_exp2f((float)(total - u)));
-        if (lane0 == 0) lds_st(g + 1024, __builtin_amdgcn_exp2f((float)total));
+        lds_st(gt + 4 * lane, uh);
+        lds_st(gt + 256 + 4 * lane, (float)(u - (double)uh));
+        lds_st(gt + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
+        lds_st(gt + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
+        if (lane == 0) lds_st(gt + 1024, __builtin_amdgcn_exp2f((float)total));
         if constexpr (STATE) seg_total += total;
     };
 
-    // the output rows of a chunk, stored while the next one is computed: a wait
-    // for loads waits for every store before them too
-    f32x16 O[2];           // O^T: the wave's columns by rows
-    RawN<sizeof(T) == 4, 4> W[2][4];
+    // The output rows of a chunk are stored after the next chunk is staged: a
+    // wait for loads waits for every store before them too.  bf16 rows leave
+    // through the waves' own columns of z in LDS, as whole rows; fp32 rows as
+    // the lanes hold them (64 bytes of a row per wave).
+    f32x4 O[4];            // O^T: the wave's columns by rows 16 it + lane % 16
+    typedef uint4 Pieces[BF ? NZ : 1];
+    RawN<!BF, 4> W[4];
     const bool dots = !STATE && ps.w.p != nullptr, out_bf16 = ps.out_bf16 != 0;
-    char* const gout = STATE ? nullptr : (char*)ps.out + (out_bf16 ? 2 : 4) * (b * ps.ob + hd * ps.oh);
     const int64_t ot = ps.ot, wt = ps.w.t;
+    char* const gout =
+        STATE ? nullptr : (char*)ps.out + (out_bf16 ? 2 : 4) * (b * ps.ob + hd * ps.oh);
     const char* gw = dots ? (const char*)ps.w.p + sizeof(T) * (b * ps.w.b + (hd / ps.w.group) * ps.w.h) : nullptr;
-    float* const gd = dots ? ps.dots + ((size_t)(zc0 / kLaCols) * nseq + seq) * L : nullptr;
+    float* const gd = dots ? ps.dots + (size_t)seq * L : nullptr;
+    auto token = [&](int it) { return rev ? 63 - 16 * it - l15 : 16 * it + l15; };
     auto fetch_w = [&](int n) {
         const int c = chunk(n);
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-            const int row = 32 * it + l31, tl = rev ? 63 - row : row;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (64 * c + tl < L && zc0 + 8 * q < Dz)
-                    W[it][q] = ld_rawn<sizeof(T) == 4, 4>(gw + 64 * c * wt * (int64_t)sizeof(T),
-                                                          (unsigned)tl * (unsigned)wt + zc0 + 8 * q + 4 * h);
+        for (int it = 0; it < 4; ++it) {
+            W[it] = RawN<!BF, 4>{};
+            if (64 * c + token(it) < L && zc0 + 4 * g < Dz)
+                W[it] = ld_rawn<!BF, 4>(gw + 64 * c * wt * (int64_t)sizeof(T),
+                                        (unsigned)token(it) * (unsigned)wt + zc0 + 4 * g);
         }
     };
-    auto store = [&](int n) {
-        const int c = chunk(n);
+    // at the end of a chunk: the rows' dot products, and bf16 rows into LDS
+    auto finish = [&](int n) {
+        if (dots) {
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-            const int row = 32 * it + l31, tl = rev ? 63 - row : row;
-            const bool ok = 64 * c + tl < L;
-            const unsigned at = (unsigned)tl * (unsigned)ot + zc0 + 4 * h;
-            if (out_bf16) {
-                char* base = gout + 64 * c * ot * 2;
+            for (int it = 0; it < 4; ++it) {
+                float w4[4], dot = 0.f;
+                cvt_rawn<!BF, 4>(W[it], w4);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (ok && zc0 + 8 * q < Dz)
-                        *reinterpret_cast<uint2*>(base + 2 * (at + 8 * q)) =
-                            make_uint2(la_pack(O[it][4 * q], O[it][4 * q + 1]), la_pack(O[it][4 * q + 2], O[it][4 * q + 3]));
-            } else {
-                char* base = gout + 64 * c * ot * 4;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (ok && zc0 + 8 * q < Dz)
-                        *reinterpret_cast<f32x4*>(base + 4 * (at + 8 * q)) =
-                            f32x4{O[it][4 * q], O[it][4 * q + 1], O[it][4 * q + 2], O[it][4 * q + 3]};
-            }
-            if (dots) {
-                float dot = 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float w4[4];
-                    cvt_rawn<sizeof(T) == 4, 4>(W[it][q], w4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (ok && zc0 + 8 * q < Dz) dot += O[it][4 * q + j] * w4[j];
-                }
+                for (int j = 0; j < 4; ++j) dot += O[it][j] * w4[j];
+                dot += __shfl_xor(dot, 16);
                 dot += __shfl_xor(dot, 32);
-                if (ok && h == 0 && zc0 < Dz) gd[64 * c + tl] = dot;
+                if (g == 0) lds_st(sR + 256 * wave + 4 * (16 * it + l15), dot);
             }
+        }
+        if constexpr (BF) {
+            if (out_bf16)
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int row = 16 * it + l15;
+                    lds_st(sZ + row * RZ + 16 * ((2 * wave + (g >> 1)) ^ la_swz<RZ>(row)) + 8 * (g & 1),
+                           make_uint2(la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3])));
+                }
+        }
+    };
+    auto store = [&](int n, const Pieces& ro) {
+        const int c = chunk(n), rows = L - 64 * c;
+        if (BF && out_bf16) {
+            if constexpr (BF) {
+                constexpr int STEP = NTHR / PZ;
+                char* base = gout + 64 * c * ot * 2;
+                const unsigned off = la_offset<PZ, NTHR>(2 * ot, rev, tid);
+                const bool okz = tid % PZ < pz;
+#pragma unroll
+                for (int i = 0; i < NZ; ++i) {
+                    const int row = tid / PZ + i * STEP;
+                    if (okz && (rev ? 63 - row : row) < rows)
+                        *reinterpret_cast<uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * ot * 2 + off) = ro[i];
+                }
+            }
+        } else {
+            char* base = gout + 64 * c * ot * (out_bf16 ? 2 : 4);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                if (token(it) >= rows || zc0 + 4 * g >= Dz) continue;
+                const unsigned at = (unsigned)token(it) * (unsigned)ot + wave * kLaCols + 4 * g;
+                if (out_bf16)
+                    *reinterpret_cast<uint2*>(base + 2 * at) =
+                        make_uint2(la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3]));
+                else
+                    *reinterpret_cast<f32x4*>(base + 4 * at) = O[it];
+            }
+        }
+        if (dots && tid < 64) {
+            const int t = rev ? 63 - tid : tid;
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * tid);
+            if (t < rows) gd[64 * c + t] = x;
         }
     };
     fetch(0);
     if (gate_wave) decays(0, log_alpha(0));
+    if constexpr (!STATE)   // the blocks above the diagonal stay zero
+        for (int i = tid; i < TERMS * 64 * RP / 16; i += NTHR) lds_st(sP + 16 * i, make_uint4(0u, 0u, 0u, 0u));
 
     for (int n = 0; n < nc; ++n) {
-        const lchar* g = sG + (n & 1) * kLaGateBytes;
+        const lchar* gt = sG + (n & 1) * kLaGateBytes;
         if (n) lds_barrier();   // the last chunk's tiles are done with
-        if constexpr (!STATE) la_stage<NX, PX, NTHR, sizeof(T) == 2>(sX, rx, tid);
-        la_stage<NX, PX, NTHR, sizeof(T) == 2>(sY, ry, tid);
+        fresh();
+        Pieces ro;
+        if constexpr (!STATE && BF) la_unstage<NZ, PZ, NTHR>(sZ, ro, tid);
+        if constexpr (!STATE) la_stage<NX, PX, NTHR, BF>(sX, rx, tid);
+        la_stage<NX, PX, NTHR, BF>(sY, ry, tid);
         la_stage<NZ, PZ, NTHR, false>(sZ, rz, tid);
         lds_barrier();
-        lane = la_fresh(lane0);
-        h = lane >> 5;
-        l31 = lane & 31;
-        float next_la = 0.f;
+        fresh();
         if constexpr (!STATE)
-            if (n) store(n - 1);
+            if (n) store(n - 1, ro);
+
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!STATE) {
+            // 16 x 16 blocks (it, jt), jt <= it, of the products x . y, times their decays, into LDS
+            for (int k = wave; k < 10; k += NW) {
+                const int it = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0, jt = k - it * (it + 1) / 2;
+                f32x4 P = zero;
+#pragma unroll
+                for (int m = 0; m < DX / 32; ++m)
+                    P = la_mfma(la_row<T, RX>(sY, 16 * jt + l15, m, g).v, la_row<T, RX>(sX, 16 * it + l15, m, g).v, P);
+                const int i = 16 * it + l15, j = 16 * jt + 4 * g;
+                const float ui = lds_ld<float>(gt + 4 * i), wi = lds_ld<float>(gt + 256 + 4 * i);
+                const f32x4 uj = lds_ld<f32x4>(gt + 4 * j), wj = lds_ld<f32x4>(gt + 256 + 4 * j);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float d = (ui - uj[e]) + (wi - wj[e]);
+                    const float x = P[e] * __builtin_amdgcn_exp2f(d);
+                    v[e] = j + e <= i ? x : 0.f;
+                }
+                if constexpr (BF) {
+                    // la_row's order of quads: 8-byte quad 4 (jt % 2) + g of 32 values
+                    lchar* at = sP + i * RP + 16 * ((4 * (jt >> 1) + g) ^ la_swz<RP>(i)) + 8 * (jt & 1);
+#pragma unroll
+                    for (int term = 0; term < TERMS; ++term) {
+                        const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
+                        lds_st(at + term * 64 * RP, make_uint2(lo, hi));
+                        if (term + 1 < TERMS) {
+                            la_rest(lo, neg, v[0], v[1]);
+                            la_rest(hi, neg, v[2], v[3]);
+                        }
+                    }
+                } else {
+                    lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<RP>(i)), f32x4{v[0], v[1], v[2], v[3]});
+                }
+            }
+            // what the state at the chunk's start gives the rows
+#pragma unroll
+            for (int m = 0; m < DX / 32; ++m) {
+                LaFrag<T> x[4];
+#pragma unroll
+                for (int it = 0; it < 4; ++it) x[it] = la_row<T, RX>(sX, 16 * it + l15, m, g);
+                float s8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s8[e] = S[2 * m + (e >> 2)][e & 3];
+                const LaTerms<T, NT> st = la_split<T, NT>(s8, neg);
+#pragma unroll
+                for (int term = TERMS - 1; term >= 0; --term)
+#pragma unroll
+                    for (int it = 0; it < 4; ++it)
+                        O[it] = la_mfma(la_term(st, term), x[it].v, m == 0 && term == TERMS - 1 ? zero : O[it]);
+                __builtin_amdgcn_sched_barrier(0);   // no more of x in registers at once
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const float e = lds_ld<float>(gt + 512 + 4 * (16 * it + l15));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) O[it][j] *= e;
+            }
+        }
+        const float decay = lds_ld<float>(gt + 1024);
+#pragma unroll
+        for (int t = 0; t < TX; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][j] *= decay;
+        if constexpr (!STATE) lds_barrier();   // the products are in LDS
+        fresh();
+        // the next chunk's rows: asked for here, where fewer registers are in
+        // use than above, and still a third of a chunk's time ahead
+        float next_la = 0.f;
         if (n + 1 < nc) {
             fetch(n + 1);
             if (gate_wave) next_la = log_alpha(n + 1);
         }
         if constexpr (!STATE)
             if (dots) fetch_w(n);
-
-        const f32x16 zero = {};
-        if constexpr (!STATE) {
-            // the products x . y of 32 x 32 tiles (i, j) = (0,0), (1,0), (1,1), times their decays, into LDS
-            for (int k = wave; k < 3; k += NW) {
-                const int it = (k + 1) >> 1, jt = k >> 1;
-                f32x16 P = zero;
+        // rows 32 ks .. 32 ks + 31 of y and z: into the output's later rows, then into the state
 #pragma unroll
-                for (int m = 0; m < DX / 16; ++m)
-                    P = la_mma(la_row<T, RX>(sY, 32 * jt + l31, m, h), la_row<T, RX>(sX, 32 * it + l31, m, h), P);
-                const int i = 32 * it + l31;
-                const float ui = lds_ld<float>(g + 4 * i), wi = lds_ld<float>(g + 256 + 4 * i);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int j = 32 * jt + 8 * q + 4 * h;
-                    const f32x4 uj = lds_ld<f32x4>(g + 4 * j), wj = lds_ld<f32x4>(g + 256 + 4 * j);
-                    f32x4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = (ui - uj[e]) + (wi - wj[e]);
-                        const float x = P[4 * q + e] * __builtin_amdgcn_exp2f(d);
-                        v[e] = j + e <= i ? x : 0.f;
-                    }
-                    if constexpr (sizeof(T) == 2) {
-                        // la_row's order of quads: j / 4 = 4 (j / 16) + 2 (q % 2) + h
-                        lchar* at = sP + i * RP + 16 * ((4 * jt + (q & ~1) + h) ^ la_swz<RP>(i)) + 8 * (q & 1);
-#pragma unroll
-                        for (int term = 0; term < NT; ++term) {
-                            const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
-                            lds_st(at + term * 64 * RP, make_uint2(lo, hi));
-                            if (term + 1 < NT) {
-                                float r0 = v[0], r1 = v[1], r2 = v[2], r3 = v[3];
-                                la_rest(lo, neg, r0, r1);
-                                la_rest(hi, neg, r2, r3);
-                                v = f32x4{r0, r1, r2, r3};
-                            }
-                        }
-                    } else {
-                        lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<RP>(i)), v);
-                    }
-                }
-            }
-            // what the state at the chunk's start gives the rows
-            LaFrag<T> x0 = la_row<T, RX>(sX, l31, 0, h), x1 = la_row<T, RX>(sX, 32 + l31, 0, h);
-#pragma unroll
-            for (int m = 0; m < DX / 16; ++m) {
-                const LaFrag<T> c0 = x0, c1 = x1;
-                if (m + 1 < DX / 16) {
-                    x0 = la_row<T, RX>(sX, l31, m + 1, h);
-                    x1 = la_row<T, RX>(sX, 32 + l31, m + 1, h);
-                }
-                float s8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s8[e] = S[m >> 1][8 * (m & 1) + e];
-                const LaTerms<T, NT> st = la_split<T, NT>(s8, neg);
-                O[0] = la_mma(st, c0, m ? O[0] : zero);
-                O[1] = la_mma(st, c1, m ? O[1] : zero);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-            for (int it = 0; it < 2; ++it) {
-                const float e = lds_ld<float>(g + 512 + 4 * (32 * it + l31));
-#pragma unroll
-                for (int r = 0; r < 16; ++r) O[it][r] *= e;
-            }
-        }
-        const float decay = lds_ld<float>(g + 1024);
-#pragma unroll
-        for (int t = 0; t < TX; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
-        if constexpr (!STATE) lds_barrier();   // the products are in LDS
-        // rows 16 ks .. 16 ks + 15 of y and z: into the output's later rows, then into the state
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
+        for (int ks = 0; ks < 2; ++ks) {
             const LaFrag<T> z = la_col<T, RZ, false>(sZ, ks, wave * kLaCols, lane);
-            const int j0 = 16 * ks + 4 * h;   // the lane's rows: j0 + [0, 4) and j0 + 8 + [0, 4)
             if constexpr (!STATE) {
 #pragma unroll
-                for (int it = ks >> 1; it < 2; ++it) {
-                    LaTerms<T, NT> pt;
-                    if constexpr (sizeof(T) == 2) {
+                for (int it = 2 * ks; it < 4; ++it) {
 #pragma unroll
-                        for (int term = 0; term < NT; ++term)
-                            pt.t[term] = la_row<T, RP>(sP + term * 64 * RP, 32 * it + l31, ks, h).v;
-                    } else {
-                        const LaFrag<T> f = la_row<T, RP>(sP, 32 * it + l31, ks, h);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) pt.v[e] = f.v[e];
-                    }
-                    O[it] = la_mma(z, pt, O[it]);
+                    for (int term = TERMS - 1; term >= 0; --term)
+                        O[it] = la_mfma(z.v, la_row<T, RP>(sP + term * 64 * RP, 16 * it + l15, ks, g).v, O[it]);
                 }
             }
-            const f32x4 k0 = lds_ld<f32x4>(g + 768 + 4 * j0), k1 = lds_ld<f32x4>(g + 768 + 4 * j0 + 32);
+            const int j0 = 32 * ks + 4 * g;   // the lane's rows: j0 + [0, 4) and j0 + 16 + [0, 4)
+            const f32x4 k0 = lds_ld<f32x4>(gt + 768 + 4 * j0), k1 = lds_ld<f32x4>(gt + 768 + 4 * j0 + 64);
             float z8[8];
             la_floats(z, z8);
 #pragma unroll
             for (int e = 0; e < 8; ++e) z8[e] *= e < 4 ? k0[e & 3] : k1[e & 3];
             const LaTerms<T, 3> zt = la_split<T, 3>(z8, neg);
 #pragma unroll
-            for (int t = 0; t < TX; ++t)
-                S[t] = la_mma(la_col<T, RX, sizeof(T) == 2>(sY, ks, 32 * t, lane), zt, S[t]);
+            for (int t0 = 0; t0 < TX; t0 += 2) {
+                LaFrag<T> y[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) y[t] = la_col<T, RX, BF>(sY, ks, 16 * (t0 + t), lane);
+#pragma unroll
+                for (int term = la_terms<T, 3>() - 1; term >= 0; --term)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) S[t0 + t] = la_mfma(y[t].v, la_term(zt, term), S[t0 + t]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if (gate_wave && n + 1 < nc) decays(n + 1, next_la);
+        if constexpr (!STATE) finish(n);
     }
-    if constexpr (!STATE) store(nc - 1);
+    if constexpr (!STATE) {
+        lds_barrier();
+        Pieces ro;
+        if constexpr (BF) la_unstage<NZ, PZ, NTHR>(sZ, ro, tid);
+        store(nc - 1, ro);
+    }
 
     float* end = nullptr;
     if constexpr (STATE) {
         end = ps.seg + ((size_t)seq * a.nseg + sg) * elems;
-        if (ct == 0 && gate_wave && lane == 0)
+        if (gate_wave && lane == 0)
             ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
     } else if (ps.end && sg == (rev ? 0 : a.nseg - 1)) {
         end = ps.end + seq * elems;
     }
     if (end && zc < Dz) {
         const bool tr = ps.tr != 0;
-        float* e = tr ? end + (size_t)zc * Dx + 4 * h : end + (size_t)(4 * h) * Dz + zc;
+        float* e = tr ? end + (size_t)zc * Dx + 4 * g : end + (size_t)(4 * g) * Dz + zc;
 #pragma unroll
-        for (int t = 0; t < TX; ++t)
+        for (int t = 0; t < TX; ++t) {
+            if (16 * t + 4 * g >= Dx) continue;
+            if (tr) {
+                *reinterpret_cast<f32x4*>(e + 16 * t) = S[t];
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int d = 32 * t + 8 * q;
-                if (d >= Dx) continue;
-                if (tr) {
-                    *reinterpret_cast<f32x4*>(e + d) =
-                        f32x4{S[t][4 * q], S[t][4 * q + 1], S[t][4 * q + 2], S[t][4 * q + 3]};
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) e[(d + j) * Dz] = S[t][4 * q + j];
-                }
+                for (int j = 0; j < 4; ++j) e[(16 * t + j) * Dz] = S[t][j];
             }
+        }
     }
 }
 
@@ -663,9 +681,9 @@ hipError_t la_launch(const LaArgs& a, int slot, hipStream_t st) {
 
 template <typename T, int DX, int NT, bool STATE>
 hipError_t la_launch_w(const LaArgs& a, int waves, int slot, hipStream_t st) {
+    if (waves == 8) return la_launch<T, DX, 8, NT, STATE>(a, slot, st);
     if (waves == 4) return la_launch<T, DX, 4, NT, STATE>(a, slot, st);
-    if (waves == 2) return la_launch<T, DX, 2, NT, STATE>(a, slot, st);
-    return la_launch<T, DX, 1, NT, STATE>(a, slot, st);
+    return la_launch<T, DX, 2, NT, STATE>(a, slot, st);
 }
 
 }  // namespace dr

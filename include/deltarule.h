@@ -524,7 +524,7 @@ dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void
 
 /* Bytes of device workspace dr_linear_attn_bwd needs for `d` (0 if d is invalid
  * or there is no work): the segments' states twice; with a decay one state per
- * sequence and two floats per token and 32 key channels; with shared heads
+ * sequence and two floats per token; with shared heads
  * fp32 gradients of q and k for every state head. */
 size_t dr_linear_attn_bwd_workspace_bytes(const dr_linattn_desc* d);
 
