@@ -87,8 +87,10 @@ Span rows_span(const Rows& r) {
     return {r.p, (size_t)last * elem_size(r.dtype), r.name};
 }
 
+// A single token's row is as far from the next as it is wide: the kernels tell
+// the rows of a chunk apart by their addresses.
 dr::LaTensor tensor(const Rows& r, int group) {
-    return {r.p, r.n[0] > 1 ? r.s.b : 0, r.n[1] > 1 ? r.s.h : 0, r.n[2] > 1 ? r.s.t : 0, group};
+    return {r.p, r.n[0] > 1 ? r.s.b : 0, r.n[1] > 1 ? r.s.h : 0, r.n[2] > 1 ? r.s.t : r.d, group};
 }
 
 // ------------------------------------------------------------ linear attention

@@ -48,16 +48,25 @@ namespace dr {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// Swizzle of the 16-byte pieces of a row of RB bytes.  Row reads take the same
-// piece of 16 or 32 consecutive rows, transposing reads 64 consecutive bytes of
-// four consecutive rows: the low two bits of the row go to the piece's upper
-// bits (four rows fall on different quarters of the banks), the next two to
-// its lower bits.
-template <int RB>
+// Swizzle of the 16-byte pieces of a row of RB bytes: piece p of row r lies at
+// piece p ^ la_swz(r).  The 64 banks hold 256 bytes.
+//   bf16: a transposing read takes 32 bytes of 16 rows, half a wave (rows r to
+//   r + 7) at a time; a row read takes piece p of 16 rows for each lane group,
+//   pieces p to p + 3 over the groups, in phases of 16 lanes: rows 0-3 and
+//   12-15 of one group with rows 4-11 of the next, then the others.  The four
+//   rows of a quad go to different quarters of the banks (r & 3: the piece's
+//   upper bits, or where rows are shorter the rows themselves), and the quads to
+//   pieces 0, 2, 3, 1 of a quarter, which serves both without a conflict.
+//   fp32: a column read takes one row of each quad, so the quads go to
+//   different quarters.
+template <typename T, int RB>
 __device__ __forceinline__ int la_swz(int r) {
-    if constexpr (RB >= 256) return ((r & 3) << 2) | ((r >> 2) & 3);
-    else if constexpr (RB == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    else return 0;
+    if constexpr (sizeof(T) == 4) return RB >= 256 ? r & 15 : (((r >> 2) & 1) << 2) | ((r >> 1) & 3);
+    const int b0 = (r >> 2) & 1, b1 = (r >> 3) & 1;
+    const int low = ((b0 ^ b1) << 1) | b1;
+    if constexpr (RB >= 256) return ((r & 3) << 2) | low;
+    else if constexpr (RB == 128) return (((r >> 1) & 1) << 2) | low;
+    else return low;
 }
 
 template <typename T>
@@ -145,19 +154,31 @@ __device__ __forceinline__ auto& la_term(const LaTerms<T, NT>& a, int n) {
 template <typename T, int NT>
 constexpr int la_terms() { return sizeof(T) == 4 ? 1 : NT; }
 
-// Row `row`, contraction values 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8.  bf16
-// tiles that are read so hold the eight 8-byte quads of each 32 values in the
-// order 0, 4, 1, 5, 2, 6, 3, 7 (la_stage), so that this is one 16-byte read.
-template <typename T, int RB>
-__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, int g) {
+// LDS addresses.  A lane's address in a tile is a value of its own, the tile's
+// step in the contraction flips bits of it (the swizzle is a flip too), and
+// whole 16-row steps add to it: one register and at most one instruction per
+// read.
+//
+// Rows, contraction values 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8, of row
+// l15 (+ 16 per step).  QUADS: a bf16 tile that holds the eight 8-byte quads of
+// each 32 values in the order 0, 4, 1, 5, 2, 6, 3, 7 (la_stage), so that a lane's
+// values are one 16-byte read; else two.
+template <typename T, int RB, bool QUADS>
+__device__ __forceinline__ int la_row_at(int l15, int g) {
+    const int s = la_swz<T, RB>(l15);
+    if constexpr (sizeof(T) == 2 && !QUADS) return l15 * RB + 16 * ((g >> 1) ^ s) + 8 * (g & 1);
+    else return l15 * RB + 16 * (g ^ s);
+}
+template <typename T, bool QUADS>
+__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int at, int m) {
     LaFrag<T> f;
-    const lchar* r = tile + row * RB;
-    const int s = la_swz<RB>(row);
-    if constexpr (sizeof(T) == 2) {
-        f.v = lds_ld<uint4>(r + 16 * ((4 * m + g) ^ s));
+    if constexpr (sizeof(T) == 2 && QUADS) {
+        f.v = lds_ld<uint4>(tile + (at ^ (64 * m)));
+    } else if constexpr (sizeof(T) == 2) {
+        const uint2 a = lds_ld<uint2>(tile + (at ^ (64 * m))), b = lds_ld<uint2>(tile + (at ^ (64 * m + 32)));
+        f.v = make_uint4(a.x, a.y, b.x, b.y);
     } else {
-        const f32x4 a = lds_ld<f32x4>(r + 16 * ((8 * m + g) ^ s));
-        const f32x4 b = lds_ld<f32x4>(r + 16 * ((8 * m + 4 + g) ^ s));
+        const f32x4 a = lds_ld<f32x4>(tile + (at ^ (128 * m))), b = lds_ld<f32x4>(tile + (at ^ (128 * m + 64)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f.v[j] = a[j];
@@ -167,29 +188,36 @@ __device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int row, int m, i
     return f;
 }
 
-// Column c0 + lane % 16, rows 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8.  QUADS:
-// the tile is in la_row's order.
-template <typename T, int RB, bool QUADS>
-__device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, int m, int c0, int lane) {
-    LaFrag<T> f;
-    const int g = lane >> 4, i = lane & 15;
+// Columns 16 c + lane % 16, rows 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8, of a
+// tile in its own order: the four rows of a transposing read lie on different
+// quarters of the banks and the lane groups' rows on both halves of a quarter
+// (in the QUADS order a read would touch every other 8 bytes only).  fp32
+// reads take one address per row of a quad (e % 4).
+template <typename T, int RB>
+__device__ __forceinline__ int la_col_at(int l15, int g, int j) {
     if constexpr (sizeof(T) == 2) {
-        const int piece = QUADS ? 4 * (c0 >> 5) + (i & 3) : (c0 >> 3) + ((i >> 1) & 1);
-        const int sub = QUADS ? 8 * ((c0 >> 4) & 1) : 8 * (i & 1);
-        uint2 w[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int row = 32 * m + 16 * q + 4 * g + (i >> 2);
-            w[q] = lds_tr4(tile + row * RB + 16 * (piece ^ la_swz<RB>(row)) + sub);
-        }
-        f.v = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        const int row = 4 * g + (l15 >> 2);
+        return row * RB + 16 * (((l15 >> 1) & 1) ^ la_swz<T, RB>(row)) + 8 * (l15 & 1);
     } else {
-        const int col = c0 + i;
+        const int row = 4 * g + j;
+        return row * RB + 16 * ((l15 >> 2) ^ la_swz<T, RB>(row)) + 4 * (l15 & 3);
+    }
+}
+template <typename T>
+struct LaColAt {
+    int at[sizeof(T) == 2 ? 1 : 4];
+};
+template <typename T, int RB>
+__device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, const LaColAt<T>& a, int m, int c) {
+    LaFrag<T> f;
+    if constexpr (sizeof(T) == 2) {
+        const lchar* p = tile + (a.at[0] ^ (32 * c)) + 32 * m * RB;
+        const uint2 x = lds_tr4(p), y = lds_tr4(p + 16 * RB);
+        f.v = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int row = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
-            f.v[e] = lds_ld<float>(tile + row * RB + 16 * ((col >> 2) ^ la_swz<RB>(row)) + 4 * (col & 3));
-        }
+        for (int e = 0; e < 8; ++e)
+            f.v[e] = lds_ld<float>(tile + (a.at[e & 3] ^ (64 * c)) + (32 * m + 16 * (e >> 2)) * RB);
     }
     return f;
 }
@@ -205,70 +233,81 @@ __device__ __forceinline__ void la_floats(const LaFrag<T>& f, float (&x)[8]) {
 }
 
 // A value that the compiler takes as new here, so that what follows from it is
-// computed in the loop and not held in registers across it.
+// computed where it is used and not held in registers across the loop.
 __device__ __forceinline__ int la_fresh(int x) {
     asm volatile("" : "+v"(x));
     return x;
 }
 
-// 64 x PPR 16-byte pieces of a chunk's rows (in the pass's order) into
-// registers.  A thread takes the same piece of rows row0 + i STEP; `base` (the
-// chunk's first token, the same for all lanes) moves by STEP rows at a time and
-// `off` is the thread's own part, so that the addresses are a scalar base and
-// one 32-bit offset.  Rows behind the last token and (ok) pieces behind the
-// width are zero.
-template <int N, int PPR, int NTHR>
-__device__ __forceinline__ void la_fetch(uint4 (&r)[N], const char* base, int64_t row_bytes, unsigned off, bool rev,
-                                         int rows, bool ok, int tid) {
-    constexpr int STEP = NTHR / PPR;
-    const int row0 = tid / PPR;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (rows >= 64) {
-        if (ok) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                r[i] = *reinterpret_cast<const uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * row_bytes + off);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = row0 + i * STEP;
-            if (ok && (rev ? 63 - row : row) < rows)
-                r[i] = *reinterpret_cast<const uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * row_bytes + off);
-        }
-    }
+// Global memory goes through buffer instructions: a scalar descriptor with the
+// range of a chunk's rows and one 32-bit offset per access; reads outside the
+// range give zeros and writes outside are dropped, so that rows behind the last
+// token and columns behind the width (an offset of kLaOut or more) need no
+// branches.  Only the offset in the vector register is checked, so everything
+// that varies is in it.
+constexpr unsigned kLaOut = 0x80000000u;   // behind every range (host: 64 rows span less)
+typedef __amdgpu_buffer_rsrc_t LaRange;
+
+__device__ __forceinline__ LaRange la_range(const void* p, int64_t offset, int rows, unsigned row_bytes, unsigned width) {
+    const unsigned n = rows <= 0 ? 0u : (unsigned)((rows < 64 ? rows : 64) - 1) * row_bytes + width;
+    return __builtin_amdgcn_make_buffer_rsrc((char*)p + offset, 0, (int)n, 0x00027000);
 }
-// The thread's part of la_fetch's addresses.
+
+// 64 x PPR 16-byte pieces of a chunk's rows (in the pass's order): a thread
+// takes piece tid % PPR of rows tid / PPR + i STEP.  flip: 63 for a pass that
+// runs backwards, else 0.
 template <int PPR, int NTHR>
-__device__ __forceinline__ unsigned la_offset(int64_t row_bytes, bool rev, int tid) {
-    constexpr int STEP = NTHR / PPR;
-    const int row0 = tid / PPR;
-    return (unsigned)(rev ? STEP - 1 - row0 : row0) * (unsigned)row_bytes + 16 * (tid % PPR);
+__device__ __forceinline__ int la_offset(unsigned tid, unsigned row_bytes, int flip, int pieces) {
+    constexpr unsigned STEP = NTHR / PPR;
+    const unsigned p = tid % PPR, row = (tid / PPR) ^ (flip & (STEP - 1));
+    return ((int)p < pieces ? 16 * p : kLaOut) + row * row_bytes;
 }
-template <int N, int PPR, int NTHR, bool QUADS>
-__device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], int tid) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int row = tid / PPR + i * (NTHR / PPR), p = tid % PPR;
-        const int s = la_swz<PPR * 16>(row);
-        lchar* at = tile + row * (PPR * 16);
-        if constexpr (QUADS) {
-            const int first = (p & ~3) + 2 * (p & 1), sub = 8 * ((p >> 1) & 1);
-            lds_st(at + 16 * (first ^ s) + sub, make_uint2(r[i].x, r[i].y));
-            lds_st(at + 16 * ((first + 1) ^ s) + sub, make_uint2(r[i].z, r[i].w));
-        } else {
-            lds_st(at + 16 * (p ^ s), r[i]);
-        }
-    }
-}
-// What lies where la_stage (not QUADS) puts a thread's pieces.
 template <int N, int PPR, int NTHR>
-__device__ __forceinline__ void la_unstage(const lchar* tile, uint4 (&r)[N], int tid) {
+__device__ __forceinline__ unsigned la_step(int i, unsigned row_bytes, int flip) {
+    constexpr unsigned STEP = NTHR / PPR;
+    return (flip ? N - 1 - i : i) * STEP * row_bytes;
+}
+template <int N, int PPR, int NTHR>
+__device__ __forceinline__ void la_fetch(uint4 (&r)[N], LaRange range, int offset, unsigned row_bytes, int flip) {
+    const unsigned off = la_fresh(offset);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        r[i] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(range, off + la_step<N, PPR, NTHR>(i, row_bytes, flip), 0, 0));
+}
+
+// A thread's place in a tile: row tid / PPR, piece tid % PPR (QUADS: where the
+// first half of the piece goes; the second half's place is 16 bytes away, a
+// flip).  Rows STEP apart have the same swizzle where STEP is a multiple of 16.
+template <typename T, int PPR, bool QUADS>
+__device__ __forceinline__ int la_slot(unsigned tid, int rows) {
+    const unsigned row = tid / PPR + rows, p = tid % PPR;
+    const int s = la_swz<T, PPR * 16>(row);
+    if constexpr (!QUADS) return row * (PPR * 16) + 16 * (p ^ s);
+    return row * (PPR * 16) + 16 * (((p & ~3u) + 2 * (p & 1)) ^ s) + 8 * ((p >> 1) & 1);
+}
+template <typename T, int PPR, int NTHR, bool QUADS>
+struct LaSlots {
+    static constexpr int STEP = NTHR / PPR, N = STEP >= 16 ? 1 : 16 / STEP;
+    int at[N];
+    __device__ __forceinline__ explicit LaSlots(unsigned tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) at[i] = la_slot<T, PPR, QUADS>(tid, i * STEP);
+    }
+    __device__ __forceinline__ int operator[](int i) const {
+        return at[i % N] + i / N * (N * STEP) * (PPR * 16);
+    }
+};
+template <typename T, int N, int PPR, int NTHR, bool QUADS>
+__device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], const LaSlots<T, PPR, NTHR, QUADS>& slot) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int row = tid / PPR + i * (NTHR / PPR), p = tid % PPR;
-        r[i] = lds_ld<uint4>(tile + row * (PPR * 16) + 16 * (p ^ la_swz<PPR * 16>(row)));
+        if constexpr (QUADS) {
+            lds_st(tile + slot[i], make_uint2(r[i].x, r[i].y));
+            lds_st(tile + (slot[i] ^ 16), make_uint2(r[i].z, r[i].w));
+        } else {
+            lds_st(tile + slot[i], r[i]);
+        }
     }
 }
 
@@ -343,15 +382,9 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     // nothing starts from behind the last segment
     if (STATE && sg == (rev ? 0 : a.nseg - 1)) return;
 
-    int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l15 = lane & 15;
+    const unsigned tid = threadIdx.x;
+    const int lane = tid & 63, g = lane >> 4, l15 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // nothing that follows from the thread's index is held in registers across this
-    auto fresh = [&]() {
-        tid = la_fresh(tid);
-        lane = tid & 63;
-        g = lane >> 4;
-        l15 = lane & 15;
-    };
     const int zc0 = wave * kLaCols;     // the wave's first column
     const int Dx = ps.Dx, Dz = ps.Dz, L = a.L;
     const int px = Dx / EPP, pz = Dz / EPP;
@@ -360,7 +393,10 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         gx = (const char*)ps.x.p + sizeof(T) * (b * ps.x.b + (hd / ps.x.group) * ps.x.h);
     const char* gy = (const char*)ps.y.p + sizeof(T) * (b * ps.y.b + (hd / ps.y.group) * ps.y.h);
     const char* gz = (const char*)ps.z.p + sizeof(T) * (b * ps.z.b + (hd / ps.z.group) * ps.z.h);
-    const int64_t bx = sizeof(T) * ps.x.t, by = sizeof(T) * ps.y.t, bz = sizeof(T) * ps.z.t;
+    // bytes between rows (host: below 2^25) and of a row
+    const unsigned bx = STATE ? 0u : (unsigned)(sizeof(T) * ps.x.t), by = (unsigned)(sizeof(T) * ps.y.t),
+                   bz = (unsigned)(sizeof(T) * ps.z.t);
+    const int flip = rev ? 63 : 0;
     const float* la = a.la ? (a.la_head ? a.la + hd : a.la + (size_t)seq * L) : nullptr;
     const LaNeg neg = la_neg();
 
@@ -397,30 +433,39 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 
     uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
     auto chunk = [&](int n) { return rev ? c_hi - 1 - n : c_lo + n; };
+    const int ox = STATE ? 0 : la_offset<PX, NTHR>(tid, bx, flip, px), oy = la_offset<PX, NTHR>(tid, by, flip, px),
+              oz = la_offset<PZ, NTHR>(tid, bz, flip, pz);
+    const LaSlots<T, PX, NTHR, BF> slot_x(tid);
+    const LaSlots<T, PX, NTHR, false> slot_y(tid);
+    const LaSlots<T, PZ, NTHR, false> slot_z(tid);
     auto fetch = [&](int n) {
         const int c = chunk(n), rows = L - 64 * c;
-        const bool okx = tid % PX < px, okz = tid % PZ < pz;
         if constexpr (!STATE)
-            la_fetch<NX, PX, NTHR>(rx, gx + 64 * c * bx, bx, la_offset<PX, NTHR>(bx, rev, tid), rev, rows, okx, tid);
-        la_fetch<NX, PX, NTHR>(ry, gy + 64 * c * by, by, la_offset<PX, NTHR>(by, rev, tid), rev, rows, okx, tid);
-        la_fetch<NZ, PZ, NTHR>(rz, gz + 64 * c * bz, bz, la_offset<PZ, NTHR>(bz, rev, tid), rev, rows, okz, tid);
+            la_fetch<NX, PX, NTHR>(rx, la_range(gx, (int64_t)(64 * c) * bx, rows, bx, Dx * sizeof(T)), ox, bx, flip);
+        la_fetch<NX, PX, NTHR>(ry, la_range(gy, (int64_t)(64 * c) * by, rows, by, Dx * sizeof(T)), oy, by, flip);
+        la_fetch<NZ, PZ, NTHR>(rz, la_range(gz, (int64_t)(64 * c) * bz, rows, bz, Dz * sizeof(T)), oz, bz, flip);
     };
     auto log_alpha = [&](int n) {
-        const int t = 64 * chunk(n) + (rev ? 63 - lane : lane);
+        const int t = 64 * chunk(n) + (la_fresh(lane) ^ flip);
         return la && t < L ? la[a.la_head ? 0 : t] : 0.f;
     };
     auto decays = [&](int n, float x) {
-        lchar* gt = sG + (n & 1) * kLaGateBytes;
+        const int l = la_fresh(lane);
+        lchar* gt = sG + (n & 1) * kLaGateBytes + 4 * l;
         const double l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
         const double s = la_scan(l2);
         const double total = __shfl(s, 63);
         const double u = rev ? s - l2 : s;
         const float uh = (float)u;
-        lds_st(gt + 4 * lane, uh);
-        lds_st(gt + 256 + 4 * lane, (float)(u - (double)uh));
-        lds_st(gt + 512 + 4 * lane, __builtin_amdgcn_exp2f(uh));
-        lds_st(gt + 768 + 4 * lane, __builtin_amdgcn_exp2f((float)(total - u)));
-        if (lane == 0) lds_st(gt + 1024, __builtin_amdgcn_exp2f((float)total));
+        // a row behind the last token adds nothing to others: its u is beyond
+        // every other row's and its e^{total - u} zero (where rows of an input
+        // share memory, its loads are not zeros)
+        const bool in = 64 * chunk(n) + (l ^ flip) < L;
+        lds_st(gt, in ? uh : 1e30f);
+        lds_st(gt + 256, (float)(u - (double)uh));
+        lds_st(gt + 512, __builtin_amdgcn_exp2f(uh));
+        lds_st(gt + 768, in ? __builtin_amdgcn_exp2f((float)(total - u)) : 0.f);
+        if (l == 0) lds_st(gt + 1024, __builtin_amdgcn_exp2f((float)total));
         if constexpr (STATE) seg_total += total;
     };
 
@@ -431,25 +476,35 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     f32x4 O[4];            // O^T: the wave's columns by rows 16 it + lane % 16
     typedef uint4 Pieces[BF ? NZ : 1];
     RawN<!BF, 4> W[4];
-    const bool dots = !STATE && ps.w.p != nullptr, out_bf16 = ps.out_bf16 != 0;
-    const int64_t ot = ps.ot, wt = ps.w.t;
-    char* const gout =
-        STATE ? nullptr : (char*)ps.out + (out_bf16 ? 2 : 4) * (b * ps.ob + hd * ps.oh);
+    const bool dots = !STATE && NT != 2 && ps.w.p != nullptr, out_bf16 = ps.out_bf16 != 0;
+    const int osz = out_bf16 ? 2 : 4;
+    const unsigned bo = (unsigned)(osz * ps.ot), bw = (unsigned)(sizeof(T) * ps.w.t);
+    char* const gout = STATE ? nullptr : (char*)ps.out + osz * (b * ps.ob + hd * ps.oh);
     const char* gw = dots ? (const char*)ps.w.p + sizeof(T) * (b * ps.w.b + (hd / ps.w.group) * ps.w.h) : nullptr;
     float* const gd = dots ? ps.dots + (size_t)seq * L : nullptr;
-    auto token = [&](int it) { return rev ? 63 - 16 * it - l15 : 16 * it + l15; };
+    const int oo = la_offset<PZ, NTHR>(tid, bo, flip, pz);
+    // the lane's four columns of row 16 it + l15, in a tensor of `size`-byte values
+    auto out_offset = [&](int it, unsigned row_bytes, int size) {
+        const int l = la_fresh(lane), col = zc0 + 4 * (l >> 4);
+        const unsigned t = (16 * it + (l & 15)) ^ flip;
+        return (col < Dz ? (unsigned)(size * col) : kLaOut) + t * row_bytes;
+    };
     auto fetch_w = [&](int n) {
         const int c = chunk(n);
+        const LaRange r = la_range(gw, (int64_t)(64 * c) * bw, L - 64 * c, bw, Dz * sizeof(T));
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-            W[it] = RawN<!BF, 4>{};
-            if (64 * c + token(it) < L && zc0 + 4 * g < Dz)
-                W[it] = ld_rawn<!BF, 4>(gw + 64 * c * wt * (int64_t)sizeof(T),
-                                        (unsigned)token(it) * (unsigned)wt + zc0 + 4 * g);
+            if constexpr (BF)
+                W[it] = __builtin_bit_cast(RawN<!BF, 4>,
+                                           __builtin_amdgcn_raw_buffer_load_b64(r, out_offset(it, bw, 2), 0, 0));
+            else
+                W[it] = __builtin_bit_cast(RawN<!BF, 4>,
+                                           __builtin_amdgcn_raw_buffer_load_b128(r, out_offset(it, bw, 4), 0, 0));
         }
     };
     // at the end of a chunk: the rows' dot products, and bf16 rows into LDS
-    auto finish = [&](int n) {
+    auto finish = [&]() {
+        const int l = la_fresh(lane), g = l >> 4, l15 = l & 15;
         if (dots) {
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -463,79 +518,86 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             }
         }
         if constexpr (BF) {
-            if (out_bf16)
+            if (out_bf16) {
+                lchar* at = sZ + l15 * RZ + 16 * ((2 * wave + (g >> 1)) ^ la_swz<T, RZ>(l15)) + 8 * (g & 1);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const int row = 16 * it + l15;
-                    lds_st(sZ + row * RZ + 16 * ((2 * wave + (g >> 1)) ^ la_swz<RZ>(row)) + 8 * (g & 1),
-                           make_uint2(la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3])));
-                }
+                for (int it = 0; it < 4; ++it)
+                    lds_st(at + 16 * it * RZ, make_uint2(la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3])));
+            }
         }
     };
     auto store = [&](int n, const Pieces& ro) {
+        typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
         const int c = chunk(n), rows = L - 64 * c;
+        const LaRange r = la_range(gout, (int64_t)(64 * c) * bo, rows, bo, Dz * osz);
         if (BF && out_bf16) {
             if constexpr (BF) {
-                constexpr int STEP = NTHR / PZ;
-                char* base = gout + 64 * c * ot * 2;
-                const unsigned off = la_offset<PZ, NTHR>(2 * ot, rev, tid);
-                const bool okz = tid % PZ < pz;
+                const unsigned off = la_fresh(oo);
 #pragma unroll
-                for (int i = 0; i < NZ; ++i) {
-                    const int row = tid / PZ + i * STEP;
-                    if (okz && (rev ? 63 - row : row) < rows)
-                        *reinterpret_cast<uint4*>(base + (rev ? 64 - (i + 1) * STEP : i * STEP) * ot * 2 + off) = ro[i];
-                }
+                for (int i = 0; i < NZ; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, ro[i]), r,
+                                                           off + la_step<NZ, PZ, NTHR>(i, bo, flip), 0, 0);
             }
         } else {
-            char* base = gout + 64 * c * ot * (out_bf16 ? 2 : 4);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                if (token(it) >= rows || zc0 + 4 * g >= Dz) continue;
-                const unsigned at = (unsigned)token(it) * (unsigned)ot + wave * kLaCols + 4 * g;
-                if (out_bf16)
-                    *reinterpret_cast<uint2*>(base + 2 * at) =
-                        make_uint2(la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3]));
-                else
-                    *reinterpret_cast<f32x4*>(base + 4 * at) = O[it];
+                if (!BF && out_bf16) {
+                    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+                    const u32x2 v = {la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3])};
+                    __builtin_amdgcn_raw_buffer_store_b64(v, r, out_offset(it, bo, 2), 0, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), r, out_offset(it, bo, 4), 0,
+                                                           0);
+                }
             }
         }
         if (dots && tid < 64) {
-            const int t = rev ? 63 - tid : tid;
+            const int t = (int)tid ^ flip;
             float x = 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * tid);
             if (t < rows) gd[64 * c + t] = x;
         }
     };
+    const int ax0 = la_row_at<T, RX, true>(l15, g), yrow0 = la_row_at<T, RX, false>(l15, g),
+              ap = la_row_at<T, RP, true>(l15, g);
+    LaColAt<T> ay0, az;
+#pragma unroll
+    for (int j = 0; j < (BF ? 1 : 4); ++j) {
+        ay0.at[j] = la_col_at<T, RX>(l15, g, j);
+        az.at[j] = la_col_at<T, RZ>(l15, g, j) ^ (2 * (int)sizeof(T) * 8 * wave);
+    }
     fetch(0);
     if (gate_wave) decays(0, log_alpha(0));
     if constexpr (!STATE)   // the blocks above the diagonal stay zero
-        for (int i = tid; i < TERMS * 64 * RP / 16; i += NTHR) lds_st(sP + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+        for (unsigned i = tid; i < TERMS * 64 * RP / 16; i += NTHR) lds_st(sP + 16 * i, make_uint4(0u, 0u, 0u, 0u));
 
     for (int n = 0; n < nc; ++n) {
         const lchar* gt = sG + (n & 1) * kLaGateBytes;
         if (n) lds_barrier();   // the last chunk's tiles are done with
-        fresh();
         Pieces ro;
-        if constexpr (!STATE && BF) la_unstage<NZ, PZ, NTHR>(sZ, ro, tid);
-        if constexpr (!STATE) la_stage<NX, PX, NTHR, BF>(sX, rx, tid);
-        la_stage<NX, PX, NTHR, BF>(sY, ry, tid);
-        la_stage<NZ, PZ, NTHR, false>(sZ, rz, tid);
+        if constexpr (!STATE && BF)
+#pragma unroll
+            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
+        if constexpr (!STATE) la_stage(sX, rx, slot_x);
+        la_stage(sY, ry, slot_y);
+        la_stage(sZ, rz, slot_z);
         lds_barrier();
-        fresh();
         if constexpr (!STATE)
             if (n) store(n - 1, ro);
 
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         if constexpr (!STATE) {
+            const int ax = la_fresh(ax0), yrow = la_fresh(yrow0);
+            const int l = la_fresh(lane), g = l >> 4, l15 = l & 15;
             // 16 x 16 blocks (it, jt), jt <= it, of the products x . y, times their decays, into LDS
             for (int k = wave; k < 10; k += NW) {
                 const int it = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0, jt = k - it * (it + 1) / 2;
                 f32x4 P = zero;
 #pragma unroll
                 for (int m = 0; m < DX / 32; ++m)
-                    P = la_mfma(la_row<T, RX>(sY, 16 * jt + l15, m, g).v, la_row<T, RX>(sX, 16 * it + l15, m, g).v, P);
+                    P = la_mfma(la_row<T, false>(sY + 16 * jt * RX, yrow, m).v, la_row<T, true>(sX + 16 * it * RX, ax, m).v,
+                                P);
                 const int i = 16 * it + l15, j = 16 * jt + 4 * g;
                 const float ui = lds_ld<float>(gt + 4 * i), wi = lds_ld<float>(gt + 256 + 4 * i);
                 const f32x4 uj = lds_ld<f32x4>(gt + 4 * j), wj = lds_ld<f32x4>(gt + 256 + 4 * j);
@@ -548,7 +610,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 }
                 if constexpr (BF) {
                     // la_row's order of quads: 8-byte quad 4 (jt % 2) + g of 32 values
-                    lchar* at = sP + i * RP + 16 * ((4 * (jt >> 1) + g) ^ la_swz<RP>(i)) + 8 * (jt & 1);
+                    lchar* at = sP + i * RP + 16 * ((4 * (jt >> 1) + g) ^ la_swz<T, RP>(i)) + 8 * (jt & 1);
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
                         const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
@@ -559,7 +621,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                         }
                     }
                 } else {
-                    lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<RP>(i)), f32x4{v[0], v[1], v[2], v[3]});
+                    lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<T, RP>(i)), f32x4{v[0], v[1], v[2], v[3]});
                 }
             }
             // what the state at the chunk's start gives the rows
@@ -567,7 +629,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             for (int m = 0; m < DX / 32; ++m) {
                 LaFrag<T> x[4];
 #pragma unroll
-                for (int it = 0; it < 4; ++it) x[it] = la_row<T, RX>(sX, 16 * it + l15, m, g);
+                for (int it = 0; it < 4; ++it) x[it] = la_row<T, true>(sX + 16 * it * RX, ax, m);
                 float s8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s8[e] = S[2 * m + (e >> 2)][e & 3];
@@ -592,7 +654,6 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 #pragma unroll
             for (int j = 0; j < 4; ++j) S[t][j] *= decay;
         if constexpr (!STATE) lds_barrier();   // the products are in LDS
-        fresh();
         // the next chunk's rows: asked for here, where fewer registers are in
         // use than above, and still a third of a chunk's time ahead
         float next_la = 0.f;
@@ -600,20 +661,25 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             fetch(n + 1);
             if (gate_wave) next_la = log_alpha(n + 1);
         }
-        if constexpr (!STATE)
-            if (dots) fetch_w(n);
+        LaColAt<T> ay;
+#pragma unroll
+        for (int j = 0; j < (BF ? 1 : 4); ++j) ay.at[j] = la_fresh(ay0.at[j]);
+        const int g = la_fresh(lane) >> 4;
         // rows 32 ks .. 32 ks + 31 of y and z: into the output's later rows, then into the state
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            const LaFrag<T> z = la_col<T, RZ, false>(sZ, ks, wave * kLaCols, lane);
+            const LaFrag<T> z = la_col<T, RZ>(sZ, az, ks, 0);
             if constexpr (!STATE) {
 #pragma unroll
                 for (int it = 2 * ks; it < 4; ++it) {
 #pragma unroll
                     for (int term = TERMS - 1; term >= 0; --term)
-                        O[it] = la_mfma(z.v, la_row<T, RP>(sP + term * 64 * RP, 16 * it + l15, ks, g).v, O[it]);
+                        O[it] = la_mfma(z.v, la_row<T, true>(sP + term * 64 * RP + 16 * it * RP, ap, ks).v, O[it]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!STATE)
+                if (ks == 1 && dots) fetch_w(n);
             const int j0 = 32 * ks + 4 * g;   // the lane's rows: j0 + [0, 4) and j0 + 16 + [0, 4)
             const f32x4 k0 = lds_ld<f32x4>(gt + 768 + 4 * j0), k1 = lds_ld<f32x4>(gt + 768 + 4 * j0 + 64);
             float z8[8];
@@ -625,7 +691,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             for (int t0 = 0; t0 < TX; t0 += 2) {
                 LaFrag<T> y[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) y[t] = la_col<T, RX, BF>(sY, ks, 16 * (t0 + t), lane);
+                for (int t = 0; t < 2; ++t) y[t] = la_col<T, RX>(sY, ay, ks, t0 + t);
 #pragma unroll
                 for (int term = la_terms<T, 3>() - 1; term >= 0; --term)
 #pragma unroll
@@ -634,12 +700,14 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             }
         }
         if (gate_wave && n + 1 < nc) decays(n + 1, next_la);
-        if constexpr (!STATE) finish(n);
+        if constexpr (!STATE) finish();
     }
     if constexpr (!STATE) {
         lds_barrier();
         Pieces ro;
-        if constexpr (BF) la_unstage<NZ, PZ, NTHR>(sZ, ro, tid);
+        if constexpr (BF)
+#pragma unroll
+            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
         store(nc - 1, ro);
     }
 
