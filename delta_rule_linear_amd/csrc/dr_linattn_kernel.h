@@ -239,6 +239,9 @@ __device__ __forceinline__ int la_fresh(int x) {
     return x;
 }
 
+// A product whose upper half no register is kept for.
+__device__ __forceinline__ unsigned la_mul(unsigned a, unsigned b) { return (unsigned)la_fresh((int)(a * b)); }
+
 // Global memory goes through buffer instructions: a scalar descriptor with the
 // range of a chunk's rows and one 32-bit offset per access; reads outside the
 // range give zeros and writes outside are dropped, so that rows behind the last
@@ -260,7 +263,7 @@ template <int PPR, int NTHR>
 __device__ __forceinline__ int la_offset(unsigned tid, unsigned row_bytes, int flip, int pieces) {
     constexpr unsigned STEP = NTHR / PPR;
     const unsigned p = tid % PPR, row = (tid / PPR) ^ (flip & (STEP - 1));
-    return ((int)p < pieces ? 16 * p : kLaOut) + row * row_bytes;
+    return ((int)p < pieces ? 16 * p : kLaOut) + la_mul(row, row_bytes);
 }
 template <int N, int PPR, int NTHR>
 __device__ __forceinline__ unsigned la_step(int i, unsigned row_bytes, int flip) {
@@ -268,8 +271,7 @@ __device__ __forceinline__ unsigned la_step(int i, unsigned row_bytes, int flip)
     return (flip ? N - 1 - i : i) * STEP * row_bytes;
 }
 template <int N, int PPR, int NTHR>
-__device__ __forceinline__ void la_fetch(uint4 (&r)[N], LaRange range, int offset, unsigned row_bytes, int flip) {
-    const unsigned off = la_fresh(offset);
+__device__ __forceinline__ void la_fetch(uint4 (&r)[N], LaRange range, unsigned off, unsigned row_bytes, int flip) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
         r[i] = __builtin_bit_cast(
@@ -433,24 +435,25 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 
     uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
     auto chunk = [&](int n) { return rev ? c_hi - 1 - n : c_lo + n; };
-    const int ox = STATE ? 0 : la_offset<PX, NTHR>(tid, bx, flip, px), oy = la_offset<PX, NTHR>(tid, by, flip, px),
-              oz = la_offset<PZ, NTHR>(tid, bz, flip, pz);
-    const LaSlots<T, PX, NTHR, BF> slot_x(tid);
     const LaSlots<T, PX, NTHR, false> slot_y(tid);
     const LaSlots<T, PZ, NTHR, false> slot_z(tid);
     auto fetch = [&](int n) {
         const int c = chunk(n), rows = L - 64 * c;
+        const unsigned t = la_fresh(tid);
         if constexpr (!STATE)
-            la_fetch<NX, PX, NTHR>(rx, la_range(gx, (int64_t)(64 * c) * bx, rows, bx, Dx * sizeof(T)), ox, bx, flip);
-        la_fetch<NX, PX, NTHR>(ry, la_range(gy, (int64_t)(64 * c) * by, rows, by, Dx * sizeof(T)), oy, by, flip);
-        la_fetch<NZ, PZ, NTHR>(rz, la_range(gz, (int64_t)(64 * c) * bz, rows, bz, Dz * sizeof(T)), oz, bz, flip);
+            la_fetch<NX, PX, NTHR>(rx, la_range(gx, (int64_t)(64 * c) * bx, rows, bx, Dx * sizeof(T)),
+                                   la_offset<PX, NTHR>(t, bx, flip, px), bx, flip);
+        la_fetch<NX, PX, NTHR>(ry, la_range(gy, (int64_t)(64 * c) * by, rows, by, Dx * sizeof(T)),
+                               la_offset<PX, NTHR>(t, by, flip, px), by, flip);
+        la_fetch<NZ, PZ, NTHR>(rz, la_range(gz, (int64_t)(64 * c) * bz, rows, bz, Dz * sizeof(T)),
+                               la_offset<PZ, NTHR>(t, bz, flip, pz), bz, flip);
     };
     auto log_alpha = [&](int n) {
-        const int t = 64 * chunk(n) + (la_fresh(lane) ^ flip);
+        const int t = 64 * chunk(n) + ((la_fresh(tid) & 63) ^ flip);
         return la && t < L ? la[a.la_head ? 0 : t] : 0.f;
     };
     auto decays = [&](int n, float x) {
-        const int l = la_fresh(lane);
+        const int l = (la_fresh(tid) & 63);
         lchar* gt = sG + (n & 1) * kLaGateBytes + 4 * l;
         const double l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
         const double s = la_scan(l2);
@@ -482,12 +485,11 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     char* const gout = STATE ? nullptr : (char*)ps.out + osz * (b * ps.ob + hd * ps.oh);
     const char* gw = dots ? (const char*)ps.w.p + sizeof(T) * (b * ps.w.b + (hd / ps.w.group) * ps.w.h) : nullptr;
     float* const gd = dots ? ps.dots + (size_t)seq * L : nullptr;
-    const int oo = la_offset<PZ, NTHR>(tid, bo, flip, pz);
     // the lane's four columns of row 16 it + l15, in a tensor of `size`-byte values
     auto out_offset = [&](int it, unsigned row_bytes, int size) {
-        const int l = la_fresh(lane), col = zc0 + 4 * (l >> 4);
+        const int l = (la_fresh(tid) & 63), col = zc0 + 4 * (l >> 4);
         const unsigned t = (16 * it + (l & 15)) ^ flip;
-        return (col < Dz ? (unsigned)(size * col) : kLaOut) + t * row_bytes;
+        return (col < Dz ? (unsigned)(size * col) : kLaOut) + la_mul(t, row_bytes);
     };
     auto fetch_w = [&](int n) {
         const int c = chunk(n);
@@ -502,21 +504,31 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                                            __builtin_amdgcn_raw_buffer_load_b128(r, out_offset(it, bw, 4), 0, 0));
         }
     };
-    // at the end of a chunk: the rows' dot products, and bf16 rows into LDS
-    auto finish = [&]() {
-        const int l = la_fresh(lane), g = l >> 4, l15 = l & 15;
-        if (dots) {
+    // the rows' dot products, per wave into LDS, then their sums
+    auto dot_rows = [&]() {
+        const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15;
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                float w4[4], dot = 0.f;
-                cvt_rawn<!BF, 4>(W[it], w4);
+        for (int it = 0; it < 4; ++it) {
+            float w4[4], dot = 0.f;
+            cvt_rawn<!BF, 4>(W[it], w4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dot += O[it][j] * w4[j];
-                dot += __shfl_xor(dot, 16);
-                dot += __shfl_xor(dot, 32);
-                if (g == 0) lds_st(sR + 256 * wave + 4 * (16 * it + l15), dot);
-            }
+            for (int j = 0; j < 4; ++j) dot += O[it][j] * w4[j];
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            if (g == 0) lds_st(sR + 256 * wave + 4 * (16 * it + l15), dot);
         }
+    };
+    auto store_dots = [&](int n) {
+        if (tid >= 64) return;
+        const int t = 64 * chunk(n) + ((int)tid ^ flip);
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * tid);
+        if (t < L) gd[t] = x;
+    };
+    // at the end of a chunk: bf16 rows into LDS
+    auto finish = [&]() {
+        const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15;
         if constexpr (BF) {
             if (out_bf16) {
                 lchar* at = sZ + l15 * RZ + 16 * ((2 * wave + (g >> 1)) ^ la_swz<T, RZ>(l15)) + 8 * (g & 1);
@@ -532,7 +544,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         const LaRange r = la_range(gout, (int64_t)(64 * c) * bo, rows, bo, Dz * osz);
         if (BF && out_bf16) {
             if constexpr (BF) {
-                const unsigned off = la_fresh(oo);
+                const unsigned off = la_offset<PZ, NTHR>(la_fresh(tid), bo, flip, pz);
 #pragma unroll
                 for (int i = 0; i < NZ; ++i)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, ro[i]), r,
@@ -551,16 +563,8 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 }
             }
         }
-        if (dots && tid < 64) {
-            const int t = (int)tid ^ flip;
-            float x = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * tid);
-            if (t < rows) gd[64 * c + t] = x;
-        }
     };
-    const int ax0 = la_row_at<T, RX, true>(l15, g), yrow0 = la_row_at<T, RX, false>(l15, g),
-              ap = la_row_at<T, RP, true>(l15, g);
+    const int ax0 = la_row_at<T, RX, true>(l15, g), ap = la_row_at<T, RP, true>(l15, g);
     LaColAt<T> ay0, az;
 #pragma unroll
     for (int j = 0; j < (BF ? 1 : 4); ++j) {
@@ -579,17 +583,20 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         if constexpr (!STATE && BF)
 #pragma unroll
             for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
-        if constexpr (!STATE) la_stage(sX, rx, slot_x);
+        if constexpr (!STATE) la_stage(sX, rx, LaSlots<T, PX, NTHR, BF>(la_fresh(tid)));
         la_stage(sY, ry, slot_y);
         la_stage(sZ, rz, slot_z);
         lds_barrier();
         if constexpr (!STATE)
-            if (n) store(n - 1, ro);
+            if (n) {
+                store(n - 1, ro);
+                if (dots) dot_rows();
+            }
 
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         if constexpr (!STATE) {
-            const int ax = la_fresh(ax0), yrow = la_fresh(yrow0);
-            const int l = la_fresh(lane), g = l >> 4, l15 = l & 15;
+            const int ax = la_fresh(ax0);
+            const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15, yrow = la_row_at<T, RX, false>(l15, g);
             // 16 x 16 blocks (it, jt), jt <= it, of the products x . y, times their decays, into LDS
             for (int k = wave; k < 10; k += NW) {
                 const int it = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0, jt = k - it * (it + 1) / 2;
@@ -654,6 +661,8 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 #pragma unroll
             for (int j = 0; j < 4; ++j) S[t][j] *= decay;
         if constexpr (!STATE) lds_barrier();   // the products are in LDS
+        if constexpr (!STATE)
+            if (dots && n) store_dots(n - 1);
         // the next chunk's rows: asked for here, where fewer registers are in
         // use than above, and still a third of a chunk's time ahead
         float next_la = 0.f;
@@ -664,7 +673,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         LaColAt<T> ay;
 #pragma unroll
         for (int j = 0; j < (BF ? 1 : 4); ++j) ay.at[j] = la_fresh(ay0.at[j]);
-        const int g = la_fresh(lane) >> 4;
+        const int g = (la_fresh(tid) & 63) >> 4;
         // rows 32 ks .. 32 ks + 31 of y and z: into the output's later rows, then into the state
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -678,8 +687,6 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (!STATE)
-                if (ks == 1 && dots) fetch_w(n);
             const int j0 = 32 * ks + 4 * g;   // the lane's rows: j0 + [0, 4) and j0 + 16 + [0, 4)
             const f32x4 k0 = lds_ld<f32x4>(gt + 768 + 4 * j0), k1 = lds_ld<f32x4>(gt + 768 + 4 * j0 + 64);
             float z8[8];
@@ -700,7 +707,10 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             }
         }
         if (gate_wave && n + 1 < nc) decays(n + 1, next_la);
-        if constexpr (!STATE) finish();
+        if constexpr (!STATE) {
+            if (dots) fetch_w(n);
+            finish();
+        }
     }
     if constexpr (!STATE) {
         lds_barrier();
@@ -709,6 +719,11 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 #pragma unroll
             for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
         store(nc - 1, ro);
+        if (dots) {
+            dot_rows();
+            lds_barrier();
+            store_dots(nc - 1);
+        }
     }
 
     float* end = nullptr;
