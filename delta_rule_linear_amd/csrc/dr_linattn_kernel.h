@@ -374,11 +374,15 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     const int per = (a.total + 7) / 8;
     int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if (id >= a.total || (int)(blockIdx.x >> 3) >= per) return;
+    // The passes of one segment run side by side, so that what they share is
+    // read from memory once; the segments are taken from the last, which the
+    // state pass has left in the caches.
+    const LaPass& ps = a.pass[id % a.npass];
+    id /= a.npass;
     const int nseq = a.B * a.H;
+    if constexpr (!STATE) id = nseq * a.nseg - 1 - id;
     const int seq = id % nseq;
-    id /= nseq;
-    const int sg = id % a.nseg;
-    const LaPass& ps = a.pass[id / a.nseg];
+    const int sg = id / nseq;
     const int b = seq / a.H, hd = seq % a.H;
     const bool rev = ps.rev != 0;
     // nothing starts from behind the last segment
