@@ -596,6 +596,11 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 store(n - 1, ro);
                 if (dots) dot_rows();
             }
+        float next_la = 0.f;
+        if (n + 1 < nc) {
+            fetch(n + 1);
+            if (gate_wave) next_la = log_alpha(n + 1);
+        }
 
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         if constexpr (!STATE) {
@@ -667,13 +672,6 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         if constexpr (!STATE) lds_barrier();   // the products are in LDS
         if constexpr (!STATE)
             if (dots && n) store_dots(n - 1);
-        // the next chunk's rows: asked for here, where fewer registers are in
-        // use than above, and still a third of a chunk's time ahead
-        float next_la = 0.f;
-        if (n + 1 < nc) {
-            fetch(n + 1);
-            if (gate_wave) next_la = log_alpha(n + 1);
-        }
         LaColAt<T> ay;
 #pragma unroll
         for (int j = 0; j < (BF ? 1 : 4); ++j) ay.at[j] = la_fresh(ay0.at[j]);
