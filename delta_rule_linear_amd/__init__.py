@@ -38,6 +38,7 @@ Layer norm of rows, such as those outputs, and its gradients:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -591,9 +592,10 @@ def _decode(S, q, k, v, log_alpha, beta, beta_v, gate, beta_mode, out_dtype, o, 
 # linear attention with a decay per head; layer norm
 # ---------------------------------------------------------------------------
 
-def _strides(t) -> Strides:
+def _strides(t):
     """The strides of a [B,H,L,D] view in elements (0 where a dimension is 1)."""
-    return Strides(*(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])))
+    n, s = t.shape, t.stride()
+    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
 def _need_rows(t, name, device, dtype=None, shape=None):
@@ -605,15 +607,19 @@ def _need_rows(t, name, device, dtype=None, shape=None):
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _need_on(t, name, device, dtype, shape):
+    torch = _torch()
+    if (isinstance(t, torch.Tensor) and t.device == device and t.shape == shape and t.is_contiguous() and
+            (dtype is None or t.dtype == dtype)):
+        return
     _need(t, name, dtype, shape)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -621,21 +627,26 @@ def _need_on(t, name, device, dtype, shape):
 
 class _on:
     """Runs on `device`, on `stream` (default: the device's current stream), so
-    that what is allocated inside belongs to that stream."""
+    that what is allocated inside belongs to that stream; gives the raw stream."""
 
     def __init__(self, device, stream):
         torch = _torch()
         if stream is not None and stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+            stream = torch.cuda.current_stream(device)
+        self.stream = stream.cuda_stream
 
     def __enter__(self):
-        self.ctx.__enter__()
-        return self.stream.cuda_stream
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream
 
     def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+        return None if self.ctx is None else self.ctx.__exit__(*exc)
 
 
 def _workspace(workspace, nbytes, device):
@@ -663,6 +674,27 @@ def linattn_desc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, decay: str) -> LinAtt
     """A descriptor for dense tensors; the strides can be set afterwards."""
     qk, vo = Strides(Hk * L * Dk, L * Dk, Dk), Strides(H * L * Dv, L * Dv, Dv)
     return LinAttnDesc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, DECAYS[decay], qk, qk, vo, vo, qk, qk, vo)
+
+
+# Descriptors and workspace sizes of the shapes in use (they depend on sizes,
+# types and strides alone).
+@functools.lru_cache(maxsize=512)
+def _linattn_plan(bwd: bool, sizes, *strides):
+    desc = LinAttnDesc(*sizes, *(Strides(*s) for s in strides))
+    fn = lib().dr_linear_attn_bwd_workspace_bytes if bwd else lib().dr_linear_attn_fwd_workspace_bytes
+    return desc, ctypes.byref(desc), int(fn(ctypes.byref(desc)))
+
+
+@functools.lru_cache(maxsize=512)
+def _linattn_step_plan(*sizes):
+    desc = LinAttnStepDesc(*sizes)
+    return desc, ctypes.byref(desc)
+
+
+@functools.lru_cache(maxsize=512)
+def _layernorm_plan(sizes, *strides):
+    desc = LayerNormDesc(*sizes, *(Strides(*s) for s in strides))
+    return desc, ctypes.byref(desc), int(lib().dr_layernorm_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
 def dr_linear_attn_fwd_workspace_bytes(desc: LinAttnDesc) -> int:
@@ -713,10 +745,11 @@ def dr_linear_attn_fwd(q, k, v, log_alpha=None, S0=None, *, decay: str, out_dtyp
             _need_on(S_final, "S_final", dev, torch.float32, (B, H, Dk, Dv))
         elif want_state:
             S_final = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-        desc = LinAttnDesc(B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay],
-                           _strides(q), _strides(k), _strides(v), _strides(o))
-        workspace, wbytes = _workspace(workspace, dr_linear_attn_fwd_workspace_bytes(desc), dev)
-        _check(lib().dr_linear_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
+        _, desc, nbytes = _linattn_plan(
+            False, (B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay]),
+            _strides(q), _strides(k), _strides(v), _strides(o))
+        workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_linear_attn_fwd(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
                                         _ptr(o), _ptr(S_final), _ptr(workspace), wbytes, st))
     return o, S_final
 
@@ -741,11 +774,12 @@ def dr_linear_attn_bwd(q, k, v, log_alpha, S0, dO, dS_final=None, *, decay: str,
                "dv": torch.empty_like(v, dtype=to),
                "dlog_alpha": None if log_alpha is None else torch.empty_like(log_alpha),
                "dS0": torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if want_dS0 else None}
-        desc = LinAttnDesc(B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(to), DECAYS[decay], _strides(q),
-                           _strides(k), _strides(v), _strides(dO), _strides(out["dq"]), _strides(out["dk"]),
-                           _strides(out["dv"]))
-        workspace, wbytes = _workspace(workspace, dr_linear_attn_bwd_workspace_bytes(desc), dev)
-        _check(lib().dr_linear_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
+        _, desc, nbytes = _linattn_plan(
+            True, (B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(to), DECAYS[decay]),
+            _strides(q), _strides(k), _strides(v), _strides(dO), _strides(out["dq"]), _strides(out["dk"]),
+            _strides(out["dv"]))
+        workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_linear_attn_bwd(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S0),
                                         _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                                         _ptr(out["dlog_alpha"]), _ptr(out["dS0"]), _ptr(workspace), wbytes, st))
     return out
@@ -771,8 +805,8 @@ def dr_linear_attn_step(S, q, k, v, log_alpha=None, *, decay: str, out_dtype=Non
             o = torch.empty((N, H, Dv), dtype=torch.float32 if out_dtype is None else out_dtype, device=dev)
         else:
             _need_on(o, "o", dev, out_dtype, (N, H, Dv))
-        desc = LinAttnStepDesc(N, H, Hk, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay])
-        _check(lib().dr_linear_attn_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S),
+        _, desc = _linattn_step_plan(N, H, Hk, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay])
+        _check(lib().dr_linear_attn_step(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(S),
                                          _ptr(o), st))
     return o
 
@@ -835,9 +869,9 @@ def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=
                 _need_on(t, name, dev, torch.float32, lead)
             stats.append(t)
         y4 = _norm_rows(y, 2 if per_head else 1)
-        desc = LayerNormDesc(B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32, eps,
-                             _strides(x4), _strides(y4))
-        _check(lib().dr_layernorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(stats[0]),
+        _, desc, _ = _layernorm_plan((B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32,
+                                      float(eps)), _strides(x4), _strides(y4))
+        _check(lib().dr_layernorm_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(stats[0]),
                                       _ptr(stats[1]), st))
     return y, stats[0], stats[1]
 
@@ -867,16 +901,16 @@ def dr_layernorm_bwd(x, weight, mean, rstd, dy, *, per_head=None, grad_dtype=Non
         else:
             _need_rows(dx, "dx", dev, grad_dtype, tuple(x.shape))
         dims = 2 if per_head else 1
-        desc = LayerNormDesc(B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
-                             _dtype_code(dy.dtype), 0.0, _strides(x4), _strides(_norm_rows(dx, dims)),
-                             _strides(_norm_rows(dy, dims)))
+        _, desc, nbytes = _layernorm_plan((B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
+                                           _dtype_code(dy.dtype), 0.0), _strides(x4), _strides(_norm_rows(dx, dims)),
+                                          _strides(_norm_rows(dy, dims)))
         out = {"dx": dx, "dweight": None, "dbias": None}
         wbytes = 0
         if want_sums:
             out["dweight"] = torch.empty(wshape, dtype=torch.float32, device=dev)
             out["dbias"] = torch.empty(wshape, dtype=torch.float32, device=dev)
-            workspace, wbytes = _workspace(workspace, dr_layernorm_bwd_workspace_bytes(desc), dev)
-        _check(lib().dr_layernorm_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
+            workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_layernorm_bwd(desc, _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
                                       _ptr(dx), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), wbytes,
                                       st))
     return out

@@ -41,6 +41,8 @@ struct LnShape {
     int lanes, vecs;
 };
 LnShape ln_shape(int D);
+// Rows that a workgroup takes in one pass.
+int ln_pass_rows(int D, bool bwd);
 // vec: rows are read and written in 16-byte pieces (D and every stride a
 // multiple of 8 elements)
 hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st);

@@ -121,9 +121,15 @@ __device__ __forceinline__ void ln_row(const LnArgs& a, unsigned g, unsigned r, 
     }
 }
 
+// Rows that a lane group has in flight: short rows leave room for several.
+template <int VPT>
+constexpr int ln_rows_fwd() { return VPT == 1 ? 4 : VPT == 2 ? 2 : 1; }
+template <int VPT>
+constexpr int ln_rows_bwd() { return VPT == 1 ? 2 : 1; }
+
 template <bool VEC, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
-    constexpr int RPB = kLnThreads / LPR;   // rows at a time
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_fwd<VPT>();   // rows at a time, and in flight of each
     __shared__ float red[4];
     const unsigned g = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
     const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
@@ -137,45 +143,50 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             bs[v][e] = c < a.D && a.bias ? a.bias[(size_t)g * a.D + c] : 0.f;
         }
     const float rD = (float)a.D;
-    for (unsigned r0 = blk * RPB; r0 < a.rows; r0 += a.blocks * RPB) {
-        const unsigned r = r0 + sub;
-        const bool ok = r < a.rows;
-        unsigned b = 0, h = 0, l = 0;
-        ln_row(a, g, ok ? r : a.rows - 1, b, h, l);
-        float x[VPT][8];
-        ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b * a.sx.b + h * a.sx.h + l * a.sx.t, a.D, lane, x);
-        float s = 0.f;
+    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += a.blocks * (RPB * RU)) {
+        float x[RU][VPT][8];
+        unsigned b[RU], h[RU], l[RU];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int u = 0; u < RU; ++u) {
+            const unsigned r = r0 + u * RPB + sub;
+            ln_row(a, g, r < a.rows ? r : a.rows - 1, b[u], h[u], l[u]);
+            ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b[u] * a.sx.b + h[u] * a.sx.h + l[u] * a.sx.t, a.D, lane, x[u]);
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[v][e];
-        const float mean = ln_sum<LPR>(s, red) / rD;
-        s = 0.f;
+        for (int u = 0; u < RU; ++u) {
+            float s = 0.f;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+            for (int v = 0; v < VPT; ++v)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[v][e] - mean : 0.f;
-                s += x[v][e] * x[v][e];
+                for (int e = 0; e < 8; ++e) s += x[u][v][e];
+            const float mean = ln_sum<LPR>(s, red) / rD;
+            s = 0.f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[u][v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[u][v][e] - mean : 0.f;
+                    s += x[u][v][e] * x[u][v][e];
+                }
+            const float rstd = 1.f / sqrtf(ln_sum<LPR>(s, red) / rD + a.eps);
+            if (r0 + u * RPB + sub >= a.rows) continue;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[u][v][e] = x[u][v][e] * rstd * w[v][e] + bs[v][e];
+            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b[u] * a.sy.b + h[u] * a.sy.h + l[u] * a.sy.t, a.D, lane, x[u]);
+            if (lane == 0) {
+                const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
+                if (a.mean_out) a.mean_out[at] = mean;
+                if (a.rstd_out) a.rstd_out[at] = rstd;
             }
-        const float rstd = 1.f / sqrtf(ln_sum<LPR>(s, red) / rD + a.eps);
-        if (!ok) continue;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * w[v][e] + bs[v][e];
-        ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b * a.sy.b + h * a.sy.h + l * a.sy.t, a.D, lane, x);
-        if (lane == 0) {
-            const size_t at = ((size_t)b * a.H + h) * a.L + l;
-            if (a.mean_out) a.mean_out[at] = mean;
-            if (a.rstd_out) a.rstd_out[at] = rstd;
         }
     }
 }
 
 template <bool VEC, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
-    constexpr int RPB = kLnThreads / LPR;
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_bwd<VPT>();
     constexpr int NCOL = 8 * VPT * LPR;   // columns that the lanes of a row hold
     __shared__ float red[4];
     __shared__ float acc[LPR <= 64 ? 4 : 1][LPR <= 64 ? NCOL : 1];
@@ -191,38 +202,45 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             dw[v][e] = db[v][e] = 0.f;
         }
     const float rD = (float)a.D;
-    for (unsigned r0 = blk * RPB; r0 < a.rows; r0 += a.blocks * RPB) {
-        const unsigned r = r0 + sub;
-        const bool ok = r < a.rows;
-        unsigned b = 0, h = 0, l = 0;
-        ln_row(a, g, ok ? r : a.rows - 1, b, h, l);
-        const size_t at = ((size_t)b * a.H + h) * a.L + l;
-        const float mean = a.mean[at], rstd = a.rstd[at];
-        float x[VPT][8], dy[VPT][8];
-        ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b * a.sx.b + h * a.sx.h + l * a.sx.t, a.D, lane, x);
-        ln_load<VEC, LPR, VPT>(a.dy, a.dy_f32, b * a.sdy.b + h * a.sdy.h + l * a.sdy.t, a.D, lane, dy);
-        float s1 = 0.f, s2 = 0.f;
+    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += a.blocks * (RPB * RU)) {
+        float x[RU][VPT][8], dy[RU][VPT][8], mean[RU], rstd[RU];
+        unsigned b[RU], h[RU], l[RU];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int u = 0; u < RU; ++u) {
+            const unsigned r = r0 + u * RPB + sub;
+            ln_row(a, g, r < a.rows ? r : a.rows - 1, b[u], h[u], l[u]);
+            const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
+            mean[u] = a.mean[at];
+            rstd[u] = a.rstd[at];
+            ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b[u] * a.sx.b + h[u] * a.sx.h + l[u] * a.sx.t, a.D, lane, x[u]);
+            ln_load<VEC, LPR, VPT>(a.dy, a.dy_f32, b[u] * a.sdy.b + h[u] * a.sdy.h + l[u] * a.sdy.t, a.D, lane, dy[u]);
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[v][e] = (x[v][e] - mean) * rstd;   // behind D: dy and w are zero there
-                if (ok) {
-                    dw[v][e] += dy[v][e] * x[v][e];
-                    db[v][e] += dy[v][e];
+        for (int u = 0; u < RU; ++u) {
+            const bool ok = r0 + u * RPB + sub < a.rows;
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[u][v][e] = (x[u][v][e] - mean[u]) * rstd[u];   // behind D: dy and w are zero there
+                    if (ok) {
+                        dw[v][e] += dy[u][v][e] * x[u][v][e];
+                        db[v][e] += dy[u][v][e];
+                    }
+                    dy[u][v][e] *= w[v][e];
+                    s1 += dy[u][v][e];
+                    s2 += dy[u][v][e] * x[u][v][e];
                 }
-                dy[v][e] *= w[v][e];
-                s1 += dy[v][e];
-                s2 += dy[v][e] * x[v][e];
-            }
-        s1 = ln_sum<LPR>(s1, red) / rD;
-        s2 = ln_sum<LPR>(s2, red) / rD;
-        if (!ok) continue;
+            s1 = ln_sum<LPR>(s1, red) / rD;
+            s2 = ln_sum<LPR>(s2, red) / rD;
+            if (!ok) continue;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+            for (int v = 0; v < VPT; ++v)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[v][e] = rstd * (dy[v][e] - s1 - x[v][e] * s2);
-        ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b * a.sy.b + h * a.sy.h + l * a.sy.t, a.D, lane, x);
+                for (int e = 0; e < 8; ++e) x[u][v][e] = rstd[u] * (dy[u][v][e] - s1 - x[u][v][e] * s2);
+            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b[u] * a.sy.b + h[u] * a.sy.h + l[u] * a.sy.t, a.D, lane, x[u]);
+        }
     }
     if (!a.part) return;
     // the workgroup's sums: over the rows of a wave by shuffles, then over the
@@ -257,23 +275,27 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
     }
 }
 
-// dw and db from the workgroups' sums: 64 columns per workgroup, four waves
-// take every fourth workgroup's sum each.
-__global__ __launch_bounds__(kLnThreads) void ln_bwd_sum_kernel(LnArgs a) {
-    __shared__ float red[4][64];
-    const int cols = 2 * a.D;
-    const unsigned per = (unsigned)(cols + 63) / 64;
+// dw and db from the workgroups' sums: 32 columns per workgroup; each of 32
+// threads per column adds every 32nd workgroup's sum, then the 32 are added.
+__global__ __launch_bounds__(1024) void ln_bwd_sum_kernel(LnArgs a) {
+    __shared__ float red[32][33];
+    const unsigned cols = 2 * (unsigned)a.D, per = (cols + 31) / 32;
     const unsigned g = blockIdx.x / per;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = (int)(blockIdx.x % per) * 64 + lane;
+    const unsigned lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const unsigned c = (blockIdx.x % per) * 32 + lane;
     float s = 0.f;
-    if (c < cols)
-        for (unsigned k = wave; k < a.blocks; k += 4) s += a.part[((size_t)g * a.blocks + k) * cols + c];
-    red[wave][lane] = s;
+    if (c < cols) {
+        const float* p = a.part + (size_t)g * a.blocks * cols + c;
+#pragma unroll 8
+        for (unsigned k = slice; k < a.blocks; k += 32) s += p[(size_t)k * cols];
+    }
+    red[slice][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < cols) {
-        s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-        if (c < a.D) {
+    if (slice == 0 && c < cols) {
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s += red[k][lane];
+        if (c < (unsigned)a.D) {
             if (a.dw) a.dw[(size_t)g * a.D + c] = s;
         } else if (a.db) {
             a.db[(size_t)g * a.D + c - a.D] = s;
@@ -283,6 +305,13 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_sum_kernel(LnArgs a) {
 
 __global__ __launch_bounds__(256) void ln_zero_kernel(float* p, size_t n) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0.f;
+}
+
+int ln_pass_rows(int D, bool bwd) {
+    const LnShape s = ln_shape(D);
+    const int rows = bwd ? (s.vecs == 1 ? ln_rows_bwd<1>() : ln_rows_bwd<2>())
+                         : (s.vecs == 1 ? ln_rows_fwd<1>() : s.vecs == 2 ? ln_rows_fwd<2>() : ln_rows_fwd<4>());
+    return kLnThreads / s.lanes * rows;
 }
 
 template <bool BWD, bool VEC, int LPR, int VPT>
@@ -315,8 +344,8 @@ hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
 hipError_t launch_ln_bwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
     hipError_t e = vec ? ln_launch_shape<true, true>(a, slot, st) : ln_launch_shape<true, false>(a, slot, st);
     if (e == hipSuccess && a.part) {
-        const unsigned per = (unsigned)(2 * a.D + 63) / 64;
-        e = launch_k(slot, ln_bwd_sum_kernel, dim3(a.groups * per), dim3(kLnThreads), 0, st, a);
+        const unsigned per = (unsigned)(2 * a.D + 31) / 32;
+        e = launch_k(slot, ln_bwd_sum_kernel, dim3(a.groups * per), dim3(1024), 0, st, a);
     }
     return e;
 }

@@ -528,14 +528,17 @@ dr_status check_ln_desc(const dr_layernorm_desc* d) {
     return DR_OK;
 }
 
-// Groups of rows with one weight, and the workgroups of each: about four per
-// compute unit in all, each with four passes over its rows at least.
-void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a) {
+// Groups of rows with one weight, and the workgroups of each.  Forward: up to
+// eight workgroups per compute unit in all.  Backward: every workgroup writes two
+// rows of sums, so four, or two where a row is wide (of 8191 x 2048 bf16: 1024
+// workgroups 112 us with a slower joining, 512 measured below).
+void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
     a.groups = d.per_head ? d.H : 1;
     a.rows = d.per_head ? (unsigned)d.B * d.L : (unsigned)d.B * d.H * d.L;
-    const unsigned rpb = 256u / dr::ln_shape(d.D).lanes;
-    const unsigned passes = (a.rows + rpb - 1) / rpb;
-    const unsigned want = std::max(1u, (1024 + a.groups - 1) / a.groups);
+    const unsigned pass = (unsigned)dr::ln_pass_rows(d.D, bwd);
+    const unsigned passes = (a.rows + pass - 1) / pass;
+    const unsigned most = !bwd ? 2048 : d.D <= 512 ? 1024 : 512;
+    const unsigned want = std::max(1u, (most + a.groups - 1) / a.groups);
     a.blocks = std::max(1u, std::min(want, passes));
 }
 
@@ -549,7 +552,7 @@ dr::LnRows ln_rows(const dr_layernorm_desc& d, const dr_strides& s) {
 
 size_t ln_part_bytes(const dr_layernorm_desc& d) {
     dr::LnArgs a{};
-    ln_groups(d, a);
+    ln_groups(d, a, true);
     return (size_t)a.groups * a.blocks * 2 * d.D * sizeof(float);
 }
 
@@ -591,7 +594,7 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     a.eps = d->eps;
     a.x_f32 = d->x_dtype == DR_F32;
     a.y_f32 = d->y_dtype == DR_F32;
-    ln_groups(*d, a);
+    ln_groups(*d, a, false);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->y);
     return hip_status(dr::launch_ln_fwd(a, vec, dr::kProfLnFwd, (hipStream_t)stream), "layer norm launch");
 }
@@ -653,7 +656,7 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     a.x_f32 = d->x_dtype == DR_F32;
     a.y_f32 = d->y_dtype == DR_F32;
     a.dy_f32 = d->dy_dtype == DR_F32;
-    ln_groups(*d, a);
+    ln_groups(*d, a, true);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->dy) && ln_vec(*d, d->y);
     return hip_status(dr::launch_ln_bwd(a, vec, slot, st), "layer norm backward launch");
 }
