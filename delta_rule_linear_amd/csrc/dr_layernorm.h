@@ -34,6 +34,7 @@ struct LnArgs {
     unsigned blocks;         // workgroups per group
     float eps;
     int x_f32, y_f32, dy_f32;
+    int near_ok;         // 128 rows' distance in tokens fits 32 bits
 };
 
 // Lanes per row and 8-value vectors per lane for rows of D values.

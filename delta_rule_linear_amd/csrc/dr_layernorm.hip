@@ -26,14 +26,15 @@ typedef float lnf8 __attribute__((ext_vector_type(8)));
 constexpr int kLnThreads = 256;
 
 LnShape ln_shape(int D) {
-    // the least lanes that hold a row in 8 values each, up to a wave; then
-    // more values per lane; wider rows take the whole workgroup
+    // the least lanes that hold a row in 8 values each, up to the workgroup; then
+    // more values per lane (a wave with 32 values per lane holds 2048 as well,
+    // but the backward's 200 registers leave one wave per SIMD)
     if (D <= 64) return {8, 1};
     if (D <= 128) return {16, 1};
     if (D <= 256) return {32, 1};
     if (D <= 512) return {64, 1};
-    if (D <= 1024) return {64, 2};
-    if (D <= 2048) return {64, 4};
+    if (D <= 1024) return {128, 1};
+    if (D <= 2048) return {256, 1};
     if (D <= 4096) return {256, 2};
     if (D <= 8192) return {256, 4};
     return {256, 8};
@@ -46,15 +47,22 @@ __device__ __forceinline__ int ln_col(int lane, int v, int e) {
     return VEC ? 8 * (v * LPR + lane) + e : (8 * v + e) * LPR + lane;
 }
 
-template <bool VEC, int LPR, int VPT>
-__device__ __forceinline__ void ln_load(const void* base, bool f32, int64_t at, int D, int lane, float (&x)[VPT][8]) {
+// A row's values, at element offset `at` from base (32 bits where base is the
+// first row of a pass, so that the address is a scalar and one register).
+template <bool VEC, int LPR, int VPT, typename Off>
+__device__ __forceinline__ void ln_load(const char* base, bool f32, Off at, int D, int lane, float (&x)[VPT][8]) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if constexpr (VEC) {
             const int c = ln_col<VEC, LPR>(lane, v, 0);
             if (c < D) {
-                if (f32) load_n<true, 8>(base, (size_t)(at + c), x[v]);
-                else load_n<false, 8>(base, (size_t)(at + c), x[v]);
+                if (f32) {
+                    const lnf8 f = *reinterpret_cast<const lnf8*>(base + (Off)((at + c) * 4));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[v][e] = f[e];
+                } else {
+                    unpack_bf16x8(*reinterpret_cast<const uint4*>(base + (Off)((at + c) * 2)), x[v]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[v][e] = 0.f;
@@ -64,14 +72,16 @@ __device__ __forceinline__ void ln_load(const void* base, bool f32, int64_t at, 
             for (int e = 0; e < 8; ++e) {
                 const int c = ln_col<VEC, LPR>(lane, v, e);
                 x[v][e] = 0.f;
-                if (c < D) x[v][e] = f32 ? load1<true>(base, (size_t)(at + c)) : load1<false>(base, (size_t)(at + c));
+                if (c >= D) continue;
+                if (f32) x[v][e] = *reinterpret_cast<const float*>(base + (Off)((at + c) * 4));
+                else x[v][e] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(base + (Off)((at + c) * 2)));
             }
         }
     }
 }
 
-template <bool VEC, int LPR, int VPT>
-__device__ __forceinline__ void ln_store(void* base, bool f32, int64_t at, int D, int lane, const float (&x)[VPT][8]) {
+template <bool VEC, int LPR, int VPT, typename Off>
+__device__ __forceinline__ void ln_store(char* base, bool f32, Off at, int D, int lane, const float (&x)[VPT][8]) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if constexpr (VEC) {
@@ -80,35 +90,70 @@ __device__ __forceinline__ void ln_store(void* base, bool f32, int64_t at, int D
             lnf8 f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = x[v][e];
-            if (f32) *reinterpret_cast<lnf8*>((float*)base + at + c) = f;
-            else *reinterpret_cast<lnbf8*>((__bf16*)base + at + c) = __builtin_convertvector(f, lnbf8);
+            if (f32) *reinterpret_cast<lnf8*>(base + (Off)((at + c) * 4)) = f;
+            else *reinterpret_cast<lnbf8*>(base + (Off)((at + c) * 2)) = __builtin_convertvector(f, lnbf8);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = ln_col<VEC, LPR>(lane, v, e);
                 if (c >= D) continue;
-                if (f32) ((float*)base)[at + c] = x[v][e];
-                else ((__bf16*)base)[at + c] = (__bf16)x[v][e];
+                if (f32) *reinterpret_cast<float*>(base + (Off)((at + c) * 4)) = x[v][e];
+                else *reinterpret_cast<__bf16*>(base + (Off)((at + c) * 2)) = (__bf16)x[v][e];
             }
         }
     }
 }
 
-// Sum over the lanes of a row, in every one of them.  red: one float per wave.
+// Sums of two values over the lanes of a row, in every one of them.  Rows of
+// several waves add their waves' sums through LDS; `turn` alternates between two
+// places, so that one barrier a time is enough.
 template <int LPR>
-__device__ __forceinline__ float ln_sum(float x, float* red) {
-#pragma unroll
-    for (int d = 1; d < (LPR < 64 ? LPR : 64); d <<= 1) x += __shfl_xor(x, d);
-    if constexpr (LPR > 64) {
-        __syncthreads();   // the last sum has been read
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-        __syncthreads();
-        x = (red[0] + red[1]) + (red[2] + red[3]);
+__device__ __forceinline__ void ln_sum2(float& x, float& y, float2* red, int& turn) {
+    x = group_sum<(LPR < 32 ? LPR : 32)>(x);
+    y = group_sum<(LPR < 32 ? LPR : 32)>(y);
+    if constexpr (LPR >= 64) {
+        x += __shfl_xor(x, 32);
+        y += __shfl_xor(y, 32);
     }
+    if constexpr (LPR > 64) {
+        const int wave = threadIdx.x >> 6;
+        float2* at = red + 4 * turn;
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0) at[wave] = make_float2(x, y);
+        __syncthreads();
+        if constexpr (LPR == 128) {
+            const float2 p = at[wave & ~1], q = at[wave | 1];
+            x = p.x + q.x;
+            y = p.y + q.y;
+        } else {
+            x = (at[0].x + at[1].x) + (at[2].x + at[3].x);
+            y = (at[0].y + at[1].y) + (at[2].y + at[3].y);
+        }
+    }
+}
+template <int LPR>
+__device__ __forceinline__ float ln_sum(float x, float2* red, int& turn) {
+    float y = 0.f;
+    ln_sum2<LPR>(x, y, red, turn);
     return x;
 }
 
-// Row r of a group: its index among the statistics and its strided offset.
+// s / D to the nearest (one correction of s times the rounded 1 / D), so that a
+// row of one value has that value as its mean.
+__device__ __forceinline__ float ln_div(float s, float D, float inv) {
+    const float q = s * inv;
+    const float c = __builtin_fmaf(__builtin_fmaf(-q, D, s), inv, q);
+    return __builtin_isfinite(q) ? c : q;
+}
+// 1 / sqrt(v): the hardware's estimate and one Newton step; zero, infinity, NaN
+// and values whose products would be subnormal take the plain form.
+__device__ __forceinline__ float ln_rsqrt(float v) {
+    if (!(v > 1e-30f && v < 1e30f)) return 1.f / sqrtf(v);
+    const float y = __builtin_amdgcn_rsqf(v);
+    return y * __builtin_fmaf(-0.5f * v * y, y, 1.5f);
+}
+
+// Row r of a group.
 __device__ __forceinline__ void ln_row(const LnArgs& a, unsigned g, unsigned r, unsigned& b, unsigned& h, unsigned& l) {
     const unsigned q = r / (unsigned)a.L;
     l = r - q * (unsigned)a.L;
@@ -120,18 +165,108 @@ __device__ __forceinline__ void ln_row(const LnArgs& a, unsigned g, unsigned r, 
         h = q - b * (unsigned)a.H;
     }
 }
+__device__ __forceinline__ int64_t ln_at(const LnRows& s, unsigned b, unsigned h, unsigned l) {
+    return b * s.b + h * s.h + l * s.t;
+}
 
 // Rows that a lane group has in flight: short rows leave room for several.
 template <int VPT>
-constexpr int ln_rows_fwd() { return VPT == 1 ? 4 : VPT == 2 ? 2 : 1; }
+constexpr int ln_rows_fwd() { return VPT == 1 ? 2 : 1; }
 template <int VPT>
 constexpr int ln_rows_bwd() { return VPT == 1 ? 2 : 1; }
 
+// A pass over the rows from r0 that a workgroup holds at a time.  NEAR: they are
+// tokens of one (b, h), all of them there, so that a scalar base and a lane's own
+// 32-bit offset address them (the divisions by L and the 64-bit products per row
+// cost as much as the norm itself); else each row is located on its own.
+template <bool NEAR>
+struct LnOff {
+    typedef unsigned type;
+};
+template <>
+struct LnOff<false> {
+    typedef int64_t type;
+};
+
+template <bool VEC, int LPR, int VPT, bool NEAR>
+__device__ __forceinline__ void ln_fwd_pass(const LnArgs& a, unsigned g, unsigned r0, int lane, int sub, float2* red, int& turn,
+                                            const float (&w)[VPT][8], const float (&bs)[VPT][8]) {
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_fwd<VPT>();
+    typedef typename LnOff<NEAR>::type Off;
+    const int xs = a.x_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2;
+    const float D = (float)a.D, inv = 1.f / D;
+    const char* xb = (const char*)a.x;
+    char* yb = (char*)a.y;
+    size_t stat0 = 0;
+    unsigned b, h, l;
+    if constexpr (NEAR) {
+        ln_row(a, g, r0, b, h, l);
+        xb += ln_at(a.sx, b, h, l) * xs;
+        yb += ln_at(a.sy, b, h, l) * ys;
+        stat0 = ((size_t)b * a.H + h) * a.L + l;
+    }
+    float x[RU][VPT][8];
+    Off yat[RU];
+    size_t stat[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        const unsigned r = u * RPB + sub;
+        Off xat;
+        if constexpr (NEAR) {
+            xat = r * (unsigned)a.sx.t;
+            yat[u] = r * (unsigned)a.sy.t;
+            stat[u] = r;
+        } else {
+            ln_row(a, g, min(r0 + r, a.rows - 1), b, h, l);
+            xat = ln_at(a.sx, b, h, l);
+            yat[u] = ln_at(a.sy, b, h, l);
+            stat[u] = ((size_t)b * a.H + h) * a.L + l;
+        }
+        ln_load<VEC, LPR, VPT>(xb, a.x_f32, xat, a.D, lane, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += x[u][v][e];
+        const float mean = ln_div(ln_sum<LPR>(s, red, turn), D, inv);
+        s = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[u][v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[u][v][e] - mean : 0.f;
+                s += x[u][v][e] * x[u][v][e];
+            }
+        const float rstd = ln_rsqrt(ln_div(ln_sum<LPR>(s, red, turn), D, inv) + a.eps);
+        if (!NEAR && r0 + u * RPB + sub >= a.rows) continue;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[u][v][e] = x[u][v][e] * rstd * w[v][e] + bs[v][e];
+        ln_store<VEC, LPR, VPT>(yb, a.y_f32, yat[u], a.D, lane, x[u]);
+        if (lane == 0) {
+            if (a.mean_out) a.mean_out[stat0 + stat[u]] = mean;
+            if (a.rstd_out) a.rstd_out[stat0 + stat[u]] = rstd;
+        }
+    }
+}
+
+// Whether the rows r0 .. r0 + n - 1 of a group are tokens of one (b, h).
+__device__ __forceinline__ bool ln_near(const LnArgs& a, unsigned r0, unsigned n) {
+    return a.near_ok && r0 + n <= a.rows && r0 % (unsigned)a.L + n <= (unsigned)a.L;
+}
+
 template <bool VEC, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
-    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_fwd<VPT>();   // rows at a time, and in flight of each
-    __shared__ float red[4];
-    const unsigned g = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
+    constexpr unsigned ROWS = kLnThreads / LPR * ln_rows_fwd<VPT>();
+    __shared__ float2 red[8];
+    int turn = 0;
+    // groups side by side: rows of the same tokens are near each other in a
+    // token-major tensor
+    const unsigned g = blockIdx.x % a.groups, blk = blockIdx.x / a.groups;
     const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     float w[VPT][8], bs[VPT][8];
 #pragma unroll
@@ -142,55 +277,93 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             bs[v][e] = c < a.D && a.bias ? a.bias[(size_t)g * a.D + c] : 0.f;
         }
-    const float rD = (float)a.D;
-    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += a.blocks * (RPB * RU)) {
-        float x[RU][VPT][8];
-        unsigned b[RU], h[RU], l[RU];
+    for (unsigned r0 = blk * ROWS; r0 < a.rows; r0 += a.blocks * ROWS) {
+        if (ln_near(a, r0, ROWS)) ln_fwd_pass<VEC, LPR, VPT, true>(a, g, r0, lane, sub, red, turn, w, bs);
+        else ln_fwd_pass<VEC, LPR, VPT, false>(a, g, r0, lane, sub, red, turn, w, bs);
+    }
+}
+
+template <bool VEC, int LPR, int VPT, bool NEAR>
+__device__ __forceinline__ void ln_bwd_pass(const LnArgs& a, unsigned g, unsigned r0, int lane, int sub, float2* red, int& turn,
+                                            const float (&w)[VPT][8], float (&dw)[VPT][8], float (&db)[VPT][8]) {
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_bwd<VPT>();
+    typedef typename LnOff<NEAR>::type Off;
+    const int xs = a.x_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2, dys = a.dy_f32 ? 4 : 2;
+    const float D = (float)a.D, inv = 1.f / D;
+    const char *xb = (const char*)a.x, *dyb = (const char*)a.dy;
+    char* yb = (char*)a.y;
+    const float *mb = a.mean, *rb = a.rstd;
+    unsigned b, h, l;
+    if constexpr (NEAR) {
+        ln_row(a, g, r0, b, h, l);
+        xb += ln_at(a.sx, b, h, l) * xs;
+        dyb += ln_at(a.sdy, b, h, l) * dys;
+        yb += ln_at(a.sy, b, h, l) * ys;
+        const size_t stat0 = ((size_t)b * a.H + h) * a.L + l;
+        mb += stat0;
+        rb += stat0;
+    }
+    float x[RU][VPT][8], dy[RU][VPT][8], mean[RU], rstd[RU];
+    Off yat[RU];
 #pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            const unsigned r = r0 + u * RPB + sub;
-            ln_row(a, g, r < a.rows ? r : a.rows - 1, b[u], h[u], l[u]);
-            ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b[u] * a.sx.b + h[u] * a.sx.h + l[u] * a.sx.t, a.D, lane, x[u]);
+    for (int u = 0; u < RU; ++u) {
+        const unsigned r = u * RPB + sub;
+        Off xat, dyat;
+        size_t stat = r;
+        if constexpr (NEAR) {
+            xat = r * (unsigned)a.sx.t;
+            dyat = r * (unsigned)a.sdy.t;
+            yat[u] = r * (unsigned)a.sy.t;
+        } else {
+            ln_row(a, g, min(r0 + r, a.rows - 1), b, h, l);
+            xat = ln_at(a.sx, b, h, l);
+            dyat = ln_at(a.sdy, b, h, l);
+            yat[u] = ln_at(a.sy, b, h, l);
+            stat = ((size_t)b * a.H + h) * a.L + l;
         }
+        mean[u] = mb[stat];
+        rstd[u] = rb[stat];
+        ln_load<VEC, LPR, VPT>(xb, a.x_f32, xat, a.D, lane, x[u]);
+        ln_load<VEC, LPR, VPT>(dyb, a.dy_f32, dyat, a.D, lane, dy[u]);
+    }
 #pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            float s = 0.f;
+    for (int u = 0; u < RU; ++u) {
+        const bool ok = NEAR || r0 + u * RPB + sub < a.rows;
+        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
+        for (int v = 0; v < VPT; ++v)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += x[u][v][e];
-            const float mean = ln_sum<LPR>(s, red) / rD;
-            s = 0.f;
-#pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[u][v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[u][v][e] - mean : 0.f;
-                    s += x[u][v][e] * x[u][v][e];
+            for (int e = 0; e < 8; ++e) {
+                x[u][v][e] = (x[u][v][e] - mean[u]) * rstd[u];   // behind D: dy and w are zero there
+                if (ok) {
+                    dw[v][e] += dy[u][v][e] * x[u][v][e];
+                    db[v][e] += dy[u][v][e];
                 }
-            const float rstd = 1.f / sqrtf(ln_sum<LPR>(s, red) / rD + a.eps);
-            if (r0 + u * RPB + sub >= a.rows) continue;
-#pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[u][v][e] = x[u][v][e] * rstd * w[v][e] + bs[v][e];
-            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b[u] * a.sy.b + h[u] * a.sy.h + l[u] * a.sy.t, a.D, lane, x[u]);
-            if (lane == 0) {
-                const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
-                if (a.mean_out) a.mean_out[at] = mean;
-                if (a.rstd_out) a.rstd_out[at] = rstd;
+                dy[u][v][e] *= w[v][e];
+                s1 += dy[u][v][e];
+                s2 += dy[u][v][e] * x[u][v][e];
             }
-        }
+        ln_sum2<LPR>(s1, s2, red, turn);
+        s1 = ln_div(s1, D, inv);
+        s2 = ln_div(s2, D, inv);
+        if (!ok) continue;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[u][v][e] = rstd[u] * (dy[u][v][e] - s1 - x[u][v][e] * s2);
+        ln_store<VEC, LPR, VPT>(yb, a.y_f32, yat[u], a.D, lane, x[u]);
     }
 }
 
 template <bool VEC, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
-    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_bwd<VPT>();
+    constexpr unsigned ROWS = kLnThreads / LPR * ln_rows_bwd<VPT>();
     constexpr int NCOL = 8 * VPT * LPR;   // columns that the lanes of a row hold
-    __shared__ float red[4];
-    __shared__ float acc[LPR <= 64 ? 4 : 1][LPR <= 64 ? NCOL : 1];
-    const unsigned g = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
+    constexpr int PARTS = LPR <= 64 ? 4 : LPR == 128 ? 2 : 1;
+    __shared__ float2 red[8];
+    __shared__ float acc[PARTS][PARTS > 1 ? NCOL : 1];
+    int turn = 0;
+    const unsigned g = blockIdx.x % a.groups, blk = blockIdx.x / a.groups;
     const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     float w[VPT][8], dw[VPT][8], db[VPT][8];
 #pragma unroll
@@ -201,46 +374,9 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             dw[v][e] = db[v][e] = 0.f;
         }
-    const float rD = (float)a.D;
-    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += a.blocks * (RPB * RU)) {
-        float x[RU][VPT][8], dy[RU][VPT][8], mean[RU], rstd[RU];
-        unsigned b[RU], h[RU], l[RU];
-#pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            const unsigned r = r0 + u * RPB + sub;
-            ln_row(a, g, r < a.rows ? r : a.rows - 1, b[u], h[u], l[u]);
-            const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
-            mean[u] = a.mean[at];
-            rstd[u] = a.rstd[at];
-            ln_load<VEC, LPR, VPT>(a.x, a.x_f32, b[u] * a.sx.b + h[u] * a.sx.h + l[u] * a.sx.t, a.D, lane, x[u]);
-            ln_load<VEC, LPR, VPT>(a.dy, a.dy_f32, b[u] * a.sdy.b + h[u] * a.sdy.h + l[u] * a.sdy.t, a.D, lane, dy[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            const bool ok = r0 + u * RPB + sub < a.rows;
-            float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[u][v][e] = (x[u][v][e] - mean[u]) * rstd[u];   // behind D: dy and w are zero there
-                    if (ok) {
-                        dw[v][e] += dy[u][v][e] * x[u][v][e];
-                        db[v][e] += dy[u][v][e];
-                    }
-                    dy[u][v][e] *= w[v][e];
-                    s1 += dy[u][v][e];
-                    s2 += dy[u][v][e] * x[u][v][e];
-                }
-            s1 = ln_sum<LPR>(s1, red) / rD;
-            s2 = ln_sum<LPR>(s2, red) / rD;
-            if (!ok) continue;
-#pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[u][v][e] = rstd[u] * (dy[u][v][e] - s1 - x[u][v][e] * s2);
-            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, b[u] * a.sy.b + h[u] * a.sy.h + l[u] * a.sy.t, a.D, lane, x[u]);
-        }
+    for (unsigned r0 = blk * ROWS; r0 < a.rows; r0 += a.blocks * ROWS) {
+        if (ln_near(a, r0, ROWS)) ln_bwd_pass<VEC, LPR, VPT, true>(a, g, r0, lane, sub, red, turn, w, dw, db);
+        else ln_bwd_pass<VEC, LPR, VPT, false>(a, g, r0, lane, sub, red, turn, w, dw, db);
     }
     if (!a.part) return;
     // the workgroup's sums: over the rows of a wave by shuffles, then over the
@@ -249,7 +385,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         float(&s)[VPT][8] = k == 0 ? dw : db;
-        if constexpr (LPR > 64) {
+        if constexpr (PARTS == 1) {
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -258,18 +394,21 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
                     if (c < a.D) part[(size_t)k * a.D + c] = s[v][e];
                 }
         } else {
-            const int wave = threadIdx.x >> 6;
+            const int at = threadIdx.x / (kLnThreads / PARTS);
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
 #pragma unroll
                     for (int d = LPR; d < 64; d <<= 1) s[v][e] += __shfl_xor(s[v][e], d);
-                    if ((threadIdx.x & 63) < LPR) acc[wave][ln_col<VEC, LPR>(lane, v, e)] = s[v][e];
+                    if (LPR >= 64 || (threadIdx.x & 63) < LPR) acc[at][ln_col<VEC, LPR>(lane, v, e)] = s[v][e];
                 }
             __syncthreads();
-            for (int c = threadIdx.x; c < a.D; c += kLnThreads)
-                part[(size_t)k * a.D + c] = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
+            for (int c = threadIdx.x; c < a.D; c += kLnThreads) {
+                float x = acc[0][c] + acc[1][c];
+                if constexpr (PARTS == 4) x += acc[2][c] + acc[3][c];
+                part[(size_t)k * a.D + c] = x;
+            }
             __syncthreads();
         }
     }
@@ -310,7 +449,7 @@ __global__ __launch_bounds__(256) void ln_zero_kernel(float* p, size_t n) {
 int ln_pass_rows(int D, bool bwd) {
     const LnShape s = ln_shape(D);
     const int rows = bwd ? (s.vecs == 1 ? ln_rows_bwd<1>() : ln_rows_bwd<2>())
-                         : (s.vecs == 1 ? ln_rows_fwd<1>() : s.vecs == 2 ? ln_rows_fwd<2>() : ln_rows_fwd<4>());
+                         : (s.vecs == 1 ? ln_rows_fwd<1>() : ln_rows_fwd<2>());
     return kLnThreads / s.lanes * rows;
 }
 
@@ -327,11 +466,9 @@ static hipError_t ln_launch_shape(const LnArgs& a, int slot, hipStream_t st) {
     if (s.lanes == 8) return ln_launch<BWD, VEC, 8, 1>(a, slot, st);
     if (s.lanes == 16) return ln_launch<BWD, VEC, 16, 1>(a, slot, st);
     if (s.lanes == 32) return ln_launch<BWD, VEC, 32, 1>(a, slot, st);
-    if (s.lanes == 64) {
-        if (s.vecs == 1) return ln_launch<BWD, VEC, 64, 1>(a, slot, st);
-        if (s.vecs == 2) return ln_launch<BWD, VEC, 64, 2>(a, slot, st);
-        return ln_launch<BWD, VEC, 64, 4>(a, slot, st);
-    }
+    if (s.lanes == 64) return ln_launch<BWD, VEC, 64, 1>(a, slot, st);
+    if (s.lanes == 128) return ln_launch<BWD, VEC, 128, 1>(a, slot, st);
+    if (s.vecs == 1) return ln_launch<BWD, VEC, 256, 1>(a, slot, st);
     if (s.vecs == 2) return ln_launch<BWD, VEC, 256, 2>(a, slot, st);
     if (s.vecs == 4) return ln_launch<BWD, VEC, 256, 4>(a, slot, st);
     return ln_launch<BWD, VEC, 256, 8>(a, slot, st);

@@ -546,6 +546,10 @@ bool ln_vec(const dr_layernorm_desc& d, const dr_strides& s) {
     return (d.B <= 1 || s.b % 8 == 0) && (d.H <= 1 || s.h % 8 == 0) && (d.L <= 1 || s.t % 8 == 0);
 }
 
+// 128 rows (the most of a pass) and a row's width, in bytes of 4-byte values,
+// within 32 bits: tokens up to 2^21 elements apart.
+bool ln_near(const dr_strides& s) { return s.t <= ((int64_t)1 << 21); }
+
 dr::LnRows ln_rows(const dr_layernorm_desc& d, const dr_strides& s) {
     return {d.B > 1 ? s.b : 0, d.H > 1 ? s.h : 0, d.L > 1 ? s.t : 0};
 }
@@ -596,6 +600,7 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     a.y_f32 = d->y_dtype == DR_F32;
     ln_groups(*d, a, false);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->y);
+    a.near_ok = ln_near(d->x) && ln_near(d->y);
     return hip_status(dr::launch_ln_fwd(a, vec, dr::kProfLnFwd, (hipStream_t)stream), "layer norm launch");
 }
 
@@ -658,6 +663,7 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     a.dy_f32 = d->dy_dtype == DR_F32;
     ln_groups(*d, a, true);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->dy) && ln_vec(*d, d->y);
+    a.near_ok = ln_near(d->x) && ln_near(d->dy) && ln_near(d->y);
     return hip_status(dr::launch_ln_bwd(a, vec, slot, st), "layer norm backward launch");
 }
 
