@@ -34,7 +34,6 @@ struct LnArgs {
     unsigned blocks;         // workgroups per group
     float eps;
     int x_f32, y_f32, dy_f32;
-    int near_ok;         // 128 rows' distance in tokens fits 32 bits
 };
 
 // Lanes per row and 8-value vectors per lane for rows of D values.
@@ -43,7 +42,7 @@ struct LnShape {
 };
 LnShape ln_shape(int D);
 // Rows that a workgroup takes in one pass.
-int ln_pass_rows(int D, bool bwd);
+int ln_pass_rows(int D);
 // vec: rows are read and written in 16-byte pieces (D and every stride a
 // multiple of 8 elements)
 hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st);

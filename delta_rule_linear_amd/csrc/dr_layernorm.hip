@@ -47,41 +47,57 @@ __device__ __forceinline__ int ln_col(int lane, int v, int e) {
     return VEC ? 8 * (v * LPR + lane) + e : (8 * v + e) * LPR + lane;
 }
 
-// A row's values, at element offset `at` from base (32 bits where base is the
-// first row of a pass, so that the address is a scalar and one register).
-template <bool VEC, int LPR, int VPT, typename Off>
-__device__ __forceinline__ void ln_load(const char* base, bool f32, Off at, int D, int lane, float (&x)[VPT][8]) {
+// A lane's part of a row as loaded: bf16 or fp32 bits (VEC), or fp32 values.
+template <bool VEC, bool F32, int VPT>
+struct LnRaw {
+    uint4 v[VPT][F32 || !VEC ? 2 : 1];
+};
+
+template <bool VEC, bool F32, int LPR, int VPT>
+__device__ __forceinline__ void ln_fetch(const void* base, int64_t at, int D, int lane, LnRaw<VEC, F32, VPT>& r) {
+    constexpr int W = F32 || !VEC ? 2 : 1;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if constexpr (VEC) {
             const int c = ln_col<VEC, LPR>(lane, v, 0);
-            if (c < D) {
-                if (f32) {
-                    const lnf8 f = *reinterpret_cast<const lnf8*>(base + (Off)((at + c) * 4));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[v][e] = f[e];
-                } else {
-                    unpack_bf16x8(*reinterpret_cast<const uint4*>(base + (Off)((at + c) * 2)), x[v]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[v][e] = 0.f;
+            for (int i = 0; i < W; ++i) {
+                r.v[v][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < D) r.v[v][i] = reinterpret_cast<const uint4*>((const char*)base + (at + c) * (F32 ? 4 : 2))[i];
             }
         } else {
+            float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = ln_col<VEC, LPR>(lane, v, e);
-                x[v][e] = 0.f;
-                if (c >= D) continue;
-                if (f32) x[v][e] = *reinterpret_cast<const float*>(base + (Off)((at + c) * 4));
-                else x[v][e] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(base + (Off)((at + c) * 2)));
+                x[e] = 0.f;
+                if (c < D) x[e] = load1<F32>(base, (size_t)(at + c));
+            }
+            r.v[v][0] = __builtin_bit_cast(uint4, f32x4{x[0], x[1], x[2], x[3]});
+            r.v[v][1] = __builtin_bit_cast(uint4, f32x4{x[4], x[5], x[6], x[7]});
+        }
+    }
+}
+template <bool VEC, bool F32, int VPT>
+__device__ __forceinline__ void ln_values(const LnRaw<VEC, F32, VPT>& r, float (&x)[VPT][8]) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        if constexpr (VEC && !F32) {
+            unpack_bf16x8(r.v[v][0], x[v]);
+        } else {
+            const f32x4 a = __builtin_bit_cast(f32x4, r.v[v][0]), b = __builtin_bit_cast(f32x4, r.v[v][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[v][e] = a[e];
+                x[v][4 + e] = b[e];
             }
         }
     }
 }
 
-template <bool VEC, int LPR, int VPT, typename Off>
-__device__ __forceinline__ void ln_store(char* base, bool f32, Off at, int D, int lane, const float (&x)[VPT][8]) {
+template <bool VEC, int LPR, int VPT>
+__device__ __forceinline__ void ln_store(void* to, bool f32, int64_t at, int D, int lane, const float (&x)[VPT][8]) {
+    char* base = (char*)to;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if constexpr (VEC) {
@@ -90,15 +106,15 @@ __device__ __forceinline__ void ln_store(char* base, bool f32, Off at, int D, in
             lnf8 f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = x[v][e];
-            if (f32) *reinterpret_cast<lnf8*>(base + (Off)((at + c) * 4)) = f;
-            else *reinterpret_cast<lnbf8*>(base + (Off)((at + c) * 2)) = __builtin_convertvector(f, lnbf8);
+            if (f32) *reinterpret_cast<lnf8*>(base + (at + c) * 4) = f;
+            else *reinterpret_cast<lnbf8*>(base + (at + c) * 2) = __builtin_convertvector(f, lnbf8);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = ln_col<VEC, LPR>(lane, v, e);
                 if (c >= D) continue;
-                if (f32) *reinterpret_cast<float*>(base + (Off)((at + c) * 4)) = x[v][e];
-                else *reinterpret_cast<__bf16*>(base + (Off)((at + c) * 2)) = (__bf16)x[v][e];
+                if (f32) *reinterpret_cast<float*>(base + (at + c) * 4) = x[v][e];
+                else *reinterpret_cast<__bf16*>(base + (at + c) * 2) = (__bf16)x[v][e];
             }
         }
     }
@@ -169,99 +185,14 @@ __device__ __forceinline__ int64_t ln_at(const LnRows& s, unsigned b, unsigned h
     return b * s.b + h * s.h + l * s.t;
 }
 
-// Rows that a lane group has in flight: short rows leave room for several.
+// Rows of a lane group's pass.  The next pass's rows are loaded while one is
+// computed, so that memory is never waited for by every workgroup at once.
 template <int VPT>
-constexpr int ln_rows_fwd() { return VPT == 1 ? 2 : 1; }
-template <int VPT>
-constexpr int ln_rows_bwd() { return VPT == 1 ? 2 : 1; }
+constexpr int ln_rows() { return VPT == 1 ? 2 : 1; }
 
-// A pass over the rows from r0 that a workgroup holds at a time.  NEAR: they are
-// tokens of one (b, h), all of them there, so that a scalar base and a lane's own
-// 32-bit offset address them (the divisions by L and the 64-bit products per row
-// cost as much as the norm itself); else each row is located on its own.
-template <bool NEAR>
-struct LnOff {
-    typedef unsigned type;
-};
-template <>
-struct LnOff<false> {
-    typedef int64_t type;
-};
-
-template <bool VEC, int LPR, int VPT, bool NEAR>
-__device__ __forceinline__ void ln_fwd_pass(const LnArgs& a, unsigned g, unsigned r0, int lane, int sub, float2* red, int& turn,
-                                            const float (&w)[VPT][8], const float (&bs)[VPT][8]) {
-    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_fwd<VPT>();
-    typedef typename LnOff<NEAR>::type Off;
-    const int xs = a.x_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2;
-    const float D = (float)a.D, inv = 1.f / D;
-    const char* xb = (const char*)a.x;
-    char* yb = (char*)a.y;
-    size_t stat0 = 0;
-    unsigned b, h, l;
-    if constexpr (NEAR) {
-        ln_row(a, g, r0, b, h, l);
-        xb += ln_at(a.sx, b, h, l) * xs;
-        yb += ln_at(a.sy, b, h, l) * ys;
-        stat0 = ((size_t)b * a.H + h) * a.L + l;
-    }
-    float x[RU][VPT][8];
-    Off yat[RU];
-    size_t stat[RU];
-#pragma unroll
-    for (int u = 0; u < RU; ++u) {
-        const unsigned r = u * RPB + sub;
-        Off xat;
-        if constexpr (NEAR) {
-            xat = r * (unsigned)a.sx.t;
-            yat[u] = r * (unsigned)a.sy.t;
-            stat[u] = r;
-        } else {
-            ln_row(a, g, min(r0 + r, a.rows - 1), b, h, l);
-            xat = ln_at(a.sx, b, h, l);
-            yat[u] = ln_at(a.sy, b, h, l);
-            stat[u] = ((size_t)b * a.H + h) * a.L + l;
-        }
-        ln_load<VEC, LPR, VPT>(xb, a.x_f32, xat, a.D, lane, x[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < RU; ++u) {
-        float s = 0.f;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[u][v][e];
-        const float mean = ln_div(ln_sum<LPR>(s, red, turn), D, inv);
-        s = 0.f;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[u][v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[u][v][e] - mean : 0.f;
-                s += x[u][v][e] * x[u][v][e];
-            }
-        const float rstd = ln_rsqrt(ln_div(ln_sum<LPR>(s, red, turn), D, inv) + a.eps);
-        if (!NEAR && r0 + u * RPB + sub >= a.rows) continue;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[u][v][e] = x[u][v][e] * rstd * w[v][e] + bs[v][e];
-        ln_store<VEC, LPR, VPT>(yb, a.y_f32, yat[u], a.D, lane, x[u]);
-        if (lane == 0) {
-            if (a.mean_out) a.mean_out[stat0 + stat[u]] = mean;
-            if (a.rstd_out) a.rstd_out[stat0 + stat[u]] = rstd;
-        }
-    }
-}
-
-// Whether the rows r0 .. r0 + n - 1 of a group are tokens of one (b, h).
-__device__ __forceinline__ bool ln_near(const LnArgs& a, unsigned r0, unsigned n) {
-    return a.near_ok && r0 + n <= a.rows && r0 % (unsigned)a.L + n <= (unsigned)a.L;
-}
-
-template <bool VEC, int LPR, int VPT>
+template <bool VEC, bool FX, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
-    constexpr unsigned ROWS = kLnThreads / LPR * ln_rows_fwd<VPT>();
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows<VPT>();
     __shared__ float2 red[8];
     int turn = 0;
     // groups side by side: rows of the same tokens are near each other in a
@@ -277,87 +208,63 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             bs[v][e] = c < a.D && a.bias ? a.bias[(size_t)g * a.D + c] : 0.f;
         }
-    for (unsigned r0 = blk * ROWS; r0 < a.rows; r0 += a.blocks * ROWS) {
-        if (ln_near(a, r0, ROWS)) ln_fwd_pass<VEC, LPR, VPT, true>(a, g, r0, lane, sub, red, turn, w, bs);
-        else ln_fwd_pass<VEC, LPR, VPT, false>(a, g, r0, lane, sub, red, turn, w, bs);
-    }
-}
-
-template <bool VEC, int LPR, int VPT, bool NEAR>
-__device__ __forceinline__ void ln_bwd_pass(const LnArgs& a, unsigned g, unsigned r0, int lane, int sub, float2* red, int& turn,
-                                            const float (&w)[VPT][8], float (&dw)[VPT][8], float (&db)[VPT][8]) {
-    constexpr int RPB = kLnThreads / LPR, RU = ln_rows_bwd<VPT>();
-    typedef typename LnOff<NEAR>::type Off;
-    const int xs = a.x_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2, dys = a.dy_f32 ? 4 : 2;
     const float D = (float)a.D, inv = 1.f / D;
-    const char *xb = (const char*)a.x, *dyb = (const char*)a.dy;
-    char* yb = (char*)a.y;
-    const float *mb = a.mean, *rb = a.rstd;
-    unsigned b, h, l;
-    if constexpr (NEAR) {
-        ln_row(a, g, r0, b, h, l);
-        xb += ln_at(a.sx, b, h, l) * xs;
-        dyb += ln_at(a.sdy, b, h, l) * dys;
-        yb += ln_at(a.sy, b, h, l) * ys;
-        const size_t stat0 = ((size_t)b * a.H + h) * a.L + l;
-        mb += stat0;
-        rb += stat0;
-    }
-    float x[RU][VPT][8], dy[RU][VPT][8], mean[RU], rstd[RU];
-    Off yat[RU];
+    LnRaw<VEC, FX, VPT> raw[RU], next[RU];
+    unsigned b[RU], h[RU], l[RU], nb[RU], nh[RU], nl[RU];
+    auto fetch = [&](unsigned r0) {
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-        const unsigned r = u * RPB + sub;
-        Off xat, dyat;
-        size_t stat = r;
-        if constexpr (NEAR) {
-            xat = r * (unsigned)a.sx.t;
-            dyat = r * (unsigned)a.sdy.t;
-            yat[u] = r * (unsigned)a.sy.t;
-        } else {
-            ln_row(a, g, min(r0 + r, a.rows - 1), b, h, l);
-            xat = ln_at(a.sx, b, h, l);
-            dyat = ln_at(a.sdy, b, h, l);
-            yat[u] = ln_at(a.sy, b, h, l);
-            stat = ((size_t)b * a.H + h) * a.L + l;
+        for (int u = 0; u < RU; ++u) {
+            ln_row(a, g, min(r0 + u * RPB + sub, a.rows - 1), nb[u], nh[u], nl[u]);
+            ln_fetch<VEC, FX, LPR, VPT>(a.x, ln_at(a.sx, nb[u], nh[u], nl[u]), a.D, lane, next[u]);
         }
-        mean[u] = mb[stat];
-        rstd[u] = rb[stat];
-        ln_load<VEC, LPR, VPT>(xb, a.x_f32, xat, a.D, lane, x[u]);
-        ln_load<VEC, LPR, VPT>(dyb, a.dy_f32, dyat, a.D, lane, dy[u]);
-    }
+    };
+    const unsigned step = a.blocks * (RPB * RU);
+    fetch(blk * (RPB * RU));
+    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += step) {
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-        const bool ok = NEAR || r0 + u * RPB + sub < a.rows;
-        float s1 = 0.f, s2 = 0.f;
+        for (int u = 0; u < RU; ++u) {
+            raw[u] = next[u];
+            b[u] = nb[u];
+            h[u] = nh[u];
+            l[u] = nl[u];
+        }
+        if (r0 + step < a.rows) fetch(r0 + step);
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int u = 0; u < RU; ++u) {
+            float x[VPT][8], s = 0.f;
+            ln_values(raw[u], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[u][v][e] = (x[u][v][e] - mean[u]) * rstd[u];   // behind D: dy and w are zero there
-                if (ok) {
-                    dw[v][e] += dy[u][v][e] * x[u][v][e];
-                    db[v][e] += dy[u][v][e];
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += x[v][e];
+            const float mean = ln_div(ln_sum<LPR>(s, red, turn), D, inv);
+            s = 0.f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[v][e] - mean : 0.f;
+                    s += x[v][e] * x[v][e];
                 }
-                dy[u][v][e] *= w[v][e];
-                s1 += dy[u][v][e];
-                s2 += dy[u][v][e] * x[u][v][e];
+            const float rstd = ln_rsqrt(ln_div(ln_sum<LPR>(s, red, turn), D, inv) + a.eps);
+            if (r0 + u * RPB + sub >= a.rows) continue;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * w[v][e] + bs[v][e];
+            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, ln_at(a.sy, b[u], h[u], l[u]), a.D, lane, x);
+            if (lane == 0) {
+                const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
+                if (a.mean_out) a.mean_out[at] = mean;
+                if (a.rstd_out) a.rstd_out[at] = rstd;
             }
-        ln_sum2<LPR>(s1, s2, red, turn);
-        s1 = ln_div(s1, D, inv);
-        s2 = ln_div(s2, D, inv);
-        if (!ok) continue;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[u][v][e] = rstd[u] * (dy[u][v][e] - s1 - x[u][v][e] * s2);
-        ln_store<VEC, LPR, VPT>(yb, a.y_f32, yat[u], a.D, lane, x[u]);
+        }
     }
 }
 
-template <bool VEC, int LPR, int VPT>
+template <bool VEC, bool FX, bool FDY, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
-    constexpr unsigned ROWS = kLnThreads / LPR * ln_rows_bwd<VPT>();
+    constexpr int RPB = kLnThreads / LPR, RU = ln_rows<VPT>();
     constexpr int NCOL = 8 * VPT * LPR;   // columns that the lanes of a row hold
     constexpr int PARTS = LPR <= 64 ? 4 : LPR == 128 ? 2 : 1;
     __shared__ float2 red[8];
@@ -374,9 +281,65 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             dw[v][e] = db[v][e] = 0.f;
         }
-    for (unsigned r0 = blk * ROWS; r0 < a.rows; r0 += a.blocks * ROWS) {
-        if (ln_near(a, r0, ROWS)) ln_bwd_pass<VEC, LPR, VPT, true>(a, g, r0, lane, sub, red, turn, w, dw, db);
-        else ln_bwd_pass<VEC, LPR, VPT, false>(a, g, r0, lane, sub, red, turn, w, dw, db);
+    const float D = (float)a.D, inv = 1.f / D;
+    LnRaw<VEC, FX, VPT> rx[RU], nx[RU];
+    LnRaw<VEC, FDY, VPT> ry[RU], ny[RU];
+    float mean[RU], rstd[RU], nm[RU], nr[RU];
+    int64_t at[RU], nat[RU];
+    auto fetch = [&](unsigned r0) {
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            unsigned b, h, l;
+            ln_row(a, g, min(r0 + u * RPB + sub, a.rows - 1), b, h, l);
+            const size_t stat = ((size_t)b * a.H + h) * a.L + l;
+            nm[u] = a.mean[stat];
+            nr[u] = a.rstd[stat];
+            nat[u] = ln_at(a.sy, b, h, l);
+            ln_fetch<VEC, FX, LPR, VPT>(a.x, ln_at(a.sx, b, h, l), a.D, lane, nx[u]);
+            ln_fetch<VEC, FDY, LPR, VPT>(a.dy, ln_at(a.sdy, b, h, l), a.D, lane, ny[u]);
+        }
+    };
+    const unsigned step = a.blocks * (RPB * RU);
+    fetch(blk * (RPB * RU));
+    for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += step) {
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            rx[u] = nx[u];
+            ry[u] = ny[u];
+            mean[u] = nm[u];
+            rstd[u] = nr[u];
+            at[u] = nat[u];
+        }
+        if (r0 + step < a.rows) fetch(r0 + step);
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            const bool ok = r0 + u * RPB + sub < a.rows;
+            float x[VPT][8], dy[VPT][8], s1 = 0.f, s2 = 0.f;
+            ln_values(rx[u], x);
+            ln_values(ry[u], dy);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[v][e] = (x[v][e] - mean[u]) * rstd[u];   // behind D: dy and w are zero there
+                    if (ok) {
+                        dw[v][e] += dy[v][e] * x[v][e];
+                        db[v][e] += dy[v][e];
+                    }
+                    dy[v][e] *= w[v][e];
+                    s1 += dy[v][e];
+                    s2 += dy[v][e] * x[v][e];
+                }
+            ln_sum2<LPR>(s1, s2, red, turn);
+            s1 = ln_div(s1, D, inv);
+            s2 = ln_div(s2, D, inv);
+            if (!ok) continue;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[v][e] = rstd[u] * (dy[v][e] - s1 - x[v][e] * s2);
+            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, at[u], a.D, lane, x);
+        }
     }
     if (!a.part) return;
     // the workgroup's sums: over the rows of a wave by shuffles, then over the
@@ -446,40 +409,52 @@ __global__ __launch_bounds__(256) void ln_zero_kernel(float* p, size_t n) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0.f;
 }
 
-int ln_pass_rows(int D, bool bwd) {
+int ln_pass_rows(int D) {
     const LnShape s = ln_shape(D);
-    const int rows = bwd ? (s.vecs == 1 ? ln_rows_bwd<1>() : ln_rows_bwd<2>())
-                         : (s.vecs == 1 ? ln_rows_fwd<1>() : ln_rows_fwd<2>());
-    return kLnThreads / s.lanes * rows;
+    return kLnThreads / s.lanes * (s.vecs == 1 ? ln_rows<1>() : ln_rows<2>());
 }
 
-template <bool BWD, bool VEC, int LPR, int VPT>
+template <bool BWD, bool VEC, bool FX, bool FDY, int LPR, int VPT>
 static hipError_t ln_launch(const LnArgs& a, int slot, hipStream_t st) {
     const dim3 grid(a.groups * a.blocks);
-    if constexpr (BWD) return launch_k(slot, ln_bwd_kernel<VEC, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
-    else return launch_k(slot, ln_fwd_kernel<VEC, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
+    if constexpr (BWD) return launch_k(slot, ln_bwd_kernel<VEC, FX, FDY, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
+    else return launch_k(slot, ln_fwd_kernel<VEC, FX, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
+}
+
+template <bool BWD, bool VEC, bool FX, bool FDY>
+static hipError_t ln_launch_shape(const LnArgs& a, int slot, hipStream_t st) {
+    const LnShape s = ln_shape(a.D);
+    if (s.lanes == 8) return ln_launch<BWD, VEC, FX, FDY, 8, 1>(a, slot, st);
+    if (s.lanes == 16) return ln_launch<BWD, VEC, FX, FDY, 16, 1>(a, slot, st);
+    if (s.lanes == 32) return ln_launch<BWD, VEC, FX, FDY, 32, 1>(a, slot, st);
+    if (s.lanes == 64) return ln_launch<BWD, VEC, FX, FDY, 64, 1>(a, slot, st);
+    if (s.lanes == 128) return ln_launch<BWD, VEC, FX, FDY, 128, 1>(a, slot, st);
+    if (s.vecs == 1) return ln_launch<BWD, VEC, FX, FDY, 256, 1>(a, slot, st);
+    if (s.vecs == 2) return ln_launch<BWD, VEC, FX, FDY, 256, 2>(a, slot, st);
+    if (s.vecs == 4) return ln_launch<BWD, VEC, FX, FDY, 256, 4>(a, slot, st);
+    return ln_launch<BWD, VEC, FX, FDY, 256, 8>(a, slot, st);
 }
 
 template <bool BWD, bool VEC>
-static hipError_t ln_launch_shape(const LnArgs& a, int slot, hipStream_t st) {
-    const LnShape s = ln_shape(a.D);
-    if (s.lanes == 8) return ln_launch<BWD, VEC, 8, 1>(a, slot, st);
-    if (s.lanes == 16) return ln_launch<BWD, VEC, 16, 1>(a, slot, st);
-    if (s.lanes == 32) return ln_launch<BWD, VEC, 32, 1>(a, slot, st);
-    if (s.lanes == 64) return ln_launch<BWD, VEC, 64, 1>(a, slot, st);
-    if (s.lanes == 128) return ln_launch<BWD, VEC, 128, 1>(a, slot, st);
-    if (s.vecs == 1) return ln_launch<BWD, VEC, 256, 1>(a, slot, st);
-    if (s.vecs == 2) return ln_launch<BWD, VEC, 256, 2>(a, slot, st);
-    if (s.vecs == 4) return ln_launch<BWD, VEC, 256, 4>(a, slot, st);
-    return ln_launch<BWD, VEC, 256, 8>(a, slot, st);
+static hipError_t ln_launch_types(const LnArgs& a, int slot, hipStream_t st) {
+    if constexpr (BWD) {
+        if (a.x_f32)
+            return a.dy_f32 ? ln_launch_shape<BWD, VEC, true, true>(a, slot, st)
+                            : ln_launch_shape<BWD, VEC, true, false>(a, slot, st);
+        return a.dy_f32 ? ln_launch_shape<BWD, VEC, false, true>(a, slot, st)
+                        : ln_launch_shape<BWD, VEC, false, false>(a, slot, st);
+    } else {
+        return a.x_f32 ? ln_launch_shape<BWD, VEC, true, false>(a, slot, st)
+                       : ln_launch_shape<BWD, VEC, false, false>(a, slot, st);
+    }
 }
 
 hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
-    return vec ? ln_launch_shape<false, true>(a, slot, st) : ln_launch_shape<false, false>(a, slot, st);
+    return vec ? ln_launch_types<false, true>(a, slot, st) : ln_launch_types<false, false>(a, slot, st);
 }
 
 hipError_t launch_ln_bwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
-    hipError_t e = vec ? ln_launch_shape<true, true>(a, slot, st) : ln_launch_shape<true, false>(a, slot, st);
+    hipError_t e = vec ? ln_launch_types<true, true>(a, slot, st) : ln_launch_types<true, false>(a, slot, st);
     if (e == hipSuccess && a.part) {
         const unsigned per = (unsigned)(2 * a.D + 31) / 32;
         e = launch_k(slot, ln_bwd_sum_kernel, dim3(a.groups * per), dim3(1024), 0, st, a);

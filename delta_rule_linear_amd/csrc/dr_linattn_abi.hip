@@ -535,7 +535,7 @@ dr_status check_ln_desc(const dr_layernorm_desc* d) {
 void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
     a.groups = d.per_head ? d.H : 1;
     a.rows = d.per_head ? (unsigned)d.B * d.L : (unsigned)d.B * d.H * d.L;
-    const unsigned pass = (unsigned)dr::ln_pass_rows(d.D, bwd);
+    const unsigned pass = (unsigned)dr::ln_pass_rows(d.D);
     const unsigned passes = (a.rows + pass - 1) / pass;
     const unsigned most = !bwd ? 2048 : d.D <= 512 ? 1024 : 512;
     const unsigned want = std::max(1u, (most + a.groups - 1) / a.groups);
@@ -545,10 +545,6 @@ void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
 bool ln_vec(const dr_layernorm_desc& d, const dr_strides& s) {
     return (d.B <= 1 || s.b % 8 == 0) && (d.H <= 1 || s.h % 8 == 0) && (d.L <= 1 || s.t % 8 == 0);
 }
-
-// 128 rows (the most of a pass) and a row's width, in bytes of 4-byte values,
-// within 32 bits: tokens up to 2^21 elements apart.
-bool ln_near(const dr_strides& s) { return s.t <= ((int64_t)1 << 21); }
 
 dr::LnRows ln_rows(const dr_layernorm_desc& d, const dr_strides& s) {
     return {d.B > 1 ? s.b : 0, d.H > 1 ? s.h : 0, d.L > 1 ? s.t : 0};
@@ -600,7 +596,6 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     a.y_f32 = d->y_dtype == DR_F32;
     ln_groups(*d, a, false);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->y);
-    a.near_ok = ln_near(d->x) && ln_near(d->y);
     return hip_status(dr::launch_ln_fwd(a, vec, dr::kProfLnFwd, (hipStream_t)stream), "layer norm launch");
 }
 
@@ -663,7 +658,6 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     a.dy_f32 = d->dy_dtype == DR_F32;
     ln_groups(*d, a, true);
     const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->dy) && ln_vec(*d, d->y);
-    a.near_ok = ln_near(d->x) && ln_near(d->dy) && ln_near(d->y);
     return hip_status(dr::launch_ln_bwd(a, vec, slot, st), "layer norm backward launch");
 }
 
