@@ -230,9 +230,15 @@ def dr_profile_end() -> dict:
 # torch-facing wrappers (argument marshalling only)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -629,16 +635,17 @@ class _on:
     """Runs on `device`, on `stream` (default: the device's current stream), so
     that what is allocated inside belongs to that stream; gives the raw stream."""
 
+    __slots__ = ("ctx", "stream")
+
     def __init__(self, device, stream):
-        torch = _torch()
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
+        cuda = _torch().cuda
+        if stream is None:
+            self.ctx = None if cuda.current_device() == device.index else cuda.device(device)
+            self.stream = _raw_stream(device)
         else:
-            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-            stream = torch.cuda.current_stream(device)
-        self.stream = stream.cuda_stream
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.ctx, self.stream = cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
         if self.ctx is not None:
@@ -647,6 +654,14 @@ class _on:
 
     def __exit__(self, *exc):
         return None if self.ctx is None else self.ctx.__exit__(*exc)
+
+
+def _raw_stream(device) -> int:
+    """The device's current stream, without building a Stream object where
+    PyTorch offers that."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
 
 
 def _workspace(workspace, nbytes, device):
@@ -811,35 +826,40 @@ def dr_linear_attn_step(S, q, k, v, log_alpha=None, *, decay: str, out_dtype=Non
     return o
 
 
-def _norm_rows(t, weight_dims):
-    """x of two to four dimensions as [B, H, L, D]: [N, D], and with a weight
-    for each head [N, H, D] or [B, H, L, D]; with one weight also [B, H, L, D]
-    and [B, L, D]."""
-    if t.dim() == 4:
-        return t
-    if t.dim() == 2 and weight_dims == 1:
-        return t[None, None]
-    if t.dim() == 3:
-        return t[:, :, None] if weight_dims == 2 else t[:, None]
-    raise ValueError("x must be [N, D], [B, L, D], [N, H, D] or [B, H, L, D], with a weight [D] or [H, D]")
+def _norm_dims(t, per_head: bool):
+    """Sizes and strides of x as [B, H, L, D] rows: [N, D], and with a weight for
+    each head [N, H, D] or [B, H, L, D]; with one weight also [B, L, D] and
+    [B, H, L, D]."""
+    n, s = t.shape, t.stride()
+    if len(n) == 4:
+        dims, steps = (n[0], n[1], n[2], n[3]), (s[0], s[1], s[2])
+    elif len(n) == 3:
+        dims, steps = ((n[0], n[1], 1, n[2]), (s[0], s[1], 0)) if per_head else ((n[0], 1, n[1], n[2]), (s[0], 0, s[1]))
+    elif len(n) == 2 and not per_head:
+        dims, steps = (1, 1, n[0], n[1]), (0, 0, s[0])
+    else:
+        raise ValueError("x must be [N, D], [B, L, D], [N, H, D] or [B, H, L, D], with a weight [D] or [H, D]")
+    return dims, tuple(st if k > 1 else 0 for k, st in zip(dims, steps))
 
 
-def _norm_args(x, per_head, weight, bias, names=("weight", "bias")):
-    """The [B, H, L, D] view of x and whether the weights are one per head."""
+def _norm_args(x, per_head, weight, bias):
+    """The sizes and strides of x's rows and whether the weights are one per head."""
     torch = _torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    dims = {t.dim() for t in (weight, bias) if t is not None}
-    if len(dims) > 1:
+    if weight is not None and bias is not None and weight.dim() != bias.dim():
         raise ValueError("weight and bias must have the same shape")
-    per_head = per_head if per_head is not None else dims == {2}
-    x4 = _norm_rows(x, 2 if per_head else 1)
+    if per_head is None:
+        first = bias if weight is None else weight
+        per_head = first is not None and first.dim() == 2
+    dims, steps = _norm_dims(x, per_head)
     _need_rows(x, "x", None)
-    shape = (x4.shape[1], x4.shape[3]) if per_head else (x4.shape[3],)
-    for t, name in zip((weight, bias), names):
-        if t is not None:
-            _need_on(t, name, x.device, torch.float32, shape)
-    return x4, per_head, shape
+    shape = (dims[1], dims[3]) if per_head else (dims[3],)
+    if weight is not None:
+        _need_on(weight, "weight", x.device, torch.float32, shape)
+    if bias is not None:
+        _need_on(bias, "bias", x.device, torch.float32, shape)
+    return dims, steps, per_head, shape
 
 
 def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=None, y=None, mean=None, rstd=None,
@@ -853,27 +873,25 @@ def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=
     order of dimensions; mean and rstd are fp32, contiguous, of x's leading shape.
     """
     torch = _torch()
-    x4, per_head, _ = _norm_args(x, None, weight, bias)
-    B, H, L, D = x4.shape
-    dev, lead = x.device, tuple(x.shape[:-1])
+    dims, steps, per_head, _ = _norm_args(x, None, weight, bias)
+    dev, lead = x.device, x.shape[:-1]
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty_like(x, dtype=x.dtype if out_dtype is None else out_dtype)
+            y = torch.empty_like(x, dtype=out_dtype)
         else:
-            _need_rows(y, "y", dev, out_dtype, tuple(x.shape))
-        stats = []
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is None:
-                t = torch.empty(lead, dtype=torch.float32, device=dev)
-            else:
-                _need_on(t, name, dev, torch.float32, lead)
-            stats.append(t)
-        y4 = _norm_rows(y, 2 if per_head else 1)
-        _, desc, _ = _layernorm_plan((B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32,
-                                      float(eps)), _strides(x4), _strides(y4))
-        _check(lib().dr_layernorm_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(stats[0]),
-                                      _ptr(stats[1]), st))
-    return y, stats[0], stats[1]
+            _need_rows(y, "y", dev, out_dtype, x.shape)
+        if mean is None:
+            mean = torch.empty(lead, dtype=torch.float32, device=dev)
+        else:
+            _need_on(mean, "mean", dev, torch.float32, lead)
+        if rstd is None:
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+        else:
+            _need_on(rstd, "rstd", dev, torch.float32, lead)
+        _, desc, _ = _layernorm_plan(dims + (int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32,
+                                             float(eps)), steps, _norm_dims(y, per_head)[1])
+        _check(lib().dr_layernorm_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), st))
+    return y, mean, rstd
 
 
 def dr_layernorm_bwd_workspace_bytes(desc: LayerNormDesc) -> int:
@@ -889,21 +907,19 @@ def dr_layernorm_bwd(x, weight, mean, rstd, dy, *, per_head=None, grad_dtype=Non
     torch = _torch()
     if weight is not None and per_head is not None and per_head != (weight.dim() == 2):
         raise ValueError("per_head does not fit the weight's shape")
-    x4, per_head, wshape = _norm_args(x, per_head, weight, None)
-    B, H, L, D = x4.shape
-    dev, lead = x.device, tuple(x.shape[:-1])
+    dims, steps, per_head, wshape = _norm_args(x, per_head, weight, None)
+    dev, lead = x.device, x.shape[:-1]
     _need_on(mean, "mean", dev, torch.float32, lead)
     _need_on(rstd, "rstd", dev, torch.float32, lead)
-    _need_rows(dy, "dy", dev, None, tuple(x.shape))
+    _need_rows(dy, "dy", dev, None, x.shape)
     with _on(dev, stream) as st:
         if dx is None:
-            dx = torch.empty_like(x, dtype=x.dtype if grad_dtype is None else grad_dtype)
+            dx = torch.empty_like(x, dtype=grad_dtype)
         else:
-            _need_rows(dx, "dx", dev, grad_dtype, tuple(x.shape))
-        dims = 2 if per_head else 1
-        _, desc, nbytes = _layernorm_plan((B, H, L, D, int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
-                                           _dtype_code(dy.dtype), 0.0), _strides(x4), _strides(_norm_rows(dx, dims)),
-                                          _strides(_norm_rows(dy, dims)))
+            _need_rows(dx, "dx", dev, grad_dtype, x.shape)
+        _, desc, nbytes = _layernorm_plan(dims + (int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
+                                                  _dtype_code(dy.dtype), 0.0), steps, _norm_dims(dx, per_head)[1],
+                                          _norm_dims(dy, per_head)[1])
         out = {"dx": dx, "dweight": None, "dbias": None}
         wbytes = 0
         if want_sums:
