@@ -75,9 +75,8 @@ struct LaGateArgs {
     const float* segR;      // dS at the segments' ends
     const float* S_end;     // S behind the last token, dS there (NULL: zero)
     const float* dS_end;
-    float* dla;             // [B][H][L] or, per head, partial sums [B*H][nseg]
-    float* dla_head;        // [H], per-head decays
-    int head;
+    float* dla;             // [B][H][L], or
+    double* part;           // per-head decays: sums over a segment, [B*H][nseg]
     int B, H, L, nseg, cps, elems;
 };
 
@@ -93,14 +92,20 @@ struct LaStepArgs {
     int out_bf16;
 };
 
-// Gradients of q and k heads shared by `group` state heads: per-state-head
-// gradients [B][H][L][D] fp32 summed in head order into [B][H/group][L][D].
-struct LaGroupArgs {
-    const float* in;
-    void* out;
-    int64_t ob, oh, ot;
+// What is left after the passes of a backward, in one launch: gradients of q and
+// k heads shared by `group` state heads (per-state-head gradients [B][H][L][D]
+// fp32 summed in head order into [B][H/group][L][D]; in NULL: none), and per-head
+// decays' gradients from the partial sums [B*H][nseg] (part NULL: none).
+struct LaFinishArgs {
+    const float* in[2];
+    void* out[2];
+    int64_t ob[2], oh[2], ot[2];
     int out_bf16;
     int B, Hk, L, D, group;
+    const double* part;
+    float* dla_head;
+    int H, nseg;
+    unsigned blocks;     // workgroups per gradient
 };
 
 // terms: bf16 terms per fp32 operand value of the output's products (2 or 3;
@@ -111,7 +116,7 @@ hipError_t launch_la_join(const LaJoinArgs* a, int n, int slot, hipStream_t st);
 hipError_t launch_la_gate(const LaGateArgs& a, int slot, hipStream_t st);
 // dst = src, or zeros (src NULL)
 hipError_t launch_la_copy(float* dst, const float* src, size_t n, int slot, hipStream_t st);
-hipError_t launch_la_group(const LaGroupArgs& a, int slot, hipStream_t st);
+hipError_t launch_la_finish(LaFinishArgs a, int slot, hipStream_t st);
 hipError_t launch_la_step(const LaStepArgs& a, bool f32in, int slot, hipStream_t st);
 
 }  // namespace dr

@@ -112,39 +112,23 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
         carry += red[255];
         __syncthreads();
         if (t >= t0) {
-            if (!a.head) a.dla[(size_t)seq * a.L + t] = (float)v;
+            if (!a.part) a.dla[(size_t)seq * a.L + t] = (float)v;
             total += v;
         }
     }
-    if (a.head) {
+    if (a.part) {
         red[tid] = total;
         __syncthreads();
         for (int n = 128; n > 0; n >>= 1) {
             if (tid < n) red[tid] += red[tid + n];
             __syncthreads();
         }
-        if (tid == 0) reinterpret_cast<double*>(a.dla)[(size_t)seq * a.nseg + sg] = red[0];
+        if (tid == 0) a.part[(size_t)seq * a.nseg + sg] = red[0];
     }
-}
-
-// one workgroup per head: the sum over sequences and segments, in their order
-__global__ __launch_bounds__(64) void la_gate_head_kernel(LaGateArgs a) {
-    const double* part = reinterpret_cast<const double*>(a.dla);
-    const int hd = blockIdx.x;
-    double acc = 0.0;
-    for (size_t i = threadIdx.x; i < (size_t)a.B * a.nseg; i += 64) {
-        const size_t b = i / a.nseg, s = i % a.nseg;
-        acc += part[(b * a.H + hd) * a.nseg + s];
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) acc += __shfl_xor(acc, d);
-    if (threadIdx.x == 0) a.dla_head[hd] = (float)acc;
 }
 
 hipError_t launch_la_gate(const LaGateArgs& a, int slot, hipStream_t st) {
-    hipError_t e = launch_k(slot, la_gate_kernel, dim3((unsigned)(a.B * a.H * a.nseg)), dim3(256), 0, st, a);
-    if (e == hipSuccess && a.head) e = launch_k(slot, la_gate_head_kernel, dim3(a.H), dim3(64), 0, st, a);
-    return e;
+    return launch_k(slot, la_gate_kernel, dim3((unsigned)(a.B * a.H * a.nseg)), dim3(256), 0, st, a);
 }
 
 __global__ __launch_bounds__(256) void la_copy_kernel(float* dst, const float* src, size_t n) {
@@ -158,30 +142,54 @@ hipError_t launch_la_copy(float* dst, const float* src, size_t n, int slot, hipS
                     n);
 }
 
-// ------------------------------------------------------ shared heads
-__global__ __launch_bounds__(256) void la_group_kernel(LaGroupArgs a) {
+// ------------------------------------------------------ shared heads, per-head decays
+// One wave per head: the sum over sequences and segments, in their order.
+__device__ __forceinline__ void la_finish_heads(const LaFinishArgs& a, unsigned block) {
+    const int hd = block * 4 + (threadIdx.x >> 6);
+    if (hd >= a.H) return;
+    double acc = 0.0;
+    for (size_t i = threadIdx.x & 63; i < (size_t)a.B * a.nseg; i += 64) {
+        const size_t b = i / a.nseg, s = i % a.nseg;
+        acc += a.part[(b * a.H + hd) * a.nseg + s];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) acc += __shfl_xor(acc, d);
+    if ((threadIdx.x & 63) == 0) a.dla_head[hd] = (float)acc;
+}
+
+__global__ __launch_bounds__(256) void la_finish_heads_kernel(LaFinishArgs a) { la_finish_heads(a, blockIdx.x); }
+
+__global__ __launch_bounds__(256) void la_finish_kernel(LaFinishArgs a) {
+    const unsigned which = blockIdx.x / a.blocks;
+    if (which >= 2) return la_finish_heads(a, blockIdx.x - 2 * a.blocks);
     const int n4 = a.D / 4;
     const size_t n = (size_t)a.B * a.Hk * a.L * n4;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+    for (size_t i = (size_t)(blockIdx.x % a.blocks) * 256 + threadIdx.x; i < n; i += (size_t)a.blocks * 256) {
         const int c = (int)(i % n4);
         size_t r = i / n4;
         const int64_t t = r % a.L;
         r /= a.L;
         const int64_t hk = r % a.Hk, b = r / a.Hk;
-        const f32x4* in = reinterpret_cast<const f32x4*>(a.in) +
+        const f32x4* in = reinterpret_cast<const f32x4*>(a.in[which]) +
                           (((size_t)b * a.Hk + hk) * a.group * a.L + t) * n4 + c;
         f32x4 v = in[0];
         for (int g = 1; g < a.group; ++g) v = v + in[(size_t)g * a.L * n4];
-        const int64_t at = b * a.ob + hk * a.oh + t * a.ot + 4 * c;
-        if (a.out_bf16) *reinterpret_cast<bf16x4*>((__bf16*)a.out + at) = __builtin_convertvector(v, bf16x4);
-        else *reinterpret_cast<f32x4*>((float*)a.out + at) = v;
+        const int64_t at = b * a.ob[which] + hk * a.oh[which] + t * a.ot[which] + 4 * c;
+        if (a.out_bf16) *reinterpret_cast<bf16x4*>((__bf16*)a.out[which] + at) = __builtin_convertvector(v, bf16x4);
+        else *reinterpret_cast<f32x4*>((float*)a.out[which] + at) = v;
     }
 }
 
-hipError_t launch_la_group(const LaGroupArgs& a, int slot, hipStream_t st) {
+hipError_t launch_la_finish(LaFinishArgs a, int slot, hipStream_t st) {
     const size_t n = (size_t)a.B * a.Hk * a.L * (a.D / 4);
-    const size_t blocks = (n + 255) / 256;
-    return launch_k(slot, la_group_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, a);
+    const size_t want = (n + 255) / 256;
+    a.blocks = a.in[0] ? (unsigned)(want < 8192 ? want : 8192) : 0;
+    const unsigned heads = a.part ? (a.H + 3) / 4 : 0;
+    if (a.blocks == 0) {
+        if (heads == 0) return hipSuccess;
+        return launch_k(slot, la_finish_heads_kernel, dim3(heads), dim3(256), 0, st, a);
+    }
+    return launch_k(slot, la_finish_kernel, dim3(2 * a.blocks + heads), dim3(256), 0, st, a);
 }
 
 // ------------------------------------------------------ one token

@@ -116,14 +116,22 @@ struct Split {
 
 int waves_of(int D) { return D <= 32 ? 2 : D <= 64 ? 4 : 8; }
 
-// Workgroups that fill the GPU: two on each of 256 compute units.
-constexpr int64_t kFill = 512;
-constexpr int kMinChunks = 4;
+// Segments: as many as make two workgroups for each of 256 compute units, of
+// four chunks at least; or, where that leaves compute units without work, one
+// workgroup for each, of two chunks at least.  A segment costs its state (64 KB
+// at 128 x 128) written, joined and read; a chunk takes a workgroup about 4 us.
+// bf16, 128 x 128, 16 heads: 512 tokens 36.6 us in two segments, 27.1 in four;
+// 1024 tokens 39.3 in four, 31.5 in eight; 4096 tokens 47.6 in 16, 55.8 in 32;
+// 256 tokens 21.6 in one, 24.9 in two (the two more launches).
+constexpr int64_t kUnits = 256;
 
-Split la_split_of(int L, int64_t units) {
+Split la_split_of(int L, int64_t nseq) {
     const int NC = (int)(((int64_t)L + 63) / 64);
-    int64_t want = units ? (kFill + units - 1) / units : 1;
-    want = std::min<int64_t>(want, NC / kMinChunks);
+    auto segments = [&](int64_t workgroups, int chunks) {
+        return std::min<int64_t>((workgroups + nseq - 1) / std::max<int64_t>(nseq, 1), NC / chunks);
+    };
+    int64_t want = segments(2 * kUnits, 4);
+    if (NC >= 8) want = std::max(want, segments(kUnits, 2));
     want = std::max<int64_t>(want, 1);
     const int cps = (int)((NC + want - 1) / want);
     return {(NC + cps - 1) / cps, cps};
@@ -458,9 +466,8 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
         g.segR = seg[1];
         g.S_end = S_end;
         g.dS_end = dS_final;
-        g.head = d->decay == DR_DECAY_HEAD;
-        g.dla = g.head ? (float*)(ws + w.part) : dlog_alpha;
-        g.dla_head = dlog_alpha;
+        g.dla = dlog_alpha;
+        g.part = d->decay == DR_DECAY_HEAD ? (double*)(ws + w.part) : nullptr;
         g.B = d->B;
         g.H = d->H;
         g.L = d->L;
@@ -470,14 +477,27 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
         s = hip_status(dr::launch_la_gate(g, slot, st), "decay gradient launch");
         if (s != DR_OK) return s;
     }
-    if (group > 1)
-        for (int i = 0; i < 2; ++i) {
-            const dr::LaTensor t = tensor(*rg[i], 1);
-            const dr::LaGroupArgs g{(const float*)(ws + w.dqk[i]), const_cast<void*>(t.p), t.b, t.h, t.t,
-                                    od == DR_BF16, d->B, d->Hk, d->L, d->Dk, group};
-            s = hip_status(dr::launch_la_group(g, slot, st), "shared heads launch");
-            if (s != DR_OK) return s;
-        }
+    dr::LaFinishArgs f{};
+    for (int i = 0; i < 2 && group > 1; ++i) {
+        const dr::LaTensor t = tensor(*rg[i], 1);
+        f.in[i] = (const float*)(ws + w.dqk[i]);
+        f.out[i] = const_cast<void*>(t.p);
+        f.ob[i] = t.b;
+        f.oh[i] = t.h;
+        f.ot[i] = t.t;
+    }
+    f.out_bf16 = od == DR_BF16;
+    f.B = d->B;
+    f.Hk = d->Hk;
+    f.L = d->L;
+    f.D = d->Dk;
+    f.group = group;
+    f.part = d->decay == DR_DECAY_HEAD ? (const double*)(ws + w.part) : nullptr;
+    f.dla_head = dlog_alpha;
+    f.H = d->H;
+    f.nseg = a.nseg;
+    s = hip_status(dr::launch_la_finish(f, slot, st), "backward's last launch");
+    if (s != DR_OK) return s;
     return DR_OK;
 }
 
