@@ -378,14 +378,15 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
 }
 
 // dw and db from the workgroups' sums: 32 columns per workgroup; each of 32
-// threads per column adds every 32nd workgroup's sum, then the 32 are added.
+// threads per column adds every 32nd workgroup's sum, then the 32 are added, in
+// fp64 (a sum of many rows is small against its terms).
 __global__ __launch_bounds__(1024) void ln_bwd_sum_kernel(LnArgs a) {
-    __shared__ float red[32][33];
+    __shared__ double red[32][33];
     const unsigned cols = 2 * (unsigned)a.D, per = (cols + 31) / 32;
     const unsigned g = blockIdx.x / per;
     const unsigned lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const unsigned c = (blockIdx.x % per) * 32 + lane;
-    float s = 0.f;
+    double s = 0.0;
     if (c < cols) {
         const float* p = a.part + (size_t)g * a.blocks * cols + c;
 #pragma unroll 8
@@ -394,13 +395,13 @@ __global__ __launch_bounds__(1024) void ln_bwd_sum_kernel(LnArgs a) {
     red[slice][lane] = s;
     __syncthreads();
     if (slice == 0 && c < cols) {
-        s = 0.f;
+        s = 0.0;
 #pragma unroll
         for (int k = 0; k < 32; ++k) s += red[k][lane];
         if (c < (unsigned)a.D) {
-            if (a.dw) a.dw[(size_t)g * a.D + c] = s;
+            if (a.dw) a.dw[(size_t)g * a.D + c] = (float)s;
         } else if (a.db) {
-            a.db[(size_t)g * a.D + c - a.D] = s;
+            a.db[(size_t)g * a.D + c - a.D] = (float)s;
         }
     }
 }

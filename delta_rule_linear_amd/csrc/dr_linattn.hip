@@ -62,11 +62,21 @@ hipError_t launch_la_join(const LaJoinArgs* a, int n, int slot, hipStream_t st) 
 // One workgroup per (sequence, segment): <S, dS> at the segment's end, then the
 // sums over the tokens behind each token.  The differences are small against
 // their terms, so the sums are fp64.
+// Sum over the workgroup's 256 threads, in every one of them.
+__device__ __forceinline__ double la_block_sum(double x, double* red) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
 __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
-    __shared__ double red[256];
+    __shared__ double red[4];
     const int nseq = a.B * a.H;
     const int seq = blockIdx.x % nseq, sg = blockIdx.x / nseq;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const float *S = nullptr, *D = nullptr;
     if (sg + 1 < a.nseg) {
         S = a.segF + ((size_t)seq * a.nseg + sg + 1) * a.elems;
@@ -77,20 +87,15 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
     }
     double acc = 0.0;
     if (S)
+#pragma unroll 8
         for (int i = tid; i < a.elems / 4; i += 256) {
             const f32x4 s = reinterpret_cast<const f32x4*>(S)[i], d = reinterpret_cast<const f32x4*>(D)[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc += (double)s[j] * (double)d[j];
         }
-    red[tid] = acc;
-    __syncthreads();
-    for (int n = 128; n > 0; n >>= 1) {
-        if (tid < n) red[tid] += red[tid + n];
-        __syncthreads();
-    }
-    double carry = red[0];
-    __syncthreads();
-    // 256 tokens at a time, from the segment's last
+    double carry = la_block_sum(acc, red);
+    // 256 tokens at a time, from the segment's last; a running sum within each
+    // wave, then over the waves
     const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
     double total = 0.0;
     for (int hi = t1; hi > t0; hi -= 256) {
@@ -100,30 +105,23 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
             const size_t at = (size_t)seq * a.L + t;
             d = (double)a.dq_dots[at] - (double)a.dk_dots[at];
         }
-        red[tid] = d;
+        d = la_scan(d);
         __syncthreads();
-        for (int n = 1; n < 256; n <<= 1) {
-            const double y = tid >= n ? red[tid - n] : 0.0;
-            __syncthreads();
-            red[tid] += y;
-            __syncthreads();
-        }
-        const double v = carry + red[tid];
-        carry += red[255];
+        if (lane == 63) red[wave] = d;
         __syncthreads();
+        double v = carry + d;
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+            if (w < wave) v += red[w];
+        carry += (red[0] + red[1]) + (red[2] + red[3]);
         if (t >= t0) {
             if (!a.part) a.dla[(size_t)seq * a.L + t] = (float)v;
             total += v;
         }
     }
     if (a.part) {
-        red[tid] = total;
-        __syncthreads();
-        for (int n = 128; n > 0; n >>= 1) {
-            if (tid < n) red[tid] += red[tid + n];
-            __syncthreads();
-        }
-        if (tid == 0) a.part[(size_t)seq * a.nseg + sg] = red[0];
+        total = la_block_sum(total, red);
+        if (tid == 0) a.part[(size_t)seq * a.nseg + sg] = total;
     }
 }
 
