@@ -73,6 +73,7 @@ struct LaGateArgs {
     const float* dk_dots;
     const float* segF;      // S at the segments' starts, [B*H][nseg][elems]
     const float* segR;      // dS at the segments' ends
+    const float* la;        // log alpha: [H] (part) or [B][H][L]
     const float* S_end;     // S behind the last token, dS there (NULL: zero)
     const float* dS_end;
     float* dla;             // [B][H][L], or

@@ -61,7 +61,8 @@ hipError_t launch_la_join(const LaJoinArgs* a, int n, int slot, hipStream_t st) 
 // ------------------------------------------------------ the gate's gradient
 // One workgroup per (sequence, segment): <S, dS> at the segment's end, then the
 // sums over the tokens behind each token.  The differences are small against
-// their terms, so the sums are fp64.
+// their terms, so the sums are fp64.  Where alpha is zero its gradient is too,
+// exactly.
 // Sum over the workgroup's 256 threads, in every one of them.
 __device__ __forceinline__ double la_block_sum(double x, double* red) {
 #pragma unroll
@@ -115,13 +116,13 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
             if (w < wave) v += red[w];
         carry += (red[0] + red[1]) + (red[2] + red[3]);
         if (t >= t0) {
-            if (!a.part) a.dla[(size_t)seq * a.L + t] = (float)v;
+            if (!a.part) a.dla[(size_t)seq * a.L + t] = a.la[(size_t)seq * a.L + t] < kLaZero ? 0.f : (float)v;
             total += v;
         }
     }
     if (a.part) {
         total = la_block_sum(total, red);
-        if (tid == 0) a.part[(size_t)seq * a.nseg + sg] = total;
+        if (tid == 0) a.part[(size_t)seq * a.nseg + sg] = a.la[seq % a.H] < kLaZero ? 0.0 : total;
     }
 }
 

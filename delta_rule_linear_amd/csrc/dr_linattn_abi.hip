@@ -464,6 +464,7 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
         g.dk_dots = dots[1];
         g.segF = seg[0];
         g.segR = seg[1];
+        g.la = log_alpha;
         g.S_end = S_end;
         g.dS_end = dS_final;
         g.dla = dlog_alpha;

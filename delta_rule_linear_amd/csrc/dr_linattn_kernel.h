@@ -19,11 +19,18 @@
 // y rows are staged there in that order.  The 64 x 64 matrix of products x . y
 // is made once per workgroup, a 16 x 16 block or two per wave, and shared
 // through LDS with its decays applied.  Products that contract over tokens read
-// y and z transposed (ds_read_b64_tr_b16 for bf16).  Sixteen columns per wave
-// and eight waves keep the registers at 128, i.e. four waves per SIMD: 32
-// columns and four waves read LDS half as often, but two waves per SIMD left
-// the matrix cores idle (forward, B2 H16 L16384 d128 bf16: 187 us, see DESIGN
-// of the waves' count in la_threads).
+// y and z transposed (ds_read_b64_tr_b16 for bf16).
+//
+// Why 16 columns and eight waves: the registers stay at 128, four waves per SIMD
+// in two workgroups per CU.  32 columns per wave on the 32x32 ops read LDS half
+// as often, but with two waves per SIMD this kernel took 187 us for the forward
+// at B2 H16 L16384 d128 bf16, against 163 with four at the same stage.  Now it
+// takes 142 us for 570 MB (4.0 TB/s; a large copy reaches 5.2), the state pass 67
+// us for 300 MB.  With its products left out it takes 110 us, so memory bounds it
+// first; then the VALU (480 instructions per wave and chunk, a third of them
+// splitting fp32 values into bf16 terms) together with the issue of 97 matrix
+// ops.  The backward's three passes (three terms, row dot products) are bound by
+// those: 540-630 us for 1.97 GB.
 //
 // Precision.  bf16 inputs are operands as they are.  fp32 quantities that meet
 // them are split into bf16 terms: the decayed z of the state update into three
@@ -334,6 +341,9 @@ __device__ __forceinline__ double la_scan(double x) {
     return la_scan_step<0x143, 0xC>(x);
 }
 
+// log alpha below -256 / log2(e) counts as that: its e^ is 0 in fp32.
+constexpr float kLaZero = -177.445678f;
+
 // The decays of a chunk in LDS: u as hi + lo floats, e^u, e^{total - u}, and
 // e^total; two buffers, the next chunk's made while this one's are read.
 constexpr int kLaGateBytes = 4 * 64 * 4 + 16;
@@ -459,7 +469,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     auto decays = [&](int n, float x) {
         const int l = (la_fresh(tid) & 63);
         lchar* gt = sG + (n & 1) * kLaGateBytes + 4 * l;
-        const double l2 = x < -177.445678f ? -256.0 : (double)x * 1.4426950408889634;
+        const double l2 = x < kLaZero ? -256.0 : (double)x * 1.4426950408889634;
         const double s = la_scan(l2);
         const double total = __shfl(s, 63);
         const double u = rev ? s - l2 : s;

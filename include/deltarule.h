@@ -448,7 +448,8 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  *   DR_DECAY_HEAD   one constant per head, log_alpha [H]
  *   DR_DECAY_TOKEN  one value per token and head, log_alpha [B][H][L]
  * log_alpha is fp32, expected <= 0 (not checked; larger values grow the state).
- * -inf (alpha = 0) starts the state anew at that token; its gradient is 0.
+ * -inf (alpha = 0) starts the state anew at that token; its gradient is 0
+ * (below -177.4, where e^log_alpha is 0 in fp32, likewise).
  * Any size of decay is exact to fp32: nothing is divided by a decay.
  *
  * Heads.  q and k have Hk heads, Hk a divisor of H: state head h reads q and k

@@ -136,8 +136,8 @@ def test_a_decay_of_zero_starts_anew(dtype):
     check_fwd(p, "token")
     check_bwd(p, "token")
     g = run_bwd(p, "token")
-    # nothing passes a reset, so its own gradient is exactly zero in exact
-    # arithmetic, and here the sums' rounding
+    # nothing passes a reset: neither a gradient of its own nor one of S0, and no S0
+    assert not g["dlog_alpha"][:, :, [0, 64, 65, 131]].any()
     S0 = p["S0"]
     p["S0"] = torch.zeros_like(S0)
     o0, _ = run_fwd(p, "token")
@@ -272,6 +272,24 @@ def test_broadcast_rows_and_slices_of_one_projection():
     assert torch.equal(o, run_fwd(p, "head")[0])
 
 
+@pytest.mark.parametrize("L", [1, 40, 100, 700])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_row_for_every_token(L, dtype):
+    """q, k, v and dO broadcast over tokens (stride 0), with a chunk that is not
+    full: rows behind the last token must not count."""
+    gen = torch.Generator().manual_seed(L)
+    one = lambda n, D: torch.randn((2, n, 1, D), generator=gen).to(DT[dtype]).cuda().expand(2, n, L, D)  # noqa: E731
+    p = dict(q=one(2, 64), k=one(2, 64), v=one(4, 72), dO=one(4, 72), la=decays(gen, "token", 2, 4, L),
+             S0=torch.randn((2, 4, 64, 72), generator=gen).cuda(), dS=torch.randn((2, 4, 64, 72), generator=gen).cuda())
+    check_fwd(p, "token")
+    check_bwd(p, "token")
+    # rows that overlap: each token's starts 8 channels after the last one's
+    buf = torch.randn(8 * L + 64, generator=gen).to(DT[dtype]).cuda()
+    p["q"] = p["k"] = buf.as_strided((2, 2, L, 64), (0, 0, 8, 1))
+    check_fwd(p, "token")
+    check_bwd(p, "token")
+
+
 def test_offsets_past_32_bits():
     """Heads of q, k, v and o more than 2^31 elements apart."""
     gen = torch.Generator().manual_seed(4)
@@ -317,22 +335,24 @@ def test_same_bits_every_time_and_on_other_streams():
         assert all(torch.equal(g[n], g2[n]) for n in g)
 
 
-def test_captured_and_replayed():
-    p = problem(1, 2, 2, 1500, 64, 64, "token", "bf16", grad=True)
-    run_fwd(p, "token"), run_bwd(p, "token")
+@pytest.mark.parametrize("L,D,Hk,decay,dtype", [(1500, 64, 2, "token", "bf16"), (700, 128, 1, "head", "bf16"),
+                                                (700, 128, 2, "token", "f32")])
+def test_captured_and_replayed(L, D, Hk, decay, dtype):
+    p = problem(1, 2, Hk, L, D, D, decay, dtype, grad=True)
+    run_fwd(p, decay), run_bwd(p, decay)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        o, S = run_fwd(p, "token")
-        g = run_bwd(p, "token")
+        o, S = run_fwd(p, decay)
+        g = run_bwd(p, decay)
     for n in range(4):
         gen = torch.Generator().manual_seed(100 + n)
         p["v"].copy_(torch.randn(p["v"].shape, generator=gen))
         p["S0"].copy_(torch.randn(p["S0"].shape, generator=gen))
         graph.replay()
         torch.cuda.synchronize()
-        eo, eS = run_fwd(p, "token")
-        eg = run_bwd(p, "token")
+        eo, eS = run_fwd(p, decay)
+        eg = run_bwd(p, decay)
         assert torch.equal(o, eo) and torch.equal(S, eS)
         assert all(torch.equal(g[k], eg[k]) for k in g)
 
