@@ -246,6 +246,11 @@ __device__ __forceinline__ int la_fresh(int x) {
     return x;
 }
 
+__device__ __forceinline__ int la_fresh_s(int x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
 // A product whose upper half no register is kept for.
 __device__ __forceinline__ unsigned la_mul(unsigned a, unsigned b) { return (unsigned)la_fresh((int)(a * b)); }
 
@@ -339,6 +344,14 @@ __device__ __forceinline__ double la_scan(double x) {
     x = la_scan_step<0x118, 0xF>(x);
     x = la_scan_step<0x142, 0xA>(x);
     return la_scan_step<0x143, 0xC>(x);
+}
+
+// The last lane's value.
+__device__ __forceinline__ double la_last(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)u, 63);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(u >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 // log alpha below -256 / log2(e) counts as that: its e^ is 0 in fp32.
@@ -471,7 +484,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         lchar* gt = sG + (n & 1) * kLaGateBytes + 4 * l;
         const double l2 = x < kLaZero ? -256.0 : (double)x * 1.4426950408889634;
         const double s = la_scan(l2);
-        const double total = __shfl(s, 63);
+        const double total = la_last(s);
         const double u = rev ? s - l2 : s;
         const float uh = (float)u;
         // a row behind the last token adds nothing to others: its u is beyond
@@ -499,38 +512,46 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     char* const gout = STATE ? nullptr : (char*)ps.out + osz * (b * ps.ob + hd * ps.oh);
     const char* gw = dots ? (const char*)ps.w.p + sizeof(T) * (b * ps.w.b + (hd / ps.w.group) * ps.w.h) : nullptr;
     float* const gd = dots ? ps.dots + (size_t)seq * L : nullptr;
-    // the lane's four columns of row 16 it + l15, in a tensor of `size`-byte values
-    auto out_offset = [&](int it, unsigned row_bytes, int size) {
+    // the lane's four columns of row l15 (in the pass's order), in a tensor of
+    // `size`-byte values, and the step to row 16 it + l15
+    auto out_offset = [&](unsigned row_bytes, int size) {
         const int l = (la_fresh(tid) & 63), col = zc0 + 4 * (l >> 4);
-        const unsigned t = (16 * it + (l & 15)) ^ flip;
-        return (col < Dz ? (unsigned)(size * col) : kLaOut) + la_mul(t, row_bytes);
+        return (col < Dz ? (unsigned)(size * col) : kLaOut) + la_mul((l & 15) ^ (flip & 15), row_bytes);
     };
+    auto out_step = [&](int it, unsigned row_bytes) { return 16u * (unsigned)(it ^ (flip & 3)) * row_bytes; };
     auto fetch_w = [&](int n) {
         const int c = chunk(n);
         const LaRange r = la_range(gw, (int64_t)(64 * c) * bw, L - 64 * c, bw, Dz * sizeof(T));
+        const unsigned off = out_offset(bw, sizeof(T));
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
+            const unsigned at = off + out_step(it, bw);
             if constexpr (BF)
-                W[it] = __builtin_bit_cast(RawN<!BF, 4>,
-                                           __builtin_amdgcn_raw_buffer_load_b64(r, out_offset(it, bw, 2), 0, 0));
+                W[it] = __builtin_bit_cast(RawN<!BF, 4>, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
             else
-                W[it] = __builtin_bit_cast(RawN<!BF, 4>,
-                                           __builtin_amdgcn_raw_buffer_load_b128(r, out_offset(it, bw, 4), 0, 0));
+                W[it] = __builtin_bit_cast(RawN<!BF, 4>, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
         }
     };
-    // the rows' dot products, per wave into LDS, then their sums
+    // the rows' dot products, per wave into LDS, then their sums.  A sum over
+    // the four lane groups takes two exchanges of groups, each of which adds two
+    // rows' halves at once and leaves them to a group each.
     auto dot_rows = [&]() {
-        const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15;
+        float dot[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-            float w4[4], dot = 0.f;
+            float w4[4];
             cvt_rawn<!BF, 4>(W[it], w4);
+            dot[it] = O[it][0] * w4[0];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dot += O[it][j] * w4[j];
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
-            if (g == 0) lds_st(sR + 256 * wave + 4 * (16 * it + l15), dot);
+            for (int j = 1; j < 4; ++j) dot[it] += O[it][j] * w4[j];
         }
+        auto add = [](auto r) { return __uint_as_float(r[0]) + __uint_as_float(r[1]); };
+#pragma unroll
+        for (int it = 0; it < 4; it += 2)
+            dot[it] = add(__builtin_amdgcn_permlane16_swap(__float_as_uint(dot[it]), __float_as_uint(dot[it + 1]), false,
+                                                           false));
+        dot[0] = add(__builtin_amdgcn_permlane32_swap(__float_as_uint(dot[0]), __float_as_uint(dot[2]), false, false));
+        lds_st(sR + 256 * wave + 4 * (la_fresh(tid) & 63), dot[0]);   // group g: row 16 g + l15
     };
     auto store_dots = [&](int n) {
         if (tid >= 64) return;
@@ -565,15 +586,16 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                                                            off + la_step<NZ, PZ, NTHR>(i, bo, flip), 0, 0);
             }
         } else {
+            const unsigned off = out_offset(bo, osz);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
+                const unsigned at = off + out_step(it, bo);
                 if (!BF && out_bf16) {
                     typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
                     const u32x2 v = {la_pack(O[it][0], O[it][1]), la_pack(O[it][2], O[it][3])};
-                    __builtin_amdgcn_raw_buffer_store_b64(v, r, out_offset(it, bo, 2), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b64(v, r, at, 0, 0);
                 } else {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), r, out_offset(it, bo, 4), 0,
-                                                           0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), r, at, 0, 0);
                 }
             }
         }
@@ -613,30 +635,33 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         }
 
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const float decay = lds_ld<float>(gt + 1024);
         if constexpr (!STATE) {
             const int ax = la_fresh(ax0);
-            const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15, yrow = la_row_at<T, RX, false>(l15, g);
             // 16 x 16 blocks (it, jt), jt <= it, of the products x . y, times their decays, into LDS
-            for (int k = wave; k < 10; k += NW) {
-                const int it = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0, jt = k - it * (it + 1) / 2;
+            for (int n = wave; n < 10; n += NW) {
+                const int k = 2 * la_fresh_s(n), it = (0xFFA94 >> k) & 3, jt = (0xE4910 >> k) & 3;   // row by row
+                const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15;
+                const int yrow = la_fresh(la_row_at<T, RX, false>(l15, g) + 16 * jt * RX), xrow = la_fresh(ax + 16 * it * RX);
                 f32x4 P = zero;
 #pragma unroll
                 for (int m = 0; m < DX / 32; ++m)
-                    P = la_mfma(la_row<T, false>(sY + 16 * jt * RX, yrow, m).v, la_row<T, true>(sX + 16 * it * RX, ax, m).v,
-                                P);
-                const int i = 16 * it + l15, j = 16 * jt + 4 * g;
-                const float ui = lds_ld<float>(gt + 4 * i), wi = lds_ld<float>(gt + 256 + 4 * i);
-                const f32x4 uj = lds_ld<f32x4>(gt + 4 * j), wj = lds_ld<f32x4>(gt + 256 + 4 * j);
+                    P = la_mfma(la_row<T, false>(sY, yrow, m).v, la_row<T, true>(sX, xrow, m).v, P);
+                const lchar* ti = gt + la_fresh(4 * l15) + 64 * it;
+                const lchar* tj = gt + la_fresh(16 * g) + 64 * jt;
+                const float ui = lds_ld<float>(ti), wi = lds_ld<float>(ti + 256);
+                const f32x4 uj = lds_ld<f32x4>(tj), wj = lds_ld<f32x4>(tj + 256);
+                const int last = 16 * (it - jt) + l15 - 4 * g;   // of the lane's j that row i takes
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float d = (ui - uj[e]) + (wi - wj[e]);
                     const float x = P[e] * __builtin_amdgcn_exp2f(d);
-                    v[e] = j + e <= i ? x : 0.f;
+                    v[e] = e <= last ? x : 0.f;
                 }
                 if constexpr (BF) {
                     // la_row's order of quads: 8-byte quad 4 (jt % 2) + g of 32 values
-                    lchar* at = sP + i * RP + 16 * ((4 * (jt >> 1) + g) ^ la_swz<T, RP>(i)) + 8 * (jt & 1);
+                    lchar* at = sP + (la_fresh(ap) ^ (64 * (jt >> 1))) + 16 * it * RP + 8 * (jt & 1);
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
                         const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
@@ -647,39 +672,49 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                         }
                     }
                 } else {
-                    lds_st(sP + i * RP + 16 * ((j >> 2) ^ la_swz<T, RP>(i)), f32x4{v[0], v[1], v[2], v[3]});
+                    lds_st(sP + (la_fresh(ap) ^ (64 * jt)) + 16 * it * RP, f32x4{v[0], v[1], v[2], v[3]});
                 }
             }
             // what the state at the chunk's start gives the rows
 #pragma unroll
             for (int m = 0; m < DX / 32; ++m) {
-                LaFrag<T> x[4];
-#pragma unroll
-                for (int it = 0; it < 4; ++it) x[it] = la_row<T, true>(sX + 16 * it * RX, ax, m);
                 float s8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s8[e] = S[2 * m + (e >> 2)][e & 3];
+                for (int e = 0; e < 8; ++e) {
+                    s8[e] = S[2 * m + (e >> 2)][e & 3];
+                    S[2 * m + (e >> 2)][e & 3] *= decay;   // here: the split takes the old one's register
+                }
                 const LaTerms<T, NT> st = la_split<T, NT>(s8, neg);
 #pragma unroll
-                for (int term = TERMS - 1; term >= 0; --term)
+                for (int i0 = 0; i0 < 4; i0 += 2) {
+                    LaFrag<T> x[2];
 #pragma unroll
-                    for (int it = 0; it < 4; ++it)
-                        O[it] = la_mfma(la_term(st, term), x[it].v, m == 0 && term == TERMS - 1 ? zero : O[it]);
+                    for (int i = 0; i < 2; ++i) x[i] = la_row<T, true>(sX + 16 * (i0 + i) * RX, ax, m);
+#pragma unroll
+                    for (int term = TERMS - 1; term >= 0; --term)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            O[i0 + i] = la_mfma(la_term(st, term), x[i].v,
+                                                m == 0 && term == TERMS - 1 ? zero : O[i0 + i]);
+                }
                 __builtin_amdgcn_sched_barrier(0);   // no more of x in registers at once
             }
+            const lchar* eu = gt + 512 + 4 * (la_fresh(tid) & 15);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                const float e = lds_ld<float>(gt + 512 + 4 * (16 * it + l15));
+                const float e = lds_ld<float>(eu + 64 * it);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) O[it][j] *= e;
             }
         }
-        const float decay = lds_ld<float>(gt + 1024);
+        if constexpr (STATE) {
 #pragma unroll
-        for (int t = 0; t < TX; ++t)
+            for (int t = 0; t < TX; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[t][j] *= decay;
-        if constexpr (!STATE) lds_barrier();   // the products are in LDS
+                for (int j = 0; j < 4; ++j) S[t][j] *= decay;
+        } else {
+            lds_barrier();   // the products are in LDS
+        }
         if constexpr (!STATE)
             if (dots && n) store_dots(n - 1);
         LaColAt<T> ay;
@@ -691,11 +726,12 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         for (int ks = 0; ks < 2; ++ks) {
             const LaFrag<T> z = la_col<T, RZ>(sZ, az, ks, 0);
             if constexpr (!STATE) {
+                const int pr = la_fresh(ap);
 #pragma unroll
                 for (int it = 2 * ks; it < 4; ++it) {
 #pragma unroll
                     for (int term = TERMS - 1; term >= 0; --term)
-                        O[it] = la_mfma(z.v, la_row<T, true>(sP + term * 64 * RP + 16 * it * RP, ap, ks).v, O[it]);
+                        O[it] = la_mfma(z.v, la_row<T, true>(sP + term * 64 * RP + 16 * it * RP, pr, ks).v, O[it]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -741,17 +777,18 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     float* end = nullptr;
     if constexpr (STATE) {
         end = ps.seg + ((size_t)seq * a.nseg + sg) * elems;
-        if (gate_wave && lane == 0)
+        if (gate_wave && (la_fresh(tid) & 63) == 0)
             ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
     } else if (ps.end && sg == (rev ? 0 : a.nseg - 1)) {
         end = ps.end + seq * elems;
     }
-    if (end && zc < Dz) {
+    const int l_end = la_fresh(tid) & 63, g_end = l_end >> 4, zc_end = zc0 + (l_end & 15);
+    if (end && zc_end < Dz) {
         const bool tr = ps.tr != 0;
-        float* e = tr ? end + (size_t)zc * Dx + 4 * g : end + (size_t)(4 * g) * Dz + zc;
+        float* e = tr ? end + (size_t)zc_end * Dx + 4 * g_end : end + (size_t)(4 * g_end) * Dz + zc_end;
 #pragma unroll
         for (int t = 0; t < TX; ++t) {
-            if (16 * t + 4 * g >= Dx) continue;
+            if (16 * t + 4 * g_end >= Dx) continue;
             if (tr) {
                 *reinterpret_cast<f32x4*>(e + 16 * t) = S[t];
             } else {
