@@ -161,10 +161,11 @@ __device__ __forceinline__ auto& la_term(const LaTerms<T, NT>& a, int n) {
 template <typename T, int NT>
 constexpr int la_terms() { return sizeof(T) == 4 ? 1 : NT; }
 
-// LDS addresses.  A lane's address in a tile is a value of its own, the tile's
-// step in the contraction flips bits of it (the swizzle is a flip too), and
-// whole 16-row steps add to it: one register and at most one instruction per
-// read.
+// LDS addresses.  A lane's address in a tile is a value of its own (the tile's
+// start, a multiple of its row bytes, included), the tile's step in the
+// contraction flips bits of it (the swizzle is a flip too), and whole 16-row
+// steps are the instruction's offset: one register and at most one instruction
+// per read.
 //
 // Rows, contraction values 32 m + 16 (e / 4) + 4 g + (e % 4), e < 8, of row
 // l15 (+ 16 per step).  QUADS: a bf16 tile that holds the eight 8-byte quads of
@@ -176,16 +177,21 @@ __device__ __forceinline__ int la_row_at(int l15, int g) {
     if constexpr (sizeof(T) == 2 && !QUADS) return l15 * RB + 16 * ((g >> 1) ^ s) + 8 * (g & 1);
     else return l15 * RB + 16 * (g ^ s);
 }
+__device__ __forceinline__ lchar* la_lds(int at) { return (lchar*)(uintptr_t)(unsigned)at; }
+__device__ __forceinline__ int la_lds_at(const lchar* p) { return (int)(uintptr_t)p; }
+
 template <typename T, bool QUADS>
-__device__ __forceinline__ LaFrag<T> la_row(const lchar* tile, int at, int m) {
+__device__ __forceinline__ LaFrag<T> la_row(int at, int m, int offset) {
     LaFrag<T> f;
     if constexpr (sizeof(T) == 2 && QUADS) {
-        f.v = lds_ld<uint4>(tile + (at ^ (64 * m)));
+        f.v = lds_ld<uint4>(la_lds(at ^ (64 * m)) + offset);
     } else if constexpr (sizeof(T) == 2) {
-        const uint2 a = lds_ld<uint2>(tile + (at ^ (64 * m))), b = lds_ld<uint2>(tile + (at ^ (64 * m + 32)));
+        const uint2 a = lds_ld<uint2>(la_lds(at ^ (64 * m)) + offset),
+                    b = lds_ld<uint2>(la_lds(at ^ (64 * m + 32)) + offset);
         f.v = make_uint4(a.x, a.y, b.x, b.y);
     } else {
-        const f32x4 a = lds_ld<f32x4>(tile + (at ^ (128 * m))), b = lds_ld<f32x4>(tile + (at ^ (128 * m + 64)));
+        const f32x4 a = lds_ld<f32x4>(la_lds(at ^ (128 * m)) + offset),
+                    b = lds_ld<f32x4>(la_lds(at ^ (128 * m + 64)) + offset);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f.v[j] = a[j];
@@ -215,16 +221,16 @@ struct LaColAt {
     int at[sizeof(T) == 2 ? 1 : 4];
 };
 template <typename T, int RB>
-__device__ __forceinline__ LaFrag<T> la_col(const lchar* tile, const LaColAt<T>& a, int m, int c) {
+__device__ __forceinline__ LaFrag<T> la_col(const LaColAt<T>& a, int m, int c) {
     LaFrag<T> f;
     if constexpr (sizeof(T) == 2) {
-        const lchar* p = tile + (a.at[0] ^ (32 * c)) + 32 * m * RB;
+        const lchar* p = la_lds(a.at[0] ^ (32 * c)) + 32 * m * RB;
         const uint2 x = lds_tr4(p), y = lds_tr4(p + 16 * RB);
         f.v = make_uint4(x.x, x.y, y.x, y.y);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f.v[e] = lds_ld<float>(tile + (a.at[e & 3] ^ (64 * c)) + (32 * m + 16 * (e >> 2)) * RB);
+            f.v[e] = lds_ld<float>(la_lds(a.at[e & 3] ^ (64 * c)) + (32 * m + 16 * (e >> 2)) * RB);
     }
     return f;
 }
@@ -304,23 +310,23 @@ template <typename T, int PPR, int NTHR, bool QUADS>
 struct LaSlots {
     static constexpr int STEP = NTHR / PPR, N = STEP >= 16 ? 1 : 16 / STEP;
     int at[N];
-    __device__ __forceinline__ explicit LaSlots(unsigned tid) {
+    __device__ __forceinline__ LaSlots(const lchar* tile, unsigned tid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) at[i] = la_slot<T, PPR, QUADS>(tid, i * STEP);
+        for (int i = 0; i < N; ++i) at[i] = la_lds_at(tile) + la_slot<T, PPR, QUADS>(tid, i * STEP);
     }
     __device__ __forceinline__ int operator[](int i) const {
         return at[i % N] + i / N * (N * STEP) * (PPR * 16);
     }
 };
 template <typename T, int N, int PPR, int NTHR, bool QUADS>
-__device__ __forceinline__ void la_stage(lchar* tile, const uint4 (&r)[N], const LaSlots<T, PPR, NTHR, QUADS>& slot) {
+__device__ __forceinline__ void la_stage(const uint4 (&r)[N], const LaSlots<T, PPR, NTHR, QUADS>& slot) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if constexpr (QUADS) {
-            lds_st(tile + slot[i], make_uint2(r[i].x, r[i].y));
-            lds_st(tile + (slot[i] ^ 16), make_uint2(r[i].z, r[i].w));
+            lds_st(la_lds(slot[i]), make_uint2(r[i].x, r[i].y));
+            lds_st(la_lds(slot[i] ^ 16), make_uint2(r[i].z, r[i].w));
         } else {
-            lds_st(tile + slot[i], r[i]);
+            lds_st(la_lds(slot[i]), r[i]);
         }
     }
 }
@@ -384,13 +390,13 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     constexpr int TX = DX / 16;                           // 16-row tiles of the state
     constexpr int TERMS = la_terms<T, NT>();
     constexpr bool BF = sizeof(T) == 2;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(512))) char smem[];
     lchar* const sY = (lchar*)smem;
     lchar* const sZ = sY + 64 * RX;
-    lchar* const sG = sZ + 64 * RZ;
-    lchar* const sX = sG + 2 * kLaGateBytes;              // not with STATE, nor what follows
-    lchar* const sP = sX + 64 * RX;
-    lchar* const sR = sP + TERMS * 64 * RP;               // [NW][64] partial dot products
+    lchar* const sX = sZ + 64 * RZ;                       // not with STATE
+    lchar* const sP = sX + 64 * RX;                       // nor this
+    lchar* const sG = STATE ? sX : sP + TERMS * 64 * RP;
+    lchar* const sR = sG + 2 * kLaGateBytes;              // [NW][64] partial dot products
 
     // Workgroups go to the eight XCDs in turn; consecutive work (heads that share
     // rows) stays on one of them.
@@ -462,8 +468,8 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
 
     uint4 rx[STATE ? 1 : NX], ry[NX], rz[NZ];
     auto chunk = [&](int n) { return rev ? c_hi - 1 - n : c_lo + n; };
-    const LaSlots<T, PX, NTHR, false> slot_y(tid);
-    const LaSlots<T, PZ, NTHR, false> slot_z(tid);
+    const LaSlots<T, PX, NTHR, false> slot_y(sY, tid);
+    const LaSlots<T, PZ, NTHR, false> slot_z(sZ, tid);
     auto fetch = [&](int n) {
         const int c = chunk(n), rows = L - 64 * c;
         const unsigned t = la_fresh(tid);
@@ -555,10 +561,10 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     };
     auto store_dots = [&](int n) {
         if (tid >= 64) return;
-        const int t = 64 * chunk(n) + ((int)tid ^ flip);
+        const int l = la_fresh(tid), t = 64 * chunk(n) + (l ^ flip);
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * tid);
+        for (int w = 0; w < NW; ++w) x += lds_ld<float>(sR + 256 * w + 4 * l);
         if (t < L) gd[t] = x;
     };
     // at the end of a chunk: bf16 rows into LDS
@@ -600,12 +606,12 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             }
         }
     };
-    const int ax0 = la_row_at<T, RX, true>(l15, g), ap = la_row_at<T, RP, true>(l15, g);
+    const int ax0 = la_lds_at(sX) + la_row_at<T, RX, true>(l15, g), ap = la_lds_at(sP) + la_row_at<T, RP, true>(l15, g);
     LaColAt<T> ay0, az;
 #pragma unroll
     for (int j = 0; j < (BF ? 1 : 4); ++j) {
-        ay0.at[j] = la_col_at<T, RX>(l15, g, j);
-        az.at[j] = la_col_at<T, RZ>(l15, g, j) ^ (2 * (int)sizeof(T) * 8 * wave);
+        ay0.at[j] = la_lds_at(sY) + la_col_at<T, RX>(l15, g, j);
+        az.at[j] = la_lds_at(sZ) + (la_col_at<T, RZ>(l15, g, j) ^ (2 * (int)sizeof(T) * 8 * wave));
     }
     fetch(0);
     if (gate_wave) decays(0, log_alpha(0));
@@ -618,10 +624,10 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         Pieces ro;
         if constexpr (!STATE && BF)
 #pragma unroll
-            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
-        if constexpr (!STATE) la_stage(sX, rx, LaSlots<T, PX, NTHR, BF>(la_fresh(tid)));
-        la_stage(sY, ry, slot_y);
-        la_stage(sZ, rz, slot_z);
+            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(la_lds(slot_z[i]));
+        if constexpr (!STATE) la_stage(rx, LaSlots<T, PX, NTHR, BF>(sX, la_fresh(tid)));
+        la_stage(ry, slot_y);
+        la_stage(rz, slot_z);
         lds_barrier();
         if constexpr (!STATE)
             if (n) {
@@ -642,11 +648,11 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             for (int n = wave; n < 10; n += NW) {
                 const int k = 2 * la_fresh_s(n), it = (0xFFA94 >> k) & 3, jt = (0xE4910 >> k) & 3;   // row by row
                 const int l = (la_fresh(tid) & 63), g = l >> 4, l15 = l & 15;
-                const int yrow = la_fresh(la_row_at<T, RX, false>(l15, g) + 16 * jt * RX), xrow = la_fresh(ax + 16 * it * RX);
+                const int yrow = la_fresh(la_lds_at(sY) + la_row_at<T, RX, false>(l15, g) + 16 * jt * RX), xrow = la_fresh(ax + 16 * it * RX);
                 f32x4 P = zero;
 #pragma unroll
                 for (int m = 0; m < DX / 32; ++m)
-                    P = la_mfma(la_row<T, false>(sY, yrow, m).v, la_row<T, true>(sX, xrow, m).v, P);
+                    P = la_mfma(la_row<T, false>(yrow, m, 0).v, la_row<T, true>(xrow, m, 0).v, P);
                 const lchar* ti = gt + la_fresh(4 * l15) + 64 * it;
                 const lchar* tj = gt + la_fresh(16 * g) + 64 * jt;
                 const float ui = lds_ld<float>(ti), wi = lds_ld<float>(ti + 256);
@@ -661,7 +667,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 }
                 if constexpr (BF) {
                     // la_row's order of quads: 8-byte quad 4 (jt % 2) + g of 32 values
-                    lchar* at = sP + (la_fresh(ap) ^ (64 * (jt >> 1))) + 16 * it * RP + 8 * (jt & 1);
+                    lchar* at = la_lds(la_fresh(ap) ^ (64 * (jt >> 1))) + 16 * it * RP + 8 * (jt & 1);
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) {
                         const unsigned lo = la_pack(v[0], v[1]), hi = la_pack(v[2], v[3]);
@@ -672,7 +678,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                         }
                     }
                 } else {
-                    lds_st(sP + (la_fresh(ap) ^ (64 * jt)) + 16 * it * RP, f32x4{v[0], v[1], v[2], v[3]});
+                    lds_st(la_lds(la_fresh(ap) ^ (64 * jt)) + 16 * it * RP, f32x4{v[0], v[1], v[2], v[3]});
                 }
             }
             // what the state at the chunk's start gives the rows
@@ -689,7 +695,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
                 for (int i0 = 0; i0 < 4; i0 += 2) {
                     LaFrag<T> x[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) x[i] = la_row<T, true>(sX + 16 * (i0 + i) * RX, ax, m);
+                    for (int i = 0; i < 2; ++i) x[i] = la_row<T, true>(ax, m, 16 * (i0 + i) * RX);
 #pragma unroll
                     for (int term = TERMS - 1; term >= 0; --term)
 #pragma unroll
@@ -724,14 +730,14 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         // rows 32 ks .. 32 ks + 31 of y and z: into the output's later rows, then into the state
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            const LaFrag<T> z = la_col<T, RZ>(sZ, az, ks, 0);
+            const LaFrag<T> z = la_col<T, RZ>(az, ks, 0);
             if constexpr (!STATE) {
                 const int pr = la_fresh(ap);
 #pragma unroll
                 for (int it = 2 * ks; it < 4; ++it) {
 #pragma unroll
                     for (int term = TERMS - 1; term >= 0; --term)
-                        O[it] = la_mfma(z.v, la_row<T, true>(sP + term * 64 * RP + 16 * it * RP, pr, ks).v, O[it]);
+                        O[it] = la_mfma(z.v, la_row<T, true>(pr, ks, term * 64 * RP + 16 * it * RP).v, O[it]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -746,7 +752,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
             for (int t0 = 0; t0 < TX; t0 += 2) {
                 LaFrag<T> y[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) y[t] = la_col<T, RX>(sY, ay, ks, t0 + t);
+                for (int t = 0; t < 2; ++t) y[t] = la_col<T, RX>(ay, ks, t0 + t);
 #pragma unroll
                 for (int term = la_terms<T, 3>() - 1; term >= 0; --term)
 #pragma unroll
@@ -765,7 +771,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         Pieces ro;
         if constexpr (BF)
 #pragma unroll
-            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(sZ + slot_z[i]);
+            for (int i = 0; i < NZ; ++i) ro[i] = lds_ld<uint4>(la_lds(slot_z[i]));
         store(nc - 1, ro);
         if (dots) {
             dot_rows();
