@@ -86,6 +86,21 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
         S = a.S_end + (size_t)seq * a.elems;
         D = a.dS_end + (size_t)seq * a.elems;
     }
+    // 1024 tokens at a time, from the segment's last, four in a row per thread;
+    // the first ones are loaded along with the states
+    constexpr int kPer = 4, kSweep = 256 * kPer;
+    const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
+    float fq[kPer], fk[kPer];
+    auto load = [&](int hi) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int t = hi - 1 - kPer * tid - e;
+            const size_t at = (size_t)seq * a.L + t;
+            fq[e] = t >= t0 ? a.dq_dots[at] : 0.f;
+            fk[e] = t >= t0 ? a.dk_dots[at] : 0.f;
+        }
+    };
+    load(t1);
     double acc = 0.0;
     if (S)
 #pragma unroll 8
@@ -95,27 +110,27 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
             for (int j = 0; j < 4; ++j) acc += (double)s[j] * (double)d[j];
         }
     double carry = la_block_sum(acc, red);
-    // 256 tokens at a time, from the segment's last; a running sum within each
-    // wave, then over the waves
-    const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
     double total = 0.0;
-    for (int hi = t1; hi > t0; hi -= 256) {
-        const int t = hi - 1 - tid;
-        double d = 0.0;
-        if (t >= t0) {
-            const size_t at = (size_t)seq * a.L + t;
-            d = (double)a.dq_dots[at] - (double)a.dk_dots[at];
-        }
-        d = la_scan(d);
+    for (int hi = t1; hi > t0; hi -= kSweep) {
+        // running sums of the thread's tokens, the wave's threads, the waves
+        double run[kPer], d = 0.0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) run[e] = d += (double)fq[e] - (double)fk[e];
+        const double sum = la_scan(d);
+        if (lane == 63) red[wave] = sum;
         __syncthreads();
-        if (lane == 63) red[wave] = d;
-        __syncthreads();
-        double v = carry + d;
+        double before = carry + (sum - d);
 #pragma unroll
         for (int w = 0; w < 3; ++w)
-            if (w < wave) v += red[w];
+            if (w < wave) before += red[w];
         carry += (red[0] + red[1]) + (red[2] + red[3]);
-        if (t >= t0) {
+        __syncthreads();
+        load(hi - kSweep);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int t = hi - 1 - kPer * tid - e;
+            if (t < t0) continue;
+            const double v = before + run[e];
             if (!a.part) a.dla[(size_t)seq * a.L + t] = a.la[(size_t)seq * a.L + t] < kLaZero ? 0.f : (float)v;
             total += v;
         }
