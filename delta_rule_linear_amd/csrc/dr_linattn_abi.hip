@@ -119,7 +119,8 @@ int waves_of(int D) { return D <= 32 ? 2 : D <= 64 ? 4 : 8; }
 // Segments: as many as make two workgroups for each of 256 compute units, of
 // four chunks at least; or, where that leaves compute units without work, one
 // workgroup for each, of two chunks at least.  A segment costs its state (64 KB
-// at 128 x 128) written, joined and read; a chunk takes a workgroup about 4 us.
+// at 128 x 128) written, joined and read; a chunk takes a workgroup about 4 us
+// where it has a compute unit to itself (3.1 at 64 x 64).
 // bf16, 128 x 128, 16 heads: 512 tokens 36.6 us in two segments, 27.1 in four;
 // 1024 tokens 39.3 in four, 31.5 in eight; 4096 tokens 47.6 in 16, 55.8 in 32;
 // 256 tokens 21.6 in one, 24.9 in two (the two more launches).
@@ -549,16 +550,19 @@ dr_status check_ln_desc(const dr_layernorm_desc* d) {
     return DR_OK;
 }
 
-// Groups of rows with one weight, and the workgroups of each.  Forward: up to
-// eight workgroups per compute unit in all.  Backward: every workgroup writes two
-// rows of sums, so four, or two where a row is wide (of 8191 x 2048 bf16: 1024
-// workgroups 112 us with a slower joining, 512 measured below).
+// Groups of rows with one weight, and the workgroups of each: no more than stay
+// on the chip, so that all walk their rows with the next ones in flight.
+// Forward: four per compute unit, two where a lane holds more than eight values
+// (of 8191 x 2048 bf16 4: 21.9 us, 8: 25.5, 2: 24.1; of 4096 x 8192 2: 34.3, 4:
+// 42.4).  Backward: a workgroup also writes two rows of sums, which a second
+// launch joins: four, or two for wider rows (of 65536 x 512 4: 39.8 us, 2: 42.1;
+// of 8191 x 2048 2: 30.1, 4: 32.5).
 void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
     a.groups = d.per_head ? d.H : 1;
     a.rows = d.per_head ? (unsigned)d.B * d.L : (unsigned)d.B * d.H * d.L;
     const unsigned pass = (unsigned)dr::ln_pass_rows(d.D);
     const unsigned passes = (a.rows + pass - 1) / pass;
-    const unsigned most = !bwd ? 2048 : d.D <= 512 ? 1024 : 512;
+    const unsigned most = d.D <= (bwd ? 512 : 2048) ? 1024 : 512;
     const unsigned want = std::max(1u, (most + a.groups - 1) / a.groups);
     a.blocks = std::max(1u, std::min(want, passes));
 }

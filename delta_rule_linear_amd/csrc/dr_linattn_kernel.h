@@ -23,14 +23,20 @@
 //
 // Why 16 columns and eight waves: the registers stay at 128, four waves per SIMD
 // in two workgroups per CU.  32 columns per wave on the 32x32 ops read LDS half
-// as often, but with two waves per SIMD this kernel took 187 us for the forward
-// at B2 H16 L16384 d128 bf16, against 163 with four at the same stage.  Now it
-// takes 142 us for 570 MB (4.0 TB/s; a large copy reaches 5.2), the state pass 67
-// us for 300 MB.  With its products left out it takes 110 us, so memory bounds it
-// first; then the VALU (480 instructions per wave and chunk, a third of them
-// splitting fp32 values into bf16 terms) together with the issue of 97 matrix
-// ops.  The backward's three passes (three terms, row dot products) are bound by
-// those: 540-630 us for 1.97 GB.
+// as often, but with two waves per SIMD the kernel took 187 us for the forward at
+// B2 H16 L16384 d128 bf16, against 163 with four at the same stage.
+//
+// What bounds it, at that size: the forward's main pass takes 138 us for 570 MB
+// (4.1 TB/s; a large copy reaches 5.2) and the state pass 66 us for 300 MB.  The
+// main pass without its products took 110 us, so memory comes first, then the
+// issue of vector and matrix instructions, which overlap only in part: 420 and 97
+// per wave and chunk, a third of the former splitting fp32 values into bf16 terms.
+// The backward's three passes (three terms, row dot products; 550 and 119) are
+// bound by that issue: 470 us for 1.65 GB, and 530-640 where calls follow each
+// other without a pause and the clock falls.  Where few workgroups run, a chunk
+// is a chain of latencies: 3.1 us at d64 in a workgroup of four waves alone.
+// Tried there without gain: two blocks of the products side by side, LDS reads
+// ahead across steps, the decays made earlier in the chunk.
 //
 // Precision.  bf16 inputs are operands as they are.  fp32 quantities that meet
 // them are split into bf16 terms: the decayed z of the state update into three

@@ -459,9 +459,9 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  * Strides.  q, k, v, o (and dO) are rows of contiguous channels; the strides
  * between batches, heads and tokens are free (elements, not negative, whole
  * multiples of 16 bytes; 0 repeats a row; ignored where the dimension is 1;
- * tokens at most 2^23 elements apart), so that [B][L][H][D] projections, or slices of a fused one, are passed as they
- * are.  An output's rows must not overlap each other.  log_alpha and the states
- * are dense.
+ * tokens at most 2^23 elements apart), so that [B][L][H][D] projections, or
+ * slices of a fused one, are passed as they are.  An output's rows must not
+ * overlap each other.  log_alpha and the states are dense.
  *
  * Numerics.  Accumulations and the state are fp32; running sums of log_alpha
  * are fp64.  bf16 inputs are matrix-core operands as they are; the state and
@@ -525,8 +525,8 @@ dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void
 
 /* Bytes of device workspace dr_linear_attn_bwd needs for `d` (0 if d is invalid
  * or there is no work): the segments' states twice; with a decay one state per
- * sequence and two floats per token; with shared heads
- * fp32 gradients of q and k for every state head. */
+ * sequence and two floats per token; with shared heads fp32 gradients of q and k
+ * for every state head. */
 size_t dr_linear_attn_bwd_workspace_bytes(const dr_linattn_desc* d);
 
 /*
@@ -622,8 +622,8 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
 /*
  * Per-kernel timing, for benchmarks and profiling (not part of the method).
  * Between dr_profile_begin and dr_profile_end every chunked-forward, backward,
- * decode, linear-attention and layer-norm call launches each of its kernels with a start and a stop event
- * of its own, set from the kernel dispatch's timestamps (no marker packets
+ * decode, linear-attention and layer-norm call launches each of its kernels with
+ * a start and a stop event of its own, set from the kernel dispatch's timestamps (no marker packets
  * between the kernels); dr_profile_end waits for those events and reports the
  * summed kernel durations.  Calls made while profiling must come from one
  * host thread.  dr_profile_begin discards any earlier unreported records.  The
