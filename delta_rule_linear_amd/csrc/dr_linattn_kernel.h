@@ -380,10 +380,12 @@ constexpr int la_lds_bytes() {
 }
 
 // Waves per SIMD that the registers are held to: four for bf16 workgroups of
-// eight waves, two of which share a CU; else two, all that the tiles in LDS
-// leave room for.
+// eight waves, two of which share a CU; one for fp32 workgroups of two waves,
+// whose tiles (88 KB at d_k 128) leave a CU to one of them (H16 L4096, 128 x 32:
+// 76 us, with two and 67 registers spilled 94); else two, all that the tiles in
+// LDS leave room for.
 template <typename T, int NW>
-constexpr int la_waves() { return sizeof(T) == 2 && NW == 8 ? 4 : 2; }
+constexpr int la_waves() { return sizeof(T) == 2 ? (NW == 8 ? 4 : 2) : NW == 2 ? 1 : 2; }
 
 template <typename T, int DX, int NW, int NT, bool STATE>
 __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs a) {
