@@ -27,7 +27,7 @@
 // B2 H16 L16384 d128 bf16, against 163 with four at the same stage.
 //
 // What bounds it, at that size: the forward's main pass takes 138 us for 570 MB
-// (4.1 TB/s; a large copy reaches 5.2) and the state pass 66 us for 300 MB.  The
+// (4.1 TB/s; a large copy reaches 5.2) and the state pass 66 us for 285 MB.  The
 // main pass without its products took 110 us, so memory comes first, then the
 // issue of vector and matrix instructions, which overlap only in part: 420 and 97
 // per wave and chunk, a third of the former splitting fp32 values into bf16 terms.
