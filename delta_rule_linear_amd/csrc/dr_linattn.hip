@@ -79,7 +79,7 @@ __device__ __forceinline__ double la_block_sum(double x, double* red) {
 }
 
 __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
-    __shared__ double red[4];
+    __shared__ double red[4], waves[4];   // of their own: no barrier lies between their uses
     const int nseq = a.B * a.H;
     const int seq = blockIdx.x % nseq, sg = blockIdx.x / nseq;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
     // 1024 tokens at a time, from the segment's last, four in a row per thread;
     // the first ones are loaded along with the states
     constexpr int kPer = 4, kSweep = 256 * kPer;
-    const int t0 = sg * a.cps * 64, t1 = min(a.L, t0 + a.cps * 64);
+    const int t0 = sg * a.cps * 64, t1 = (int)min((int64_t)a.L, (int64_t)t0 + a.cps * 64);
     float fq[kPer], fk[kPer];
     auto load = [&](int hi) {
 #pragma unroll
@@ -122,13 +122,13 @@ __global__ __launch_bounds__(256) void la_gate_kernel(LaGateArgs a) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) run[e] = d += (double)fq[e] - (double)fk[e];
         const double sum = la_scan(d);
-        if (lane == 63) red[wave] = sum;
+        if (lane == 63) waves[wave] = sum;
         __syncthreads();
         double before = carry + (sum - d);
 #pragma unroll
         for (int w = 0; w < 3; ++w)
-            if (w < wave) before += red[w];
-        carry += (red[0] + red[1]) + (red[2] + red[3]);
+            if (w < wave) before += waves[w];
+        carry += (waves[0] + waves[1]) + (waves[2] + waves[3]);
         __syncthreads();
         load(hi - kSweep);
 #pragma unroll
