@@ -43,10 +43,10 @@ struct LnShape {
 LnShape ln_shape(int D);
 // Rows that a workgroup takes in one pass.
 int ln_pass_rows(int D);
-// vec: rows are read and written in 16-byte pieces (D and every stride a
-// multiple of 8 elements)
-hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st);
-hipError_t launch_ln_bwd(const LnArgs& a, bool vec, int slot, hipStream_t st);
+// width: values read or written at once, 8, 2 or 1 (D and every stride a
+// multiple of it)
+hipError_t launch_ln_fwd(const LnArgs& a, int width, int slot, hipStream_t st);
+hipError_t launch_ln_bwd(const LnArgs& a, int width, int slot, hipStream_t st);
 hipError_t launch_ln_zero(float* p, size_t n, int slot, hipStream_t st);
 
 }  // namespace dr

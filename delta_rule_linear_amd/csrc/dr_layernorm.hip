@@ -26,9 +26,6 @@
 
 namespace dr {
 
-typedef __bf16 lnbf8 __attribute__((ext_vector_type(8)));
-typedef float lnf8 __attribute__((ext_vector_type(8)));
-
 constexpr int kLnThreads = 256;
 
 LnShape ln_shape(int D) {
@@ -46,82 +43,89 @@ LnShape ln_shape(int D) {
     return {256, 8};
 }
 
-// Column of value e of vector v of a lane.  VEC: eight consecutive values;
-// otherwise consecutive lanes take consecutive values.
-template <bool VEC, int LPR>
+// Rows are read and written W values at a time: 8 where every row starts at a
+// multiple of 8 values and D is one, else 2 or 1.  Columns behind D are clamped
+// when loading and left out when used, so that the loads of a row are all in
+// flight at once: with a branch and a conversion for each, the backward of 286884
+// x 100 bf16 took 172 us and that of 65536 x 501 232; now 42 (W = 2) and 58 (W =
+// 1).  Column of value e of vector v of a lane: consecutive lanes take
+// consecutive groups of W.
+template <int W, int LPR>
 __device__ __forceinline__ int ln_col(int lane, int v, int e) {
-    return VEC ? 8 * (v * LPR + lane) + e : (8 * v + e) * LPR + lane;
+    return ((8 * v + e) / W * LPR + lane) * W + e % W;
 }
 
-// A lane's part of a row as loaded: bf16 or fp32 bits (VEC), or fp32 values.
-template <bool VEC, bool F32, int VPT>
+// A lane's part of a row as loaded: 8 / W groups of W values, bf16 or fp32 bits
+// (nothing waits for them until they are used).
+template <int W, bool F32, int VPT>
 struct LnRaw {
-    uint4 v[VPT][F32 || !VEC ? 2 : 1];
+    static constexpr int WORDS = F32 ? 8 : W == 1 ? 8 : 4;
+    unsigned v[VPT][WORDS];
 };
 
-template <bool VEC, bool F32, int LPR, int VPT>
-__device__ __forceinline__ void ln_fetch(const void* base, int64_t at, int D, int lane, LnRaw<VEC, F32, VPT>& r) {
-    constexpr int W = F32 || !VEC ? 2 : 1;
+template <int W, bool F32, int LPR, int VPT>
+__device__ __forceinline__ void ln_fetch(const void* base, int64_t at, int D, int lane, LnRaw<W, F32, VPT>& r) {
+    const char* row = (const char*)base + at * (F32 ? 4 : 2);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        if constexpr (VEC) {
-            const int c = ln_col<VEC, LPR>(lane, v, 0);
+        if constexpr (W == 8) {
+            const int c = ln_col<W, LPR>(lane, v, 0);
+            uint4* to = reinterpret_cast<uint4*>(r.v[v]);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                r.v[v][i] = make_uint4(0u, 0u, 0u, 0u);
-                if (c < D) r.v[v][i] = reinterpret_cast<const uint4*>((const char*)base + (at + c) * (F32 ? 4 : 2))[i];
+            for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+                to[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < D) to[i] = reinterpret_cast<const uint4*>(row + c * (F32 ? 4 : 2))[i];
             }
         } else {
-            float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = ln_col<VEC, LPR>(lane, v, e);
-                x[e] = 0.f;
-                if (c < D) x[e] = load1<F32>(base, (size_t)(at + c));
+            for (int e = 0; e < 8; e += W) {
+                const int c = min(ln_col<W, LPR>(lane, v, e), D - W);   // ln_values leaves out what is behind D
+                if constexpr (F32 && W == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(row + 4 * c);
+                    r.v[v][e] = x.x;
+                    r.v[v][e + 1] = x.y;
+                } else if constexpr (F32) {
+                    r.v[v][e] = *reinterpret_cast<const unsigned*>(row + 4 * c);
+                } else if constexpr (W == 2) {
+                    r.v[v][e / 2] = *reinterpret_cast<const unsigned*>(row + 2 * c);
+                } else {
+                    r.v[v][e] = *reinterpret_cast<const unsigned short*>(row + 2 * c);
+                }
             }
-            r.v[v][0] = __builtin_bit_cast(uint4, f32x4{x[0], x[1], x[2], x[3]});
-            r.v[v][1] = __builtin_bit_cast(uint4, f32x4{x[4], x[5], x[6], x[7]});
         }
     }
 }
-template <bool VEC, bool F32, int VPT>
-__device__ __forceinline__ void ln_values(const LnRaw<VEC, F32, VPT>& r, float (&x)[VPT][8]) {
+template <int W, bool F32, int LPR, int VPT>
+__device__ __forceinline__ void ln_values(const LnRaw<W, F32, VPT>& r, int D, int lane, float (&x)[VPT][8]) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        if constexpr (VEC && !F32) {
-            unpack_bf16x8(r.v[v][0], x[v]);
-        } else {
-            const f32x4 a = __builtin_bit_cast(f32x4, r.v[v][0]), b = __builtin_bit_cast(f32x4, r.v[v][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[v][e] = a[e];
-                x[v][4 + e] = b[e];
-            }
+        for (int e = 0; e < 8; ++e) {
+            unsigned u;
+            if constexpr (F32) u = r.v[v][e];
+            else if constexpr (W == 1) u = r.v[v][e] << 16;
+            else u = e % 2 ? r.v[v][e / 2] & 0xffff0000u : r.v[v][e / 2] << 16;
+            x[v][e] = W == 8 || ln_col<W, LPR>(lane, v, e) < D ? __uint_as_float(u) : 0.f;
         }
     }
 }
 
-template <bool VEC, int LPR, int VPT>
+template <int W, int LPR, int VPT>
 __device__ __forceinline__ void ln_store(void* to, bool f32, int64_t at, int D, int lane, const float (&x)[VPT][8]) {
+    typedef float lnfw __attribute__((ext_vector_type(W)));
+    typedef __bf16 lnbw __attribute__((ext_vector_type(W)));
     char* base = (char*)to;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        if constexpr (VEC) {
-            const int c = ln_col<VEC, LPR>(lane, v, 0);
+#pragma unroll
+        for (int e0 = 0; e0 < 8; e0 += W) {
+            const int c = ln_col<W, LPR>(lane, v, e0);
             if (c >= D) continue;
-            lnf8 f;
+            lnfw f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = x[v][e];
-            if (f32) *reinterpret_cast<lnf8*>(base + (at + c) * 4) = f;
-            else *reinterpret_cast<lnbf8*>(base + (at + c) * 2) = __builtin_convertvector(f, lnbf8);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = ln_col<VEC, LPR>(lane, v, e);
-                if (c >= D) continue;
-                if (f32) *reinterpret_cast<float*>(base + (at + c) * 4) = x[v][e];
-                else *reinterpret_cast<__bf16*>(base + (at + c) * 2) = (__bf16)x[v][e];
-            }
+            for (int e = 0; e < W; ++e) f[e] = x[v][e0 + e];
+            if (f32) *reinterpret_cast<lnfw*>(base + (at + c) * 4) = f;
+            else *reinterpret_cast<lnbw*>(base + (at + c) * 2) = __builtin_convertvector(f, lnbw);
         }
     }
 }
@@ -192,11 +196,15 @@ __device__ __forceinline__ int64_t ln_at(const LnRows& s, unsigned b, unsigned h
 }
 
 // Rows of a lane group's pass.  The next pass's rows are loaded while one is
-// computed, so that memory is never waited for by every workgroup at once.
+// computed, so that memory is never waited for by every workgroup at once; not
+// where a row's 64 values per lane leave no registers for that (backward of 2048
+// x 16384 bf16: 110 us, with it 166).
 template <int VPT>
 constexpr int ln_rows() { return VPT == 1 ? 2 : 1; }
+template <int VPT>
+constexpr bool ln_ahead() { return VPT < 8; }
 
-template <bool VEC, bool FX, int LPR, int VPT>
+template <int W, bool FX, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
     constexpr int RPB = kLnThreads / LPR, RU = ln_rows<VPT>();
     __shared__ float2 red[8];
@@ -210,23 +218,24 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = ln_col<VEC, LPR>(lane, v, e);
+            const int c = ln_col<W, LPR>(lane, v, e);
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             bs[v][e] = c < a.D && a.bias ? a.bias[(size_t)g * a.D + c] : 0.f;
         }
     const float D = (float)a.D, inv = 1.f / D;
-    LnRaw<VEC, FX, VPT> raw[RU], next[RU];
+    LnRaw<W, FX, VPT> raw[RU], next[RU];
     unsigned b[RU], h[RU], l[RU], nb[RU], nh[RU], nl[RU];
     auto fetch = [&](unsigned r0) {
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             ln_row(a, g, min(r0 + u * RPB + sub, a.rows - 1), nb[u], nh[u], nl[u]);
-            ln_fetch<VEC, FX, LPR, VPT>(a.x, ln_at(a.sx, nb[u], nh[u], nl[u]), a.D, lane, next[u]);
+            ln_fetch<W, FX, LPR, VPT>(a.x, ln_at(a.sx, nb[u], nh[u], nl[u]), a.D, lane, next[u]);
         }
     };
     const unsigned step = a.blocks * (RPB * RU);
-    fetch(blk * (RPB * RU));
+    if (ln_ahead<VPT>()) fetch(blk * (RPB * RU));
     for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += step) {
+        if (!ln_ahead<VPT>()) fetch(r0);
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             raw[u] = next[u];
@@ -234,11 +243,11 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             h[u] = nh[u];
             l[u] = nl[u];
         }
-        if (r0 + step < a.rows) fetch(r0 + step);
+        if (ln_ahead<VPT>() && r0 + step < a.rows) fetch(r0 + step);
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             float x[VPT][8], s = 0.f;
-            ln_values(raw[u], x);
+            ln_values<W, FX, LPR>(raw[u], a.D, lane, x);
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -249,7 +258,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[v][e] = ln_col<VEC, LPR>(lane, v, e) < a.D ? x[v][e] - mean : 0.f;
+                    x[v][e] = ln_col<W, LPR>(lane, v, e) < a.D ? x[v][e] - mean : 0.f;
                     s += x[v][e] * x[v][e];
                 }
             const float rstd = ln_rsqrt(ln_div(ln_sum<LPR>(s, red, turn), D, inv) + a.eps);
@@ -258,7 +267,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * rstd * w[v][e] + bs[v][e];
-            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, ln_at(a.sy, b[u], h[u], l[u]), a.D, lane, x);
+            ln_store<W, LPR, VPT>(a.y, a.y_f32, ln_at(a.sy, b[u], h[u], l[u]), a.D, lane, x);
             if (lane == 0) {
                 const size_t at = ((size_t)b[u] * a.H + h[u]) * a.L + l[u];
                 if (a.mean_out) a.mean_out[at] = mean;
@@ -268,7 +277,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
     }
 }
 
-template <bool VEC, bool FX, bool FDY, int LPR, int VPT>
+template <int W, bool FX, bool FDY, int LPR, int VPT>
 __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
     constexpr int RPB = kLnThreads / LPR, RU = ln_rows<VPT>();
     constexpr int NCOL = 8 * VPT * LPR;   // columns that the lanes of a row hold
@@ -283,13 +292,13 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = ln_col<VEC, LPR>(lane, v, e);
+            const int c = ln_col<W, LPR>(lane, v, e);
             w[v][e] = c < a.D ? (a.w ? a.w[(size_t)g * a.D + c] : 1.f) : 0.f;
             dw[v][e] = db[v][e] = 0.f;
         }
     const float D = (float)a.D, inv = 1.f / D;
-    LnRaw<VEC, FX, VPT> rx[RU], nx[RU];
-    LnRaw<VEC, FDY, VPT> ry[RU], ny[RU];
+    LnRaw<W, FX, VPT> rx[RU], nx[RU];
+    LnRaw<W, FDY, VPT> ry[RU], ny[RU];
     float mean[RU], rstd[RU], nm[RU], nr[RU];
     int64_t at[RU], nat[RU];
     auto fetch = [&](unsigned r0) {
@@ -301,13 +310,14 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             nm[u] = a.mean[stat];
             nr[u] = a.rstd[stat];
             nat[u] = ln_at(a.sy, b, h, l);
-            ln_fetch<VEC, FX, LPR, VPT>(a.x, ln_at(a.sx, b, h, l), a.D, lane, nx[u]);
-            ln_fetch<VEC, FDY, LPR, VPT>(a.dy, ln_at(a.sdy, b, h, l), a.D, lane, ny[u]);
+            ln_fetch<W, FX, LPR, VPT>(a.x, ln_at(a.sx, b, h, l), a.D, lane, nx[u]);
+            ln_fetch<W, FDY, LPR, VPT>(a.dy, ln_at(a.sdy, b, h, l), a.D, lane, ny[u]);
         }
     };
     const unsigned step = a.blocks * (RPB * RU);
-    fetch(blk * (RPB * RU));
+    if (ln_ahead<VPT>()) fetch(blk * (RPB * RU));
     for (unsigned r0 = blk * (RPB * RU); r0 < a.rows; r0 += step) {
+        if (!ln_ahead<VPT>()) fetch(r0);
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             rx[u] = nx[u];
@@ -316,13 +326,13 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             rstd[u] = nr[u];
             at[u] = nat[u];
         }
-        if (r0 + step < a.rows) fetch(r0 + step);
+        if (ln_ahead<VPT>() && r0 + step < a.rows) fetch(r0 + step);
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             const bool ok = r0 + u * RPB + sub < a.rows;
             float x[VPT][8], dy[VPT][8], s1 = 0.f, s2 = 0.f;
-            ln_values(rx[u], x);
-            ln_values(ry[u], dy);
+            ln_values<W, FX, LPR>(rx[u], a.D, lane, x);
+            ln_values<W, FDY, LPR>(ry[u], a.D, lane, dy);
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[v][e] = rstd[u] * (dy[v][e] - s1 - x[v][e] * s2);
-            ln_store<VEC, LPR, VPT>(a.y, a.y_f32, at[u], a.D, lane, x);
+            ln_store<W, LPR, VPT>(a.y, a.y_f32, at[u], a.D, lane, x);
         }
     }
     if (!a.part) return;
@@ -359,7 +369,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int c = ln_col<VEC, LPR>(lane, v, e);
+                    const int c = ln_col<W, LPR>(lane, v, e);
                     if (c < a.D) part[(size_t)k * a.D + c] = s[v][e];
                 }
         } else {
@@ -370,7 +380,7 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
                 for (int e = 0; e < 8; ++e) {
 #pragma unroll
                     for (int d = LPR; d < 64; d <<= 1) s[v][e] += __shfl_xor(s[v][e], d);
-                    if (LPR >= 64 || (threadIdx.x & 63) < LPR) acc[at][ln_col<VEC, LPR>(lane, v, e)] = s[v][e];
+                    if (LPR >= 64 || (threadIdx.x & 63) < LPR) acc[at][ln_col<W, LPR>(lane, v, e)] = s[v][e];
                 }
             __syncthreads();
             for (int c = threadIdx.x; c < a.D; c += kLnThreads) {
@@ -421,47 +431,54 @@ int ln_pass_rows(int D) {
     return kLnThreads / s.lanes * (s.vecs == 1 ? ln_rows<1>() : ln_rows<2>());
 }
 
-template <bool BWD, bool VEC, bool FX, bool FDY, int LPR, int VPT>
+template <bool BWD, int W, bool FX, bool FDY, int LPR, int VPT>
 static hipError_t ln_launch(const LnArgs& a, int slot, hipStream_t st) {
     const dim3 grid(a.groups * a.blocks);
-    if constexpr (BWD) return launch_k(slot, ln_bwd_kernel<VEC, FX, FDY, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
-    else return launch_k(slot, ln_fwd_kernel<VEC, FX, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
+    if constexpr (BWD) return launch_k(slot, ln_bwd_kernel<W, FX, FDY, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
+    else return launch_k(slot, ln_fwd_kernel<W, FX, LPR, VPT>, grid, dim3(kLnThreads), 0, st, a);
 }
 
-template <bool BWD, bool VEC, bool FX, bool FDY>
+template <bool BWD, int W, bool FX, bool FDY>
 static hipError_t ln_launch_shape(const LnArgs& a, int slot, hipStream_t st) {
     const LnShape s = ln_shape(a.D);
-    if (s.lanes == 8) return ln_launch<BWD, VEC, FX, FDY, 8, 1>(a, slot, st);
-    if (s.lanes == 16) return ln_launch<BWD, VEC, FX, FDY, 16, 1>(a, slot, st);
-    if (s.lanes == 32) return ln_launch<BWD, VEC, FX, FDY, 32, 1>(a, slot, st);
-    if (s.lanes == 64) return ln_launch<BWD, VEC, FX, FDY, 64, 1>(a, slot, st);
-    if (s.lanes == 128) return ln_launch<BWD, VEC, FX, FDY, 128, 1>(a, slot, st);
-    if (s.vecs == 1) return ln_launch<BWD, VEC, FX, FDY, 256, 1>(a, slot, st);
-    if (s.vecs == 2) return ln_launch<BWD, VEC, FX, FDY, 256, 2>(a, slot, st);
-    if (s.vecs == 4) return ln_launch<BWD, VEC, FX, FDY, 256, 4>(a, slot, st);
-    return ln_launch<BWD, VEC, FX, FDY, 256, 8>(a, slot, st);
+    if (s.lanes == 8) return ln_launch<BWD, W, FX, FDY, 8, 1>(a, slot, st);
+    if (s.lanes == 16) return ln_launch<BWD, W, FX, FDY, 16, 1>(a, slot, st);
+    if (s.lanes == 32) return ln_launch<BWD, W, FX, FDY, 32, 1>(a, slot, st);
+    if (s.lanes == 64) return ln_launch<BWD, W, FX, FDY, 64, 1>(a, slot, st);
+    if (s.lanes == 128) return ln_launch<BWD, W, FX, FDY, 128, 1>(a, slot, st);
+    if (s.vecs == 1) return ln_launch<BWD, W, FX, FDY, 256, 1>(a, slot, st);
+    if (s.vecs == 2) return ln_launch<BWD, W, FX, FDY, 256, 2>(a, slot, st);
+    if (s.vecs == 4) return ln_launch<BWD, W, FX, FDY, 256, 4>(a, slot, st);
+    return ln_launch<BWD, W, FX, FDY, 256, 8>(a, slot, st);
 }
 
-template <bool BWD, bool VEC>
+template <bool BWD, int W>
 static hipError_t ln_launch_types(const LnArgs& a, int slot, hipStream_t st) {
     if constexpr (BWD) {
         if (a.x_f32)
-            return a.dy_f32 ? ln_launch_shape<BWD, VEC, true, true>(a, slot, st)
-                            : ln_launch_shape<BWD, VEC, true, false>(a, slot, st);
-        return a.dy_f32 ? ln_launch_shape<BWD, VEC, false, true>(a, slot, st)
-                        : ln_launch_shape<BWD, VEC, false, false>(a, slot, st);
+            return a.dy_f32 ? ln_launch_shape<BWD, W, true, true>(a, slot, st)
+                            : ln_launch_shape<BWD, W, true, false>(a, slot, st);
+        return a.dy_f32 ? ln_launch_shape<BWD, W, false, true>(a, slot, st)
+                        : ln_launch_shape<BWD, W, false, false>(a, slot, st);
     } else {
-        return a.x_f32 ? ln_launch_shape<BWD, VEC, true, false>(a, slot, st)
-                       : ln_launch_shape<BWD, VEC, false, false>(a, slot, st);
+        return a.x_f32 ? ln_launch_shape<BWD, W, true, false>(a, slot, st)
+                       : ln_launch_shape<BWD, W, false, false>(a, slot, st);
     }
 }
 
-hipError_t launch_ln_fwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
-    return vec ? ln_launch_types<false, true>(a, slot, st) : ln_launch_types<false, false>(a, slot, st);
+template <bool BWD>
+static hipError_t ln_launch_width(const LnArgs& a, int width, int slot, hipStream_t st) {
+    if (width == 8) return ln_launch_types<BWD, 8>(a, slot, st);
+    if (width == 2) return ln_launch_types<BWD, 2>(a, slot, st);
+    return ln_launch_types<BWD, 1>(a, slot, st);
 }
 
-hipError_t launch_ln_bwd(const LnArgs& a, bool vec, int slot, hipStream_t st) {
-    hipError_t e = vec ? ln_launch_types<true, true>(a, slot, st) : ln_launch_types<true, false>(a, slot, st);
+hipError_t launch_ln_fwd(const LnArgs& a, int width, int slot, hipStream_t st) {
+    return ln_launch_width<false>(a, width, slot, st);
+}
+
+hipError_t launch_ln_bwd(const LnArgs& a, int width, int slot, hipStream_t st) {
+    hipError_t e = ln_launch_width<true>(a, width, slot, st);
     if (e == hipSuccess && a.part) {
         const unsigned per = (unsigned)(2 * a.D + 31) / 32;
         e = launch_k(slot, ln_bwd_sum_kernel, dim3(a.groups * per), dim3(1024), 0, st, a);

@@ -567,8 +567,16 @@ void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
     a.blocks = std::max(1u, std::min(want, passes));
 }
 
-bool ln_vec(const dr_layernorm_desc& d, const dr_strides& s) {
-    return (d.B <= 1 || s.b % 8 == 0) && (d.H <= 1 || s.h % 8 == 0) && (d.L <= 1 || s.t % 8 == 0);
+// Values of a row that can be read or written at once: 8 or 2 where that divides
+// D and every stride (the tensors start at multiples of 16 bytes), else 1.
+int ln_width(const dr_layernorm_desc& d, std::initializer_list<const dr_strides*> strides) {
+    long long all = d.D;
+    for (const dr_strides* s : strides) {
+        if (d.B > 1) all |= s->b;
+        if (d.H > 1) all |= s->h;
+        if (d.L > 1) all |= s->t;
+    }
+    return all % 8 == 0 ? 8 : all % 2 == 0 ? 2 : 1;
 }
 
 dr::LnRows ln_rows(const dr_layernorm_desc& d, const dr_strides& s) {
@@ -620,8 +628,8 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     a.x_f32 = d->x_dtype == DR_F32;
     a.y_f32 = d->y_dtype == DR_F32;
     ln_groups(*d, a, false);
-    const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->y);
-    return hip_status(dr::launch_ln_fwd(a, vec, dr::kProfLnFwd, (hipStream_t)stream), "layer norm launch");
+    return hip_status(dr::launch_ln_fwd(a, ln_width(*d, {&d->x, &d->y}), dr::kProfLnFwd, (hipStream_t)stream),
+                      "layer norm launch");
 }
 
 size_t dr_layernorm_bwd_workspace_bytes(const dr_layernorm_desc* d) {
@@ -682,8 +690,7 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     a.y_f32 = d->y_dtype == DR_F32;
     a.dy_f32 = d->dy_dtype == DR_F32;
     ln_groups(*d, a, true);
-    const bool vec = d->D % 8 == 0 && ln_vec(*d, d->x) && ln_vec(*d, d->dy) && ln_vec(*d, d->y);
-    return hip_status(dr::launch_ln_bwd(a, vec, slot, st), "layer norm backward launch");
+    return hip_status(dr::launch_ln_bwd(a, ln_width(*d, {&d->x, &d->dy, &d->y}), slot, st), "layer norm backward launch");
 }
 
 }  // extern "C"

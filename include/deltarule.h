@@ -581,8 +581,8 @@ dr_status dr_linear_attn_step(const dr_linattn_step_desc* d, const void* q, cons
  *   per_head   1: weight and bias [H][D], one row per head; 0: [D]
  *   x_dtype, y_dtype, dy_dtype  of x; of y or dx; of dy (backward)
  *   x, y, dy   strides of x; of y or dx; of dy (free, not negative, 0 repeats a
- *              row of an input; any alignment: rows whose strides and D are
- *              multiples of 8 run on 16-byte accesses)
+ *              row of an input; rows whose strides and D are multiples of 8 run
+ *              on 16-byte accesses, else on two values or one at a time)
  */
 typedef struct {
     int B, H, L, D;

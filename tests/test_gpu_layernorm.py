@@ -99,6 +99,13 @@ CASES = [
     (1, 1, 3, 16384, False, "bf16", "bf16", "dense"),
     (1, 1, 2, 16383, False, "f32", "f32", "dense"),
     (2, 16, 1500, 48, True, "bf16", "bf16", "dense"),
+    # even widths that are no multiples of 8
+    (1, 1, 1, 2, False, "bf16", "bf16", "dense"),
+    (2, 3, 37, 100, True, "bf16", "bf16", "token"),
+    (1, 2, 65, 250, True, "f32", "f32", "padded"),
+    (1, 1, 19, 1002, False, "bf16", "f32", "dense"),
+    (1, 1, 5, 6002, False, "f32", "bf16", "dense"),
+    (1, 1, 3, 16382, False, "bf16", "bf16", "dense"),
 ]
 
 
