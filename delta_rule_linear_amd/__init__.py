@@ -735,6 +735,12 @@ def _linattn_inputs(q, k, v, log_alpha, S0, decay):
     return B, H, Hk, L, Dk, Dv
 
 
+def _state(like, shape, device):
+    """A new fp32 state, like another if there is one (less work than by sizes)."""
+    torch = _torch()
+    return torch.empty(shape, dtype=torch.float32, device=device) if like is None else torch.empty_like(like)
+
+
 def dr_linear_attn_fwd(q, k, v, log_alpha=None, S0=None, *, decay: str, out_dtype=None, o=None, S_final=None,
                        want_state: bool = True, workspace=None, stream=None):
     """Linear attention with a decay per head, S_t = alpha_t S_{t-1} + k_t v_t^T,
@@ -759,7 +765,7 @@ def dr_linear_attn_fwd(q, k, v, log_alpha=None, S0=None, *, decay: str, out_dtyp
         if S_final is not None:
             _need_on(S_final, "S_final", dev, torch.float32, (B, H, Dk, Dv))
         elif want_state:
-            S_final = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+            S_final = _state(S0, (B, H, Dk, Dv), dev)
         _, desc, nbytes = _linattn_plan(
             False, (B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay]),
             _strides(q), _strides(k), _strides(v), _strides(o))
@@ -788,7 +794,7 @@ def dr_linear_attn_bwd(q, k, v, log_alpha, S0, dO, dS_final=None, *, decay: str,
         out = {"dq": torch.empty_like(q, dtype=to), "dk": torch.empty_like(k, dtype=to),
                "dv": torch.empty_like(v, dtype=to),
                "dlog_alpha": None if log_alpha is None else torch.empty_like(log_alpha),
-               "dS0": torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if want_dS0 else None}
+               "dS0": _state(S0, (B, H, Dk, Dv), dev) if want_dS0 else None}
         _, desc, nbytes = _linattn_plan(
             True, (B, H, Hk, L, Dk, Dv, _dtype_code(q.dtype), _dtype_code(to), DECAYS[decay]),
             _strides(q), _strides(k), _strides(v), _strides(dO), _strides(out["dq"]), _strides(out["dk"]),
@@ -817,7 +823,7 @@ def dr_linear_attn_step(S, q, k, v, log_alpha=None, *, decay: str, out_dtype=Non
     _decay_arg(log_alpha, decay, H, (N, H), dev)
     with _on(dev, stream) as st:
         if o is None:
-            o = torch.empty((N, H, Dv), dtype=torch.float32 if out_dtype is None else out_dtype, device=dev)
+            o = torch.empty_like(v, dtype=torch.float32 if out_dtype is None else out_dtype)
         else:
             _need_on(o, "o", dev, out_dtype, (N, H, Dv))
         _, desc = _linattn_step_plan(N, H, Hk, Dk, Dv, _dtype_code(q.dtype), _dtype_code(o.dtype), DECAYS[decay])
@@ -880,16 +886,17 @@ def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=
             y = torch.empty_like(x, dtype=out_dtype)
         else:
             _need_rows(y, "y", dev, out_dtype, x.shape)
+        ysteps = steps if y.stride() == x.stride() else _norm_dims(y, per_head)[1]
         if mean is None:
             mean = torch.empty(lead, dtype=torch.float32, device=dev)
         else:
             _need_on(mean, "mean", dev, torch.float32, lead)
         if rstd is None:
-            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+            rstd = torch.empty_like(mean)   # a like tensor takes half the time of one by its sizes
         else:
             _need_on(rstd, "rstd", dev, torch.float32, lead)
         _, desc, _ = _layernorm_plan(dims + (int(per_head), _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32,
-                                             float(eps)), steps, _norm_dims(y, per_head)[1])
+                                             float(eps)), steps, ysteps)
         _check(lib().dr_layernorm_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), st))
     return y, mean, rstd
 
@@ -918,13 +925,15 @@ def dr_layernorm_bwd(x, weight, mean, rstd, dy, *, per_head=None, grad_dtype=Non
         else:
             _need_rows(dx, "dx", dev, grad_dtype, x.shape)
         _, desc, nbytes = _layernorm_plan(dims + (int(per_head), _dtype_code(x.dtype), _dtype_code(dx.dtype),
-                                                  _dtype_code(dy.dtype), 0.0), steps, _norm_dims(dx, per_head)[1],
-                                          _norm_dims(dy, per_head)[1])
+                                                  _dtype_code(dy.dtype), 0.0), steps,
+                                          *(steps if t.stride() == x.stride() else _norm_dims(t, per_head)[1]
+                                            for t in (dx, dy)))
         out = {"dx": dx, "dweight": None, "dbias": None}
         wbytes = 0
         if want_sums:
-            out["dweight"] = torch.empty(wshape, dtype=torch.float32, device=dev)
-            out["dbias"] = torch.empty(wshape, dtype=torch.float32, device=dev)
+            out["dweight"] = (torch.empty(wshape, dtype=torch.float32, device=dev) if weight is None else
+                              torch.empty_like(weight))
+            out["dbias"] = torch.empty_like(out["dweight"])
             workspace, wbytes = _workspace(workspace, nbytes, dev)
         _check(lib().dr_layernorm_bwd(desc, _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
                                       _ptr(dx), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), wbytes,
