@@ -13,10 +13,10 @@
 // fp64, by a second kernel.  All other arithmetic is fp32.
 //
 // Measured: forward of 524288 rows of 128 bf16 (a weight for each of 16 heads,
-// y token-major) 58 us for 272 MB, 4.7 TB/s (a large copy reaches 5.2); its
+// y token-major) 60 us for 272 MB, 4.5 TB/s (a large copy reaches 5.2); its
 // backward 82 us for 403 MB, 4.9 TB/s, and 4.5 for the sums; 8191 x 2048 bf16
-// backward 27 us for 101 MB (3.7 TB/s, of which four rows per workgroup and 256
-// workgroups' start are a part) and 4.
+// backward 27 us for 110 MB (4.0 TB/s; 512 workgroups of 16 rows each have a
+// start and an end) and 4.
 
 #include <hip/hip_runtime.h>
 
