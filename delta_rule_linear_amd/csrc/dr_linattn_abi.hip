@@ -53,7 +53,8 @@ dr_status check_strides(const Rows& r, bool vec) {
         if (vec && i == 2 && s[i] > ((int64_t)1 << 23))
             return fail(DR_ERR_UNSUPPORTED, "%s: tokens %lld elements apart, at most 2^23 are supported", r.name,
                         (long long)s[i]);
-        if (s[i] > ((int64_t)1 << 48)) return fail(DR_ERR_SHAPE, "%s: stride %lld too large", r.name, (long long)s[i]);
+        if (s[i] > ((int64_t)1 << 48) / (r.n[i] - 1))
+            return fail(DR_ERR_SHAPE, "%s: stride %lld too large", r.name, (long long)s[i]);
     }
     return DR_OK;
 }

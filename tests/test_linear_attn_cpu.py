@@ -200,6 +200,18 @@ def test_layernorm_refusals():
     assert lnf(ln(L=0)) == drl.DR_OK
 
 
+def test_strides_past_any_memory():
+    """A last row more than 2^48 elements behind the first is refused, also
+    where the product of stride and rows passes 64 bits."""
+    for f in ("q", "k", "v", "o"):
+        d = desc(B=2 ** 12, H=3)
+        getattr(d, f).b = 2 ** 40
+        assert fwd(d) == drl.DR_ERR_SHAPE and "too large" in drl.dr_last_error()
+    d = ln(B=2 ** 20, H=1, L=2)
+    d.x.b = 2 ** 47
+    assert lnf(d) == lnb(d) == drl.DR_ERR_SHAPE
+
+
 def test_binding_needs_device_tensors():
     x = torch.zeros(1, 2, 4, 64)
     with pytest.raises(ValueError, match="device tensor"):
