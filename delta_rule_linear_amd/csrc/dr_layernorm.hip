@@ -393,31 +393,38 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_kernel(LnArgs a) {
     }
 }
 
-// dw and db from the workgroups' sums: 32 columns per workgroup; each of 32
-// threads per column adds every 32nd workgroup's sum, then the 32 are added, in
-// fp64 (a sum of many rows is small against its terms).
-__global__ __launch_bounds__(1024) void ln_bwd_sum_kernel(LnArgs a) {
+// dw and db from the workgroups' sums: 32 columns per workgroup and turn; each of
+// 32 threads per column adds every 32nd workgroup's sum, then the 32 are added, in
+// fp64 (a sum of many rows is small against its terms).  The grid is capped (a
+// launch holds fewer than 2^32 threads, which 65536 heads of 1024 columns pass);
+// below the cap every workgroup has one turn.
+constexpr unsigned kLnSumGrid = 1u << 16;
+
+__global__ __launch_bounds__(1024) void ln_bwd_sum_kernel(LnArgs a, unsigned tiles) {
     __shared__ double red[32][33];
     const unsigned cols = 2 * (unsigned)a.D, per = (cols + 31) / 32;
-    const unsigned g = blockIdx.x / per;
     const unsigned lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const unsigned c = (blockIdx.x % per) * 32 + lane;
-    double s = 0.0;
-    if (c < cols) {
-        const float* p = a.part + (size_t)g * a.blocks * cols + c;
+    for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const unsigned g = tile / per;
+        const unsigned c = (tile % per) * 32 + lane;
+        double s = 0.0;
+        if (c < cols) {
+            const float* p = a.part + (size_t)g * a.blocks * cols + c;
 #pragma unroll 8
-        for (unsigned k = slice; k < a.blocks; k += 32) s += p[(size_t)k * cols];
-    }
-    red[slice][lane] = s;
-    __syncthreads();
-    if (slice == 0 && c < cols) {
-        s = 0.0;
+            for (unsigned k = slice; k < a.blocks; k += 32) s += p[(size_t)k * cols];
+        }
+        if (tile != blockIdx.x) __syncthreads();   // the last turn's sums are read
+        red[slice][lane] = s;
+        __syncthreads();
+        if (slice == 0 && c < cols) {
+            s = 0.0;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s += red[k][lane];
-        if (c < (unsigned)a.D) {
-            if (a.dw) a.dw[(size_t)g * a.D + c] = (float)s;
-        } else if (a.db) {
-            a.db[(size_t)g * a.D + c - a.D] = (float)s;
+            for (int k = 0; k < 32; ++k) s += red[k][lane];
+            if (c < (unsigned)a.D) {
+                if (a.dw) a.dw[(size_t)g * a.D + c] = (float)s;
+            } else if (a.db) {
+                a.db[(size_t)g * a.D + c - a.D] = (float)s;
+            }
         }
     }
 }
@@ -480,8 +487,8 @@ hipError_t launch_ln_fwd(const LnArgs& a, int width, int slot, hipStream_t st) {
 hipError_t launch_ln_bwd(const LnArgs& a, int width, int slot, hipStream_t st) {
     hipError_t e = ln_launch_width<true>(a, width, slot, st);
     if (e == hipSuccess && a.part) {
-        const unsigned per = (unsigned)(2 * a.D + 31) / 32;
-        e = launch_k(slot, ln_bwd_sum_kernel, dim3(a.groups * per), dim3(1024), 0, st, a);
+        const unsigned tiles = a.groups * ((unsigned)(2 * a.D + 31) / 32);   // at most 2^20 * 2^10
+        e = launch_k(slot, ln_bwd_sum_kernel, dim3(tiles < kLnSumGrid ? tiles : kLnSumGrid), dim3(1024), 0, st, a, tiles);
     }
     return e;
 }
