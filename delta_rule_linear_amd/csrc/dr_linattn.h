@@ -91,6 +91,7 @@ struct LaStepArgs {
     int la_head;      // log alpha [H] instead of [N][H]
     int N, H, group, Dk, Dv;
     int out_bf16;
+    unsigned total;   // workgroups (launch_la_step sets it)
 };
 
 // What is left after the passes of a backward, in one launch: gradients of q and
@@ -118,6 +119,6 @@ hipError_t launch_la_gate(const LaGateArgs& a, int slot, hipStream_t st);
 // dst = src, or zeros (src NULL)
 hipError_t launch_la_copy(float* dst, const float* src, size_t n, int slot, hipStream_t st);
 hipError_t launch_la_finish(LaFinishArgs a, int slot, hipStream_t st);
-hipError_t launch_la_step(const LaStepArgs& a, bool f32in, int slot, hipStream_t st);
+hipError_t launch_la_step(LaStepArgs a, bool f32in, int slot, hipStream_t st);
 
 }  // namespace dr

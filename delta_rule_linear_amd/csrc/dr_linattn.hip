@@ -221,12 +221,18 @@ hipError_t launch_la_finish(LaFinishArgs a, int slot, hipStream_t st) {
 // the first is used.  256 x 16 states of 128 x 128: 96 us, 5.6 TB/s of states (a
 // copy of this size reaches 5.2); a single sequence's 16 states 5.5 us, a launch.
 // The state's loads and stores are non-temporal, so that they displace nothing.
+// Workgroups are counted over two grid dimensions: one of them holds fewer than
+// 2^32 threads, 2^24 workgroups, which small states pass (4.3 GB of 8 x 8).
+constexpr unsigned kLaStepRow = 1u << 22;   // workgroups of the first dimension
+
 template <bool F32IN>
 __global__ __launch_bounds__(256) void la_step_kernel(LaStepArgs a) {
     __shared__ float sq[128], sk[128];
     __shared__ float red[16][64];
     const int nslab = (a.Dv + 63) / 64;
-    const int sidx = blockIdx.x / nslab, slab = blockIdx.x % nslab;
+    const unsigned id = blockIdx.y * kLaStepRow + blockIdx.x;   // below 2^31 + 2^22
+    if (id >= a.total) return;
+    const int sidx = (int)(id / nslab), slab = (int)(id % nslab);
     const int n = sidx / a.H, hd = sidx % a.H;
     const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
     const int col = slab * 64 + 4 * cg;
@@ -273,8 +279,9 @@ __global__ __launch_bounds__(256) void la_step_kernel(LaStepArgs a) {
     }
 }
 
-hipError_t launch_la_step(const LaStepArgs& a, bool f32in, int slot, hipStream_t st) {
-    const dim3 grid((unsigned)((size_t)a.N * a.H * ((a.Dv + 63) / 64)));
+hipError_t launch_la_step(LaStepArgs a, bool f32in, int slot, hipStream_t st) {
+    a.total = (unsigned)((size_t)a.N * a.H * ((a.Dv + 63) / 64));   // host: below 2^31
+    const dim3 grid(a.total < kLaStepRow ? a.total : kLaStepRow, (a.total + kLaStepRow - 1) / kLaStepRow);
     return f32in ? launch_k(slot, la_step_kernel<true>, grid, dim3(256), 0, st, a)
                  : launch_k(slot, la_step_kernel<false>, grid, dim3(256), 0, st, a);
 }

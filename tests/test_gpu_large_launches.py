@@ -38,3 +38,29 @@ def test_norm_weight_sums_of_many_heads(H, D):
     last = drl.dr_layernorm_bwd(x[:, -1:].contiguous(), w[-1:].contiguous(), mean[:, -1:].clone(),
                                 rstd[:, -1:].clone(), dy[:, -1:].contiguous())
     assert torch.equal(g["dx"][:, -1:], last["dx"])
+
+
+@pytest.mark.parametrize("N,H,Dk,Dv", [((1 << 24) + 3, 1, 8, 8), ((1 << 22) + 1, 2, 8, 72)])
+def test_step_of_many_small_states(N, H, Dk, Dv):
+    """N H ceil(Dv / 64) workgroups of 256 threads: past 2^32 threads.  Every state
+    is checked: alpha S + k v^T takes four roundings (alpha's among them), and o a
+    sum of Dk products of it."""
+    import delta_rule_linear_amd as drl
+    announce("step", N, H, Dk, Dv)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    S, q, k, v = r(N, H, Dk, Dv), r(N, 1, Dk), r(N, 1, Dk), r(N, H, Dv)
+    la = -torch.rand(H, generator=gen, device="cuda")
+    S0 = S.clone()
+    o = drl.dr_linear_attn_step(S, q, k, v, la, decay="head")
+    u = 2.0 ** -24
+    for a in range(0, N, 1 << 20):   # a part at a time, in float64
+        at = slice(a, min(N, a + (1 << 20)))
+        old = S0[at].double() * la.double().exp()[None, :, None, None]
+        new = k[at].double()[..., None] * v[at].double()[:, :, None]
+        want = old + new
+        size = old.abs() + new.abs()
+        assert bool(((S[at].double() - want).abs() <= 5 * u * size).all())
+        qd = q[at].double()[..., None]
+        err = (o[at].double() - (want * qd).sum(2)).abs()
+        assert bool((err <= (Dk + 6) * u * (size * qd.abs()).sum(2)).all())
