@@ -875,7 +875,8 @@ def dr_layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype=
 
     x: [N,D], [B,L,D] or [B,H,L,D] (bf16 or fp32) with weight and bias [D] fp32;
     or, with one weight per head [H,D], [N,H,D] or [B,H,L,D].  Channels are
-    contiguous, other strides free.  y defaults to out_dtype (x's dtype) in x's
+    contiguous, other strides free; tensors start at multiples of 16 bytes where
+    D and the strides are multiples of 8, else anywhere.  y defaults to out_dtype (x's dtype) in x's
     order of dimensions; mean and rstd are fp32, contiguous, of x's leading shape.
     """
     torch = _torch()

@@ -281,7 +281,7 @@ const char* dr_status_str(dr_status s) {
         case DR_ERR_NULL: return "DR_ERR_NULL: required pointer missing";
         case DR_ERR_SHAPE: return "DR_ERR_SHAPE: invalid dimension";
         case DR_ERR_UNSUPPORTED: return "DR_ERR_UNSUPPORTED: unsupported size, mode or dtype";
-        case DR_ERR_ALIGN: return "DR_ERR_ALIGN: pointer not 16-byte aligned";
+        case DR_ERR_ALIGN: return "DR_ERR_ALIGN: pointer not aligned";
         case DR_ERR_WORKSPACE: return "DR_ERR_WORKSPACE: workspace missing or too small";
         case DR_ERR_HIP: return "DR_ERR_HIP: HIP runtime or launch failure";
     }

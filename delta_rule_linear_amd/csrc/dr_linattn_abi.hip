@@ -199,6 +199,21 @@ dr_status check_aligned(const Span* t, int n) {
     return DR_OK;
 }
 
+// Read and written one element at a time.
+dr_status check_elements(const void* p, size_t elem, const char* name) {
+    if ((uintptr_t)p % elem) return fail(DR_ERR_ALIGN, "%s is not %zu-byte aligned", name, elem);
+    return DR_OK;
+}
+
+// log alpha, and its gradient, are taken one value at a time: a table's row of one
+// value per head, or the sequences of a batch that are no multiples of 16 bytes,
+// start at any of them.
+dr_status check_decay_aligned(int decay, int64_t row, const float* p, const char* name) {
+    if (decay == DR_DECAY_HEAD || row % 4) return check_elements(p, 4, name);
+    const Span t{p, 4, name};
+    return check_aligned(&t, 1);
+}
+
 dr_status hip_status(hipError_t e, const char* what) {
     return e == hipSuccess ? DR_OK : fail(DR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
@@ -272,10 +287,12 @@ dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void
         if ((s = check_strides(*r, true)) != DR_OK) return s;
     if ((s = check_rows_apart(ro)) != DR_OK) return s;
     const LaLayout w = tokens ? la_layout(*d, false) : LaLayout{};
-    const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), {log_alpha, la_elems(*d) * 4, "log_alpha"},
-                        {S0, state * 4, "S0"}, {workspace, w.total, "workspace"}};
+    const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), {S0, state * 4, "S0"},
+                        {workspace, w.total, "workspace"}, {log_alpha, la_elems(*d) * 4, "log_alpha"}};
     const Span outs[] = {rows_span(ro), {S_final, state * 4, "S_final"}};
-    if ((s = check_aligned(ins, 6)) != DR_OK || (s = check_aligned(outs, 2)) != DR_OK) return s;
+    if ((s = check_aligned(ins, 5)) != DR_OK || (s = check_aligned(outs, 2)) != DR_OK ||
+        (s = check_decay_aligned(d->decay, d->L, log_alpha, "log_alpha")) != DR_OK)
+        return s;
     if ((s = check_disjoint(outs, 2, ins, 6, S_final, S0)) != DR_OK) return s;
     if ((s = check_workspace(w.total, workspace, workspace_bytes)) != DR_OK) return s;
     if (nseq == 0) return DR_OK;
@@ -346,12 +363,15 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
     for (int i = 4; i < 7; ++i)
         if ((s = check_rows_apart(*rows[i])) != DR_OK) return s;
     const LaLayout w = tokens ? la_layout(*d, true) : LaLayout{};
-    const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), rows_span(rdo),
-                        {log_alpha, la_elems(*d) * 4, "log_alpha"}, {S0, state * 4, "S0"},
-                        {dS_final, state * 4, "dS_final"}, {workspace, w.total, "workspace"}};
-    const Span outs[] = {rows_span(rdq), rows_span(rdk), rows_span(rdv),
-                         {dlog_alpha, la_elems(*d) * 4, "dlog_alpha"}, {dS0, state * 4, "dS0"}};
-    if ((s = check_aligned(ins, 8)) != DR_OK || (s = check_aligned(outs, 5)) != DR_OK) return s;
+    const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), rows_span(rdo), {S0, state * 4, "S0"},
+                        {dS_final, state * 4, "dS_final"}, {workspace, w.total, "workspace"},
+                        {log_alpha, la_elems(*d) * 4, "log_alpha"}};
+    const Span outs[] = {rows_span(rdq), rows_span(rdk), rows_span(rdv), {dS0, state * 4, "dS0"},
+                         {dlog_alpha, la_elems(*d) * 4, "dlog_alpha"}};
+    if ((s = check_aligned(ins, 7)) != DR_OK || (s = check_aligned(outs, 4)) != DR_OK ||
+        (s = check_decay_aligned(d->decay, d->L, log_alpha, "log_alpha")) != DR_OK ||
+        (s = check_decay_aligned(d->decay, d->L, dlog_alpha, "dlog_alpha")) != DR_OK)
+        return s;
     if ((s = check_disjoint(outs, 5, ins, 8)) != DR_OK) return s;
     if ((s = check_workspace(w.total, workspace, workspace_bytes)) != DR_OK) return s;
     const int slot = dr::kProfLaBwd;
@@ -520,7 +540,9 @@ dr_status dr_linear_attn_step(const dr_linattn_step_desc* d, const void* q, cons
     const Span ins[] = {{q, nk * inb, "q"}, {k, nk * inb, "k"}, {v, nst * d->Dv * inb, "v"},
                         {log_alpha, nla * 4, "log_alpha"}};
     const Span outs[] = {{o, nst * d->Dv * elem_size(d->out_dtype), "o"}, {S, nst * d->Dk * d->Dv * 4, "S"}};
-    if ((s = check_aligned(ins, 4)) != DR_OK || (s = check_aligned(outs, 2)) != DR_OK) return s;
+    if ((s = check_aligned(ins, 3)) != DR_OK || (s = check_aligned(outs, 2)) != DR_OK ||
+        (s = check_decay_aligned(d->decay, 0, log_alpha, "log_alpha")) != DR_OK)
+        return s;
     if ((s = check_disjoint(outs, 2, ins, 4)) != DR_OK) return s;
     const dr::LaStepArgs a{q, k, v, log_alpha, S, o, d->decay == DR_DECAY_HEAD, d->N, d->H, d->H / d->Hk,
                            d->Dk, d->Dv, d->out_dtype == DR_BF16};
@@ -568,8 +590,8 @@ void ln_groups(const dr_layernorm_desc& d, dr::LnArgs& a, bool bwd) {
     a.blocks = std::max(1u, std::min(want, passes));
 }
 
-// Values of a row that can be read or written at once: 8 or 2 where that divides
-// D and every stride (the tensors start at multiples of 16 bytes), else 1.
+// Values of a row that its strides allow to be read or written at once: 8 or 2
+// where that divides D and every stride, else 1.
 int ln_width(const dr_layernorm_desc& d, std::initializer_list<const dr_strides*> strides) {
     long long all = d.D;
     for (const dr_strides* s : strides) {
@@ -578,6 +600,28 @@ int ln_width(const dr_layernorm_desc& d, std::initializer_list<const dr_strides*
         if (d.L > 1) all |= s->t;
     }
     return all % 8 == 0 ? 8 : all % 2 == 0 ? 2 : 1;
+}
+
+// At width 8 every tensor starts at a multiple of 16 bytes, as everywhere else
+// (and so do slices over rows).  Rows of other widths start anywhere, and so may
+// the tensors: at whole elements, with one value at a time where a row tensor
+// does not start at two.
+dr_status check_ln_aligned(int& width, std::initializer_list<const Rows*> rows, const Span* t, int n) {
+    dr_status s;
+    for (const Rows* r : rows) {
+        const size_t elem = elem_size(r->dtype);
+        if (width == 8) {
+            const Span x{r->p, elem, r->name};
+            if ((s = check_aligned(&x, 1)) != DR_OK) return s;
+        } else {
+            if ((s = check_elements(r->p, elem, r->name)) != DR_OK) return s;
+            if ((uintptr_t)r->p % (2 * elem)) width = 1;
+        }
+    }
+    if (width == 8) return check_aligned(t, n);
+    for (int i = 0; i < n; ++i)
+        if ((s = check_elements(t[i].p, 4, t[i].name)) != DR_OK) return s;
+    return DR_OK;
 }
 
 dr::LnRows ln_rows(const dr_layernorm_desc& d, const dr_strides& s) {
@@ -609,7 +653,10 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     const size_t wb = (size_t)(d->per_head ? d->H : 1) * d->D * 4;
     const Span ins[] = {rows_span(rx), {weight, wb, "weight"}, {bias, wb, "bias"}};
     const Span outs[] = {rows_span(ry), {mean, nrow * 4, "mean"}, {rstd, nrow * 4, "rstd"}};
-    if ((s = check_aligned(ins, 3)) != DR_OK || (s = check_aligned(outs, 3)) != DR_OK) return s;
+    int width = ln_width(*d, {&d->x, &d->y});
+    if ((s = check_ln_aligned(width, {&rx, &ry}, ins + 1, 2)) != DR_OK ||
+        (s = check_ln_aligned(width, {}, outs + 1, 2)) != DR_OK)
+        return s;
     if ((s = check_disjoint(outs, 3, ins, 3)) != DR_OK) return s;
     dr::LnArgs a{};
     a.x = x;
@@ -629,7 +676,7 @@ dr_status dr_layernorm_fwd(const dr_layernorm_desc* d, const void* x, const floa
     a.x_f32 = d->x_dtype == DR_F32;
     a.y_f32 = d->y_dtype == DR_F32;
     ln_groups(*d, a, false);
-    return hip_status(dr::launch_ln_fwd(a, ln_width(*d, {&d->x, &d->y}), dr::kProfLnFwd, (hipStream_t)stream),
+    return hip_status(dr::launch_ln_fwd(a, width, dr::kProfLnFwd, (hipStream_t)stream),
                       "layer norm launch");
 }
 
@@ -660,7 +707,13 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     const Span ins[] = {rows_span(rx), {weight, wn * 4, "weight"}, {mean, nrow * 4, "mean"}, {rstd, nrow * 4, "rstd"},
                         rows_span(rdy), {workspace, need, "workspace"}};
     const Span outs[] = {rows_span(rdx), {dweight, wn * 4, "dweight"}, {dbias, wn * 4, "dbias"}};
-    if ((s = check_aligned(ins, 6)) != DR_OK || (s = check_aligned(outs, 3)) != DR_OK) return s;
+    int width = ln_width(*d, {&d->x, &d->dy, &d->y});
+    // the statistics are one value per row: those of a slice over rows start anywhere
+    if ((s = check_ln_aligned(width, {&rx, &rdy, &rdx}, ins + 1, 1)) != DR_OK ||
+        (s = check_ln_aligned(width, {}, outs + 1, 2)) != DR_OK ||
+        (s = check_elements(mean, 4, "mean")) != DR_OK || (s = check_elements(rstd, 4, "rstd")) != DR_OK ||
+        (s = check_aligned(ins + 5, 1)) != DR_OK)
+        return s;
     if ((s = check_disjoint(outs, 3, ins, 6)) != DR_OK) return s;
     if ((s = check_workspace(need, workspace, workspace_bytes)) != DR_OK) return s;
     if (nrow == 0) {
@@ -691,7 +744,7 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
     a.y_f32 = d->y_dtype == DR_F32;
     a.dy_f32 = d->dy_dtype == DR_F32;
     ln_groups(*d, a, true);
-    return hip_status(dr::launch_ln_bwd(a, ln_width(*d, {&d->x, &d->dy, &d->y}), slot, st), "layer norm backward launch");
+    return hip_status(dr::launch_ln_bwd(a, width, slot, st), "layer norm backward launch");
 }
 
 }  // extern "C"

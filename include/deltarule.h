@@ -52,7 +52,8 @@
  * Memory.  Every tensor pointer is a DEVICE pointer owned by the caller; the
  *   library never allocates, frees or retains memory, and keeps no state
  *   between calls apart from the per-thread error text.  Every tensor pointer
- *   must be 16-byte aligned.  Tensors are dense, row-major (C order).
+ *   must be 16-byte aligned (where an operator asks for less, it says so).
+ *   Tensors are dense, row-major (C order).
  * Streams.  `stream` is a hipStream_t passed as void* (NULL = the default
  *   stream).  Work is enqueued asynchronously; inputs, outputs and workspace
  *   must stay untouched until the stream reaches the enqueued work's end.
@@ -104,7 +105,7 @@ typedef enum {
     DR_ERR_NULL = 1,        /* a required pointer is NULL (or a forbidden one is not) */
     DR_ERR_SHAPE = 2,       /* a dimension is negative (0 is valid: no work) */
     DR_ERR_UNSUPPORTED = 3, /* d_k / d_v / mode / dtype combination not provided */
-    DR_ERR_ALIGN = 4,       /* a tensor pointer is not 16-byte aligned */
+    DR_ERR_ALIGN = 4,       /* a tensor pointer is not aligned */
     DR_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than required */
     DR_ERR_HIP = 6          /* a HIP runtime call or kernel launch failed */
 } dr_status;
@@ -461,7 +462,9 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  * multiples of 16 bytes; 0 repeats a row; ignored where the dimension is 1;
  * tokens at most 2^23 elements apart), so that [B][L][H][D] projections, or
  * slices of a fused one, are passed as they are.  An output's rows must not
- * overlap each other.  log_alpha and the states are dense.
+ * overlap each other.  log_alpha and the states are dense.  log_alpha and
+ * dlog_alpha need only be 4-byte aligned with DR_DECAY_HEAD, and in the chunked
+ * calls also where L is no multiple of 4.
  *
  * Numerics.  Accumulations and the state are fp32; running sums of log_alpha
  * are fp64.  bf16 inputs are matrix-core operands as they are; the state and
@@ -583,6 +586,9 @@ dr_status dr_linear_attn_step(const dr_linattn_step_desc* d, const void* q, cons
  *   x, y, dy   strides of x; of y or dx; of dy (free, not negative, 0 repeats a
  *              row of an input; rows whose strides and D are multiples of 8 run
  *              on 16-byte accesses, else on two values or one at a time)
+ * Alignment: 16 bytes where D and all strides are multiples of 8 (so that slices
+ * over rows are aligned too), but 4 for the backward's mean and rstd; else whole
+ * elements, for every tensor but the workspace.
  */
 typedef struct {
     int B, H, L, D;
