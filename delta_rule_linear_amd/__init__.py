@@ -685,8 +685,17 @@ def _decay_arg(log_alpha, decay, H, token_shape, device):
         _need_on(log_alpha, "log_alpha", device, torch.float32, (H,) if decay == "head" else token_shape)
 
 
+def _fit_int(sizes):
+    """A descriptor's sizes are C ints: ctypes would keep the low 32 bits of a
+    larger one, and the call would treat that many rows as all of them."""
+    for n in sizes:
+        if n > 2 ** 31 - 1 or n < -2 ** 31:
+            raise ValueError(f"a dimension of {n}: at most 2^31 - 1 is supported")
+
+
 def linattn_desc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, decay: str) -> LinAttnDesc:
     """A descriptor for dense tensors; the strides can be set afterwards."""
+    _fit_int((B, H, Hk, L, Dk, Dv))
     qk, vo = Strides(Hk * L * Dk, L * Dk, Dk), Strides(H * L * Dv, L * Dv, Dv)
     return LinAttnDesc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, DECAYS[decay], qk, qk, vo, vo, qk, qk, vo)
 
@@ -695,6 +704,7 @@ def linattn_desc(B, H, Hk, L, Dk, Dv, in_dtype, out_dtype, decay: str) -> LinAtt
 # types and strides alone).
 @functools.lru_cache(maxsize=512)
 def _linattn_plan(bwd: bool, sizes, *strides):
+    _fit_int(sizes)
     desc = LinAttnDesc(*sizes, *(Strides(*s) for s in strides))
     fn = lib().dr_linear_attn_bwd_workspace_bytes if bwd else lib().dr_linear_attn_fwd_workspace_bytes
     return desc, ctypes.byref(desc), int(fn(ctypes.byref(desc)))
@@ -702,12 +712,14 @@ def _linattn_plan(bwd: bool, sizes, *strides):
 
 @functools.lru_cache(maxsize=512)
 def _linattn_step_plan(*sizes):
+    _fit_int(sizes)
     desc = LinAttnStepDesc(*sizes)
     return desc, ctypes.byref(desc)
 
 
 @functools.lru_cache(maxsize=512)
 def _layernorm_plan(sizes, *strides):
+    _fit_int(sizes[:4])   # B, H, L, D
     desc = LayerNormDesc(*sizes, *(Strides(*s) for s in strides))
     return desc, ctypes.byref(desc), int(lib().dr_layernorm_bwd_workspace_bytes(ctypes.byref(desc)))
 
