@@ -64,6 +64,10 @@ CASES = [
     *[(1, 2, 1, 200, 64, 64, "token", t, -0.1, -0.001, (0, 64, 65, 131), True, False) for t in ("bf16", "f32")],
     # q, k, v and dO one row for all tokens
     *[(2, 4, 2, L, 64, 72, "token", t, -0.1, -0.001, (), True, True) for t in ("bf16", "f32") for L in (1, 40, 100, 700)],
+    # so many sequences that each is one segment, of more than 1024 tokens
+    *[(8, 64, 32, L, 8, 8, decay, t, -0.02, -0.0001, (), True, False)
+      for L, decay, t in ((1025, "token", "bf16"), (1100, "head", "bf16"), (1100, "token", "f32"), (2100, "token", "bf16"),
+                          (2100, "head", "f32"))],
 ]
 
 

@@ -1,6 +1,7 @@
 """The decay's gradient on the GPU, within a bound that no wrong one passes
 (tests/linattn_gate.py; tests/test_linear_attn_gate_cpu.py shows that for each of
-these configurations)."""
+these configurations).  The last ones are segments of more than 1024 tokens, which
+the kernel sums in several sweeps."""
 import pytest
 
 import linattn_gate as gate

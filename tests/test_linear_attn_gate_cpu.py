@@ -6,6 +6,9 @@ import pytest
 torch = pytest.importorskip("torch")
 import linattn_gate as gate  # noqa: E402
 
+SWEEP = 1024   # tokens that the kernel sums at a time
+
+
 @pytest.fixture(autouse=True)
 def _one_thread():
     """Token by token the tensors are small: threads only wait for each other."""
@@ -40,6 +43,13 @@ def wrong(r, decay, strong=False):
         for i in range(len(ends) - 1):
             seg[:, :, starts[i]:ends[i]] -= r["carry"][i][..., None]
         yield "without <S, dS> between segments", seg
+    if ends[0] > SWEEP:
+        # one segment; the later tokens' sum is lost, or counted twice, for all before them
+        after = r["terms"][:, :, L - SWEEP:].sum(-1)
+        for name, f in (("carry lost", -1), ("carry twice", 1)):
+            c = dla.clone()
+            c[:, :, :L - SWEEP] += f * after[..., None]
+            yield name, c
 
 
 @pytest.mark.parametrize("case", gate.CASES, ids=lambda c: "-".join(str(x) for x in c))
