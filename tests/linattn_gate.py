@@ -145,3 +145,25 @@ def check(got, r, decay):
     bad = (got - want).abs() / bound
     assert bool((bad <= 1).all()), f"dlog_alpha: {int((bad > 1).sum())} entries off, worst {float(bad.max()):.3g} of the bound"
     return float(bad.max())
+
+
+def difference(p, decay, direction, h=2.0 ** -12):
+    """The derivative of <dO, o> + <dS, S_L> along `direction` of log alpha, by
+    differences of the float64 forward at h and 2 h, off by h^4 / 30 of a fifth
+    derivative (2^-52) and 2^-52 / h of the loss's terms."""
+    d = lambda t: t.detach().double().cpu()  # noqa: E731
+    B, H, L, _ = p["v"].shape
+    q, k, v, S0, dO, dS = (d(p[n]) for n in ("q", "k", "v", "S0", "dO", "dS"))
+    q, k = ref.heads(q, H), ref.heads(k, H)
+
+    def loss(x):
+        o, S = ref.forward(q, k, v, ref.gates(d(p["la"]) + x * direction, decay, B, H, L), S0)
+        return float((dO * o).sum() + (dS * S).sum())
+
+    return (8 * (loss(h) - loss(-h)) - (loss(2 * h) - loss(-2 * h))) / (12 * h)
+
+
+def check_difference(got, r, decay, direction, want):
+    got = float((got.detach().double().cpu() * direction).sum())
+    bound = float((total(r["bound"], decay) * direction.abs()).sum())
+    assert abs(got - want) <= bound, f"off the differences: {got} instead of {want}, bound {bound:.3g}"

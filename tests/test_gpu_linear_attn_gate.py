@@ -43,3 +43,15 @@ def test_decay_gradient(case, grad):
                                state(p["dS"]), decay=decay, grad_dtype=gate.DT[grad])
     r = gate.reference(p, decay, gate.segment_tokens(B, H, Hk, L, Dk, Dv))
     print("worst", gate.check(g["dlog_alpha"], r, decay))
+
+
+@pytest.mark.parametrize("case", [c for c in gate.CASES if c[3] == 90], ids=lambda c: c[6])
+def test_decay_gradient_against_differences(case):
+    import delta_rule_linear_amd as drl
+    announce("decay gradient, differences", *case)
+    p, decay = gate.problem(*case), case[6]
+    a = [p[n].cuda() for n in ("q", "k", "v", "la", "S0", "dO", "dS")]
+    g = drl.dr_linear_attn_bwd(*a, decay=decay)
+    r = gate.reference(p, decay, gate.segment_tokens(*case[:6]))
+    d = torch.randn(p["la"].shape, generator=torch.Generator().manual_seed(9), dtype=torch.float64)
+    gate.check_difference(g["dlog_alpha"], r, decay, d, gate.difference(p, decay, d))

@@ -68,3 +68,16 @@ def test_wrong_gradients_are_rejected(case):
         with pytest.raises(AssertionError, match="entries off"):
             gate.check(gate.total(x, decay), r, decay)
             pytest.fail(f"{name}: passes")
+
+
+@pytest.mark.parametrize("case", [c for c in gate.CASES if c[3] == 90], ids=lambda c: c[6])
+def test_wrong_gradients_are_off_the_differences(case):
+    p, decay = gate.problem(*case), case[6]
+    r = gate.reference(p, decay, gate.segment_tokens(*case[:6]))
+    d = torch.randn(p["la"].shape, generator=torch.Generator().manual_seed(9), dtype=torch.float64)
+    want = gate.difference(p, decay, d)
+    gate.check_difference(gate.total(r["dla"], decay).float(), r, decay, d, want)
+    for name, x in wrong(r, decay):
+        with pytest.raises(AssertionError, match="off the differences"):
+            gate.check_difference(gate.total(x, decay), r, decay, d, want)
+            pytest.fail(f"{name}: passes")
