@@ -45,7 +45,9 @@
 // or feeds the gate's gradient, else 2 (16 bits, below the output's own
 // rounding to bf16).  fp32 inputs use the fp32 matrix ops throughout.  Running
 // sums of log alpha are fp64; differences are taken between hi + lo float
-// pairs, so a long or strong decay loses nothing to cancellation.  log alpha
+// pairs, so a long or strong decay loses nothing to cancellation, and the
+// exponentials that a state is scaled by take hi and lo (la_exp2; between two
+// tokens of a chunk the difference is one float).  log alpha
 // below -256 / log2(e) counts as that (its e^ is 0 in fp32 either way), so a
 // decay of exactly zero (log alpha = -inf) resets the state.
 #pragma once
@@ -366,6 +368,15 @@ __device__ __forceinline__ double la_last(double x) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// 2^x to fp32: the hardware's 2^hi (one unit in the last place) times 2^lo, where
+// x = hi + lo; hi alone would be off by up to |x| 2^-24 ln 2 (e^-75: 44 units of
+// 2^-24).  Three per lane and chunk, in one wave: within 0.6% of the time.
+__device__ __forceinline__ float la_exp2(double x) {
+    const float hi = (float)x, lo = (float)(x - (double)hi);
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return e * __builtin_fmaf(lo, 0.693147180559945f, 1.f);
+}
+
 // log alpha below -256 / log2(e) counts as that: its e^ is 0 in fp32.
 constexpr float kLaZero = -177.445678f;
 
@@ -507,9 +518,9 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
         const bool in = 64 * chunk(n) + (l ^ flip) < L;
         lds_st(gt, in ? uh : 1e30f);
         lds_st(gt + 256, (float)(u - (double)uh));
-        lds_st(gt + 512, __builtin_amdgcn_exp2f(uh));
-        lds_st(gt + 768, in ? __builtin_amdgcn_exp2f((float)(total - u)) : 0.f);
-        if (l == 0) lds_st(gt + 1024, __builtin_amdgcn_exp2f((float)total));
+        lds_st(gt + 512, la_exp2(u));
+        lds_st(gt + 768, in ? la_exp2(total - u) : 0.f);
+        if (l == 0) lds_st(gt + 1024, la_exp2(total));
         if constexpr (STATE) seg_total += total;
     };
 
@@ -792,7 +803,7 @@ __global__ __launch_bounds__(64 * NW, (la_waves<T, NW>())) void la_kernel(LaArgs
     if constexpr (STATE) {
         end = ps.seg + ((size_t)seq * a.nseg + sg) * elems;
         if (gate_wave && (la_fresh(tid) & 63) == 0)
-            ps.segdec[(size_t)seq * a.nseg + sg] = __builtin_amdgcn_exp2f((float)seg_total);
+            ps.segdec[(size_t)seq * a.nseg + sg] = la_exp2(seg_total);
     } else if (ps.end && sg == (rev ? 0 : a.nseg - 1)) {
         end = ps.end + seq * elems;
     }

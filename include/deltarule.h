@@ -451,7 +451,10 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  * log_alpha is fp32, expected <= 0 (not checked; larger values grow the state).
  * -inf (alpha = 0) starts the state anew at that token; its gradient is 0
  * (below -177.4, where e^log_alpha is 0 in fp32, likewise).
- * Any size of decay is exact to fp32: nothing is divided by a decay.
+ * Nothing is divided by a decay, so that strong ones cost no accuracy.  The
+ * decay of a state over a chunk of 64 tokens, or a part of one, is exact to a few
+ * fp32 roundings; e^x between two tokens of a chunk is off by up to (2 |x| + 8)
+ * 2^-24 of itself.
  *
  * Heads.  q and k have Hk heads, Hk a divisor of H: state head h reads q and k
  * head h / (H / Hk).  Their gradients are summed over the heads that share them.

@@ -1,0 +1,80 @@
+"""How exact the decays themselves are, on the GPU: inputs that leave nothing else
+in the outputs.  u = 2^-24."""
+import pytest
+
+from gpu_common import announce
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import delta_rule_linear_amd as drl
+    drl.lib()
+
+
+def decays(decay, H, L, x, seed):
+    """log alpha whose sum over the tokens is about x."""
+    gen = torch.Generator().manual_seed(seed)
+    shape = (H,) if decay == "head" else (1, H, L)
+    return x / L * (0.5 + torch.rand(shape, generator=gen))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", ["head", "token"])
+@pytest.mark.parametrize("L,x", [(64, -75.0), (64, -1.0), (130, -70.0), (500, -75.0), (2000, -60.0)])
+def test_decays_of_states(L, x, decay, dtype):
+    """k = 0, S0 = 1 and one-hot q: o_t = e^{u_t} and S_L = e^{u_L}, whatever the size
+    of u.  An exponential is off by 4 u (two of the hardware's, one of the factor for
+    the exponent's low part, one of their product) and its use by one more, in
+    every chunk (or segment) before; bf16 adds up three terms of the state, 2 u."""
+    import delta_rule_linear_amd as drl
+    announce("decays of states", L, x, decay, dtype)
+    H, D = 3, 64
+    la = decays(decay, H, L, x, L)
+    q = torch.zeros(1, H, L, D)
+    q[..., 5] = 1
+    v = torch.randn((1, H, L, D), generator=torch.Generator().manual_seed(1))
+    t = lambda a: a.to(DT[dtype]).cuda()  # noqa: E731
+    S0 = torch.ones(1, H, D, D).cuda()
+    o, S = drl.dr_linear_attn_fwd(t(q), t(0 * q), t(v), la.cuda(), S0, decay=decay)
+    a = la.double() if decay == "token" else la.double()[None, :, None].expand(1, H, L)
+    want = a.cumsum(-1).exp()[..., None]
+    chunk = (torch.arange(L) // 64).double()[:, None]
+    # below 2^-126 fp32 has no normal values: a result there may be zero
+    for got, exact, c, what in ((o, want, chunk, "o"), (S, want[:, :, -1:], chunk[-1], "S")):
+        err = ((got.double().cpu() - exact).abs() - 2.0 ** -126).clamp(min=0) / exact
+        assert bool((err <= (5 * c + 8) * U).all()), f"{what}: {float((err / U).max()):.3g} u"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("x", [-1.0, -20.0, -75.0])
+def test_decays_between_tokens(x, dtype):
+    """One k of a chunk is not zero: o_i = e^{x} with x the log alphas behind it.
+    The difference of two fp32 exponents is rounded twice, 2 |x| u, the exponential
+    off by 2 u, and three products and sums by one each (bf16: two terms more)."""
+    import delta_rule_linear_amd as drl
+    announce("decays between tokens", x, dtype)
+    H, L, D, j = 2, 64, 64, 3
+    la = decays("token", H, L, x, 7)
+    q = torch.zeros(1, H, L, D)
+    q[..., 5] = 1
+    k = torch.zeros(1, H, L, D)
+    k[:, :, j, 5] = 1
+    t = lambda a: a.to(DT[dtype]).cuda()  # noqa: E731
+    o, S = drl.dr_linear_attn_fwd(t(q), t(k), t(torch.ones(1, H, L, D)), la.cuda(), decay="token")
+    a = la.double().cumsum(-1)
+    e = (a - a[:, :, j:j + 1])[:, :, j:]
+    err = (o.double().cpu()[:, :, j:] - e.exp()[..., None]).abs() / e.exp()[..., None]
+    assert bool((err <= (2 * e.abs() + 8)[..., None] * U).all()), f"{float((err / U).max()):.3g} u"
+    assert not o[:, :, :j].any()
+    # the state's: 4 u and its use
+    err = (S[:, :, 5].double().cpu() - e[:, :, -1:].exp()).abs() / e[:, :, -1:].exp()
+    assert bool((err <= 8 * U).all()), f"S: {float((err / U).max()):.3g} u"
