@@ -472,8 +472,10 @@ dr_status dr_chunk_bwd_precond(const dr_chunk_desc* d, const void* q, const void
  * Numerics.  Accumulations and the state are fp32; running sums of log_alpha
  * are fp64.  bf16 inputs are matrix-core operands as they are; the state and
  * every fp32 quantity they meet are carried in two or three bf16 terms, so that
- * fp32 results are fp32-accurate and bf16 results are rounded once.  There is
- * no limit on magnitudes but that of fp32.  A NaN or Inf in a row reaches every
+ * fp32 results are fp32-accurate and bf16 results are rounded once.  Magnitudes
+ * up to 2^126 keep that accuracy, and down to 2^-100 (2^-116 with fp32 inputs):
+ * the last terms of smaller states are below fp32's normal range (at 2^-112 16
+ * bits are left).  A NaN or Inf in a row reaches every
  * row of its 64-token chunk and the later ones, also through a zero decay.
  * Every sum has a fixed order: repeated calls give the same bits.
  */

@@ -78,3 +78,26 @@ def test_decays_between_tokens(x, dtype):
     # the state's: 4 u and its use
     err = (S[:, :, 5].double().cpu() - e[:, :, -1:].exp()).abs() / e[:, :, -1:].exp()
     assert bool((err <= 8 * U).all()), f"S: {float((err / U).max()):.3g} u"
+
+
+@pytest.mark.parametrize("dtype,e", [("bf16", 120), ("bf16", -100), ("f32", 120), ("f32", -116)])
+def test_magnitudes(dtype, e):
+    """v and S0 scaled by 2^e (to 2^126 in the state): every 2-norm within the
+    expected size, 8 standard deviations of n roundings, as in linattn_ref.check."""
+    import delta_rule_linear_amd as drl
+    import linattn_ref as ref
+    announce("magnitudes", dtype, e)
+    gen = torch.Generator().manual_seed(3)
+    L, D = 100, 64
+    r = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    q, k = (r(1, 1, L, D).to(DT[dtype]) for _ in range(2))
+    q = q * 2.0 ** -8
+    v, S0 = (r(1, 1, L, D) * 2.0 ** (e - 4)).to(DT[dtype]), r(1, 1, D, D) * 2.0 ** (e - 2)
+    la = -0.1 * torch.rand((1, 1, L), generator=gen)
+    o, S = drl.dr_linear_attn_fwd(q.cuda(), k.cuda(), v.cuda(), la.cuda(), S0.cuda(), decay="token")
+    wo, wS = ref.forward(q.double(), k.double(), v.double(), la.double().exp(), S0.double())
+    n = L + 2 * D + 256
+    for got, want in ((o, wo), (S, wS)):
+        assert bool(torch.isfinite(got).all())
+        err = float((got.double().cpu() - want).norm() / want.norm())
+        assert err <= 8 * n ** 0.5 * U, err
