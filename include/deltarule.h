@@ -548,6 +548,11 @@ size_t dr_linear_attn_bwd_workspace_bytes(const dr_linattn_desc* d);
  *   dq, dk      [B][Hk][L][Dk] out_dtype, strided, written
  *   dv          [B][H][L][Dv]  out_dtype, strided, written
  *   dlog_alpha  log_alpha's shape, fp32, written; NULL iff DR_DECAY_NONE
+ *               (taken from sums of q . dq - k . dk over the later tokens of a
+ *               segment, so its error is absolute, fp32's in their terms: where
+ *               alpha is so small that the gradient lies below that, rounding of
+ *               that size is what is returned, down to the log_alpha of -177.4
+ *               from which on it is 0)
  *   dS0         [B][H][Dk][Dv] fp32, written, or NULL to skip
  *   workspace   at least dr_linear_attn_bwd_workspace_bytes(d) bytes
  * Outputs must not overlap each other or any input (whole byte ranges, from a
