@@ -288,12 +288,13 @@ dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void
     if ((s = check_rows_apart(ro)) != DR_OK) return s;
     const LaLayout w = tokens ? la_layout(*d, false) : LaLayout{};
     const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), {S0, state * 4, "S0"},
-                        {workspace, w.total, "workspace"}, {log_alpha, la_elems(*d) * 4, "log_alpha"}};
-    const Span outs[] = {rows_span(ro), {S_final, state * 4, "S_final"}};
-    if ((s = check_aligned(ins, 5)) != DR_OK || (s = check_aligned(outs, 2)) != DR_OK ||
+                        {log_alpha, la_elems(*d) * 4, "log_alpha"}};
+    // what is written, the workspace too
+    const Span outs[] = {rows_span(ro), {S_final, state * 4, "S_final"}, {workspace, w.total, "workspace"}};
+    if ((s = check_aligned(ins, 4)) != DR_OK || (s = check_aligned(outs, 3)) != DR_OK ||
         (s = check_decay_aligned(d->decay, d->L, log_alpha, "log_alpha")) != DR_OK)
         return s;
-    if ((s = check_disjoint(outs, 2, ins, 6, S_final, S0)) != DR_OK) return s;
+    if ((s = check_disjoint(outs, 3, ins, 5, S_final, S0)) != DR_OK) return s;
     if ((s = check_workspace(w.total, workspace, workspace_bytes)) != DR_OK) return s;
     if (nseq == 0) return DR_OK;
     if (d->L == 0) {
@@ -364,15 +365,14 @@ dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void
         if ((s = check_rows_apart(*rows[i])) != DR_OK) return s;
     const LaLayout w = tokens ? la_layout(*d, true) : LaLayout{};
     const Span ins[] = {rows_span(rq), rows_span(rk), rows_span(rv), rows_span(rdo), {S0, state * 4, "S0"},
-                        {dS_final, state * 4, "dS_final"}, {workspace, w.total, "workspace"},
-                        {log_alpha, la_elems(*d) * 4, "log_alpha"}};
+                        {dS_final, state * 4, "dS_final"}, {log_alpha, la_elems(*d) * 4, "log_alpha"}};
     const Span outs[] = {rows_span(rdq), rows_span(rdk), rows_span(rdv), {dS0, state * 4, "dS0"},
-                         {dlog_alpha, la_elems(*d) * 4, "dlog_alpha"}};
-    if ((s = check_aligned(ins, 7)) != DR_OK || (s = check_aligned(outs, 4)) != DR_OK ||
+                         {workspace, w.total, "workspace"}, {dlog_alpha, la_elems(*d) * 4, "dlog_alpha"}};
+    if ((s = check_aligned(ins, 6)) != DR_OK || (s = check_aligned(outs, 5)) != DR_OK ||
         (s = check_decay_aligned(d->decay, d->L, log_alpha, "log_alpha")) != DR_OK ||
         (s = check_decay_aligned(d->decay, d->L, dlog_alpha, "dlog_alpha")) != DR_OK)
         return s;
-    if ((s = check_disjoint(outs, 5, ins, 8)) != DR_OK) return s;
+    if ((s = check_disjoint(outs, 6, ins, 7)) != DR_OK) return s;
     if ((s = check_workspace(w.total, workspace, workspace_bytes)) != DR_OK) return s;
     const int slot = dr::kProfLaBwd;
     if (!tokens) {
@@ -705,16 +705,17 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
         return s;
     const size_t need = nrow && sums ? ln_part_bytes(*d) : 0;
     const Span ins[] = {rows_span(rx), {weight, wn * 4, "weight"}, {mean, nrow * 4, "mean"}, {rstd, nrow * 4, "rstd"},
-                        rows_span(rdy), {workspace, need, "workspace"}};
-    const Span outs[] = {rows_span(rdx), {dweight, wn * 4, "dweight"}, {dbias, wn * 4, "dbias"}};
+                        rows_span(rdy)};
+    const Span outs[] = {rows_span(rdx), {dweight, wn * 4, "dweight"}, {dbias, wn * 4, "dbias"},
+                         {workspace, need, "workspace"}};
     int width = ln_width(*d, {&d->x, &d->dy, &d->y});
     // the statistics are one value per row: those of a slice over rows start anywhere
     if ((s = check_ln_aligned(width, {&rx, &rdy, &rdx}, ins + 1, 1)) != DR_OK ||
         (s = check_ln_aligned(width, {}, outs + 1, 2)) != DR_OK ||
         (s = check_elements(mean, 4, "mean")) != DR_OK || (s = check_elements(rstd, 4, "rstd")) != DR_OK ||
-        (s = check_aligned(ins + 5, 1)) != DR_OK)
+        (s = check_aligned(outs + 3, 1)) != DR_OK)
         return s;
-    if ((s = check_disjoint(outs, 3, ins, 6)) != DR_OK) return s;
+    if ((s = check_disjoint(outs, 4, ins, 5)) != DR_OK) return s;
     if ((s = check_workspace(need, workspace, workspace_bytes)) != DR_OK) return s;
     if (nrow == 0) {
         // no rows: the sums are zero

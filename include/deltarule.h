@@ -524,8 +524,8 @@ size_t dr_linear_attn_fwd_workspace_bytes(const dr_linattn_desc* d);
  *   o          [B][H][L][Dv]  out_dtype, strided, written
  *   S_final    [B][H][Dk][Dv] fp32, written, or NULL to skip; may be S0 itself
  *   workspace  at least dr_linear_attn_fwd_workspace_bytes(d) bytes
- * The conventions at the top of this file hold.  Calls in flight at the same
- * time need workspaces of their own.
+ * The conventions at the top of this file hold; the workspace overlaps no input
+ * either.  Calls in flight at the same time need workspaces of their own.
  */
 dr_status dr_linear_attn_fwd(const dr_linattn_desc* d, const void* q, const void* k, const void* v,
                              const float* log_alpha, const float* S0, void* o, float* S_final, void* workspace,
@@ -555,8 +555,8 @@ size_t dr_linear_attn_bwd_workspace_bytes(const dr_linattn_desc* d);
  *               from which on it is 0)
  *   dS0         [B][H][Dk][Dv] fp32, written, or NULL to skip
  *   workspace   at least dr_linear_attn_bwd_workspace_bytes(d) bytes
- * Outputs must not overlap each other or any input (whole byte ranges, from a
- * tensor's first element to its last).
+ * Outputs and the workspace must not overlap each other or any input (whole byte
+ * ranges, from a tensor's first element to its last).
  */
 dr_status dr_linear_attn_bwd(const dr_linattn_desc* d, const void* q, const void* k, const void* v,
                              const float* log_alpha, const float* S0, const void* dO, const float* dS_final, void* dq,
@@ -628,8 +628,8 @@ size_t dr_layernorm_bwd_workspace_bytes(const dr_layernorm_desc* d);
  *   dy          [B][H][L][D] dy_dtype, strided
  *   dx          [B][H][L][D] y_dtype, strided as d->y, written
  *   dweight, dbias  [H][D] or [D] fp32, written, or NULL to skip
- *   workspace   at least dr_layernorm_bwd_workspace_bytes(d) bytes; may be NULL
- *               when both dweight and dbias are
+ *   workspace   at least dr_layernorm_bwd_workspace_bytes(d) bytes, apart from
+ *               every tensor; may be NULL when both dweight and dbias are
  */
 dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const float* weight, const float* mean,
                            const float* rstd, const void* dy, void* dx, float* dweight, float* dbias, void* workspace,
