@@ -101,3 +101,25 @@ def test_magnitudes(dtype, e):
         assert bool(torch.isfinite(got).all())
         err = float((got.double().cpu() - want).norm() / want.norm())
         assert err <= 8 * n ** 0.5 * U, err
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_roundings_of_a_long_state(dtype):
+    """S_L = sum of k v^T over 64 chunks without a decay, in one segment.  A rounding
+    to nearest is off by 0.425 u of the value, root mean square over mantissas; S
+    grows like the square root of the tokens, so r of them in each of N chunks make
+    0.425 u sqrt(r N / 2) of S_L.  fp32: 32 tokens are summed at a time, r = 2 and
+    3.4 u, which those sums, small against S_L, bring to 3.8 u at most.  bf16: each
+    instruction takes 32 tokens and one of z's three terms, r = 6 and 5.9 u.  Half
+    as much again is allowed."""
+    import delta_rule_linear_amd as drl
+    announce("roundings of a long state", dtype)
+    B, H, L, D = 8, 64, 4096, 8
+    d = drl.linattn_desc(B, H, H, L, D, D, drl.DR_F32, drl.DR_F32, "none")
+    assert drl.dr_linear_attn_fwd_workspace_bytes(d) == 0   # one segment
+    gen = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn((B, H, L, D), generator=gen).to(DT[dtype]) for _ in range(3))
+    _, S = drl.dr_linear_attn_fwd(q.cuda(), k.cuda(), v.cuda(), decay="none")
+    want = k.double().transpose(2, 3).contiguous() @ v.double()
+    err = float((S.double().cpu() - want).norm() / want.norm())
+    assert err <= 1.5 * (3.8 if dtype == "f32" else 5.9) * U, f"{err / U:.3g} u"
