@@ -164,8 +164,9 @@ hipError_t launch_la_copy(float* dst, const float* src, size_t n, int slot, hipS
 // ------------------------------------------------------ shared heads, per-head decays
 // The last launch of a backward: gradients of q and k summed over the state
 // heads that share them (fp32, in the heads' order), and per-head decay gradients
-// summed over sequences and segments, one wave per head, in a fixed order.  A few
-// us where it is launched (5.6 at B3 H12 Hk4 L1111 d64), most of them the launch.
+// summed over sequences and segments, one wave per head, in a fixed order.  5.6 us
+// at B3 H12 Hk4 L1111 d64, most of them the launch; bound by memory where there is
+// more: 88 us of 475 at B3 H16 Hk8 L7596, 128 x 64 (373 MB read, 94 written).
 __device__ __forceinline__ void la_finish_heads(const LaFinishArgs& a, unsigned block) {
     const int hd = block * 4 + (threadIdx.x >> 6);
     if (hd >= a.H) return;
@@ -219,7 +220,7 @@ hipError_t launch_la_finish(LaFinishArgs a, int slot, hipStream_t st) {
 // and written once, and nothing else is large.  One workgroup takes 64 columns
 // of a state; a thread holds four columns of every 16th row, all loaded before
 // the first is used.  256 x 16 states of 128 x 128: 96 us, 5.6 TB/s of states (a
-// copy of this size reaches 5.2); a single sequence's 16 states 5.5 us, a launch.
+// copy of this size reaches 5.2); a single sequence's 16 states 5.2 us, a launch.
 // The state's loads and stores are non-temporal, so that they displace nothing.
 // Workgroups are counted over two grid dimensions: one of them holds fewer than
 // 2^32 threads, 2^24 workgroups, which small states pass (4.3 GB of 8 x 8).

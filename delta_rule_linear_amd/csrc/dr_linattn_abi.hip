@@ -125,6 +125,9 @@ int waves_of(int D) { return D <= 32 ? 2 : D <= 64 ? 4 : 8; }
 // bf16, 128 x 128, 16 heads: 512 tokens 36.6 us in two segments, 27.1 in four;
 // 1024 tokens 39.3 in four, 31.5 in eight; 4096 tokens 47.6 in 16, 55.8 in 32;
 // 256 tokens 21.6 in one, 24.9 in two (the two more launches).
+// The rule does not count rounds: with two workgroups of 128 x 128 to a compute
+// unit, 576 sequences of 2048 tokens are one round and a ninth, 363 us against 289
+// for 512.
 constexpr int64_t kUnits = 256;
 
 Split la_split_of(int L, int64_t nseq) {

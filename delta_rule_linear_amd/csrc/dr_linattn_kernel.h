@@ -29,9 +29,9 @@
 // What bounds it, at that size: the forward's main pass takes 138 us for 570 MB
 // (4.1 TB/s; a large copy reaches 5.2) and the state pass 66 us for 285 MB.  The
 // main pass without its products took 110 us, so memory comes first, then the
-// issue of vector and matrix instructions, which overlap only in part: 420 and 97
+// issue of vector and matrix instructions, which overlap only in part: 424 and 97
 // per wave and chunk, a third of the former splitting fp32 values into bf16 terms.
-// The backward's three passes (three terms, row dot products; 550 and 119) are
+// The backward's three passes (three terms, row dot products; 552 and 119) are
 // bound by that issue: 470 us for 1.65 GB, and 530-640 where calls follow each
 // other without a pause and the clock falls.  Where few workgroups run, a chunk
 // is a chain of latencies: 3.1 us at d64 in a workgroup of four waves alone.
