@@ -34,6 +34,14 @@ Layer norm of rows, such as those outputs, and its gradients:
 
     y, mean, rstd = dr_layernorm_fwd(o, weight, bias)
     g = dr_layernorm_bwd(o, weight, mean, rstd, dy)
+
+RMS norm with the residual's addition (also to 8 bits with scales), the short causal
+convolution and the gated linear recurrence of a layer:
+
+    y, rstd, total = dr_rmsnorm_fwd(x, weight, residual)
+    y8, scale, rstd, total = dr_rmsnorm_fwd_e4m3(x, weight, residual)
+    y, state = dr_short_conv_fwd(x, weight, bias, state)
+    h, h_final = dr_gated_scan_fwd(x, gate, h0, decay="logit", inputs="unit")
 """
 from __future__ import annotations
 
@@ -45,12 +53,15 @@ from typing import Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdeltarule.so")
 
-DR_ABI_VERSION = 11
+DR_ABI_VERSION = 12
 DR_OK, DR_ERR_NULL, DR_ERR_SHAPE, DR_ERR_UNSUPPORTED, DR_ERR_ALIGN, DR_ERR_WORKSPACE, DR_ERR_HIP = range(7)
 DR_F32, DR_BF16 = 0, 1
 GATES = {"none": 0, "scalar": 1, "channel": 2}
 BETAS = {"scalar": 0, "channel": 1}
 DECAYS = {"none": 0, "head": 1, "token": 2}
+SCAN_DECAYS = {"log": 0, "logit": 1}
+SCAN_INPUTS = {"plain": 0, "blend": 1, "unit": 2}
+ACTIVATIONS = {"none": 0, "silu": 1}
 DR_IN_QK_L2NORM, DR_IN_BETA_LOGIT = 1, 2
 EXPORTS = ("dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd", "dr_chunk_fwd_kv", "dr_decode_step",
            "dr_decode_step_kv", "dr_chunk_fwd_precond_workspace_bytes", "dr_chunk_fwd_precond",
@@ -60,7 +71,11 @@ EXPORTS = ("dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd", "dr_chunk_fwd_kv", "d
            "dr_chunk_bwd_kv_workspace_bytes", "dr_chunk_bwd_precond_workspace_bytes", "dr_chunk_bwd_precond",
            "dr_chunk_bwd_workspace_bytes_min", "dr_linear_attn_fwd_workspace_bytes", "dr_linear_attn_fwd",
            "dr_linear_attn_bwd_workspace_bytes", "dr_linear_attn_bwd", "dr_linear_attn_step", "dr_layernorm_fwd",
-           "dr_layernorm_bwd_workspace_bytes", "dr_layernorm_bwd")
+           "dr_layernorm_bwd_workspace_bytes", "dr_layernorm_bwd", "dr_rmsnorm_fwd", "dr_rmsnorm_fwd_e4m3",
+           "dr_rmsnorm_bwd_workspace_bytes", "dr_rmsnorm_bwd", "dr_short_conv_fwd",
+           "dr_short_conv_bwd_workspace_bytes", "dr_short_conv_bwd", "dr_short_conv_step",
+           "dr_gated_scan_fwd_workspace_bytes", "dr_gated_scan_fwd", "dr_gated_scan_bwd_workspace_bytes",
+           "dr_gated_scan_bwd", "dr_gated_scan_step")
 DR_NOALLOC_SCRATCH_BYTES = 256 << 20
 
 
@@ -85,7 +100,11 @@ class ProfileReport(ctypes.Structure):
                 ("bwd_rscan_ms", ctypes.c_double), ("bwd_post_ms", ctypes.c_double),
                 ("linear_attn_fwd_ms", ctypes.c_double), ("linear_attn_bwd_ms", ctypes.c_double),
                 ("linear_attn_step_ms", ctypes.c_double), ("layernorm_fwd_ms", ctypes.c_double),
-                ("layernorm_bwd_ms", ctypes.c_double)]
+                ("layernorm_bwd_ms", ctypes.c_double), ("rmsnorm_fwd_ms", ctypes.c_double),
+                ("rmsnorm_bwd_ms", ctypes.c_double), ("short_conv_fwd_ms", ctypes.c_double),
+                ("short_conv_bwd_ms", ctypes.c_double), ("short_conv_step_ms", ctypes.c_double),
+                ("gated_scan_fwd_ms", ctypes.c_double), ("gated_scan_bwd_ms", ctypes.c_double),
+                ("gated_scan_step_ms", ctypes.c_double)]
 
 
 class DecodeDesc(ctypes.Structure):
@@ -116,6 +135,27 @@ class LayerNormDesc(ctypes.Structure):
                 ("per_head", ctypes.c_int), ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
                 ("dy_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("x", Strides), ("y", Strides),
                 ("dy", Strides)]
+
+
+class RMSNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("D", ctypes.c_int),
+                ("per_head", ctypes.c_int), ("x_dtype", ctypes.c_int), ("res_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("dy_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("block", ctypes.c_int), ("x", Strides), ("res", Strides), ("y", Strides), ("total", Strides),
+                ("dy", Strides)]
+
+
+class ShortConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("C", ctypes.c_int), ("W", ctypes.c_int),
+                ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int), ("dy_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("x", Strides), ("y", Strides), ("dy", Strides)]
+
+
+class GatedScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("C", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("gate_dtype", ctypes.c_int), ("h_dtype", ctypes.c_int), ("dh_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("decay", ctypes.c_int), ("inputs", ctypes.c_int), ("x", Strides),
+                ("gate", Strides), ("h", Strides), ("dh", Strides), ("dx", Strides), ("dgate", Strides)]
 
 
 _lib = None
@@ -181,6 +221,21 @@ def lib() -> ctypes.CDLL:
         L.dr_layernorm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.dr_layernorm_bwd.argtypes = [ctypes.POINTER(LayerNormDesc)] + [vp] * 9 + [ctypes.c_size_t, vp]
         L.dr_layernorm_bwd.restype = ctypes.c_int
+        # pointers behind the descriptor; then, where there is one, the workspace and its size
+        for name, desc, nptr, ws in (("dr_rmsnorm_fwd", RMSNormDesc, 6, None), ("dr_rmsnorm_fwd_e4m3", RMSNormDesc, 7, None),
+                                     ("dr_rmsnorm_bwd", RMSNormDesc, 7, "_workspace_bytes"),
+                                     ("dr_short_conv_fwd", ShortConvDesc, 6, None),
+                                     ("dr_short_conv_bwd", ShortConvDesc, 10, "_workspace_bytes"),
+                                     ("dr_short_conv_step", ShortConvDesc, 5, None),
+                                     ("dr_gated_scan_fwd", GatedScanDesc, 5, "_workspace_bytes"),
+                                     ("dr_gated_scan_bwd", GatedScanDesc, 9, "_workspace_bytes"),
+                                     ("dr_gated_scan_step", GatedScanDesc, 4, None)):
+            getattr(L, name).argtypes = ([ctypes.POINTER(desc)] + [vp] * nptr +
+                                         ([vp, ctypes.c_size_t] if ws else []) + [vp])
+            getattr(L, name).restype = ctypes.c_int
+            if ws:
+                getattr(L, name + ws).argtypes = [ctypes.POINTER(desc)]
+                getattr(L, name + ws).restype = ctypes.c_size_t
         L.dr_status_str.argtypes = [ctypes.c_int]
         L.dr_status_str.restype = ctypes.c_char_p
         L.dr_last_error.argtypes = []
@@ -952,3 +1007,381 @@ def dr_layernorm_bwd(x, weight, mean, rstd, dy, *, per_head=None, grad_dtype=Non
                                       _ptr(dx), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), wbytes,
                                       st))
     return out
+
+
+# ---------------------------------------------------------------------------
+# RMS norm with the residual's addition
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=512)
+def _rmsnorm_plan(sizes, *strides):
+    _fit_int(sizes[:4])   # B, H, L, D
+    desc = RMSNormDesc(*sizes, *(Strides(*s) for s in strides))
+    return desc, ctypes.byref(desc), int(lib().dr_rmsnorm_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def _rmsnorm_fwd(x, weight, residual, eps, out_dtype, block, y, scale, rstd, total, stream):
+    torch = _torch()
+    e4m3 = block is not None
+    dims, steps, per_head, _ = _norm_args(x, None, weight, None)
+    dev, lead = x.device, x.shape[:-1]
+    if residual is not None:
+        _need_rows(residual, "residual", dev, None, x.shape)
+    elif total is not None:
+        raise ValueError("total is the sum with the residual: there is none")
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x, dtype=torch.float8_e4m3fn if e4m3 else out_dtype)
+        else:
+            _need_rows(y, "y", dev, torch.float8_e4m3fn if e4m3 else out_dtype, x.shape)
+        if rstd is None:
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+        else:
+            _need_on(rstd, "rstd", dev, torch.float32, lead)
+        if e4m3:
+            if block not in (0, 128):
+                raise ValueError(f"block must be 128 (columns of a scale) or 0 (a row), got {block!r}")
+            shape = lead + ((x.shape[-1] + 127) // 128 if block else 1,)
+            if scale is None:
+                scale = torch.empty(shape, dtype=torch.float32, device=dev)
+            else:
+                _need_on(scale, "scale", dev, torch.float32, shape)
+        if residual is not None:
+            if total is None:
+                total = torch.empty_like(residual)
+            else:
+                _need_rows(total, "total", dev, residual.dtype, x.shape)
+        none = (0, 0, 0)
+        more = [none if t is None else steps if t.stride() == x.stride() else _norm_dims(t, per_head)[1]
+                for t in (residual, y, total)]
+        _, desc, _ = _rmsnorm_plan(dims + (int(per_head), _dtype_code(x.dtype),
+                                           _dtype_code(x.dtype if residual is None else residual.dtype),
+                                           DR_F32 if e4m3 else _dtype_code(y.dtype), DR_F32, float(eps), block or 0),
+                                   steps, *more, none)
+        if e4m3:
+            _check(lib().dr_rmsnorm_fwd_e4m3(desc, _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale),
+                                             _ptr(total), _ptr(rstd), st))
+        else:
+            _check(lib().dr_rmsnorm_fwd(desc, _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(total),
+                                        _ptr(rstd), st))
+    return y, scale, rstd, total
+
+
+def dr_rmsnorm_fwd(x, weight=None, residual=None, *, eps: float = 1e-5, out_dtype=None, y=None, rstd=None, total=None,
+                   stream=None):
+    """RMS norm over the last dimension of s = x + residual: y = s rstd weight,
+    rstd = 1 / sqrt(mean(s^2) + eps); returns (y, rstd, total).
+
+    x: [N,D], [B,L,D] or [B,H,L,D] (bf16 or fp32) with a weight [D] fp32 (None:
+    ones); or, with one weight per head [H,D], [N,H,D] or [B,H,L,D].  residual: x's
+    shape, of x's dtype or fp32; total is the sum in its dtype (None without one).
+    y and rstd come from the sum before that rounding.  Channels are contiguous,
+    other strides free, rows start at any element.  y defaults to out_dtype (x's
+    dtype) in x's order of dimensions; rstd is fp32, of x's leading shape.
+    """
+    y, _, rstd, total = _rmsnorm_fwd(x, weight, residual, eps, out_dtype, None, y, None, rstd, total, stream)
+    return y, rstd, total
+
+
+def dr_rmsnorm_fwd_e4m3(x, weight=None, residual=None, *, eps: float = 1e-5, block: int = 128, y=None, scale=None,
+                        rstd=None, total=None, stream=None):
+    """dr_rmsnorm_fwd with y in 8 bits (torch.float8_e4m3fn) and scales: y is near
+    scale * code.  block 128: a scale for each 128 columns, [..., ceil(D/128)]; 0: one
+    for a row, [..., 1].  Returns (y, scale, rstd, total)."""
+    if block is None:
+        raise ValueError("block must be 128 (columns of a scale) or 0 (a row), got None")
+    return _rmsnorm_fwd(x, weight, residual, eps, None, block, y, scale, rstd, total, stream)
+
+
+def dr_rmsnorm_bwd_workspace_bytes(desc: RMSNormDesc) -> int:
+    return int(lib().dr_rmsnorm_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_rmsnorm_bwd(x, weight, rstd, dy, ds=None, *, per_head=None, grad_dtype=None, dx=None, want_sums: bool = True,
+                   workspace=None, stream=None):
+    """Gradients of dr_rmsnorm_fwd: dx, of x and of the residual, in grad_dtype (x's
+    dtype) and in x's order of dimensions, and dweight fp32 (None with
+    want_sums=False), in a dict.  x is the forward's total (its x without a
+    residual) and rstd its rstd; dy (bf16 or fp32) has x's shape, and so has ds, the
+    gradient that reaches the total besides (None: none).  Without a weight,
+    per_head=True makes dweight one per head."""
+    torch = _torch()
+    if weight is not None and per_head is not None and per_head != (weight.dim() == 2):
+        raise ValueError("per_head does not fit the weight's shape")
+    dims, steps, per_head, wshape = _norm_args(x, per_head, weight, None)
+    dev, lead = x.device, x.shape[:-1]
+    _need_on(rstd, "rstd", dev, torch.float32, lead)
+    _need_rows(dy, "dy", dev, None, x.shape)
+    if ds is not None:
+        _need_rows(ds, "ds", dev, None, x.shape)
+    with _on(dev, stream) as st:
+        if dx is None:
+            dx = torch.empty_like(x, dtype=grad_dtype)
+        else:
+            _need_rows(dx, "dx", dev, grad_dtype, x.shape)
+        none = (0, 0, 0)
+        sds, sdx, sdy = (none if t is None else steps if t.stride() == x.stride() else _norm_dims(t, per_head)[1]
+                         for t in (ds, dx, dy))
+        _, desc, nbytes = _rmsnorm_plan(dims + (int(per_head), _dtype_code(x.dtype),
+                                                _dtype_code(x.dtype if ds is None else ds.dtype),
+                                                _dtype_code(dx.dtype), _dtype_code(dy.dtype), 0.0, 0),
+                                        steps, sds, sdx, none, sdy)
+        out = {"dx": dx, "dweight": None}
+        wbytes = 0
+        if want_sums:
+            out["dweight"] = (torch.empty(wshape, dtype=torch.float32, device=dev) if weight is None else
+                              torch.empty_like(weight))
+            workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_rmsnorm_bwd(desc, _ptr(x), _ptr(weight), _ptr(rstd), _ptr(dy), _ptr(ds), _ptr(dx),
+                                    _ptr(out["dweight"]), _ptr(workspace), wbytes, st))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# short causal convolution; gated linear recurrence
+# ---------------------------------------------------------------------------
+
+def _seq_strides(t):
+    """The strides of a [B,L,C] view in elements (0 where a dimension is 1)."""
+    n, s = t.shape, t.stride()
+    return (s[0] if n[0] > 1 else 0, 0, s[1] if n[1] > 1 else 0)
+
+
+def _need_seq(t, name, device=None, dtype=None, shape=None, dims=3):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a [B, L, C] tensor" if dims == 3 else f"{name} must be a [B, C] tensor")
+    _need_rows(t, name, device, dtype, shape)
+
+
+def _mode(value, modes, name):
+    if value not in modes:
+        raise ValueError(f"{name} must be one of {sorted(modes)}, got {value!r}")
+    return modes[value]
+
+
+@functools.lru_cache(maxsize=512)
+def _short_conv_plan(sizes, *strides):
+    _fit_int(sizes[:4])   # B, L, C, W
+    desc = ShortConvDesc(*sizes, *(Strides(*s) for s in strides))
+    return desc, ctypes.byref(desc), int(lib().dr_short_conv_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def _conv_args(C, weight, bias, dev):
+    torch = _torch()
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [C, W] tensor")
+    W = weight.shape[1]
+    _need_on(weight, "weight", dev, torch.float32, (C, W))
+    if bias is not None:
+        _need_on(bias, "bias", dev, torch.float32, (C,))
+    return W
+
+
+def dr_short_conv_fwd(x, weight, bias=None, state=None, *, activation: str = "silu", out_dtype=None, y=None,
+                      state_out=None, want_state: bool = True, stream=None):
+    """Causal convolution of each channel over W tokens, z_t = bias + sum_j weight_j
+    x_{t-W+1+j}, and y = z sigmoid(z) ("silu") or z ("none"); returns (y, state_out).
+
+    x: [B,L,C] bf16 or fp32, channels contiguous, other strides free (a slice of a
+    fused projection); weight [C,W] fp32, W in 2..8; bias [C] fp32 or None; state
+    [B,W-1,C] in x's dtype, the inputs before the first, oldest first (None: zeros).
+    state_out are the last W-1 inputs; it may be state itself; with
+    want_state=False and no state_out none is written and None is returned.  y
+    defaults to out_dtype (x's dtype) in x's order of dimensions.
+    """
+    torch = _torch()
+    act = _mode(activation, ACTIVATIONS, "activation")
+    _need_seq(x, "x")
+    dev = x.device
+    B, L, C = x.shape
+    W = _conv_args(C, weight, bias, dev)
+    if state is not None:
+        _need_on(state, "state", dev, x.dtype, (B, W - 1, C))
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x, dtype=out_dtype)
+        else:
+            _need_seq(y, "y", dev, out_dtype, x.shape)
+        if state_out is not None:
+            _need_on(state_out, "state_out", dev, x.dtype, (B, W - 1, C))
+        elif want_state:
+            state_out = torch.empty((B, max(W - 1, 0), C), dtype=x.dtype, device=dev) if state is None else torch.empty_like(state)
+        _, desc, _ = _short_conv_plan((B, L, C, W, _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32, act),
+                                      _seq_strides(x), _seq_strides(y), (0, 0, 0))
+        _check(lib().dr_short_conv_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), _ptr(state_out), st))
+    return y, state_out
+
+
+def dr_short_conv_bwd_workspace_bytes(desc: ShortConvDesc) -> int:
+    return int(lib().dr_short_conv_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_short_conv_bwd(x, weight, bias, state, dy, dstate_out=None, *, activation: str = "silu", grad_dtype=None,
+                      want_sums: bool = True, want_dstate: bool = True, workspace=None, stream=None):
+    """Gradients of dr_short_conv_fwd for the loss whose gradients with respect to y
+    and state_out are dy [B,L,C] (bf16 or fp32) and dstate_out [B,W-1,C] (fp32; None:
+    zero).  Returns a dict: dx in grad_dtype (x's dtype) and in x's order of
+    dimensions; dweight, dbias fp32 (None with want_sums=False); dstate, of the
+    initial state, fp32 (None with want_dstate=False)."""
+    torch = _torch()
+    act = _mode(activation, ACTIVATIONS, "activation")
+    _need_seq(x, "x")
+    dev = x.device
+    B, L, C = x.shape
+    W = _conv_args(C, weight, bias, dev)
+    if state is not None:
+        _need_on(state, "state", dev, x.dtype, (B, W - 1, C))
+    _need_seq(dy, "dy", dev, None, x.shape)
+    if dstate_out is not None:
+        _need_on(dstate_out, "dstate_out", dev, torch.float32, (B, W - 1, C))
+    with _on(dev, stream) as st:
+        out = {"dx": torch.empty_like(x, dtype=grad_dtype), "dweight": None, "dbias": None,
+               "dstate": _state(dstate_out, (B, max(W - 1, 0), C), dev) if want_dstate else None}
+        _, desc, nbytes = _short_conv_plan((B, L, C, W, _dtype_code(x.dtype), _dtype_code(out["dx"].dtype),
+                                            _dtype_code(dy.dtype), act),
+                                           _seq_strides(x), _seq_strides(out["dx"]), _seq_strides(dy))
+        wbytes = 0
+        if want_sums:
+            out["dweight"] = torch.empty_like(weight)
+            out["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev) if bias is None else torch.empty_like(bias)
+            workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_short_conv_bwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(dy), _ptr(dstate_out),
+                                       _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dstate"]),
+                                       _ptr(workspace), wbytes, st))
+    return out
+
+
+def dr_short_conv_step(state, x, weight, bias=None, *, activation: str = "silu", out_dtype=None, y=None, stream=None):
+    """One token of the short convolution for N states [N,W-1,C] (x's dtype, updated
+    in place); x: [N,C]; returns y [N,C]."""
+    torch = _torch()
+    act = _mode(activation, ACTIVATIONS, "activation")
+    _need(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a [N, C] tensor")
+    dev = x.device
+    N, C = x.shape
+    W = _conv_args(C, weight, bias, dev)
+    _need_on(state, "state", dev, x.dtype, (N, W - 1, C))
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x, dtype=out_dtype)
+        else:
+            _need_on(y, "y", dev, out_dtype, (N, C))
+        none = (0, 0, 0)
+        _, desc, _ = _short_conv_plan((N, 1, C, W, _dtype_code(x.dtype), _dtype_code(y.dtype), DR_F32, act),
+                                      none, none, none)
+        _check(lib().dr_short_conv_step(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), st))
+    return y
+
+
+@functools.lru_cache(maxsize=512)
+def _gated_scan_plan(bwd: bool, sizes, *strides):
+    _fit_int(sizes[:3])   # B, L, C
+    desc = GatedScanDesc(*sizes, *(Strides(*s) for s in strides))
+    fn = lib().dr_gated_scan_bwd_workspace_bytes if bwd else lib().dr_gated_scan_fwd_workspace_bytes
+    return desc, ctypes.byref(desc), int(fn(ctypes.byref(desc)))
+
+
+def dr_gated_scan_fwd_workspace_bytes(desc: GatedScanDesc) -> int:
+    return int(lib().dr_gated_scan_fwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_gated_scan_bwd_workspace_bytes(desc: GatedScanDesc) -> int:
+    return int(lib().dr_gated_scan_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def dr_gated_scan_fwd(x, gate, h0=None, *, decay: str, inputs: str = "plain", out_dtype=None, h=None, h_final=None,
+                      want_state: bool = True, workspace=None, stream=None):
+    """Gated linear recurrence of each channel, h_t = a_t h_{t-1} + c(a_t) x_t over
+    [B,L,C] device tensors; returns (h, h_final).
+
+    x: bf16 or fp32; gate: x's dtype or fp32; channels contiguous, other strides
+    free.  decay "log": a = e^gate (-inf starts anew); "logit": a = sigmoid(gate).
+    inputs "plain": c = 1; "blend": 1 - a; "unit": sqrt(1 - a^2).  h0: [B,C] fp32 or
+    None.  h defaults to out_dtype (fp32) in x's order of dimensions; h_final may be
+    h0 itself; with want_state=False and no h_final none is written and None is
+    returned for it.
+    """
+    torch = _torch()
+    modes = _mode(decay, SCAN_DECAYS, "decay"), _mode(inputs, SCAN_INPUTS, "inputs")
+    _need_seq(x, "x")
+    dev = x.device
+    B, L, C = x.shape
+    _need_seq(gate, "gate", dev, None, x.shape)
+    if h0 is not None:
+        _need_on(h0, "h0", dev, torch.float32, (B, C))
+    with _on(dev, stream) as st:
+        if h is None:
+            h = torch.empty_like(x, dtype=torch.float32 if out_dtype is None else out_dtype)
+        else:
+            _need_seq(h, "h", dev, out_dtype, x.shape)
+        if h_final is not None:
+            _need_on(h_final, "h_final", dev, torch.float32, (B, C))
+        elif want_state:
+            h_final = _state(h0, (B, C), dev)
+        none = (0, 0, 0)
+        _, desc, nbytes = _gated_scan_plan(
+            False, (B, L, C, _dtype_code(x.dtype), _dtype_code(gate.dtype), _dtype_code(h.dtype), DR_F32, DR_F32) + modes,
+            _seq_strides(x), _seq_strides(gate), _seq_strides(h), none, none, none)
+        workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_gated_scan_fwd(desc, _ptr(x), _ptr(gate), _ptr(h0), _ptr(h), _ptr(h_final), _ptr(workspace),
+                                       wbytes, st))
+    return h, h_final
+
+
+def dr_gated_scan_bwd(x, gate, h0, h, dh, dh_final=None, *, decay: str, inputs: str = "plain", grad_dtype=None,
+                      want_dh0: bool = True, workspace=None, stream=None):
+    """Gradients of dr_gated_scan_fwd for the loss whose gradients with respect to h
+    and h_final are dh [B,L,C] (bf16 or fp32) and dh_final [B,C] (fp32; None: zero);
+    h is what the forward returned.  Returns a dict: dx and dgate in grad_dtype
+    (fp32) and in their inputs' order of dimensions, dh0 [B,C] fp32 (None with
+    want_dh0=False)."""
+    torch = _torch()
+    modes = _mode(decay, SCAN_DECAYS, "decay"), _mode(inputs, SCAN_INPUTS, "inputs")
+    _need_seq(x, "x")
+    dev = x.device
+    B, L, C = x.shape
+    _need_seq(gate, "gate", dev, None, x.shape)
+    _need_seq(h, "h", dev, None, x.shape)
+    _need_seq(dh, "dh", dev, None, x.shape)
+    if h0 is not None:
+        _need_on(h0, "h0", dev, torch.float32, (B, C))
+    if dh_final is not None:
+        _need_on(dh_final, "dh_final", dev, torch.float32, (B, C))
+    to = torch.float32 if grad_dtype is None else grad_dtype
+    with _on(dev, stream) as st:
+        out = {"dx": torch.empty_like(x, dtype=to), "dgate": torch.empty_like(gate, dtype=to),
+               "dh0": _state(h0, (B, C), dev) if want_dh0 else None}
+        _, desc, nbytes = _gated_scan_plan(
+            True, (B, L, C, _dtype_code(x.dtype), _dtype_code(gate.dtype), _dtype_code(h.dtype), _dtype_code(dh.dtype),
+                   _dtype_code(to)) + modes,
+            *(_seq_strides(t) for t in (x, gate, h, dh, out["dx"], out["dgate"])))
+        workspace, wbytes = _workspace(workspace, nbytes, dev)
+        _check(lib().dr_gated_scan_bwd(desc, _ptr(x), _ptr(gate), _ptr(h0), _ptr(h), _ptr(dh), _ptr(dh_final),
+                                       _ptr(out["dx"]), _ptr(out["dgate"]), _ptr(out["dh0"]), _ptr(workspace), wbytes, st))
+    return out
+
+
+def dr_gated_scan_step(state, x, gate, *, decay: str, inputs: str = "plain", out_dtype=None, h=None, stream=None):
+    """One token of the gated recurrence for N states [N,C] (fp32, updated in place);
+    x and gate: [N,C]; returns h [N,C], the new state in out_dtype (fp32)."""
+    torch = _torch()
+    modes = _mode(decay, SCAN_DECAYS, "decay"), _mode(inputs, SCAN_INPUTS, "inputs")
+    _need(state, "state", torch.float32)
+    if state.dim() != 2:
+        raise ValueError("state must be a [N, C] tensor")
+    dev, (N, C) = state.device, state.shape
+    _need_on(x, "x", dev, None, (N, C))
+    _need_on(gate, "gate", dev, None, (N, C))
+    with _on(dev, stream) as st:
+        if h is None:
+            h = torch.empty_like(x, dtype=torch.float32 if out_dtype is None else out_dtype)
+        else:
+            _need_on(h, "h", dev, out_dtype, (N, C))
+        none = (0, 0, 0)
+        _, desc, _ = _gated_scan_plan(False, (N, 1, C, _dtype_code(x.dtype), _dtype_code(gate.dtype),
+                                              _dtype_code(h.dtype), DR_F32, DR_F32) + modes, *(none,) * 6)
+        _check(lib().dr_gated_scan_step(desc, _ptr(x), _ptr(gate), _ptr(state), _ptr(h), st))
+    return h

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdeltarule.so")
 SOURCES = ["dr_abi.hip", "dr_chunk.hip", "dr_scan16.hip", "dr_prep16.hip", "dr_prepcg16.hip", "dr_decode.hip",
-           "dr_bwd.hip", "dr_bwd16.hip", "dr_linattn_abi.hip", "dr_linattn.hip", "dr_linattn32.hip", "dr_layernorm.hip"]
+           "dr_bwd.hip", "dr_bwd16.hip", "dr_linattn_abi.hip", "dr_linattn.hip", "dr_linattn32.hip", "dr_layernorm.hip",
+           "dr_seqops_abi.hip", "dr_rmsnorm.hip", "dr_rmsnorm_bwd.hip", "dr_conv.hip", "dr_scan.hip", "dr_scan_bwd.hip"]
 ARCH = os.environ.get("DR_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

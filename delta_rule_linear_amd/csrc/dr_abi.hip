@@ -268,6 +268,14 @@ dr_status dr_profile_end(dr_profile_report* report) {
     report->linear_attn_step_ms = ms[dr::kProfLaStep];
     report->layernorm_fwd_ms = ms[dr::kProfLnFwd];
     report->layernorm_bwd_ms = ms[dr::kProfLnBwd];
+    report->rmsnorm_fwd_ms = ms[dr::kProfRnFwd];
+    report->rmsnorm_bwd_ms = ms[dr::kProfRnBwd];
+    report->short_conv_fwd_ms = ms[dr::kProfScFwd];
+    report->short_conv_bwd_ms = ms[dr::kProfScBwd];
+    report->short_conv_step_ms = ms[dr::kProfScStep];
+    report->gated_scan_fwd_ms = ms[dr::kProfGsFwd];
+    report->gated_scan_bwd_ms = ms[dr::kProfGsBwd];
+    report->gated_scan_step_ms = ms[dr::kProfGsStep];
     return DR_OK;
 }
 

@@ -183,7 +183,9 @@ enum ProfSlot {
     kProfPrep = 0, kProfScan = 1, kProfDecode = 2,
     kProfBwdPrep = 3, kProfBwdFscan = 4, kProfBwdRscan = 5, kProfBwdPost = 6,
     kProfLaFwd = 7, kProfLaBwd = 8, kProfLaStep = 9, kProfLnFwd = 10, kProfLnBwd = 11,
-    kProfSlots = 12, kProfNone = -1
+    kProfRnFwd = 12, kProfRnBwd = 13, kProfScFwd = 14, kProfScBwd = 15, kProfScStep = 16,
+    kProfGsFwd = 17, kProfGsBwd = 18, kProfGsStep = 19,
+    kProfSlots = 20, kProfNone = -1
 };
 // two new timing events while timing is on (false otherwise)
 bool prof_events(hipEvent_t* start, hipEvent_t* stop);

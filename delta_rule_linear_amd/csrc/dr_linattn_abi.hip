@@ -14,79 +14,26 @@
 #include "dr_internal.h"
 #include "dr_layernorm.h"
 #include "dr_linattn.h"
+#include "dr_rows.h"
 
 using dr::align256;
-using dr::aligned16;
+using dr::check_aligned;
 using dr::check_disjoint;
+using dr::check_elements;
+using dr::check_rows_apart;
+using dr::check_strides;
+using dr::check_workspace;
+using dr::elem_size;
 using dr::fail;
+using dr::hip_status;
+using dr::Rows;
+using dr::rows_span;
 using dr::Span;
 using dr::valid_dtype;
 
 namespace {
 
 constexpr size_t kMaxGrid = (size_t)std::numeric_limits<int>::max() - 8;
-
-size_t elem_size(int dtype) { return dtype == DR_F32 ? 4 : 2; }
-
-// A strided argument of n[0] x n[1] x n[2] rows of `d` channels.
-struct Rows {
-    const char* name;
-    const void* p;
-    dr_strides s;
-    int64_t n[3];
-    int64_t d;
-    int dtype;
-};
-
-bool rows_empty(const Rows& r) { return r.n[0] == 0 || r.n[1] == 0 || r.n[2] == 0 || r.d == 0; }
-
-// Strides: not negative, and (vec) whole 16-byte pieces.  A dimension of one
-// has no stride.
-dr_status check_strides(const Rows& r, bool vec) {
-    const int64_t s[3] = {r.s.b, r.s.h, r.s.t};
-    const int64_t unit = 16 / (int64_t)elem_size(r.dtype);
-    for (int i = 0; i < 3; ++i) {
-        if (r.n[i] <= 1) continue;
-        if (s[i] < 0) return fail(DR_ERR_SHAPE, "%s has a negative stride (%lld)", r.name, (long long)s[i]);
-        if (vec && s[i] % unit)
-            return fail(DR_ERR_ALIGN, "%s: stride %lld is not a multiple of 16 bytes", r.name, (long long)s[i]);
-        if (vec && i == 2 && s[i] > ((int64_t)1 << 23))
-            return fail(DR_ERR_UNSUPPORTED, "%s: tokens %lld elements apart, at most 2^23 are supported", r.name,
-                        (long long)s[i]);
-        if (s[i] > ((int64_t)1 << 48) / (r.n[i] - 1))
-            return fail(DR_ERR_SHAPE, "%s: stride %lld too large", r.name, (long long)s[i]);
-    }
-    return DR_OK;
-}
-
-// An output's rows must not share memory: taken by size, every stride reaches
-// behind what the smaller ones cover.
-dr_status check_rows_apart(const Rows& r) {
-    if (rows_empty(r)) return DR_OK;
-    int64_t s[3] = {r.s.b, r.s.h, r.s.t}, n[3] = {r.n[0], r.n[1], r.n[2]};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (s[j] < s[i]) {
-                std::swap(s[i], s[j]);
-                std::swap(n[i], n[j]);
-            }
-    int64_t extent = r.d;
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        if (s[i] < extent) return fail(DR_ERR_UNSUPPORTED, "%s: its strides make rows overlap", r.name);
-        extent += (n[i] - 1) * s[i];
-    }
-    return DR_OK;
-}
-
-Span rows_span(const Rows& r) {
-    if (!r.p || rows_empty(r)) return {nullptr, 0, r.name};
-    int64_t last = r.d;
-    const int64_t s[3] = {r.s.b, r.s.h, r.s.t};
-    for (int i = 0; i < 3; ++i)
-        if (r.n[i] > 1) last += (r.n[i] - 1) * s[i];
-    return {r.p, (size_t)last * elem_size(r.dtype), r.name};
-}
 
 // A single token's row is as far from the next as it is wide: the kernels tell
 // the rows of a chunk apart by their addresses.
@@ -189,25 +136,6 @@ dr_status check_la_desc(const dr_linattn_desc* d, bool bwd) {
     return DR_OK;
 }
 
-dr_status check_workspace(size_t need, const void* ws, size_t bytes) {
-    if (!need) return DR_OK;
-    if (!ws) return fail(DR_ERR_WORKSPACE, "workspace is NULL, %zu bytes needed", need);
-    if (bytes < need) return fail(DR_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", bytes, need);
-    return DR_OK;
-}
-
-dr_status check_aligned(const Span* t, int n) {
-    for (int i = 0; i < n; ++i)
-        if (t[i].p && !aligned16(t[i].p)) return fail(DR_ERR_ALIGN, "%s is not 16-byte aligned", t[i].name);
-    return DR_OK;
-}
-
-// Read and written one element at a time.
-dr_status check_elements(const void* p, size_t elem, const char* name) {
-    if ((uintptr_t)p % elem) return fail(DR_ERR_ALIGN, "%s is not %zu-byte aligned", name, elem);
-    return DR_OK;
-}
-
 // log alpha, and its gradient, are taken one value at a time: a table's row of one
 // value per head, or the sequences of a batch that are no multiples of 16 bytes,
 // start at any of them.
@@ -215,10 +143,6 @@ dr_status check_decay_aligned(int decay, int64_t row, const float* p, const char
     if (decay == DR_DECAY_HEAD || row % 4) return check_elements(p, 4, name);
     const Span t{p, 4, name};
     return check_aligned(&t, 1);
-}
-
-dr_status hip_status(hipError_t e, const char* what) {
-    return e == hipSuccess ? DR_OK : fail(DR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // One launch of passes that run in the same kernel on the same tiling.

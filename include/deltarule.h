@@ -39,8 +39,8 @@
  *                     the input values; a zero vector stays zero) -- the
  *                     L2 normalisation after the key/query feature map of the
  *                     DeltaNet page, step list, step 2.  The learned parts of
- *                     that map (a projection, SiLU, a short convolution) are
- *                     the caller's.
+ *                     that map are the caller's (the short convolution and its
+ *                     SiLU: dr_short_conv_fwd, below).
  *   DR_IN_BETA_LOGIT  the beta arrays (beta_k and beta_v too) hold logits x,
  *                     and beta = 1 / (1 + e^{-x}) -- beta from a sigmoid
  *                     projection (DeltaNet page, list of design choices).
@@ -98,7 +98,7 @@
 extern "C" {
 #endif
 
-#define DR_ABI_VERSION 11
+#define DR_ABI_VERSION 12
 
 typedef enum {
     DR_OK = 0,
@@ -636,10 +636,230 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
                            size_t workspace_bytes, void* stream);
 
 /*
+ * Operators of the layer around a recurrence: the root-mean-square norm with the
+ * residual's addition (and an output in 8 bits), the short causal convolution, and
+ * the gated linear recurrence.  The conventions at the top of this file hold but
+ * for alignment: a tensor's rows may start at any element (any width, stride or
+ * slice), so tensors need the alignment of one element; a workspace 16 bytes.
+ * Sums, states and statistics are fp32; every sum has a fixed order: repeated calls
+ * give the same bits.  Strides as above; .h is ignored where rows are [B][L].
+ */
+
+/*
+ * RMS norm over the channels of rows:
+ *
+ *   s = x + residual,  y = s rstd weight,  rstd = 1 / sqrt(mean(s^2) + eps)
+ *
+ * y and rstd come from the sum in fp32; `total` receives it rounded to the
+ * residual's type (the residual stream's next value).  Backward, for s as written
+ * (or x where there is no residual) and a gradient ds that reaches it besides:
+ *
+ *   dx = ds + rstd (t - n mean(t n)),  n = s rstd,  t = dy weight,  dweight = sum of dy n
+ *
+ * dx is the gradient of x and of the residual.  Squares are fp32: rows with values
+ * beyond 2^63 have rstd 0.
+ *
+ *   B, H, L, D, per_head, eps  as in dr_layernorm_desc; D in [1, 16384]
+ *   x_dtype    of x
+ *   res_dtype  of the residual and total: x_dtype or DR_F32; backward: of ds, any
+ *   y_dtype    of y, or of dx
+ *   dy_dtype   of dy (backward)
+ *   block      dr_rmsnorm_fwd_e4m3: 128, or 0 for one scale per row
+ *   x, res, y, total, dy  strides (y: of y or dx; res: of the residual or ds)
+ */
+typedef struct {
+    int B, H, L, D;
+    int per_head;
+    dr_dtype x_dtype, res_dtype, y_dtype, dy_dtype;
+    float eps;
+    int block;
+    dr_strides x, res, y, total, dy;
+} dr_rmsnorm_desc;
+
+/*
+ * dr_rmsnorm_fwd
+ *   x         [B][H][L][D] x_dtype, strided
+ *   residual  [B][H][L][D] res_dtype, strided, or NULL
+ *   weight    [H][D] or [D] fp32, or NULL (ones)
+ *   y         [B][H][L][D] y_dtype, strided, written
+ *   total     [B][H][L][D] res_dtype, strided, written; NULL iff residual is
+ *   rstd      [B][H][L] fp32, written, or NULL to skip
+ */
+dr_status dr_rmsnorm_fwd(const dr_rmsnorm_desc* d, const void* x, const void* residual, const float* weight, void* y,
+                         void* total, float* rstd, void* stream);
+
+/*
+ * dr_rmsnorm_fwd_e4m3 -- dr_rmsnorm_fwd with y in 8 bits, for products that read it
+ * with scales:
+ *
+ *   y ~ scale code,   scale = max(amax / 448, 2^-126),  code = y / scale in e4m3
+ *
+ * amax is the largest |y| of each 128 columns (the last ones of a row may be fewer)
+ * or of the row; a code is the nearest e4m3 value to y / scale (4 exponent bits, 3 behind the
+ * leading one, largest value 448, no infinities), ties to even.  A NaN is a code of
+ * its own; with an infinity in a block its scale is infinite and its codes NaN.
+ *
+ *   y      [B][H][L][D] bytes, strided (in bytes), written; y_dtype is ignored
+ *   scale  [B][H][L][ceil(D / 128)], or [B][H][L] with block 0; fp32, written
+ */
+dr_status dr_rmsnorm_fwd_e4m3(const dr_rmsnorm_desc* d, const void* x, const void* residual, const float* weight,
+                              void* y, float* scale, void* total, float* rstd, void* stream);
+
+/* Bytes of device workspace dr_rmsnorm_bwd needs for `d` when dweight is wanted (0
+ * if d is invalid or there are no rows). */
+size_t dr_rmsnorm_bwd_workspace_bytes(const dr_rmsnorm_desc* d);
+
+/*
+ * dr_rmsnorm_bwd
+ *   x          [B][H][L][D] x_dtype, strided: the forward's total, or its x
+ *   rstd       [B][H][L] fp32, as the forward wrote it
+ *   dy         [B][H][L][D] dy_dtype, strided
+ *   ds         [B][H][L][D] res_dtype, strided as d->res, or NULL
+ *   dx         [B][H][L][D] y_dtype, strided as d->y, written
+ *   dweight    [H][D] or [D] fp32, written, or NULL to skip
+ *   workspace  at least dr_rmsnorm_bwd_workspace_bytes(d) bytes, apart from every
+ *              tensor; may be NULL when dweight is
+ */
+dr_status dr_rmsnorm_bwd(const dr_rmsnorm_desc* d, const void* x, const float* weight, const float* rstd,
+                         const void* dy, const void* ds, void* dx, float* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Short causal convolution of each channel (the feature map of the DeltaNet page's
+ * list of design choices), with or without SiLU:
+ *
+ *   z_t = bias + sum over j < W of w_j x_{t-W+1+j},   y_t = z_t or z_t sigmoid(z_t)
+ *
+ * Tokens before the first come from a state of W - 1 rows, oldest first (zeros
+ * without one); the final state is the last W - 1 rows, as the next call takes it.
+ *
+ *   B, L >= 0; C >= 1 channels; W in [2, 8]
+ *   x_dtype of x and the state, y_dtype of y or dx, dy_dtype of dy (backward)
+ *   x, y, dy strides (y: of y or dx)
+ */
+typedef enum { DR_ACT_NONE = 0, DR_ACT_SILU = 1 } dr_activation;
+
+typedef struct {
+    int B, L, C, W;
+    dr_dtype x_dtype, y_dtype, dy_dtype;
+    dr_activation act;
+    dr_strides x, y, dy;
+} dr_short_conv_desc;
+
+/*
+ * dr_short_conv_fwd
+ *   x          [B][L][C] x_dtype, strided
+ *   weight     [C][W] fp32;  bias [C] fp32 or NULL
+ *   state      [B][W-1][C] x_dtype, or NULL for zeros
+ *   y          [B][L][C] y_dtype, strided, written
+ *   state_out  [B][W-1][C] x_dtype, written, or NULL to skip; may be state itself
+ */
+dr_status dr_short_conv_fwd(const dr_short_conv_desc* d, const void* x, const float* weight, const float* bias,
+                            const void* state, void* y, void* state_out, void* stream);
+
+/* Bytes of device workspace dr_short_conv_bwd needs for `d` when dweight or dbias is
+ * wanted (0 if d is invalid or there is no work). */
+size_t dr_short_conv_bwd_workspace_bytes(const dr_short_conv_desc* d);
+
+/*
+ * dr_short_conv_bwd -- gradients of dr_short_conv_fwd's y and state_out.
+ *   dy             [B][L][C] dy_dtype, strided
+ *   dstate_out     [B][W-1][C] fp32, or NULL (zero)
+ *   dx             [B][L][C] y_dtype, strided as d->y, written
+ *   dweight, dbias [C][W], [C] fp32, written, or NULL to skip
+ *   dstate         [B][W-1][C] fp32, written, or NULL to skip
+ *   workspace      at least dr_short_conv_bwd_workspace_bytes(d) bytes, apart from
+ *                  every tensor; may be NULL when dweight and dbias are
+ */
+dr_status dr_short_conv_bwd(const dr_short_conv_desc* d, const void* x, const float* weight, const float* bias,
+                            const void* state, const void* dy, const float* dstate_out, void* dx, float* dweight,
+                            float* dbias, float* dstate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dr_short_conv_step -- one token for d->B states, in place: y [B][C] of x [B][C]
+ * (dense; L and the strides are ignored), state [B][W-1][C] x_dtype moved on by a row.
+ * The same as dr_short_conv_fwd with L == 1 and state_out == state.
+ */
+dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const float* weight, const float* bias,
+                             void* state, void* y, void* stream);
+
+/*
+ * Gated linear recurrence, a state of one value per channel:
+ *
+ *   h_t = a_t h_{t-1} + c(a_t) x_t
+ *
+ *   decay   DR_SCAN_LOG    a = e^gate, gate expected <= 0 (not checked)
+ *           DR_SCAN_LOGIT  a = 1 / (1 + e^-gate)
+ *   inputs  DR_INPUT_PLAIN c = 1;  DR_INPUT_BLEND c = 1 - a;
+ *           DR_INPUT_UNIT  c = sqrt(1 - a^2), which keeps the variance of unit
+ *                          inputs (NaN for a > 1)
+ *
+ * A log of -inf (a = 0) starts the state anew at that token.  1 - a is made
+ * directly and a kept in two parts, so that memories of many tokens cost no
+ * accuracy.  A NaN or Inf reaches the later tokens of its channel, also through a
+ * zero decay, and no other channel.  Gradients, from the forward's h as it was
+ * written (rounded where that is bf16):
+ *
+ *   d_t = dh_t + a_{t+1} d_{t+1} (the last: dh_L + dh_final),   dx = c d,   dh0 = a_1 d_1
+ *   dgate = d (h_{t-1} + c'(a) x) da/dgate,   c' = 0, -1 or -a / c
+ * (where c = 0, at a = 1, the unit form's last term is left out).
+ *
+ *   B, L >= 0; C >= 1
+ *   x_dtype of x; gate_dtype x_dtype or DR_F32; h_dtype of h; dh_dtype of dh;
+ *   grad_dtype of dx and dgate (the last two: backward only)
+ */
+typedef enum { DR_SCAN_LOG = 0, DR_SCAN_LOGIT = 1 } dr_scan_decay;
+typedef enum { DR_INPUT_PLAIN = 0, DR_INPUT_BLEND = 1, DR_INPUT_UNIT = 2 } dr_scan_inputs;
+
+typedef struct {
+    int B, L, C;
+    dr_dtype x_dtype, gate_dtype, h_dtype, dh_dtype, grad_dtype;
+    dr_scan_decay decay;
+    dr_scan_inputs inputs;
+    dr_strides x, gate, h, dh, dx, dgate;
+} dr_gated_scan_desc;
+
+/* Bytes of device workspace dr_gated_scan_fwd and dr_gated_scan_bwd need for `d` (0
+ * if d is invalid or none is needed). */
+size_t dr_gated_scan_fwd_workspace_bytes(const dr_gated_scan_desc* d);
+size_t dr_gated_scan_bwd_workspace_bytes(const dr_gated_scan_desc* d);
+
+/*
+ * dr_gated_scan_fwd -- h_t for t = 0..L-1, from h0.
+ *   x        [B][L][C] x_dtype, strided;  gate [B][L][C] gate_dtype, strided
+ *   h0       [B][C] fp32, or NULL for zeros
+ *   h        [B][L][C] h_dtype, strided, written
+ *   h_final  [B][C] fp32, written, or NULL to skip; may be h0 itself
+ *   workspace  at least dr_gated_scan_fwd_workspace_bytes(d) bytes; calls in flight
+ *              at the same time need workspaces of their own
+ */
+dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const void* gate, const float* h0, void* h,
+                            float* h_final, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dr_gated_scan_bwd
+ *   h          [B][L][C] h_dtype, strided, the forward's;  dh [B][L][C] dh_dtype, strided
+ *   dh_final   [B][C] fp32, or NULL (zero)
+ *   dx, dgate  [B][L][C] grad_dtype, strided, written
+ *   dh0        [B][C] fp32, written, or NULL to skip
+ *   x is not read with DR_INPUT_PLAIN.
+ */
+dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const void* gate, const float* h0,
+                            const void* h, const void* dh, const float* dh_final, void* dx, void* dgate, float* dh0,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dr_gated_scan_step -- one token for d->B states, in place: state [B][C] fp32 is
+ * moved on and written to h [B][C] in h_dtype; x and gate [B][C].  Dense; L and the
+ * strides are ignored.
+ */
+dr_status dr_gated_scan_step(const dr_gated_scan_desc* d, const void* x, const void* gate, float* state, void* h,
+                             void* stream);
+
+/*
  * Per-kernel timing, for benchmarks and profiling (not part of the method).
- * Between dr_profile_begin and dr_profile_end every chunked-forward, backward,
- * decode, linear-attention and layer-norm call launches each of its kernels with
- * a start and a stop event of its own, set from the kernel dispatch's timestamps (no marker packets
+ * Between dr_profile_begin and dr_profile_end every call of an entry point above
+ * launches each of its kernels with a start and a stop event of its own, set from the kernel dispatch's timestamps (no marker packets
  * between the kernels); dr_profile_end waits for those events and reports the
  * summed kernel durations.  Calls made while profiling must come from one
  * host thread.  dr_profile_begin discards any earlier unreported records.  The
@@ -664,6 +884,14 @@ typedef struct dr_profile_report {
     double linear_attn_step_ms;  /* of dr_linear_attn_step calls */
     double layernorm_fwd_ms;     /* of dr_layernorm_fwd calls */
     double layernorm_bwd_ms;     /* of dr_layernorm_bwd calls */
+    double rmsnorm_fwd_ms;       /* of dr_rmsnorm_fwd and dr_rmsnorm_fwd_e4m3 calls */
+    double rmsnorm_bwd_ms;       /* of dr_rmsnorm_bwd calls */
+    double short_conv_fwd_ms;    /* of dr_short_conv_fwd calls */
+    double short_conv_bwd_ms;    /* of dr_short_conv_bwd calls */
+    double short_conv_step_ms;   /* of dr_short_conv_step calls */
+    double gated_scan_fwd_ms;    /* of dr_gated_scan_fwd calls */
+    double gated_scan_bwd_ms;    /* of dr_gated_scan_bwd calls */
+    double gated_scan_step_ms;   /* of dr_gated_scan_step calls */
 } dr_profile_report;
 
 dr_status dr_profile_begin(void);
