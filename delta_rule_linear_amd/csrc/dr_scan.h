@@ -96,4 +96,99 @@ __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
     x[7] = b.w;
 }
 
+// ---------------------------------------------------------------- long sequences
+// With few sequences each tile of a sequence has a workgroup of its own.  A workgroup
+// draws its tile from a counter, tiles in the order that the state passes them, so
+// that the tiles before its own belong to workgroups that already run.  It publishes
+// the map of its tile, h -> A h + B for each channel, before it waits for anything;
+// then it takes the maps of the tiles before it, in their order (the same one every
+// time), back to the last tile whose number is a multiple of kGsGroup, whose state at
+// the start is published as well.  So no wait goes on without end: maps depend on
+// nothing, and the state at a group's start on earlier tiles only.
+//
+// A map is one 64-bit word (A in the low half, B in the high one), a state another,
+// so that a word is whole when it is there at all; until then it is kGsAbsent, which
+// launch_gs_clear writes first.  Between tiles A is rounded to 24 bits, which costs half a
+// rounding of the state per tile.
+constexpr uint64_t kGsAbsent = ~(uint64_t)0;
+
+__device__ __forceinline__ void gs_publish(uint64_t* to, float a, float b) {
+    uint64_t v = ((uint64_t)__float_as_uint(b) << 32) | __float_as_uint(a);
+    if (v == kGsAbsent) v = 0x7fc000007fc00000u;   // two NaN of the one kind that means "not there"
+    __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t gs_peek(const uint64_t* from) {
+    return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that tile `seg` starts with, for one channel: maps [seg][128] and the
+// groups' states [group][128] of its column.
+__device__ __forceinline__ float gs_wait(const uint64_t* maps, const uint64_t* states, int seg) {
+    const int group = seg / kGsGroup, n = seg - group * kGsGroup;
+    // all words at once; where there are fewer maps, the last one again
+    uint64_t m[kGsGroup];
+    bool all;
+    do {
+#pragma unroll
+        for (int i = 0; i < kGsGroup - 1; ++i) m[i] = gs_peek(maps + (size_t)(group * kGsGroup + max(min(i, n - 1), 0)) * kGsTile);
+        m[kGsGroup - 1] = gs_peek(states + (size_t)group * kGsTile);
+        all = group == 0 || m[kGsGroup - 1] != kGsAbsent;
+#pragma unroll
+        for (int i = 0; i < kGsGroup - 1; ++i) all = all && (i >= n || m[i] != kGsAbsent);
+        if (!all) __builtin_amdgcn_s_sleep(1);
+    } while (!all);
+    if (group == 0) m[kGsGroup - 1] = 0;   // the first tile's map holds what came in
+    float h = __uint_as_float((unsigned)m[kGsGroup - 1]);
+#pragma unroll
+    for (int i = 0; i < kGsGroup - 1; ++i)
+        if (i < n) h = __builtin_fmaf(__uint_as_float((unsigned)m[i]), h, __uint_as_float((unsigned)(m[i] >> 32)));
+    return h;
+}
+
+// Which tile a workgroup has.
+__device__ __forceinline__ unsigned gs_draw(unsigned* counter, unsigned* lds) {
+    if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return *lds;
+}
+
+// Joins a tile's runs, [k][128] maps in LDS, for channel c; the state each run starts
+// with takes the place of its B.  FWD: runs from the first to the last.
+template <bool FWD>
+__device__ __forceinline__ float gs_join(const float* shH, const float* shL, float* shB, int ntg, int c, float h) {
+#pragma unroll 4
+    for (int i = 0; i < ntg; ++i) {
+        const int at = (FWD ? i : ntg - 1 - i) * kGsTile + c;
+        const float start = h;
+        h = gs_apply(shH[at], shL[at], h, shB[at]);
+        shB[at] = start;
+    }
+    return h;
+}
+// The same through the other workgroups: `first` is what the first tile starts with.
+template <bool FWD>
+__device__ __forceinline__ float gs_join_far(const GsArgs& a, const float* shH, const float* shL, float* shB, int c,
+                                             unsigned col, int seg, float first) {
+    float H = 1.f, L = 0.f, B = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < a.groups; ++i) {
+        const int at = (FWD ? i : a.groups - 1 - i) * kGsTile + c;
+        B = gs_apply(shH[at], shL[at], B, shB[at]);
+        gs_times(H, L, shH[at], shL[at]);
+    }
+    uint64_t* maps = a.maps + (size_t)col * a.nseg * kGsTile + c;
+    uint64_t* states = a.states + (size_t)col * ((a.nseg + kGsGroup - 1) / kGsGroup) * kGsTile + c;
+    float h = first;
+    if (seg == 0) {
+        // what comes in is part of the first tile's map, so that nobody else reads it
+        if (a.nseg > 1) gs_publish(maps, 0.f, gs_apply(H, L, h, B));
+    } else {
+        if (seg + 1 < a.nseg) gs_publish(maps + (size_t)seg * kGsTile, H + L, B);
+        h = gs_wait(maps, states, seg);
+        if (seg % kGsGroup == kGsGroup - 1 && seg + 1 < a.nseg)
+            gs_publish(states + (size_t)(seg / kGsGroup + 1) * kGsTile, gs_apply(H, L, h, B), 0.f);
+    }
+    return gs_join<FWD>(shH, shL, shB, a.groups, c, h);
+}
+
 }  // namespace dr

@@ -14,26 +14,31 @@ constexpr int kRun = 4;
 
 int gs_run(bool) { return kRun; }
 
-template <bool FX, bool FG, int DEC, int INP, bool SMALL>
+// FAR: a tile of a long sequence (dr_scan.h), else whole sequences, tile by tile.
+template <bool FX, bool FG, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(512) void gs_fwd_kernel(GsArgs a) {
     constexpr int T = kRun;
     extern __shared__ float lds[];
-    const int ntg = a.groups, tid = threadIdx.x, lane = tid & 15, tg = tid >> 4;
+    __shared__ unsigned drawn;
+    const int ntg = a.groups, tid = threadIdx.x, lane = tid & 15, tg = tid >> 4, span = ntg * T;
     float* carry = lds;                        // [128] the state between tiles
     float* shH = carry + kGsTile;              // [ntg][128] the runs' maps: A in two parts, B
     float* shL = shH + ntg * kGsTile;
     float* shB = shL + ntg * kGsTile;          // then the state that each run starts with
     const unsigned nct = ((unsigned)a.C + kGsTile - 1) / kGsTile;
     const int xs = a.x_f32 ? 4 : 2, gs = a.g_f32 ? 4 : 2, os = a.out_f32 ? 4 : 2;
-    for (unsigned col = blockIdx.x; col < a.columns; col += gridDim.x) {
+    const unsigned tile = FAR ? gs_draw(a.counter, &drawn) : 0;
+    const int seg = FAR ? (int)(tile / a.columns) : 0;
+    for (unsigned col = FAR ? tile - seg * a.columns : blockIdx.x; col < a.columns; col += gridDim.x) {
         const unsigned b = col / nct, ct = col - b * nct;
         const OctPlace pl = oct_place(ct * 16 + lane, a.C);
-        for (int c = tid; c < kGsTile; c += blockDim.x)
-            carry[c] = a.h0 ? a.h0[(size_t)b * a.C + oct_channel<SMALL>(ct * 16 + (c >> 3), c & 7, a.C)] : 0.f;
+        if (!FAR || seg == 0)
+            for (int c = tid; c < kGsTile; c += blockDim.x)
+                carry[c] = a.h0 ? a.h0[(size_t)b * a.C + oct_channel<SMALL>(ct * 16 + (c >> 3), c & 7, a.C)] : 0.f;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
         const char* gb = (const char*)a.g + b * a.sg.b * gs;
         char* ob = (char*)a.out + b * a.so.b * os;
-        for (int t0 = 0; t0 < a.L; t0 += ntg * T) {
+        for (int t0 = FAR ? seg * span : 0; t0 < a.L; t0 += span) {
             const int t = t0 + tg * T;
             Oct<FX> x[T];
             Oct<FG> g[T];
@@ -67,15 +72,8 @@ __global__ __launch_bounds__(512) void gs_fwd_kernel(GsArgs a) {
             gs_put(shB + tg * kGsTile + lane * 8, B);
             __syncthreads();
             for (int c = tid; c < kGsTile; c += blockDim.x) {
-                float s = carry[c];
-#pragma unroll 4
-                for (int k = 0; k < ntg; ++k) {
-                    const int at = k * kGsTile + c;
-                    const float start = s;
-                    s = gs_apply(shH[at], shL[at], s, shB[at]);
-                    shB[at] = start;
-                }
-                carry[c] = s;
+                if constexpr (FAR) carry[c] = gs_join_far<true>(a, shH, shL, shB, c, col, seg, carry[c]);
+                else carry[c] = gs_join<true>(shH, shL, shB, ntg, c, carry[c]);
             }
             __syncthreads();
             float s[8];
@@ -87,15 +85,29 @@ __global__ __launch_bounds__(512) void gs_fwd_kernel(GsArgs a) {
                 if (t + i < a.L && pl.own)
                     oct_store<SMALL>(ob + (int64_t)(t + i) * a.so.t * os, a.out_f32, pl, s);
             }
+            if constexpr (FAR) break;
             __syncthreads();   // the starts are read before the next tile's maps come
         }
-        if (a.last)
+        if (a.last && (!FAR || seg + 1 == a.nseg))
             for (int c = tid; c < kGsTile; c += blockDim.x) {
                 const OctPlace p = oct_place(ct * 16 + (c >> 3), a.C);
                 if (oct_own<SMALL>(p, c & 7)) a.last[(size_t)b * a.C + p.at + (c & 7)] = carry[c];
             }
+        if constexpr (FAR) break;
         __syncthreads();
     }
+}
+
+// The words of a call's maps and states, before its tiles are drawn.
+__global__ __launch_bounds__(256) void gs_clear_kernel(uint64_t* p, size_t n, unsigned* counter) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = kGsAbsent;
+}
+
+hipError_t launch_gs_clear(const GsArgs& a, int slot, hipStream_t st) {
+    const size_t blocks = (a.words + 255) / 256;
+    return launch_k(slot, gs_clear_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, a.maps,
+                    a.words, a.counter);
 }
 
 // One token: h <- a h + c x, and h in the output's type.  A lane has eight channels
@@ -133,8 +145,15 @@ static hipError_t gs_launch(const GsArgs& a, bool step, int slot, hipStream_t st
         return launch_k(slot, gs_step_kernel<FX, FG, DEC, INP, SMALL>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
                         dim3(256), 0, st, a);
     }
-    return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL>, dim3(a.columns < 65536 ? a.columns : 65536),
-                    dim3(16 * a.groups), (1 + 3 * a.groups) * kGsTile * 4, st, a);
+    const unsigned lds = (1 + 3 * a.groups) * kGsTile * 4;
+    if (a.nseg > 1) {
+        const hipError_t e = launch_gs_clear(a, slot, st);
+        if (e != hipSuccess) return e;
+        return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, true>, dim3(a.columns * a.nseg), dim3(16 * a.groups),
+                        lds, st, a);
+    }
+    return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536),
+                    dim3(16 * a.groups), lds, st, a);
 }
 
 template <int DEC, int INP>

@@ -13,10 +13,11 @@ namespace dr {
 
 constexpr int kRunBwd = 4;
 
-template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL>
+template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
     constexpr int T = kRunBwd;
     extern __shared__ float lds[];
+    __shared__ unsigned drawn;
     const int ntg = a.groups, tid = threadIdx.x, lane = tid & 15, tg = tid >> 4;
     float* carry = lds;
     float* shH = carry + kGsTile;
@@ -25,18 +26,22 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
     const unsigned nct = ((unsigned)a.C + kGsTile - 1) / kGsTile;
     const int xs = a.x_f32 ? 4 : 2, gs = a.g_f32 ? 4 : 2, hs = a.h_f32 ? 4 : 2, ds = a.dh_f32 ? 4 : 2,
               os = a.out_f32 ? 4 : 2, span = ntg * T;
-    for (unsigned col = blockIdx.x; col < a.columns; col += gridDim.x) {
+    // tiles in the order that the gradient passes them: the last tokens first
+    const unsigned tile = FAR ? gs_draw(a.counter, &drawn) : 0;
+    const int seg = FAR ? (int)(tile / a.columns) : 0;
+    for (unsigned col = FAR ? tile - seg * a.columns : blockIdx.x; col < a.columns; col += gridDim.x) {
         const unsigned b = col / nct, ct = col - b * nct;
         const OctPlace pl = oct_place(ct * 16 + lane, a.C);
-        for (int c = tid; c < kGsTile; c += blockDim.x)
-            carry[c] = a.dlast ? a.dlast[(size_t)b * a.C + oct_channel<SMALL>(ct * 16 + (c >> 3), c & 7, a.C)] : 0.f;
+        if (!FAR || seg == 0)
+            for (int c = tid; c < kGsTile; c += blockDim.x)
+                carry[c] = a.dlast ? a.dlast[(size_t)b * a.C + oct_channel<SMALL>(ct * 16 + (c >> 3), c & 7, a.C)] : 0.f;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
         const char* gb = (const char*)a.g + b * a.sg.b * gs;
         const char* hb = (const char*)a.h + b * a.sh.b * hs;
         const char* db = (const char*)a.dh + b * a.sdh.b * ds;
         char* ob = (char*)a.out + b * a.so.b * os;
         char* gob = (char*)a.dg + b * a.sdg.b * os;
-        for (int t0 = (a.L - 1) / span * span; t0 >= 0; t0 -= span) {
+        for (int t0 = FAR ? (a.nseg - 1 - seg) * span : (a.L - 1) / span * span; t0 >= 0; t0 -= span) {
             const int t = t0 + tg * T;
             Oct<FX> x[T];
             Oct<FG> g[T];
@@ -76,15 +81,8 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
             gs_put(shB + tg * kGsTile + lane * 8, B);
             __syncthreads();
             for (int c = tid; c < kGsTile; c += blockDim.x) {
-                float s = carry[c];
-#pragma unroll 4
-                for (int k = ntg - 1; k >= 0; --k) {
-                    const int at = k * kGsTile + c;
-                    const float start = s;
-                    s = gs_apply(shH[at], shL[at], s, shB[at]);
-                    shB[at] = start;
-                }
-                carry[c] = s;
+                if constexpr (FAR) carry[c] = gs_join_far<false>(a, shH, shL, shB, c, col, seg, carry[c]);
+                else carry[c] = gs_join<false>(shH, shL, shB, ntg, c, carry[c]);
             }
             __syncthreads();
             float s[8];
@@ -121,21 +119,30 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
                     oct_store<SMALL>(gob + (int64_t)(t + i) * a.sdg.t * os, a.out_f32, pl, dg);
                 }
             }
+            if constexpr (FAR) break;
             __syncthreads();
         }
-        if (a.last)
+        if (a.last && (!FAR || seg + 1 == a.nseg))
             for (int c = tid; c < kGsTile; c += blockDim.x) {
                 const OctPlace p = oct_place(ct * 16 + (c >> 3), a.C);
                 if (oct_own<SMALL>(p, c & 7)) a.last[(size_t)b * a.C + p.at + (c & 7)] = carry[c];
             }
+        if constexpr (FAR) break;
         __syncthreads();
     }
 }
 
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL>
 static hipError_t gs_launch(const GsArgs& a, int slot, hipStream_t st) {
-    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL>, dim3(a.columns < 65536 ? a.columns : 65536),
-                    dim3(16 * a.groups), (1 + 3 * a.groups) * kGsTile * 4, st, a);
+    const unsigned lds = (1 + 3 * a.groups) * kGsTile * 4;
+    if (a.nseg > 1) {
+        const hipError_t e = launch_gs_clear(a, slot, st);
+        if (e != hipSuccess) return e;
+        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.columns * a.nseg),
+                        dim3(16 * a.groups), lds, st, a);
+    }
+    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>,
+                    dim3(a.columns < 65536 ? a.columns : 65536), dim3(16 * a.groups), lds, st, a);
 }
 
 template <bool FX, bool FG, int DEC, int INP>

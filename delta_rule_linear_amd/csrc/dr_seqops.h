@@ -84,10 +84,12 @@ struct GsArgs {
     SeqRows sx, sg, sh, sdh, so, sdg;
     int B, L, C;
     int groups;           // runs of tokens side by side in a workgroup
-    int nseg;             // workgroups along a sequence
+    int nseg;             // workgroups along a sequence (1: one that walks its tiles)
     unsigned columns;     // B times the channel tiles
-    uint64_t* ends;       // nseg > 1: [columns][nseg][128] what each workgroup did
-    unsigned* ticket;
+    uint64_t* maps;       // nseg > 1: [columns][nseg][128], what each tile does to the state
+    uint64_t* states;     // [columns][groups of tiles][128], what each group starts with
+    unsigned* counter;    // tiles drawn; stands in front of the maps and the states
+    size_t words;         // 64-bit words of all three
     int x_f32, g_f32, h_f32, dh_f32, out_f32;
     int logit;            // decay: 0 e^g, 1 sigmoid(g)
     int inputs;           // 0 plain, 1 blend, 2 unit
@@ -96,6 +98,8 @@ constexpr int kGsTile = 128;   // channels of a workgroup
 int gs_run(bool bwd);          // tokens of a thread
 hipError_t launch_gs_fwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_bwd(const GsArgs& a, int slot, hipStream_t st);
+hipError_t launch_gs_clear(const GsArgs& a, int slot, hipStream_t st);
+constexpr int kGsGroup = 8;    // tiles between two published states
 hipError_t launch_gs_step(const GsArgs& a, int slot, hipStream_t st);
 
 }  // namespace dr

@@ -445,13 +445,48 @@ dr_status check_gs_desc(const dr_gated_scan_desc* d) {
 }
 
 // Runs side by side in a workgroup: the least power of two that covers the tokens,
-// 4 (a wave) to 32.
-void gs_split(const dr_gated_scan_desc& d, bool bwd, dr::GsArgs& a) {
+// 4 (a wave) to 32.  Sequences of several such tiles whose columns (128 channels of
+// one) are too few to fill the chip have a workgroup for each tile.
+constexpr int64_t kGsColumns = 512;
+
+struct GsLayout {
+    int groups, nseg;
+    size_t counter, maps, states, total;   // bytes
+};
+
+GsLayout gs_layout(const dr_gated_scan_desc& d, bool bwd) {
+    GsLayout w{};
     const int run = dr::gs_run(bwd);
-    a.groups = 4;
-    while (a.groups < 32 && (int64_t)a.groups * run < d.L) a.groups *= 2;
+    w.groups = 4;
+    while (w.groups < 32 && (int64_t)w.groups * run < d.L) w.groups *= 2;
+    const int64_t columns = d.B * channel_tiles(d.C), span = (int64_t)w.groups * run, tiles = (d.L + span - 1) / span;
+    w.nseg = columns < kGsColumns ? (int)tiles : 1;
+    if (w.nseg > 1) {
+        w.maps = 256;   // the counter is in front
+        w.states = w.maps + (size_t)columns * w.nseg * dr::kGsTile * 8;
+        w.total = w.states + (size_t)columns * ((w.nseg + dr::kGsGroup - 1) / dr::kGsGroup) * dr::kGsTile * 8;
+    }
+    return w;
+}
+
+dr_status check_gs_tiles(const dr_gated_scan_desc& d, const GsLayout& w) {
+    // a launch holds fewer than 2^32 threads
+    if (w.nseg > 1 && (double)d.B * channel_tiles(d.C) * w.nseg * 16 * w.groups > 4294967295.0)
+        return fail(DR_ERR_UNSUPPORTED, "B*C*L=%.0f too large", (double)d.B * d.C * d.L);
+    return DR_OK;
+}
+
+void gs_split(const dr_gated_scan_desc& d, const GsLayout& w, void* workspace, dr::GsArgs& a) {
+    a.groups = w.groups;
+    a.nseg = w.nseg;
     a.columns = (unsigned)(d.B * channel_tiles(d.C));
-    a.nseg = 1;
+    char* ws = (char*)workspace;
+    if (w.nseg > 1) {
+        a.counter = (unsigned*)(ws + w.counter);
+        a.maps = (uint64_t*)(ws + w.maps);
+        a.states = (uint64_t*)(ws + w.states);
+        a.words = (w.total - w.maps) / 8;
+    }
 }
 
 void gs_args(const dr_gated_scan_desc& d, const void* x, const void* gate, const float* h0, dr::GsArgs& a) {
@@ -471,24 +506,20 @@ void gs_args(const dr_gated_scan_desc& d, const void* x, const void* gate, const
     a.inputs = d.inputs;
 }
 
-size_t gs_workspace(const dr_gated_scan_desc& d, bool bwd) {
-    (void)d;
-    (void)bwd;
-    return 0;
-}
-
 }  // namespace
 
 extern "C" {
 
 size_t dr_gated_scan_fwd_workspace_bytes(const dr_gated_scan_desc* d) {
     if (check_gs_desc(d) != DR_OK || d->B == 0 || d->L == 0) return 0;
-    return gs_workspace(*d, false);
+    const GsLayout w = gs_layout(*d, false);
+    return check_gs_tiles(*d, w) == DR_OK ? w.total : 0;
 }
 
 size_t dr_gated_scan_bwd_workspace_bytes(const dr_gated_scan_desc* d) {
     if (check_gs_desc(d) != DR_OK || d->B == 0 || d->L == 0) return 0;
-    return gs_workspace(*d, true);
+    const GsLayout w = gs_layout(*d, true);
+    return check_gs_tiles(*d, w) == DR_OK ? w.total : 0;
 }
 
 dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const void* gate, const float* h0, void* h,
@@ -504,7 +535,9 @@ dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const vo
                rg = seq_tensor("gate", gate, d->B, d->L, d->C, d->gate, d->gate_dtype),
                rh = seq_tensor("h", h, d->B, d->L, d->C, d->h, d->h_dtype);
     if ((s = check_rows({&rx, &rg}, {&rh})) != DR_OK) return s;
-    const size_t need = d->L ? gs_workspace(*d, false) : 0;
+    const GsLayout w = d->L ? gs_layout(*d, false) : GsLayout{};
+    if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
+    const size_t need = w.total;
     const Span ins[] = {rows_span(rx), rows_span(rg), {h0, state, "h0"}};
     const Span outs[] = {rows_span(rh), {h_final, state, "h_final"}, {workspace, need, "workspace"}};
     if ((s = check_starts({{x, elem_size(d->x_dtype), "x"}, {gate, elem_size(d->gate_dtype), "gate"}, {h0, 4, "h0"},
@@ -520,7 +553,7 @@ dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const vo
     }
     dr::GsArgs a{};
     gs_args(*d, x, gate, h0, a);
-    gs_split(*d, false, a);
+    gs_split(*d, w, workspace, a);
     a.out = h;
     a.so = seq_strides(d->B, d->L, d->h);
     a.out_f32 = d->h_dtype == DR_F32;
@@ -546,7 +579,9 @@ dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const vo
                rdx = seq_tensor("dx", dx, d->B, d->L, d->C, d->dx, d->grad_dtype),
                rdg = seq_tensor("dgate", dgate, d->B, d->L, d->C, d->dgate, d->grad_dtype);
     if ((s = check_rows({&rx, &rg, &rh, &rdh}, {&rdx, &rdg})) != DR_OK) return s;
-    const size_t need = d->L ? gs_workspace(*d, true) : 0;
+    const GsLayout w = d->L ? gs_layout(*d, true) : GsLayout{};
+    if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
+    const size_t need = w.total;
     const Span ins[] = {rows_span(rx), rows_span(rg), {h0, state, "h0"}, rows_span(rh), rows_span(rdh),
                         {dh_final, state, "dh_final"}};
     const Span outs[] = {rows_span(rdx), rows_span(rdg), {dh0, state, "dh0"}, {workspace, need, "workspace"}};
@@ -564,7 +599,7 @@ dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const vo
     }
     dr::GsArgs a{};
     gs_args(*d, x, gate, h0, a);
-    gs_split(*d, true, a);
+    gs_split(*d, w, workspace, a);
     a.h = h;
     a.dh = dh;
     a.dlast = dh_final;
