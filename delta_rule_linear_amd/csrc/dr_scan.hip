@@ -16,7 +16,7 @@ int gs_run(bool) { return kRun; }
 
 // FAR: a tile of a long sequence (dr_scan.h), else whole sequences, tile by tile.
 template <bool FX, bool FG, int DEC, int INP, bool SMALL, bool FAR>
-__global__ __launch_bounds__(512) void gs_fwd_kernel(GsArgs a) {
+__global__ __launch_bounds__(256) void gs_fwd_kernel(GsArgs a) {
     constexpr int T = kRun;
     extern __shared__ float lds[];
     __shared__ unsigned drawn;
@@ -48,16 +48,24 @@ __global__ __launch_bounds__(512) void gs_fwd_kernel(GsArgs a) {
                 oct_load<FX, SMALL>(xb + r * a.sx.t * xs, a.x_f32, pl.at, a.C, x[i]);
                 oct_load<FG, SMALL>(gb + r * a.sg.t * gs, a.g_f32, pl.at, a.C, g[i]);
             }
+            if (t0 + span > a.L) {
+                // behind the last token the map is the identity
+#pragma unroll
+                for (int i = 0; i < T; ++i)
+                    if (t + i >= a.L) {
+                        gs_stay<DEC>(g[i]);
+                        gs_zero(x[i]);
+                    }
+            }
             float hi[T][8], lo[T][8], in[T][8], H[8], Lo[8], B[8];
 #pragma unroll
             for (int i = 0; i < T; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
-                    const bool ok = t + i < a.L;   // behind the last token the map is the identity
-                    hi[i][e] = ok ? f.hi : 1.f;
-                    lo[i][e] = ok ? f.lo : 0.f;
-                    in[i][e] = ok ? gs_input<INP>(f) * oct_value(x[i], e) : 0.f;
+                    hi[i][e] = f.hi;
+                    lo[i][e] = f.lo;
+                    in[i][e] = gs_input<INP>(f) * oct_value(x[i], e);
                     if (i == 0) {
                         H[e] = hi[i][e];
                         Lo[e] = lo[i][e];

@@ -14,7 +14,7 @@ namespace dr {
 constexpr int kRunBwd = 4;
 
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL, bool FAR>
-__global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
+__global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
     constexpr int T = kRunBwd;
     extern __shared__ float lds[];
     __shared__ unsigned drawn;
@@ -59,14 +59,22 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
                 oct_load<FH, SMALL>(hb + p * a.sh.t * hs, a.h_f32, pl.at, a.C, h[i]);
                 if (INP != kGsPlain) oct_load<FX, SMALL>(xb + r * a.sx.t * xs, a.x_f32, pl.at, a.C, x[i]);
             }
+            if (t0 + span > a.L) {
+                // behind the last token nothing changes the gradient
+#pragma unroll
+                for (int i = 0; i < T; ++i)
+                    if (t + i >= a.L) {
+                        gs_stay<DEC>(g[i]);
+                        gs_zero(d[i]);
+                    }
+            }
             float H[8], Lo[8], B[8];
 #pragma unroll
             for (int i = T - 1; i >= 0; --i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
-                    const bool ok = t + i < a.L;
-                    const float hi = ok ? f.hi : 1.f, lo = ok ? f.lo : 0.f, dh = ok ? oct_value(d[i], e) : 0.f;
+                    const float hi = f.hi, lo = f.lo, dh = oct_value(d[i], e);
                     if (i == T - 1) {
                         H[e] = hi;
                         Lo[e] = lo;
@@ -99,8 +107,7 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
-                    const bool ok = t + i < a.L;
-                    const float dt = (ok ? oct_value(d[i], e) : 0.f) + s[e];
+                    const float dt = oct_value(d[i], e) + s[e];
                     const float c = gs_input<INP>(f);
                     float before = start ? first[e] : oct_value(h[i], e);
                     if constexpr (INP == kGsBlend) before -= oct_value(x[i], e);
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(512) void gs_bwd_kernel(GsArgs a) {
                     }
                     dx[e] = c * dt;
                     dg[e] = dt * before * (DEC == kGsLog ? f.hi : f.hi * f.rest);
-                    s[e] = ok ? gs_apply(f.hi, f.lo, dt, 0.f) : dt;
+                    s[e] = gs_apply(f.hi, f.lo, dt, 0.f);
                 }
                 if (t + i < a.L && pl.own) {
                     oct_store<SMALL>(ob + (int64_t)(t + i) * a.so.t * os, a.out_f32, pl, dx);

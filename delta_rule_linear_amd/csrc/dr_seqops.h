@@ -86,10 +86,10 @@ struct GsArgs {
     int groups;           // runs of tokens side by side in a workgroup
     int nseg;             // workgroups along a sequence (1: one that walks its tiles)
     unsigned columns;     // B times the channel tiles
-    uint64_t* maps;       // nseg > 1: [columns][nseg][128], what each tile does to the state
-    uint64_t* states;     // [columns][groups of tiles][128], what each group starts with
-    unsigned* counter;    // tiles drawn; stands in front of the maps and the states
-    size_t words;         // 64-bit words of all three
+    uint64_t* maps;       // nseg > 1, for each column: [nseg][128] what each tile does to the state,
+                          // [groups of tiles][128], and [blocks][128] what each block starts with
+    unsigned* counter;    // tiles drawn
+    size_t words;         // 64-bit words of the maps
     int x_f32, g_f32, h_f32, dh_f32, out_f32;
     int logit;            // decay: 0 e^g, 1 sigmoid(g)
     int inputs;           // 0 plain, 1 blend, 2 unit
@@ -99,7 +99,7 @@ int gs_run(bool bwd);          // tokens of a thread
 hipError_t launch_gs_fwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_bwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_clear(const GsArgs& a, int slot, hipStream_t st);
-constexpr int kGsGroup = 8;    // tiles between two published states
+constexpr int kGsGroup = 8;    // tiles of a group, groups of a block
 hipError_t launch_gs_step(const GsArgs& a, int slot, hipStream_t st);
 
 }  // namespace dr

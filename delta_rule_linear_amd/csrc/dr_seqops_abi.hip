@@ -451,20 +451,20 @@ constexpr int64_t kGsColumns = 512;
 
 struct GsLayout {
     int groups, nseg;
-    size_t counter, maps, states, total;   // bytes
+    size_t counter, maps, total;   // bytes
 };
 
 GsLayout gs_layout(const dr_gated_scan_desc& d, bool bwd) {
     GsLayout w{};
     const int run = dr::gs_run(bwd);
     w.groups = 4;
-    while (w.groups < 32 && (int64_t)w.groups * run < d.L) w.groups *= 2;
+    while (w.groups < 16 && (int64_t)w.groups * run < d.L) w.groups *= 2;
     const int64_t columns = d.B * channel_tiles(d.C), span = (int64_t)w.groups * run, tiles = (d.L + span - 1) / span;
     w.nseg = columns < kGsColumns ? (int)tiles : 1;
     if (w.nseg > 1) {
         w.maps = 256;   // the counter is in front
-        w.states = w.maps + (size_t)columns * w.nseg * dr::kGsTile * 8;
-        w.total = w.states + (size_t)columns * ((w.nseg + dr::kGsGroup - 1) / dr::kGsGroup) * dr::kGsTile * 8;
+        const size_t ngroup = (w.nseg + dr::kGsGroup - 1) / dr::kGsGroup, nblock = (ngroup + dr::kGsGroup - 1) / dr::kGsGroup;
+        w.total = w.maps + (size_t)columns * (w.nseg + ngroup + nblock) * dr::kGsTile * 8;
     }
     return w;
 }
@@ -484,7 +484,6 @@ void gs_split(const dr_gated_scan_desc& d, const GsLayout& w, void* workspace, d
     if (w.nseg > 1) {
         a.counter = (unsigned*)(ws + w.counter);
         a.maps = (uint64_t*)(ws + w.maps);
-        a.states = (uint64_t*)(ws + w.states);
         a.words = (w.total - w.maps) / 8;
     }
 }
