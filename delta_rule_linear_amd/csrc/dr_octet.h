@@ -68,6 +68,14 @@ __device__ __forceinline__ void oct_load(const void* row, bool f32, int at, int 
     }
 }
 
+// Forgets what the compiler knows of the values, so that what was made of them is made
+// again instead of kept in registers.
+template <bool F32>
+__device__ __forceinline__ void oct_forget(Oct<F32>& r) {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
 template <bool F32>
 __device__ __forceinline__ float oct_value(const Oct<F32>& r, int e) {
     if constexpr (F32) return __uint_as_float(r.w[e]);

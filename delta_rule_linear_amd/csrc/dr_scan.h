@@ -1,11 +1,12 @@
-// dr_scan.h -- the gated linear recurrence's kernels (dr_scan.hip forward and
+// dr_scan.h -- what the gated linear recurrence's kernels share (dr_scan.hip forward and
 // one token, dr_scan_bwd.hip the backward).
 //
 //   h_t = a_t h_{t-1} + c(a_t) x_t      a = e^g or sigmoid(g);  c = 1, 1 - a, sqrt(1 - a^2)
 //
-// a is carried in two parts, hi + lo, where it is near one: rounded to 24 bits it
-// would be off by 2^-25, and a memory of 1 / (1 - a) tokens multiplies that.  1 - a
-// is made directly (-expm1(g), sigmoid(-g)); hi is a rounded, and lo = (1 - hi) - (1 - a).
+// Where a is near one, a h is made as h - (1 - a) h with 1 - a taken directly
+// (-expm1(g), sigmoid(-g)): a rounded to 24 bits would be off by 2^-25, and a memory
+// of 1 / (1 - a) tokens multiplies that.  Elsewhere a itself is used, so that strong
+// decays are exact relative to themselves.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -20,18 +21,25 @@ namespace dr {
 enum { kGsLog = 0, kGsLogit = 1 };
 enum { kGsPlain = 0, kGsBlend = 1, kGsUnit = 2 };
 
+// a = one + part: where a is near one, `one` is 1 and part = a - 1, its sign bit set (of
+// zero too); elsewhere `one` is 0 and part = a, its sign bit clear.  rest = 1 - a.
 struct GsFactor {
-    float hi, lo;   // a
-    float rest;     // 1 - a
+    float part, rest;
 };
+// All bits set where `part` says that a is near one.
+__device__ __forceinline__ int gs_near(float part) { return __float_as_int(part) >> 31; }
+__device__ __forceinline__ float gs_masked(int mask, float x) { return __int_as_float(mask & __float_as_int(x)); }
+__device__ __forceinline__ float gs_select(int mask, float x, float y) {
+    return __int_as_float((mask & __float_as_int(x)) | (~mask & __float_as_int(y)));
+}
 
 template <int DEC>
 __device__ __forceinline__ GsFactor gs_factor(float g) {
     constexpr float kLog2e = 1.44269504088896340736f;
     GsFactor o;
     if constexpr (DEC == kGsLog) {
-        // expm1 by its series where |g| < 0.4 (the next term, g^9 / 9!, is below
-        // 2^-28 of g), else e^g - 1
+        // expm1 by its series for -0.4 < g <= -0 (the next term, g^9 / 9!, is below
+        // 2^-28 of g), e^g elsewhere
         const float e = __builtin_amdgcn_exp2f(g * kLog2e);
         float q = 1.f / 40320.f;
         q = __builtin_fmaf(q, g, 1.f / 5040.f);
@@ -40,20 +48,21 @@ __device__ __forceinline__ GsFactor gs_factor(float g) {
         q = __builtin_fmaf(q, g, 1.f / 24.f);
         q = __builtin_fmaf(q, g, 1.f / 6.f);
         q = __builtin_fmaf(q, g, 0.5f);
-        const bool near = __builtin_fabsf(g) < 0.4f;
-        o.rest = near ? -__builtin_fmaf(g * g, q, g) : 1.f - e;
-        const float hi = 1.f - o.rest;
-        o.hi = near ? hi : e;
-        o.lo = near ? (1.f - hi) - o.rest : 0.f;
+        q = __builtin_fmaf(g * g, q, g);
+        // as integers, negative floats grow with their size, and positive ones are larger
+        o.part = __float_as_int(g) < __float_as_int(-0.4f) ? q : e;
+        o.rest = gs_masked(~gs_near(o.part), 1.f) - o.part;
     } else {
         const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
         const float big = __builtin_amdgcn_rcpf(1.f + e), little = e * big;
-        const bool near = g > 0.f;
-        o.rest = near ? little : big;
-        o.hi = near ? big : little;
-        o.lo = near ? (1.f - big) - little : 0.f;
+        o.part = gs_select(0x7fffffff, little, __int_as_float(~__float_as_int(g)));
+        o.rest = gs_select(gs_near(o.part), little, big);
     }
     return o;
+}
+__device__ __forceinline__ float gs_decay(const GsFactor& f) {
+    const int near = gs_near(f.part);
+    return gs_masked(near, 1.f) + f.part;
 }
 
 // The gate of a token that changes nothing (a = 1 exactly).
@@ -74,21 +83,66 @@ template <int INP>
 __device__ __forceinline__ float gs_input(const GsFactor& f) {
     if constexpr (INP == kGsPlain) return 1.f;
     if constexpr (INP == kGsBlend) return f.rest;
-    return __builtin_amdgcn_sqrtf(f.rest * (1.f + f.hi));
+    return __builtin_amdgcn_sqrtf(f.rest * (2.f - f.rest));
 }
 
 // a h + b
-__device__ __forceinline__ float gs_apply(float hi, float lo, float h, float b) {
-    return __builtin_fmaf(hi, h, __builtin_fmaf(lo, h, b));
-}
-// (hi, lo) <- a (hi, lo)
-__device__ __forceinline__ void gs_times(float& hi, float& lo, float ahi, float alo) {
-    const float p = hi * ahi;
-    lo = __builtin_fmaf(hi, ahi, -p) + __builtin_fmaf(hi, alo, lo * ahi);
-    hi = p;
+__device__ __forceinline__ float gs_step(float part, float h, float b) {
+    return gs_masked(gs_near(part), h) + __builtin_fmaf(part, h, b);
 }
 
-// Eight values to and from LDS (32-byte aligned there).
+// The map of several tokens, h -> (one + part) h + b, one again 0 or 1.
+struct GsMap {
+    float one, part, b;
+};
+__device__ __forceinline__ float gs_apply(const GsMap& m, float h) {
+    return __builtin_fmaf(m.one, h, __builtin_fmaf(m.part, h, m.b));
+}
+// first m, then n
+__device__ __forceinline__ GsMap gs_then(const GsMap& m, const GsMap& n) {
+    return {m.one * n.one, __builtin_fmaf(m.part, n.part, __builtin_fmaf(m.one, n.part, m.part * n.one)),
+            gs_apply(n, m.b)};
+}
+// one token's, and first m, then a token
+__device__ __forceinline__ GsMap gs_token(float part, float b) { return {gs_masked(gs_near(part), 1.f), part, b}; }
+__device__ __forceinline__ GsMap gs_then(const GsMap& m, float part, float b) {
+    const int near = gs_near(part);
+    return {gs_masked(near, m.one), __builtin_fmaf(m.part, part, __builtin_fmaf(m.one, part, gs_masked(near, m.part))),
+            gs_step(part, m.b, b)};
+}
+
+// ---------------------------------------------------------------- tiles
+// A workgroup has 64 channels of a tile of tokens, a thread eight channels of a run of
+// them; eight threads have the channels of a run, a wave the channels of eight runs.
+// Every thread makes its run's map.  A wave joins its eight runs, one channel a lane
+// (through LDS that is its own, [run][64]), and leaves its map for the other waves
+// behind the one barrier that a tile needs; from the state that the tile starts with
+// every lane then follows the waves before its own.
+struct GsLds {
+    float *one, *part, *b;   // [runs][64], a wave's own
+    float* start;            // [waves][64], a wave's own: what it starts with
+    float* waves;            // twice [3][waves][64]: the waves' maps, used in turn
+    float2* back;            // [waves][64]: maps of earlier tiles
+};
+constexpr int kGsRuns = 32, kGsWaves = 4;   // of a full workgroup
+constexpr unsigned kGsLdsBytes = (3 * kGsRuns + kGsWaves + 6 * kGsWaves + 2 * kGsWaves) * kGsTile * 4;
+__device__ __forceinline__ GsLds gs_lds(float* p) {
+    GsLds l;
+    l.one = p;
+    l.part = l.one + kGsRuns * kGsTile;
+    l.b = l.part + kGsRuns * kGsTile;
+    l.start = l.b + kGsRuns * kGsTile;
+    l.waves = l.start + kGsWaves * kGsTile;
+    l.back = reinterpret_cast<float2*>(l.waves + 6 * kGsWaves * kGsTile);
+    return l;
+}
+
+// What a wave writes to LDS it reads in the same order; only the compiler has to keep to it.
+__device__ __forceinline__ void gs_wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ void gs_put(float* to, const float (&x)[8]) {
     reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -105,27 +159,86 @@ __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
     x[7] = b.w;
 }
 
+// A wave's runs joined, channel `c` = the lane: each run's map becomes that of the runs
+// before it in the wave, and the wave's map goes to the others.  FWD: runs, and waves,
+// from the first to the last.
+template <bool FWD>
+__device__ __forceinline__ void gs_join(const GsLds& l, int turn, const float (&one)[8], const float (&part)[8],
+                                        const float (&b)[8]) {
+    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, at = (tid >> 3) * kGsTile + (tid & 7) * 8;
+    gs_put(l.one + at, one);
+    gs_put(l.part + at, part);
+    gs_put(l.b + at, b);
+    gs_wave_fence();
+    GsMap all{1.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int k = (wave * 8 + (FWD ? i : 7 - i)) * kGsTile + c;
+        const GsMap m{l.one[k], l.part[k], l.b[k]};
+        l.one[k] = all.one;
+        l.part[k] = all.part;
+        l.b[k] = all.b;
+        all = gs_then(all, m);
+    }
+    float* w = l.waves + (turn * 3 * kGsWaves + wave) * kGsTile + c;
+    w[0] = all.one;
+    w[kGsWaves * kGsTile] = all.part;
+    w[2 * kGsWaves * kGsTile] = all.b;
+}
+// Behind the barrier: wave `i`'s map, in the order that the state passes them.
+template <bool FWD>
+__device__ __forceinline__ GsMap gs_wave_map(const GsLds& l, int turn, int i, int c) {
+    const int waves = blockDim.x >> 6;
+    const float* w = l.waves + (turn * 3 * kGsWaves + (FWD ? i : waves - 1 - i)) * kGsTile + c;
+    return {w[0], w[kGsWaves * kGsTile], w[2 * kGsWaves * kGsTile]};
+}
+// The states that a thread's run starts with, in s, from what the tile starts with (h, of
+// the lane's channel).  Returns what it ends with.
+template <bool FWD>
+__device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, float (&s)[8]) {
+    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, waves = blockDim.x >> 6;
+    float mine = h;
+#pragma unroll
+    for (int i = 0; i < kGsWaves; ++i) {
+        if (i >= waves) break;
+        if ((FWD ? i : waves - 1 - i) == wave) mine = h;
+        h = gs_apply(gs_wave_map<FWD>(l, turn, i, c), h);
+    }
+    l.start[wave * kGsTile + c] = mine;
+    gs_wave_fence();
+    float one[8], part[8], b[8];
+    const int at = (tid >> 3) * kGsTile + (tid & 7) * 8;
+    gs_get(l.one + at, one);
+    gs_get(l.part + at, part);
+    gs_get(l.b + at, b);
+    gs_get(l.start + wave * kGsTile + (tid & 7) * 8, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = gs_apply({one[e], part[e], b[e]}, s[e]);
+    return h;
+}
+
 // ---------------------------------------------------------------- long sequences
-// With few sequences each tile of a sequence has a workgroup of its own.  A workgroup
-// draws its tile from a counter, tiles in the order that the state passes them, so
-// that the tiles before its own belong to workgroups that already run.  It publishes
-// the map of its tile, h -> A h + B for each channel, before it waits for anything;
-// then it takes the maps of the tiles before it, in their order (the same one every
-// time), back to the last tile whose number is a multiple of kGsGroup, whose state at
-// the start is published as well.  So no wait goes on without end: maps depend on
-// nothing, and the state at a group's start on earlier tiles only.
+// With few sequences each tile of a column (64 channels of a sequence) has a workgroup
+// of its own.  A workgroup draws its tile from its column's counter, tiles in the order
+// that the state passes them, so that the tiles before its own belong to workgroups
+// that already run.  (One counter for all columns hands out a number every 15 ns: 8192
+// tiles took 124 us.)  It publishes the map of its tile, h -> A h + B for each channel,
+// before it waits for anything; then it takes the maps of the kGsBack tiles before it
+// and the state that the first of those starts with, and publishes the state that it
+// starts with itself.  The distance is always the same, and so are the bits.  No wait
+// goes on without end: maps depend on nothing, and states on earlier tiles.
+//
+// kGsBack: about as many tiles of a column as are on the chip at once, so that the
+// state is there as a rule and only the maps of tiles that run side by side are waited
+// for, once.  (Maps joined over groups of 8 tiles and blocks of 8 groups need fewer
+// words, but three such round trips of 1.5 us and more.)
 //
 // A map is one 64-bit word (A in the low half, B in the high one), a state another,
 // so that a word is whole when it is there at all; until then it is kGsAbsent, which
 // launch_gs_clear writes first.  Between tiles A is rounded to 24 bits, which costs
 // half a rounding of the state per tile.
-//
-// kGsGroup tiles are a group, as many groups a block.  The last tile of a group
-// publishes the group's map, as soon as it has the others' maps, and the last one of
-// a block the state behind it.  A tile takes up to kGsGroup - 1 maps of each kind, and
-// the state is handed on once per block: about 0.85 us each time (one state for every 8 tiles
-// of 64 tokens held 65536 tokens up for 109 us).
 constexpr uint64_t kGsAbsent = ~(uint64_t)0;
+constexpr int kGsBack = 16;
 
 __device__ __forceinline__ void gs_publish(uint64_t* to, float a, float b) {
     uint64_t v = ((uint64_t)__float_as_uint(b) << 32) | __float_as_uint(a);
@@ -135,92 +248,75 @@ __device__ __forceinline__ void gs_publish(uint64_t* to, float a, float b) {
 __device__ __forceinline__ uint64_t gs_peek(const uint64_t* from) {
     return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ float gs_low(uint64_t m) { return __uint_as_float((unsigned)m); }
+__device__ __forceinline__ float gs_high(uint64_t m) { return __uint_as_float((unsigned)(m >> 32)); }
 
-// n words (fewer than kGsGroup, 128 apart) once all are there; all are asked for at
-// once, where there are fewer the last one again.
-__device__ __forceinline__ void gs_wait(const uint64_t* from, int n, uint64_t (&m)[kGsGroup - 1]) {
-    bool all = n == 0;
-    while (!all) {
-#pragma unroll
-        for (int i = 0; i < kGsGroup - 1; ++i) m[i] = gs_peek(from + (size_t)min(i, n - 1) * kGsTile);
-        all = true;
-#pragma unroll
-        for (int i = 0; i < kGsGroup - 1; ++i) all = all && m[i] != kGsAbsent;
-        if (!all) __builtin_amdgcn_s_sleep(1);
-    }
-}
-__device__ __forceinline__ float gs_through(const uint64_t (&m)[kGsGroup - 1], int n, float h) {
-#pragma unroll
-    for (int i = 0; i < kGsGroup - 1; ++i)
-        if (i < n) h = __builtin_fmaf(__uint_as_float((unsigned)m[i]), h, __uint_as_float((unsigned)(m[i] >> 32)));
-    return h;
+// Draws a tile of the column (thread 0).  Counters start at -1, as everything that
+// launch_gs_clear writes.
+__device__ __forceinline__ unsigned gs_draw(const GsArgs& a, unsigned col) {
+    return __hip_atomic_fetch_add(a.counters + (size_t)col * kGsCounter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
 }
 
-// Which tile a workgroup has.
-__device__ __forceinline__ unsigned gs_draw(unsigned* counter, unsigned* lds) {
-    if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    return *lds;
-}
-
-// Joins a tile's runs, [k][128] maps in LDS, for channel c; the state each run starts
-// with takes the place of its B.  FWD: runs from the first to the last.
+// The state that tile `seg` of a column starts with, for the lane's channel, by four
+// waves, behind the barrier after gs_join; `first` is what the first tile starts with.
+// Each wave takes a quarter of the maps before the tile.
 template <bool FWD>
-__device__ __forceinline__ float gs_join(const float* shH, const float* shL, float* shB, int ntg, int c, float h) {
-#pragma unroll 4
-    for (int i = 0; i < ntg; ++i) {
-        const int at = (FWD ? i : ntg - 1 - i) * kGsTile + c;
-        const float start = h;
-        h = gs_apply(shH[at], shL[at], h, shB[at]);
-        shB[at] = start;
-    }
-    return h;
-}
-// The same through the other workgroups: `first` is what the first tile starts with.
-template <bool FWD>
-__device__ __forceinline__ float gs_join_far(const GsArgs& a, const float* shH, const float* shL, float* shB, int c,
-                                             unsigned col, int seg, float first) {
-    float H = 1.f, L = 0.f, B = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < a.groups; ++i) {
-        const int at = (FWD ? i : a.groups - 1 - i) * kGsTile + c;
-        B = gs_apply(shH[at], shL[at], B, shB[at]);
-        gs_times(H, L, shH[at], shL[at]);
-    }
-    const int ngroup = (a.nseg + kGsGroup - 1) / kGsGroup, nblock = (ngroup + kGsGroup - 1) / kGsGroup;
-    uint64_t* maps = a.maps + (size_t)col * (a.nseg + ngroup + nblock) * kGsTile + c;
-    uint64_t* gmaps = maps + (size_t)a.nseg * kGsTile;
-    uint64_t* states = gmaps + (size_t)ngroup * kGsTile;
-    const int group = seg / kGsGroup, n = seg - group * kGsGroup, block = group / kGsGroup, q = group - block * kGsGroup;
-    const bool more = seg + 1 < a.nseg;
-    float h = first, A = H + L;
-    if (seg == 0) {
+__device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigned col, int seg, float first) {
+    constexpr int N = kGsBack / kGsWaves;
+    const int tid = threadIdx.x, c = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint64_t* maps = a.maps + (size_t)col * a.nseg * 2 * kGsTile;
+    uint64_t* states = maps + (size_t)a.nseg * kGsTile;
+    if (wave == 0 && seg + 1 < a.nseg) {
+        GsMap all{1.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kGsWaves; ++i) all = gs_then(all, gs_wave_map<FWD>(l, 0, i, c));
         // what comes in is part of the first tile's map, so that nobody else reads it
-        B = gs_apply(H, L, first, B);
-        A = 0.f;
-        gs_publish(maps, A, B);
-    } else {
-        if (more) gs_publish(maps + (size_t)seg * kGsTile, A, B);
-        uint64_t m[kGsGroup - 1], g[kGsGroup - 1];
-        gs_wait(maps + (size_t)group * kGsGroup * kGsTile, n, m);
-        if (n == kGsGroup - 1 && more) {
-            float ga = A, gb = gs_through(m, n, 0.f);
-#pragma unroll
-            for (int i = 0; i < kGsGroup - 1; ++i) ga *= __uint_as_float((unsigned)m[i]);
-            gs_publish(gmaps + (size_t)group * kGsTile, ga, __builtin_fmaf(A, gb, B));
-        }
-        gs_wait(gmaps + (size_t)block * kGsGroup * kGsTile, q, g);
-        h = 0.f;   // the first block's first map holds what came in
-        if (block) {
-            uint64_t s;
-            while ((s = gs_peek(states + (size_t)block * kGsTile)) == kGsAbsent) __builtin_amdgcn_s_sleep(1);
-            h = __uint_as_float((unsigned)s);
-        }
-        h = gs_through(m, n, gs_through(g, q, h));
-        if (n == kGsGroup - 1 && q == kGsGroup - 1 && more)
-            gs_publish(states + (size_t)(block + 1) * kGsTile, __builtin_fmaf(A, h, B), 0.f);
+        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? all.one + all.part : 0.f, seg ? all.b : gs_apply(all, first));
     }
-    return gs_join<FWD>(shH, shL, shB, a.groups, c, h);
+    if (seg == 0) return first;
+    const int from = seg - kGsBack + wave * N;               // this wave's maps: from .. from + N - 1
+    const bool state = wave == 0 && seg > kGsBack;
+    float A = 1.f, B = 0.f;
+    if (from + N > 0) {
+        // one lane looks for the word that comes last, as a rule
+        const uint64_t* at = maps + (int64_t)from * kGsTile;
+        if (c == 0)
+            while (gs_peek(at + (N - 1) * kGsTile) == kGsAbsent) __builtin_amdgcn_s_sleep(2);
+        uint64_t m[N], h = 0;
+        for (;;) {
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < N; ++i) m[i] = gs_peek(at + (from + i < 0 ? N - 1 : i) * kGsTile + c);
+            if (state) h = gs_peek(states + (size_t)(seg - kGsBack) * kGsTile + c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) all = all && m[i] != kGsAbsent;
+            if (all && h != kGsAbsent) break;
+            __builtin_amdgcn_s_sleep(2);
+        }
+        if (wave == 0) B = gs_low(h);   // the first of all starts with 0: its map holds what came in
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (from + i < 0) continue;
+            A *= gs_low(m[i]);
+            B = __builtin_fmaf(gs_low(m[i]), B, gs_high(m[i]));
+        }
+    }
+    if (wave == 0) A = 0.f;
+    l.back[wave * kGsTile + c] = make_float2(A, B);
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kGsWaves; ++i) {
+        const float2 m = l.back[i * kGsTile + c];
+        s = __builtin_fmaf(m.x, s, m.y);
+    }
+    if (wave == 0 && seg + kGsBack < a.nseg) gs_publish(states + (size_t)seg * kGsTile + c, s, 0.f);
+    return s;
+}
+
+// n / d by a product: d's divider from the host (dr_seqops.h).
+__device__ __forceinline__ unsigned gs_divide(unsigned n, const GsDivide& d) {
+    return (unsigned)(((uint64_t)n * d.factor) >> d.shift);
 }
 
 }  // namespace dr

@@ -16,140 +16,144 @@ constexpr int kRunBwd = 4;
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
     constexpr int T = kRunBwd;
-    extern __shared__ float lds[];
+    __shared__ __align__(16) float lds[kGsLdsBytes / 4];
     __shared__ unsigned drawn;
-    const int ntg = a.groups, tid = threadIdx.x, lane = tid & 15, tg = tid >> 4;
-    float* carry = lds;
-    float* shH = carry + kGsTile;
-    float* shL = shH + ntg * kGsTile;
-    float* shB = shL + ntg * kGsTile;
-    const unsigned nct = ((unsigned)a.C + kGsTile - 1) / kGsTile;
+    const int tid = threadIdx.x, lane = tid & 7, tg = tid >> 3, span = a.groups * T;
+    const GsLds l = gs_lds(lds);
     const int xs = a.x_f32 ? 4 : 2, gs = a.g_f32 ? 4 : 2, hs = a.h_f32 ? 4 : 2, ds = a.dh_f32 ? 4 : 2,
-              os = a.out_f32 ? 4 : 2, span = ntg * T;
+              os = a.out_f32 ? 4 : 2;
+    const unsigned xt = (unsigned)a.sx.t * xs, gt = (unsigned)a.sg.t * gs, ht = (unsigned)a.sh.t * hs,
+                   dt = (unsigned)a.sdh.t * ds, ot = (unsigned)a.so.t * os, got = (unsigned)a.sdg.t * os;
+    Oct<FX> x[T];
+    Oct<FG> g[T];
+    Oct<FH> hp[T];   // the states before the run's tokens
+    Oct<FD> d[T];
     // tiles in the order that the gradient passes them: the last tokens first
-    const unsigned tile = FAR ? gs_draw(a.counter, &drawn) : 0;
-    const int seg = FAR ? (int)(tile / a.columns) : 0;
-    for (unsigned col = FAR ? tile - seg * a.columns : blockIdx.x; col < a.columns; col += gridDim.x) {
-        const unsigned b = col / nct, ct = col - b * nct;
-        const OctPlace pl = oct_place(ct * 16 + lane, a.C);
-        if (!FAR || seg == 0)
-            for (int c = tid; c < kGsTile; c += blockDim.x)
-                carry[c] = a.dlast ? a.dlast[(size_t)b * a.C + oct_channel<SMALL>(ct * 16 + (c >> 3), c & 7, a.C)] : 0.f;
-        const char* xb = (const char*)a.x + b * a.sx.b * xs;
-        const char* gb = (const char*)a.g + b * a.sg.b * gs;
-        const char* hb = (const char*)a.h + b * a.sh.b * hs;
-        const char* db = (const char*)a.dh + b * a.sdh.b * ds;
-        char* ob = (char*)a.out + b * a.so.b * os;
-        char* gob = (char*)a.dg + b * a.sdg.b * os;
-        for (int t0 = FAR ? (a.nseg - 1 - seg) * span : (a.L - 1) / span * span; t0 >= 0; t0 -= span) {
-            const int t = t0 + tg * T;
-            Oct<FX> x[T];
-            Oct<FG> g[T];
-            Oct<FH> h[T];   // the states before the run's tokens
-            Oct<FD> d[T];
+    auto load = [&](unsigned col, int seg) {
+        const unsigned b = gs_divide(col, a.by_tiles), ct = col - b * a.tiles;
+        const OctPlace pl = oct_place(ct * 8 + lane, a.C);
+        const int t0 = (a.nseg - 1 - seg) * span, last = a.L - 1 - t0;
+        const char* xb = (const char*)a.x + (b * a.sx.b + t0 * a.sx.t) * xs;
+        const char* gb = (const char*)a.g + (b * a.sg.b + t0 * a.sg.t) * gs;
+        const char* hb = (const char*)a.h + (b * a.sh.b + t0 * a.sh.t) * hs;
+        const char* db = (const char*)a.dh + (b * a.sdh.b + t0 * a.sdh.t) * ds;
 #pragma unroll
-            for (int i = 0; i < T; ++i) {
-                const int64_t r = min(t + i, a.L - 1);
-                oct_load<FG, SMALL>(gb + r * a.sg.t * gs, a.g_f32, pl.at, a.C, g[i]);
-                oct_load<FD, SMALL>(db + r * a.sdh.t * ds, a.dh_f32, pl.at, a.C, d[i]);
-            }
+        for (int i = 0; i < T; ++i) {
+            const unsigned r = min(tg * T + i, last);
+            oct_load<FG, SMALL>(gb + r * gt, a.g_f32, pl.at, a.C, g[i]);
+            oct_load<FD, SMALL>(db + r * dt, a.dh_f32, pl.at, a.C, d[i]);
+        }
 #pragma unroll
-            for (int i = 0; i < T; ++i) {
-                const int64_t r = min(t + i, a.L - 1), p = max(r - 1, (int64_t)0);
-                oct_load<FH, SMALL>(hb + p * a.sh.t * hs, a.h_f32, pl.at, a.C, h[i]);
-                if (INP != kGsPlain) oct_load<FX, SMALL>(xb + r * a.sx.t * xs, a.x_f32, pl.at, a.C, x[i]);
-            }
-            if (t0 + span > a.L) {
+        for (int i = 0; i < T; ++i) {
+            const unsigned r = min(tg * T + i, last);
+            // the row before; the first token's comes from h0
+            oct_load<FH, SMALL>(t0 + r ? hb + (int)(r * ht) - (int)ht : hb, a.h_f32, pl.at, a.C, hp[i]);
+            if (INP != kGsPlain) oct_load<FX, SMALL>(xb + r * xt, a.x_f32, pl.at, a.C, x[i]);
+        }
+    };
+    unsigned first = blockIdx.x, seg0 = 0;
+    if constexpr (FAR) {
+        // workgroups start in their order as a rule: the rows of the tile that would then be
+        // this one's are asked for before the tile is known
+        seg0 = gs_divide(blockIdx.x, a.by_columns);
+        first = blockIdx.x - seg0 * a.columns;
+        const unsigned ticket = tid == 0 ? gs_draw(a, first) : 0;
+        load(first, seg0);
+        if (tid == 0) drawn = ticket;
+        __syncthreads();
+        const unsigned mine = __builtin_amdgcn_readfirstlane(drawn);
+        if (mine != seg0) load(first, mine);
+        seg0 = mine;
+    }
+    for (unsigned col = first; col < a.columns; col += gridDim.x) {
+        const unsigned b = gs_divide(col, a.by_tiles), ct = col - b * a.tiles;
+        const OctPlace pl = oct_place(ct * 8 + lane, a.C);
+        float h = 0.f;   // the state between tiles, of the lane's channel
+        if (a.dlast && seg0 == 0)
+            h = a.dlast[(size_t)b * a.C + oct_channel<SMALL>(ct * 8 + ((tid & 63) >> 3), tid & 7, a.C)];
+        for (int seg = seg0; seg < a.nseg; ++seg) {
+            const int t0 = (a.nseg - 1 - seg) * span, last = a.L - 1 - t0, turn = FAR ? 0 : seg & 1;
+            if (!FAR) load(col, seg);
+            if (span > last + 1) {
                 // behind the last token nothing changes the gradient
 #pragma unroll
                 for (int i = 0; i < T; ++i)
-                    if (t + i >= a.L) {
+                    if (tg * T + i > last) {
                         gs_stay<DEC>(g[i]);
                         gs_zero(d[i]);
                     }
             }
-            float H[8], Lo[8], B[8];
+            float one[8], all[8], B[8];
 #pragma unroll
             for (int i = T - 1; i >= 0; --i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
+                    // e -> a (e + dh)
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
-                    const float hi = f.hi, lo = f.lo, dh = oct_value(d[i], e);
-                    if (i == T - 1) {
-                        H[e] = hi;
-                        Lo[e] = lo;
-                        B[e] = gs_apply(hi, lo, dh, 0.f);
-                    } else {
-                        gs_times(H[e], Lo[e], hi, lo);
-                        B[e] = gs_apply(hi, lo, dh + B[e], 0.f);
-                    }
+                    const float in = gs_step(f.part, oct_value(d[i], e), 0.f);
+                    const GsMap run = i == T - 1 ? gs_token(f.part, in) : gs_then({one[e], all[e], B[e]}, f.part, in);
+                    one[e] = run.one;
+                    all[e] = run.part;
+                    B[e] = run.b;
                 }
-            gs_put(shH + tg * kGsTile + lane * 8, H);
-            gs_put(shL + tg * kGsTile + lane * 8, Lo);
-            gs_put(shB + tg * kGsTile + lane * 8, B);
+            gs_join<false>(l, turn, one, all, B);
+            asm volatile("" : "+v"(h));   // what comes in is read before anything goes out: both may be one tensor
             __syncthreads();
-            for (int c = tid; c < kGsTile; c += blockDim.x) {
-                if constexpr (FAR) carry[c] = gs_join_far<false>(a, shH, shL, shB, c, col, seg, carry[c]);
-                else carry[c] = gs_join<false>(shH, shL, shB, ntg, c, carry[c]);
-            }
-            __syncthreads();
+            if constexpr (FAR) h = gs_far<false>(a, l, col, seg, h);
             float s[8];
-            gs_get(shB + tg * kGsTile + lane * 8, s);
+            h = gs_starts<false>(l, turn, h, s);
+            char* ob = (char*)a.out + (b * a.so.b + t0 * a.so.t) * os;
+            char* gob = (char*)a.dg + (b * a.sdg.b + t0 * a.sdg.t) * os;
+            // the factors are made again: kept, they would take the registers of a second
+            // workgroup
+#pragma unroll
+            for (int i = 0; i < T; ++i) oct_forget(g[i]);
 #pragma unroll
             for (int i = T - 1; i >= 0; --i) {
-                float dx[8], dg[8], first[8];
-                const bool start = t + i == 0;
+                float dx[8], dg[8], h0[8];
+                const bool start = t0 + tg * T + i == 0;
                 if (start) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        first[e] = a.h0 ? a.h0[(size_t)b * a.C + (SMALL ? min(e, a.C - 1) : pl.at + e)] : 0.f;
+                        h0[e] = a.h0 ? a.h0[(size_t)b * a.C + (SMALL ? min(e, a.C - 1) : pl.at + e)] : 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
-                    const float dt = oct_value(d[i], e) + s[e];
-                    const float c = gs_input<INP>(f);
-                    float before = start ? first[e] : oct_value(h[i], e);
+                    const float sum = oct_value(d[i], e) + s[e], c = gs_input<INP>(f), decay = gs_decay(f);
+                    float before = start ? h0[e] : oct_value(hp[i], e);
                     if constexpr (INP == kGsBlend) before -= oct_value(x[i], e);
                     if constexpr (INP == kGsUnit) {
                         // c = 0 where a = 1: the square root has no slope there, and the
                         // input's part is left out
-                        const float k = c > 0.f ? f.hi * __builtin_amdgcn_rcpf(c) : 0.f;
+                        const float k = c > 0.f ? decay * __builtin_amdgcn_rcpf(c) : 0.f;
                         before = __builtin_fmaf(-k, oct_value(x[i], e), before);
                     }
-                    dx[e] = c * dt;
-                    dg[e] = dt * before * (DEC == kGsLog ? f.hi : f.hi * f.rest);
-                    s[e] = gs_apply(f.hi, f.lo, dt, 0.f);
+                    dx[e] = c * sum;
+                    dg[e] = sum * before * (DEC == kGsLog ? decay : decay * f.rest);
+                    s[e] = gs_step(f.part, sum, 0.f);
                 }
-                if (t + i < a.L && pl.own) {
-                    oct_store<SMALL>(ob + (int64_t)(t + i) * a.so.t * os, a.out_f32, pl, dx);
-                    oct_store<SMALL>(gob + (int64_t)(t + i) * a.sdg.t * os, a.out_f32, pl, dg);
+                if (tg * T + i <= last && pl.own) {
+                    oct_store<SMALL>(ob + (tg * T + i) * ot, a.out_f32, pl, dx);
+                    oct_store<SMALL>(gob + (tg * T + i) * got, a.out_f32, pl, dg);
+                    if (start && a.last) oct_store<SMALL>(a.last + (size_t)b * a.C, true, pl, s);
                 }
             }
             if constexpr (FAR) break;
-            __syncthreads();
         }
-        if (a.last && (!FAR || seg + 1 == a.nseg))
-            for (int c = tid; c < kGsTile; c += blockDim.x) {
-                const OctPlace p = oct_place(ct * 16 + (c >> 3), a.C);
-                if (oct_own<SMALL>(p, c & 7)) a.last[(size_t)b * a.C + p.at + (c & 7)] = carry[c];
-            }
         if constexpr (FAR) break;
-        __syncthreads();
+        __syncthreads();   // the waves' maps are read before the next column's come
     }
 }
 
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL>
 static hipError_t gs_launch(const GsArgs& a, int slot, hipStream_t st) {
-    const unsigned lds = (1 + 3 * a.groups) * kGsTile * 4;
-    if (a.nseg > 1) {
+    if (a.maps) {
         const hipError_t e = launch_gs_clear(a, slot, st);
         if (e != hipSuccess) return e;
-        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.columns * a.nseg),
-                        dim3(16 * a.groups), lds, st, a);
+        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.columns * a.nseg), dim3(256), 0, st, a);
     }
-    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>,
-                    dim3(a.columns < 65536 ? a.columns : 65536), dim3(16 * a.groups), lds, st, a);
+    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups), 0, st, a);
 }
 
 template <bool FX, bool FG, int DEC, int INP>

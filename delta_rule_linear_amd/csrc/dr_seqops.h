@@ -71,6 +71,16 @@ hipError_t launch_sc_step(const ScArgs& a, int slot, hipStream_t st);
 hipError_t launch_seq_copy(void* to, const void* from, size_t bytes, int slot, hipStream_t st);
 
 // ------------------------------------------------------------ gated linear recurrence
+// A divisor of numbers below 2^31: n / d = n factor >> shift.
+struct GsDivide {
+    unsigned factor, shift;
+};
+inline GsDivide gs_divider(unsigned d) {
+    unsigned l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    return {(unsigned)((((uint64_t)1 << (31 + l)) / d) + 1), 31 + l};
+}
+
 struct GsArgs {
     const void* x;
     const void* g;
@@ -84,22 +94,25 @@ struct GsArgs {
     SeqRows sx, sg, sh, sdh, so, sdg;
     int B, L, C;
     int groups;           // runs of tokens side by side in a workgroup
-    int nseg;             // workgroups along a sequence (1: one that walks its tiles)
+    int nseg;             // tiles of a sequence
     unsigned columns;     // B times the channel tiles
-    uint64_t* maps;       // nseg > 1, for each column: [nseg][128] what each tile does to the state,
-                          // [groups of tiles][128], and [blocks][128] what each block starts with
-    unsigned* counter;    // tiles drawn
-    size_t words;         // 64-bit words of the maps
+    unsigned tiles;       // channel tiles
+    GsDivide by_columns, by_tiles;
+    uint64_t* maps;       // where a column's tiles have workgroups of their own, else NULL; for each
+                          // column [nseg][64] what each tile does to the state, [nseg][64] what it
+                          // starts with
+    unsigned* counters;   // tiles drawn, of each column; the maps stand behind them
+    size_t words;         // 64-bit words of both
     int x_f32, g_f32, h_f32, dh_f32, out_f32;
     int logit;            // decay: 0 e^g, 1 sigmoid(g)
     int inputs;           // 0 plain, 1 blend, 2 unit
 };
-constexpr int kGsTile = 128;   // channels of a workgroup
+constexpr int kGsTile = 64;    // channels of a workgroup
 int gs_run(bool bwd);          // tokens of a thread
 hipError_t launch_gs_fwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_bwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_clear(const GsArgs& a, int slot, hipStream_t st);
-constexpr int kGsGroup = 8;    // tiles of a group, groups of a block
+constexpr int kGsCounter = 32; // a column's counter has 128 bytes to itself
 hipError_t launch_gs_step(const GsArgs& a, int slot, hipStream_t st);
 
 }  // namespace dr

@@ -249,9 +249,9 @@ int64_t channel_tiles(int C) { return ((int64_t)C + 127) / 128; }
 dr_status check_seq_dims(int B, int L, int C) {
     if (B < 0 || L < 0) return fail(DR_ERR_SHAPE, "negative dimension (B=%d L=%d)", B, L);
     if (C < 1) return fail(DR_ERR_SHAPE, "C=%d: at least one channel is needed", C);
-    if (C > (1 << 24)) return fail(DR_ERR_UNSUPPORTED, "C=%d: at most 2^24 channels are supported", C);
+    if (C > (1 << 23)) return fail(DR_ERR_UNSUPPORTED, "C=%d: at most 2^23 channels are supported", C);
     if (L > 2147483647 - 4096) return fail(DR_ERR_UNSUPPORTED, "L=%d too large", L);
-    if (B * channel_tiles(C) > kMaxSeqRows)
+    if (B * 2 * channel_tiles(C) > kMaxSeqRows)
         return fail(DR_ERR_UNSUPPORTED, "B*C=%.0f too large", (double)B * C);
     return DR_OK;
 }
@@ -444,34 +444,45 @@ dr_status check_gs_desc(const dr_gated_scan_desc* d) {
     return DR_OK;
 }
 
-// Runs side by side in a workgroup: the least power of two that covers the tokens,
-// 4 (a wave) to 32.  Sequences of several such tiles whose columns (128 channels of
-// one) are too few to fill the chip have a workgroup for each tile.
-constexpr int64_t kGsColumns = 512;
+// The kernels reach the rows of a tile by 32-bit offsets.
+dr_status check_gs_rows(std::initializer_list<const Rows*> in, std::initializer_list<const Rows*> out) {
+    for (auto list : {in, out})
+        for (const Rows* r : list)
+            if (r->n[2] > 1 && r->s.t > ((int64_t)1 << 23))
+                return fail(DR_ERR_UNSUPPORTED, "%s: tokens %lld elements apart, at most 2^23 are supported", r->name,
+                            (long long)r->s.t);
+    return check_rows(in, out);
+}
+
+int64_t gs_tiles(int C) { return ((int64_t)C + dr::kGsTile - 1) / dr::kGsTile; }
+
+// Runs side by side in a workgroup: 8 (a wave), 16 or 32, the least that cover the
+// tokens.  Sequences of several such tiles whose columns (64 channels of one) are too
+// few to fill the chip have a workgroup for each tile.
+constexpr int64_t kGsColumns = 1024;
 
 struct GsLayout {
     int groups, nseg;
-    size_t counter, maps, total;   // bytes
+    size_t maps, total;   // bytes; the counters stand first
 };
 
 GsLayout gs_layout(const dr_gated_scan_desc& d, bool bwd) {
     GsLayout w{};
     const int run = dr::gs_run(bwd);
-    w.groups = 4;
-    while (w.groups < 16 && (int64_t)w.groups * run < d.L) w.groups *= 2;
-    const int64_t columns = d.B * channel_tiles(d.C), span = (int64_t)w.groups * run, tiles = (d.L + span - 1) / span;
-    w.nseg = columns < kGsColumns ? (int)tiles : 1;
-    if (w.nseg > 1) {
-        w.maps = 256;   // the counter is in front
-        const size_t ngroup = (w.nseg + dr::kGsGroup - 1) / dr::kGsGroup, nblock = (ngroup + dr::kGsGroup - 1) / dr::kGsGroup;
-        w.total = w.maps + (size_t)columns * (w.nseg + ngroup + nblock) * dr::kGsTile * 8;
+    w.groups = 8;
+    while (w.groups < 32 && (int64_t)w.groups * run < d.L) w.groups *= 2;
+    const int64_t columns = d.B * gs_tiles(d.C), span = (int64_t)w.groups * run, tiles = (d.L + span - 1) / span;
+    w.nseg = (int)tiles;
+    if (tiles > 1 && columns < kGsColumns) {
+        w.maps = (size_t)columns * dr::kGsCounter * 4;
+        w.total = w.maps + (size_t)columns * w.nseg * 2 * dr::kGsTile * 8;
     }
     return w;
 }
 
 dr_status check_gs_tiles(const dr_gated_scan_desc& d, const GsLayout& w) {
     // a launch holds fewer than 2^32 threads
-    if (w.nseg > 1 && (double)d.B * channel_tiles(d.C) * w.nseg * 16 * w.groups > 4294967295.0)
+    if (w.total && (double)d.B * gs_tiles(d.C) * w.nseg * 256 > 4294967295.0)
         return fail(DR_ERR_UNSUPPORTED, "B*C*L=%.0f too large", (double)d.B * d.C * d.L);
     return DR_OK;
 }
@@ -479,12 +490,15 @@ dr_status check_gs_tiles(const dr_gated_scan_desc& d, const GsLayout& w) {
 void gs_split(const dr_gated_scan_desc& d, const GsLayout& w, void* workspace, dr::GsArgs& a) {
     a.groups = w.groups;
     a.nseg = w.nseg;
-    a.columns = (unsigned)(d.B * channel_tiles(d.C));
+    a.tiles = (unsigned)gs_tiles(d.C);
+    a.columns = d.B * a.tiles;
+    a.by_columns = dr::gs_divider(a.columns);
+    a.by_tiles = dr::gs_divider(a.tiles);
     char* ws = (char*)workspace;
-    if (w.nseg > 1) {
-        a.counter = (unsigned*)(ws + w.counter);
+    if (w.total) {
+        a.counters = (unsigned*)ws;
         a.maps = (uint64_t*)(ws + w.maps);
-        a.words = (w.total - w.maps) / 8;
+        a.words = w.total / 8;
     }
 }
 
@@ -533,7 +547,7 @@ dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const vo
     const Rows rx = seq_tensor("x", x, d->B, d->L, d->C, d->x, d->x_dtype),
                rg = seq_tensor("gate", gate, d->B, d->L, d->C, d->gate, d->gate_dtype),
                rh = seq_tensor("h", h, d->B, d->L, d->C, d->h, d->h_dtype);
-    if ((s = check_rows({&rx, &rg}, {&rh})) != DR_OK) return s;
+    if ((s = check_gs_rows({&rx, &rg}, {&rh})) != DR_OK) return s;
     const GsLayout w = d->L ? gs_layout(*d, false) : GsLayout{};
     if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
     const size_t need = w.total;
@@ -577,7 +591,7 @@ dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const vo
                rdh = seq_tensor("dh", dh, d->B, d->L, d->C, d->dh, d->dh_dtype),
                rdx = seq_tensor("dx", dx, d->B, d->L, d->C, d->dx, d->grad_dtype),
                rdg = seq_tensor("dgate", dgate, d->B, d->L, d->C, d->dgate, d->grad_dtype);
-    if ((s = check_rows({&rx, &rg, &rh, &rdh}, {&rdx, &rdg})) != DR_OK) return s;
+    if ((s = check_gs_rows({&rx, &rg, &rh, &rdh}, {&rdx, &rdg})) != DR_OK) return s;
     const GsLayout w = d->L ? gs_layout(*d, true) : GsLayout{};
     if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
     const size_t need = w.total;

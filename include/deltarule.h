@@ -733,7 +733,7 @@ dr_status dr_rmsnorm_bwd(const dr_rmsnorm_desc* d, const void* x, const float* w
  * Tokens before the first come from a state of W - 1 rows, oldest first (zeros
  * without one); the final state is the last W - 1 rows, as the next call takes it.
  *
- *   B, L >= 0; C >= 1 channels; W in [2, 8]
+ *   B, L >= 0; C in [1, 2^23] channels; W in [2, 8]
  *   x_dtype of x and the state, y_dtype of y or dx, dy_dtype of dy (backward)
  *   x, y, dy strides (y: of y or dx)
  */
@@ -804,7 +804,7 @@ dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const f
  *   dgate = d (h_{t-1} + c'(a) x) da/dgate,   c' = 0, -1 or -a / c
  * (where c = 0, at a = 1, the unit form's last term is left out).
  *
- *   B, L >= 0; C >= 1
+ *   B, L >= 0; C in [1, 2^23]; tokens at most 2^23 elements apart
  *   x_dtype of x; gate_dtype x_dtype or DR_F32; h_dtype of h; dh_dtype of dh;
  *   grad_dtype of dx and dgate (the last two: backward only)
  */
