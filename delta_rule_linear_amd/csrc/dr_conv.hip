@@ -19,22 +19,37 @@
 
 namespace dr {
 
-constexpr int kScAhead = 4;     // tokens loaded ahead
 constexpr int kScThreads = 256;
 constexpr int kScTile = 128;    // channels of a workgroup
+
+// Tokens loaded ahead, a multiple of W: the last W rows are kept in turn in the same
+// registers, and in a loop of so many tokens each has its place.
+constexpr int sc_ahead(int W) { return W == 2 ? 4 : W == 3 ? 6 : W; }
+int sc_run(int W) { return sc_ahead(W); }
 
 __device__ __forceinline__ float sc_sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z));
 }
-// z sigmoid(z), zero for -infinity (where the product would be NaN)
-__device__ __forceinline__ float sc_silu(float z) {
-    return z < -1e4f ? 0.f : z * sc_sigmoid(z);
-}
-// its slope, s (1 + z (1 - s))
+// z sigmoid(z); the bound makes it 0 for -infinity (a NaN comes through the sigmoid)
+__device__ __forceinline__ float sc_silu(float z) { return __builtin_fmaxf(z, -1e4f) * sc_sigmoid(z); }
+// its slope, s (1 + z (1 - s)), with bounds as above for both infinities
 __device__ __forceinline__ float sc_slope(float z) {
     const float s = sc_sigmoid(z);
-    return z < -1e4f ? 0.f : z > 1e4f ? 1.f : s * __builtin_fmaf(z, 1.f - s, 1.f);
+    return s * __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -1e4f, 1e4f), 1.f - s, 1.f);
 }
+
+// The rows of a run, one after the other; behind `last` the last one again.
+template <bool F32, bool SMALL>
+struct ScRows {
+    const char* p;
+    int64_t step;
+    int left;   // rows behind this one
+    __device__ __forceinline__ void next(bool f32, int at, int C, Oct<F32>& r) {
+        oct_load<F32, SMALL>(p, f32, at, C, r);
+        p += left > 0 ? step : 0;
+        --left;
+    }
+};
 
 // Row t of x, of the state's rows before the first token, or zeros.
 template <bool FX, bool SMALL>
@@ -56,7 +71,7 @@ __device__ __forceinline__ void sc_row(const ScArgs& a, const char* xb, unsigned
 
 template <bool FX, int W, bool SMALL>
 __global__ __launch_bounds__(kScThreads) void sc_fwd_kernel(ScArgs a) {
-    constexpr int U = kScAhead;
+    constexpr int U = sc_ahead(W);
     const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
     const unsigned nct = ((unsigned)a.C + kScTile - 1) / kScTile;
     const unsigned per = (unsigned)(((int64_t)a.L + 16 * a.run - 1) / (16 * a.run));   // tiles of a sequence
@@ -67,48 +82,39 @@ __global__ __launch_bounds__(kScThreads) void sc_fwd_kernel(ScArgs a) {
         const OctPlace pl = oct_place(ct * 16 + lane, a.C);
         const int64_t from = ((int64_t)k * 16 + sub) * a.run;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
-        char* yb = (char*)a.y + b * a.sy.b * ys;
-        float w[W][8], bias[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = SMALL ? min(e, a.C - 1) : pl.at + e;
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][e] = a.w[(size_t)c * W + j];
-            bias[e] = a.bias ? a.bias[c] : 0.f;
-        }
         if (from < a.L) {
-            const int t0 = (int)from, t1 = (int)min(from + a.run, (int64_t)a.L);
-            float past[W][8];   // rows t - W + 1 .. t
+            const int t0 = (int)from, n = (int)min((int64_t)a.run, a.L - from);
+            float w[W][8], bias[8];
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - (W - 1) + j, pl.at, past[j + 1]);
-            Oct<FX> next[U];
+            for (int e = 0; e < 8; ++e) {
+                const int c = SMALL ? min(e, a.C - 1) : pl.at + e;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                oct_load<FX, SMALL>(xb + (int64_t)min(t0 + u, t1 - 1) * a.sx.t * xs, a.x_f32, pl.at, a.C, next[u]);
-            for (int t = t0; t < t1; t += U) {
-                Oct<FX> now[U];
+                for (int j = 0; j < W; ++j) w[j][e] = a.w[(size_t)c * W + j];
+                bias[e] = a.bias ? a.bias[c] : 0.f;
+            }
+            float past[W][8];   // row t in past[(t - t0) % W]
 #pragma unroll
-                for (int u = 0; u < U; ++u) now[u] = next[u];
-                if (t + U < t1) {
+            for (int j = 1; j < W; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - W + j, pl.at, past[j]);
+            ScRows<FX, SMALL> rows{xb + t0 * a.sx.t * xs, a.sx.t * xs, n - 1};
+            char* y = (char*)a.y + (b * a.sy.b + t0 * a.sy.t) * ys;
+            Oct<FX> x[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        oct_load<FX, SMALL>(xb + (int64_t)min(t + U + u, t1 - 1) * a.sx.t * xs, a.x_f32, pl.at, a.C,
-                                            next[u]);
-                }
+            for (int u = 0; u < U; ++u) rows.next(a.x_f32, pl.at, a.C, x[u]);
+            for (int i = 0; i < n; i += U) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     float z[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) past[j][e] = past[j + 1][e];
-                        past[W - 1][e] = oct_value(now[u], e);
+                        past[u % W][e] = oct_value(x[u], e);
                         z[e] = bias[e];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) z[e] = __builtin_fmaf(w[j][e], past[j][e], z[e]);
+                        for (int j = 0; j < W; ++j) z[e] = __builtin_fmaf(w[j][e], past[(u + 1 + j) % W][e], z[e]);
                         if (a.silu) z[e] = sc_silu(z[e]);
                     }
-                    if (t + u < t1 && pl.own) oct_store<SMALL>(yb + (int64_t)(t + u) * a.sy.t * ys, a.y_f32, pl, z);
+                    if (i + U < n) rows.next(a.x_f32, pl.at, a.C, x[u]);
+                    if (i + u < n && pl.own) oct_store<SMALL>(y, a.y_f32, pl, z);
+                    y += a.sy.t * ys;
                 }
             }
         }
@@ -161,10 +167,11 @@ __global__ __launch_bounds__(kScThreads) void sc_step_kernel(ScArgs a) {
 }
 
 // dz of the run's tokens and of the W - 1 behind it (made again by the next run);
-// dx_t is whole once dz_{t+W-1} is in.
+// dx_t = sum_j w_j dz_{t+W-1-j} is whole once dz_{t+W-1} is in.  Rows behind the last
+// token have no gradient: their dy counts as 0.
 template <bool FX, bool FD, int W, bool SMALL>
 __global__ __launch_bounds__(kScThreads) void sc_bwd_kernel(ScArgs a) {
-    constexpr int U = kScAhead;
+    constexpr int U = sc_ahead(W);
     __shared__ float red[16][kScTile];
     const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
     const unsigned nct = ((unsigned)a.C + kScTile - 1) / kScTile;
@@ -189,85 +196,77 @@ __global__ __launch_bounds__(kScThreads) void sc_bwd_kernel(ScArgs a) {
         const int64_t from = ((int64_t)k * 16 + sub) * a.run;
         if (from >= a.L) continue;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
-        const char* yb = (const char*)a.dy + b * a.sdy.b * ds;
-        char* ob = (char*)a.y + b * a.sy.b * ys;
-        const int t0 = (int)from, t1 = (int)min(from + a.run, (int64_t)a.L);
-        const int end = t1 + W - 1;   // tokens from L on have no gradient
-        float past[W][8], dx[W][8];   // x and dx of rows t - W + 1 .. t
+        const int t0 = (int)from, rest = a.L - t0, n = min(a.run, rest);
+        float past[W][8], dz[W][8];   // rows t of x and dz in [(t - t0) % W]
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - (W - 1) + j, pl.at, past[j + 1]);
+        for (int j = 1; j < W; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - W + j, pl.at, past[j]);
 #pragma unroll
         for (int j = 0; j < W; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[j][e] = 0.f;
-        Oct<FX> nx[U];
-        Oct<FD> ny[U];
-        auto fetch = [&](int t) {
+            for (int e = 0; e < 8; ++e) dz[j][e] = 0.f;
+        ScRows<FX, SMALL> rx{xb + t0 * a.sx.t * xs, a.sx.t * xs, rest - 1};
+        ScRows<FD, SMALL> ry{(const char*)a.dy + (b * a.sdy.b + t0 * a.sdy.t) * ds, a.sdy.t * ds, rest - 1};
+        // the row of dx that is whole W - 1 tokens later; from the first token on also the
+        // state's rows
+        char* ob = (char*)a.y + (b * a.sy.b + ((int64_t)t0 - (W - 1)) * a.sy.t) * ys;
+        Oct<FX> x[U];
+        Oct<FD> y[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t r = min(t + u, a.L - 1);
-                oct_load<FX, SMALL>(xb + r * a.sx.t * xs, a.x_f32, pl.at, a.C, nx[u]);
-                oct_load<FD, SMALL>(yb + r * a.sdy.t * ds, a.dy_f32, pl.at, a.C, ny[u]);
+        for (int u = 0; u < U; ++u) {
+            rx.next(a.x_f32, pl.at, a.C, x[u]);
+            ry.next(a.dy_f32, pl.at, a.C, y[u]);
+        }
+        // token t0 + i, at place u of the U
+        auto token = [&](int u, int i, bool sums) {
+            if (i >= rest) {
+#pragma unroll
+                for (int q = 0; q < (FD ? 8 : 4); ++q) y[u].w[q] = 0u;
             }
+            float s[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                past[u % W][e] = oct_value(x[u], e);
+                float g = oct_value(y[u], e);
+                if (a.silu) {
+                    float z = bias[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) z = __builtin_fmaf(w[j][e], past[(u + 1 + j) % W][e], z);
+                    g *= sc_slope(z);
+                }
+                dz[u % W][e] = g;
+                if (sums) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][e] = __builtin_fmaf(g, past[(u + 1 + j) % W][e], dw[j][e]);
+                    db[e] += g;
+                }
+                s[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) s[e] = __builtin_fmaf(w[j][e], dz[(u + W - j) % W][e], s[e]);
+            }
+            const int r = i - (W - 1);   // of the run
+            if ((r >= 0 || t0 == 0) && r < n && pl.own) {
+                const int j = t0 + r + W - 1 - a.L;   // its place in the final state
+                if (j >= 0 && a.dstate_in) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s[e] += a.dstate_in[((size_t)b * (W - 1) + j) * a.C + (SMALL ? min(e, a.C - 1) : pl.at + e)];
+                }
+                if (r >= 0) oct_store<SMALL>(ob, a.y_f32, pl, s);
+                else if (a.dstate) oct_store<SMALL>(a.dstate + ((size_t)b * (W - 1) + (W - 1 + r)) * a.C, true, pl, s);
+            }
+            ob += a.sy.t * ys;
         };
-        fetch(t0);
-        for (int t = t0; t < end; t += U) {
-            Oct<FX> x[U];
-            Oct<FD> y[U];
+        int i = 0;
+        for (; i < n; i += U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                x[u] = nx[u];
-                y[u] = ny[u];
-            }
-            if (t + U < end) fetch(t + U);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int now = t + u;
-                if (now >= end) break;
-                const bool own = now < t1;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        past[j][e] = past[j + 1][e];
-                        dx[j][e] = dx[j + 1][e];
-                    }
-                    past[W - 1][e] = oct_value(x[u], e);
-                    dx[W - 1][e] = 0.f;
-                    float dz = now < a.L ? oct_value(y[u], e) : 0.f;
-                    if (a.silu) {
-                        float z = bias[e];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) z = __builtin_fmaf(w[j][e], past[j][e], z);
-                        dz = now < a.L ? dz * sc_slope(z) : 0.f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        if (now < a.L) dx[j][e] = __builtin_fmaf(w[j][e], dz, dx[j][e]);
-                        if (own) dw[j][e] = __builtin_fmaf(dz, past[j][e], dw[j][e]);
-                    }
-                    if (own) db[e] += dz;
-                }
-                // row now - W + 1 is whole: the run's own, or (before the first token) the state's
-                const int r = now - (W - 1);
-                if (r >= t0 || (t0 == 0 && r < 0)) {
-                    const int j = r + W - 1 - a.L;   // its place in the final state
-                    float s[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s[e] = dx[0][e];
-                        if (a.dstate_in && j >= 0) {
-                            const int c = SMALL ? min(e, a.C - 1) : pl.at + e;
-                            s[e] += a.dstate_in[((size_t)b * (W - 1) + j) * a.C + c];
-                        }
-                    }
-                    if (!pl.own) continue;
-                    if (r >= 0) oct_store<SMALL>(ob + (int64_t)r * a.sy.t * ys, a.y_f32, pl, s);
-                    else if (a.dstate)
-                        oct_store<SMALL>(a.dstate + ((size_t)b * (W - 1) + (W - 1 + r)) * a.C, true, pl, s);
-                }
+                token(u, i + u, true);
+                rx.next(a.x_f32, pl.at, a.C, x[u]);
+                ry.next(a.dy_f32, pl.at, a.C, y[u]);
             }
         }
+#pragma unroll
+        for (int u = 0; u < W - 1; ++u) token(u, i + u, false);
     }
     if (!a.part) return;
     float* part = a.part + (size_t)blk * a.C * (W + 1);

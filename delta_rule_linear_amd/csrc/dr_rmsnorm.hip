@@ -13,11 +13,16 @@
 
 namespace dr {
 
-LnShape rn_shape(int D) {
+// A wave per row up to 2048 values, which takes no barrier; where there are fewer rows
+// than the chip has places for waves, four waves per row of more than 512.
+constexpr size_t kRnFewRows = 1024;
+
+LnShape rn_shape(int D, size_t rows) {
     if (D <= 64) return {8, 1};
     if (D <= 128) return {16, 1};
     if (D <= 256) return {32, 1};
     if (D <= 512) return {64, 1};
+    if (D <= 2048 && rows <= kRnFewRows) return {256, 1};
     if (D <= 1024) return {64, 2};
     if (D <= 2048) return {64, 4};
     if (D <= 4096) return {256, 2};
@@ -25,8 +30,8 @@ LnShape rn_shape(int D) {
     return {256, 8};
 }
 
-int rn_pass_rows(int D) {
-    const LnShape s = rn_shape(D);
+int rn_pass_rows(int D, size_t rows) {
+    const LnShape s = rn_shape(D, rows);
     return kLnThreads / s.lanes * (s.vecs == 1 ? rn_rows<1>() : rn_rows<2>());
 }
 
@@ -197,7 +202,7 @@ static hipError_t rn_launch(const RnArgs& a, int slot, hipStream_t st) {
 
 template <bool FX, int RES, bool Q8, bool TAIL>
 static hipError_t rn_launch_shape(const RnArgs& a, int slot, hipStream_t st) {
-    const LnShape s = rn_shape(a.D);
+    const LnShape s = rn_shape(a.D, (size_t)a.groups * a.rows);
     if (s.lanes == 8) return rn_launch<FX, RES, Q8, TAIL, false, 8, 1>(a, slot, st);
     if (s.lanes == 16) return rn_launch<FX, RES, Q8, TAIL, false, 16, 1>(a, slot, st);
     if (s.lanes == 32) return rn_launch<FX, RES, Q8, TAIL, false, 32, 1>(a, slot, st);
@@ -206,6 +211,7 @@ static hipError_t rn_launch_shape(const RnArgs& a, int slot, hipStream_t st) {
         if (s.vecs == 2) return rn_launch<FX, RES, Q8, TAIL, false, 64, 2>(a, slot, st);
         return rn_launch<FX, RES, Q8, TAIL, false, 64, 4>(a, slot, st);
     }
+    if (s.vecs == 1) return rn_launch<FX, RES, Q8, TAIL, false, 256, 1>(a, slot, st);
     if (s.vecs == 2) return rn_launch<FX, RES, Q8, TAIL, false, 256, 2>(a, slot, st);
     if (s.vecs == 4) return rn_launch<FX, RES, Q8, TAIL, false, 256, 4>(a, slot, st);
     return rn_launch<FX, RES, Q8, TAIL, false, 256, 8>(a, slot, st);

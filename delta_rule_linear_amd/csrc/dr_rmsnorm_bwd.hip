@@ -169,7 +169,7 @@ static hipError_t rn_launch(const RnArgs& a, int slot, hipStream_t st) {
 
 template <bool FX, bool FDY, int DS, bool TAIL>
 static hipError_t rn_launch_shape(const RnArgs& a, int slot, hipStream_t st) {
-    const LnShape s = rn_shape(a.D);
+    const LnShape s = rn_shape(a.D, (size_t)a.groups * a.rows);
     if (s.lanes == 8) return rn_launch<FX, FDY, DS, TAIL, false, 8, 1>(a, slot, st);
     if (s.lanes == 16) return rn_launch<FX, FDY, DS, TAIL, false, 16, 1>(a, slot, st);
     if (s.lanes == 32) return rn_launch<FX, FDY, DS, TAIL, false, 32, 1>(a, slot, st);
@@ -178,6 +178,7 @@ static hipError_t rn_launch_shape(const RnArgs& a, int slot, hipStream_t st) {
         if (s.vecs == 2) return rn_launch<FX, FDY, DS, TAIL, false, 64, 2>(a, slot, st);
         return rn_launch<FX, FDY, DS, TAIL, false, 64, 4>(a, slot, st);
     }
+    if (s.vecs == 1) return rn_launch<FX, FDY, DS, TAIL, false, 256, 1>(a, slot, st);
     if (s.vecs == 2) return rn_launch<FX, FDY, DS, TAIL, false, 256, 2>(a, slot, st);
     if (s.vecs == 4) return rn_launch<FX, FDY, DS, TAIL, false, 256, 4>(a, slot, st);
     return rn_launch<FX, FDY, DS, TAIL, false, 256, 8>(a, slot, st);

@@ -37,8 +37,9 @@ struct RnArgs {
     int block;            // columns that share a scale: 128, or 0 for a row
     int x_f32, r_f32, y_f32, dy_f32;
 };
-LnShape rn_shape(int D);
-int rn_pass_rows(int D);
+// rows: of all groups
+LnShape rn_shape(int D, size_t rows);
+int rn_pass_rows(int D, size_t rows);
 hipError_t launch_rn_fwd(const RnArgs& a, int slot, hipStream_t st);
 hipError_t launch_rn_bwd(const RnArgs& a, int slot, hipStream_t st);
 
@@ -64,6 +65,7 @@ struct ScArgs {
     unsigned blocks;      // backward: workgroups that share a channel tile's tiles
     int x_f32, y_f32, dy_f32;
 };
+int sc_run(int W);    // a thread's tokens are a multiple of this
 hipError_t launch_sc_fwd(const ScArgs& a, int slot, hipStream_t st);
 hipError_t launch_sc_bwd(const ScArgs& a, int slot, hipStream_t st);
 hipError_t launch_sc_step(const ScArgs& a, int slot, hipStream_t st);

@@ -85,7 +85,7 @@ dr_status check_rn_desc(const dr_rmsnorm_desc* d, bool e4m3) {
 void rn_groups(const dr_rmsnorm_desc& d, dr::RnArgs& a, bool bwd) {
     a.groups = d.per_head ? d.H : 1;
     a.rows = d.per_head ? (unsigned)d.B * d.L : (unsigned)d.B * d.H * d.L;
-    const unsigned pass = (unsigned)dr::rn_pass_rows(d.D);
+    const unsigned pass = (unsigned)dr::rn_pass_rows(d.D, (size_t)a.groups * a.rows);
     const unsigned passes = (a.rows + pass - 1) / pass;
     const unsigned most = d.D <= (bwd ? 512 : 2048) ? 1024 : 512;
     const unsigned want = std::max(1u, (most + a.groups - 1) / a.groups);
@@ -272,13 +272,14 @@ dr_status check_sc_desc(const dr_short_conv_desc* d) {
     return DR_OK;
 }
 
-// Tokens of a thread: as many (up to 64, a run reads W - 1 rows of the one before)
-// as leave the chip about four workgroups per compute unit.
-void sc_split(const dr_short_conv_desc& d, dr::ScArgs& a, int most) {
+// Tokens of a thread: as many (up to 16 times the kernel's step; a run reads W - 1 rows
+// of the one before) as leave the chip about four workgroups per compute unit.
+void sc_split(const dr_short_conv_desc& d, dr::ScArgs& a) {
     const int64_t nct = channel_tiles(d.C);
-    a.run = most;
+    const int step = dr::sc_run(d.W);
+    a.run = 16 * step;
     auto tiles = [&] { return (int64_t)d.B * (((int64_t)d.L + 16 * a.run - 1) / (16 * a.run)); };
-    while (a.run > 4 && tiles() * nct < 1024) a.run /= 2;
+    while (a.run > step && tiles() * nct < 1024) a.run /= 2;
     a.tiles = (unsigned)std::min<int64_t>(tiles(), kMaxSeqRows);
     a.blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.tiles, (1024 + nct - 1) / nct));
 }
@@ -291,7 +292,7 @@ dr_status check_sc_tiles(const dr_short_conv_desc& d) {
 
 size_t sc_part_bytes(const dr_short_conv_desc& d) {
     dr::ScArgs a{};
-    sc_split(d, a, 64);
+    sc_split(d, a);
     return (size_t)a.blocks * d.C * (d.W + 1) * sizeof(float);
 }
 
@@ -346,7 +347,7 @@ dr_status dr_short_conv_fwd(const dr_short_conv_desc* d, const void* x, const fl
     sc_args(*d, x, weight, bias, state, a);
     a.y = y;
     a.state_out = state_out;
-    sc_split(*d, a, 64);
+    sc_split(*d, a);
     return hip_status(dr::launch_sc_fwd(a, slot, st), "short convolution launch");
 }
 
@@ -399,7 +400,7 @@ dr_status dr_short_conv_bwd(const dr_short_conv_desc* d, const void* x, const fl
     a.db = dbias;
     a.dstate = dstate;
     a.part = sums ? (float*)workspace : nullptr;
-    sc_split(*d, a, 64);
+    sc_split(*d, a);
     return hip_status(dr::launch_sc_bwd(a, slot, st), "short convolution backward launch");
 }
 
