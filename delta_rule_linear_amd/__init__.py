@@ -1020,6 +1020,11 @@ def _rmsnorm_plan(sizes, *strides):
     return desc, ctypes.byref(desc), int(lib().dr_rmsnorm_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
+def _new_f32(like, shape, device):
+    """A new fp32 tensor, from another one if there is one (less work than by a device)."""
+    return _torch().empty(shape, dtype=_torch().float32, device=device) if like is None else like.new_empty(shape)
+
+
 def _rmsnorm_fwd(x, weight, residual, eps, out_dtype, block, y, scale, rstd, total, stream):
     torch = _torch()
     e4m3 = block is not None
@@ -1035,7 +1040,7 @@ def _rmsnorm_fwd(x, weight, residual, eps, out_dtype, block, y, scale, rstd, tot
         else:
             _need_rows(y, "y", dev, torch.float8_e4m3fn if e4m3 else out_dtype, x.shape)
         if rstd is None:
-            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+            rstd = _new_f32(weight, lead, dev)
         else:
             _need_on(rstd, "rstd", dev, torch.float32, lead)
         if e4m3:
@@ -1043,7 +1048,7 @@ def _rmsnorm_fwd(x, weight, residual, eps, out_dtype, block, y, scale, rstd, tot
                 raise ValueError(f"block must be 128 (columns of a scale) or 0 (a row), got {block!r}")
             shape = lead + ((x.shape[-1] + 127) // 128 if block else 1,)
             if scale is None:
-                scale = torch.empty(shape, dtype=torch.float32, device=dev)
+                scale = _new_f32(weight, shape, dev)
             else:
                 _need_on(scale, "scale", dev, torch.float32, shape)
         if residual is not None:

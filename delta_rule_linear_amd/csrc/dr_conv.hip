@@ -38,14 +38,16 @@ __device__ __forceinline__ float sc_slope(float z) {
     return s * __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -1e4f, 1e4f), 1.f - s, 1.f);
 }
 
-// The rows of a run, one after the other; behind `last` the last one again.
+// The rows of a run, one after the other; behind the last one that one again.  They are
+// loaded as read once: the outputs stay in the last-level cache instead, for who comes
+// next (2 x 16384 x 2048 67 -> 60 us, backward 101 -> 93).
 template <bool F32, bool SMALL>
 struct ScRows {
     const char* p;
     int64_t step;
     int left;   // rows behind this one
     __device__ __forceinline__ void next(bool f32, int at, int C, Oct<F32>& r) {
-        oct_load<F32, SMALL>(p, f32, at, C, r);
+        oct_load<F32, SMALL, true>(p, f32, at, C, r);
         p += left > 0 ? step : 0;
         --left;
     }

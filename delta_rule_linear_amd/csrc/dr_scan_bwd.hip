@@ -56,7 +56,8 @@ __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
         // workgroups start in their order as a rule: the rows of the tile that would then be
         // this one's are asked for before the tile is known
         seg0 = gs_divide(blockIdx.x, a.by_columns);
-        first = blockIdx.x - seg0 * a.columns;
+        first = gs_column(a, blockIdx.x - seg0 * a.padded);
+        if (first >= a.columns) return;
         const unsigned ticket = tid == 0 ? gs_draw(a, first) : 0;
         load(first, seg0);
         if (tid == 0) drawn = ticket;
@@ -151,7 +152,7 @@ static hipError_t gs_launch(const GsArgs& a, int slot, hipStream_t st) {
     if (a.maps) {
         const hipError_t e = launch_gs_clear(a, slot, st);
         if (e != hipSuccess) return e;
-        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.columns * a.nseg), dim3(256), 0, st, a);
+        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.padded * a.nseg), dim3(256), 0, st, a);
     }
     return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups), 0, st, a);
 }

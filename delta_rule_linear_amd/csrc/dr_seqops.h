@@ -98,8 +98,9 @@ struct GsArgs {
     int groups;           // runs of tokens side by side in a workgroup
     int nseg;             // tiles of a sequence
     unsigned columns;     // B times the channel tiles
+    unsigned padded;      // columns, and some that are left out
     unsigned tiles;       // channel tiles
-    GsDivide by_columns, by_tiles;
+    GsDivide by_columns, by_tiles;   // padded columns
     uint64_t* maps;       // where a column's tiles have workgroups of their own, else NULL; for each
                           // column [nseg][64] what each tile does to the state, [nseg][64] what it
                           // starts with

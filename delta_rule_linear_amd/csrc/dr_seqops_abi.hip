@@ -81,13 +81,18 @@ dr_status check_rn_desc(const dr_rmsnorm_desc* d, bool e4m3) {
 }
 
 // Groups of rows with one weight, and the workgroups of each: no more than stay on
-// the chip, so that all walk their rows with the next ones in flight.
+// the chip, so that all walk their rows with the next ones in flight.  Forward: four per
+// compute unit, two for rows of more than 1024 (of 8191 x 2048 bf16 with a residual 4:
+// 26.2 us, 2: 25.5, 1: 26.5).  Backward, which leaves a row of sums for each: two, or
+// one where a lane holds four octets and more (of 16384 x 1024 2: 27.1, 4: 30.4, 1: 27.8;
+// of 8191 x 2048 1: 29.4, 2: 35.0, 4: 46.7).
 void rn_groups(const dr_rmsnorm_desc& d, dr::RnArgs& a, bool bwd) {
     a.groups = d.per_head ? d.H : 1;
     a.rows = d.per_head ? (unsigned)d.B * d.L : (unsigned)d.B * d.H * d.L;
     const unsigned pass = (unsigned)dr::rn_pass_rows(d.D, (size_t)a.groups * a.rows);
     const unsigned passes = (a.rows + pass - 1) / pass;
-    const unsigned most = d.D <= (bwd ? 512 : 2048) ? 1024 : 512;
+    const unsigned most = bwd ? (dr::rn_shape(d.D, (size_t)a.groups * a.rows).vecs >= 4 ? 256 : 512)
+                              : d.D <= 1024 ? 1024 : 512;
     const unsigned want = std::max(1u, (most + a.groups - 1) / a.groups);
     a.blocks = std::max(1u, std::min(want, passes));
 }
@@ -483,7 +488,7 @@ GsLayout gs_layout(const dr_gated_scan_desc& d, bool bwd) {
 
 dr_status check_gs_tiles(const dr_gated_scan_desc& d, const GsLayout& w) {
     // a launch holds fewer than 2^32 threads
-    if (w.total && (double)d.B * gs_tiles(d.C) * w.nseg * 256 > 4294967295.0)
+    if (w.total && ((double)d.B * gs_tiles(d.C) + 7) * w.nseg * 256 > 4294967295.0)
         return fail(DR_ERR_UNSUPPORTED, "B*C*L=%.0f too large", (double)d.B * d.C * d.L);
     return DR_OK;
 }
@@ -493,7 +498,9 @@ void gs_split(const dr_gated_scan_desc& d, const GsLayout& w, void* workspace, d
     a.nseg = w.nseg;
     a.tiles = (unsigned)gs_tiles(d.C);
     a.columns = d.B * a.tiles;
-    a.by_columns = dr::gs_divider(a.columns);
+    // a multiple of eight, but for few columns, of which no die may stay without
+    a.padded = a.columns < 64 ? a.columns : (a.columns + 7) / 8 * 8;
+    a.by_columns = dr::gs_divider(a.padded);
     a.by_tiles = dr::gs_divider(a.tiles);
     char* ws = (char*)workspace;
     if (w.total) {
