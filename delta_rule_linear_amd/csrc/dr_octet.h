@@ -42,8 +42,9 @@ __device__ __forceinline__ int oct_channel(int group, int e, int C) {
 }
 
 // row: the row's first channel.  SMALL converts to fp32 at once, of either type
-// (one kernel serves all types); the others take F32's.  ONCE: the values are not
-// read again soon, and leave the caches to others.
+// (one kernel serves all types); the others take F32's.  ONCE: bf16 values are
+// not read again soon, and leave the caches to others (fp32's 32 bytes a lane are two
+// accesses to the same line, which then comes twice).
 template <bool F32, bool SMALL, bool ONCE = false>
 __device__ __forceinline__ void oct_load(const void* row, bool f32, int at, int C, Oct<F32>& r) {
     if constexpr (SMALL) {
@@ -56,7 +57,7 @@ __device__ __forceinline__ void oct_load(const void* row, bool f32, int at, int 
         }
     } else if constexpr (F32) {
         const oct_u32x4* p = reinterpret_cast<const oct_u32x4*>(static_cast<const float*>(row) + at);
-        const oct_u32x4 a = ONCE ? __builtin_nontemporal_load(p) : p[0], b = ONCE ? __builtin_nontemporal_load(p + 1) : p[1];
+        const oct_u32x4 a = p[0], b = p[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             r.w[i] = a[i];

@@ -50,7 +50,8 @@ __device__ __forceinline__ GsFactor gs_factor(float g) {
         q = __builtin_fmaf(q, g, 0.5f);
         q = __builtin_fmaf(g * g, q, g);
         // as integers, negative floats grow with their size, and positive ones are larger
-        o.part = __float_as_int(g) < __float_as_int(-0.4f) ? q : e;
+        // (of -0 the series is +0, whose sign has to be set)
+        o.part = __float_as_int(g) < __float_as_int(-0.4f) ? -__builtin_fabsf(q) : e;
         o.rest = gs_masked(~gs_near(o.part), 1.f) - o.part;
     } else {
         const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
@@ -83,7 +84,8 @@ template <int INP>
 __device__ __forceinline__ float gs_input(const GsFactor& f) {
     if constexpr (INP == kGsPlain) return 1.f;
     if constexpr (INP == kGsBlend) return f.rest;
-    return __builtin_amdgcn_sqrtf(f.rest * (2.f - f.rest));
+    // 1 - a^2 = (1 - a) (2 - (1 - a)), scaled: the root takes no subnormal numbers
+    return __builtin_amdgcn_sqrtf(f.rest * __builtin_fmaf(f.rest, -0x1p64f, 0x1p65f)) * 0x1p-32f;
 }
 
 // a h + b
@@ -98,10 +100,18 @@ struct GsMap {
 __device__ __forceinline__ float gs_apply(const GsMap& m, float h) {
     return __builtin_fmaf(m.one, h, __builtin_fmaf(m.part, h, m.b));
 }
+// A decay that has become strong over several tokens is held as it is, so that it is
+// exact relative to itself (1 + part is exact from -1 to -1/2).
+__device__ __forceinline__ void gs_settle(float& one, float& part) {
+    const bool strong = part < -0.5f;
+    part = strong ? 1.f + part : part;
+    one = strong ? 0.f : one;
+}
 // first m, then n
 __device__ __forceinline__ GsMap gs_then(const GsMap& m, const GsMap& n) {
-    return {m.one * n.one, __builtin_fmaf(m.part, n.part, __builtin_fmaf(m.one, n.part, m.part * n.one)),
-            gs_apply(n, m.b)};
+    GsMap r{m.one * n.one, __builtin_fmaf(m.part, n.part, __builtin_fmaf(m.one, n.part, m.part * n.one)), gs_apply(n, m.b)};
+    gs_settle(r.one, r.part);
+    return r;
 }
 // one token's, and first m, then a token
 __device__ __forceinline__ GsMap gs_token(float part, float b) { return {gs_masked(gs_near(part), 1.f), part, b}; }
@@ -163,9 +173,12 @@ __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
 // before it in the wave, and the wave's map goes to the others.  FWD: runs, and waves,
 // from the first to the last.
 template <bool FWD>
-__device__ __forceinline__ void gs_join(const GsLds& l, int turn, const float (&one)[8], const float (&part)[8],
-                                        const float (&b)[8]) {
+__device__ __forceinline__ void gs_join(const GsLds& l, int turn, float (&one)[8], float (&part)[8], const float (&b)[8]) {
     const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, at = (tid >> 3) * kGsTile + (tid & 7) * 8;
+    // a run is short enough for this to be late enough: four tokens' decays that are near
+    // one (over 1/2) make 1/16 at least
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gs_settle(one[e], part[e]);
     gs_put(l.one + at, one);
     gs_put(l.part + at, part);
     gs_put(l.b + at, b);

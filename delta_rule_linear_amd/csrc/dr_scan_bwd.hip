@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
         for (int i = 0; i < T; ++i) {
             const unsigned r = min(tg * T + i, last);
             // the row before; the first token's comes from h0
-            oct_load<FH, SMALL>(t0 + r ? hb + (int)(r * ht) - (int)ht : hb, a.h_f32, pl.at, a.C, hp[i]);
+            oct_load<FH, SMALL>(t0 + r ? hb + ((int64_t)(r * ht) - ht) : hb, a.h_f32, pl.at, a.C, hp[i]);
             if (INP != kGsPlain) oct_load<FX, SMALL>(xb + r * xt, a.x_f32, pl.at, a.C, x[i]);
         }
     };

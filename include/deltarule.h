@@ -789,14 +789,15 @@ dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const f
  *   h_t = a_t h_{t-1} + c(a_t) x_t
  *
  *   decay   DR_SCAN_LOG    a = e^gate, gate expected <= 0 (not checked)
- *           DR_SCAN_LOGIT  a = 1 / (1 + e^-gate)
+ *           DR_SCAN_LOGIT  a = 1 / (1 + e^-gate) (beyond 87 it is 1)
  *   inputs  DR_INPUT_PLAIN c = 1;  DR_INPUT_BLEND c = 1 - a;
  *           DR_INPUT_UNIT  c = sqrt(1 - a^2), which keeps the variance of unit
  *                          inputs (NaN for a > 1)
  *
  * A log of -inf (a = 0) starts the state anew at that token.  1 - a is made
- * directly and a kept in two parts, so that memories of many tokens cost no
- * accuracy.  A NaN or Inf reaches the later tokens of its channel, also through a
+ * directly where a < 1, and a kept as 1 - (1 - a) where it is near one, so that
+ * memories of many tokens cost no accuracy; strong decays, also over many tokens, are
+ * exact relative to themselves.  A NaN or Inf reaches the later tokens of its channel, also through a
  * zero decay, and no other channel.  Gradients, from the forward's h as it was
  * written (rounded where that is bf16):
  *

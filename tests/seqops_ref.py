@@ -133,8 +133,10 @@ def scan_backward(x, g, h0, h, dh, dlast, decay, inputs):
 
 def decay_bound(g, a, rest):
     """The kernels' a: 1 - a is off by (2 |g| + 6) u of itself where a > 1/2, a by as
-    much of itself below about 2/3; the smaller of the two at most doubles between."""
-    return (4 * torch.nan_to_num(g, neginf=0.0).abs() + 12) * U * torch.minimum(a, rest)
+    much of itself below about 2/3; the smaller of the two at most doubles between.  A
+    state that grows (a > 1) has a rounded to fp32, off by (2 |g| + 4) u of itself."""
+    size = (4 * torch.nan_to_num(g, neginf=0.0).abs() + 12) * U
+    return size * torch.where(rest < 0, a, torch.minimum(a, rest))
 
 
 def scan_errors(x, g, h0, decay, inputs):
@@ -142,7 +144,7 @@ def scan_errors(x, g, h0, decay, inputs):
     absolute values M, and a and c are off by decay_bound and (2 |g| + 10) u."""
     a, rest, c = scan_factors(g, decay, inputs)
     ga = torch.nan_to_num(g, neginf=0.0).abs()
-    da, dc = decay_bound(g, a, rest), c * (2 * ga + 10) * U * (inputs != "plain")
+    da, dc = decay_bound(g, a, rest), c.abs() * (2 * ga + 10) * U * (inputs != "plain")
     B, L, C = x.shape
     M = x.new_zeros(B, C) if h0 is None else h0.abs()
     E = torch.zeros_like(M)
@@ -150,7 +152,8 @@ def scan_errors(x, g, h0, decay, inputs):
     for t in range(L):
         before = M
         M = a[:, t] * M + (c[:, t] * x[:, t]).abs()
-        E = a[:, t] * E + da[:, t] * before + dc[:, t] * x[:, t].abs() + 8 * U * M
+        grows = (rest[:, t] < 0) * (inputs != "plain") * 8 * U   # 1 - a from e^g
+        E = a[:, t] * E + da[:, t] * before + (dc[:, t] + grows) * x[:, t].abs() + 8 * U * M
         out[:, t] = E
     return out, E
 
@@ -166,6 +169,7 @@ def scan_back_errors(x, g, ref, dh, dlast, decay, inputs):
         ED[:, t] = E + 8 * U * ref["M"][:, t]
         E = a[:, t] * ED[:, t] + da[:, t] * ref["M"][:, t] + 8 * U * a[:, t] * ref["M"][:, t]
     rel = (2 * ga + 12) * U
-    dx = c * ED + c * ref["D"].abs() * rel
+    # where the state grows, 1 - a comes from e^g and is off by fp32's rounding of that
+    dx = c.abs() * ED + (c.abs() * rel + torch.where(rest < 0, rel, 0 * rel)) * ref["D"].abs()
     dg = ref["slope"] * (ED * ref["full"].abs() + ref["M"] * ref["size"] * (2 * rel + 4 * U))
     return dx, dg, E
