@@ -1079,7 +1079,8 @@ def dr_rmsnorm_fwd(x, weight=None, residual=None, *, eps: float = 1e-5, out_dtyp
 
     x: [N,D], [B,L,D] or [B,H,L,D] (bf16 or fp32) with a weight [D] fp32 (None:
     ones); or, with one weight per head [H,D], [N,H,D] or [B,H,L,D].  residual: x's
-    shape, of x's dtype or fp32; total is the sum in its dtype (None without one).
+    shape, of x's dtype or fp32; total is the sum in its dtype (None without one), and
+    may be the residual itself.
     y and rstd come from the sum before that rounding.  Channels are contiguous,
     other strides free, rows start at any element.  y defaults to out_dtype (x's
     dtype) in x's order of dimensions; rstd is fp32, of x's leading shape.

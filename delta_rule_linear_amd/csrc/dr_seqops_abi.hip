@@ -136,7 +136,11 @@ dr_status rn_forward(const dr_rmsnorm_desc* d, const void* x, const void* residu
                            {weight, 4, "weight"}, {y, e4m3 ? 1 : elem_size(d->y_dtype), "y"},
                            {total, elem_size(d->res_dtype), "total"}, {scale, 4, "scale"}, {rstd, 4, "rstd"}})) != DR_OK)
         return s;
-    if ((s = check_disjoint(outs, 4, ins, 3)) != DR_OK) return s;
+    // the sum may take the residual's place, row by row
+    auto same = [](int n, long long p, long long q) { return n <= 1 || p == q; };
+    const bool in_place = same(d->B, d->res.b, d->total.b) && same(d->H, d->res.h, d->total.h) &&
+                          same(d->L, d->res.t, d->total.t);
+    if ((s = check_disjoint(outs, 4, ins, 3, in_place ? total : nullptr, in_place ? residual : nullptr)) != DR_OK) return s;
     dr::RnArgs a{};
     a.x = x;
     a.r = residual;

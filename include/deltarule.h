@@ -682,7 +682,8 @@ typedef struct {
  *   residual  [B][H][L][D] res_dtype, strided, or NULL
  *   weight    [H][D] or [D] fp32, or NULL (ones)
  *   y         [B][H][L][D] y_dtype, strided, written
- *   total     [B][H][L][D] res_dtype, strided, written; NULL iff residual is
+ *   total     [B][H][L][D] res_dtype, strided, written; NULL iff residual is; may
+ *             be the residual itself (with its strides)
  *   rstd      [B][H][L] fp32, written, or NULL to skip
  */
 dr_status dr_rmsnorm_fwd(const dr_rmsnorm_desc* d, const void* x, const void* residual, const float* weight, void* y,

@@ -167,6 +167,20 @@ def test_shapes_layouts_and_absent_weights():
     assert not drl.dr_rmsnorm_bwd(e, w, rstd, y)["dweight"].any()
 
 
+@pytest.mark.parametrize("rows,D,dtype", [(5, 64, "f32"), (700, 129, "bf16"), (3000, 2048, "bf16"), (40, 5001, "f32"), (9, 5, "f32")])
+def test_the_sum_in_the_residuals_place(rows, D, dtype):
+    import delta_rule_linear_amd as drl
+    gen = torch.Generator().manual_seed(D)
+    x, r = (torch.randn((rows, D), generator=gen).to(DT[dtype]).cuda() for _ in range(2))
+    y, rstd, total = drl.dr_rmsnorm_fwd(x, None, r)
+    y8, scale, _, _ = drl.dr_rmsnorm_fwd_e4m3(x, None, r)
+    for f in (lambda t: drl.dr_rmsnorm_fwd(x, None, t, total=t)[0], lambda t: drl.dr_rmsnorm_fwd_e4m3(x, None, t, total=t)[0]):
+        t = r.clone()
+        got = f(t)
+        assert torch.equal(t, total)
+        assert torch.equal(got, y) if got.dtype == y.dtype else torch.equal(got.view(torch.uint8), y8.view(torch.uint8))
+
+
 def test_zero_tiny_large_and_bad_rows():
     import delta_rule_linear_amd as drl
     x = torch.zeros((4, 256), device="cuda")

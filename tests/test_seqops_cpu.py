@@ -101,6 +101,12 @@ def test_norm_overlaps_and_workspace():
         for o in ("y", "total", "rstd"):
             assert rf(rn(), **{o: F(i) + 256}) == drl.DR_ERR_UNSUPPORTED and "overlaps" in drl.dr_last_error()
     assert re_(rn(), scale=F(3) + 16) == drl.DR_ERR_UNSUPPORTED
+    # the sum in the residual's place, but with other strides
+    d = rn()
+    d.total.b += 8
+    assert rf(d, total=F(1)) == drl.DR_ERR_UNSUPPORTED and "overlaps" in drl.dr_last_error()
+    assert rf(rn(), total=F(1) + 4) == drl.DR_ERR_UNSUPPORTED
+    assert rf(rn(), total=F(1), rstd=F(0)) == drl.DR_ERR_UNSUPPORTED and "rstd" in drl.dr_last_error()   # goes on
     # the last byte of y, and the first one behind it
     size = 2 * 3 * 50 * 200
     assert re_(rn(), scale=F(3) + size - 4) == drl.DR_ERR_UNSUPPORTED
