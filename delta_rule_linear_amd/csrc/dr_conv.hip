@@ -5,10 +5,14 @@
 //   dz_t = dy_t act'(z_t),  dx_t = sum_j w_j dz_{t+W-1-j},  dw_j = sum_t dz_t x_{t-W+1+j},  db = sum_t dz_t
 //
 // The tokens before the first are the state's W - 1 rows.  A thread has eight
-// channels and runs along `run` tokens, the last W - 1 rows in registers and the
-// next kAhead rows loaded ahead; 16 lanes have 128 channels of a token side by
-// side.  Both passes read x (and dy) once, but for the W - 1 rows between two runs,
-// and write once: memory bounds them.
+// channels of a run of tokens, the last W rows in registers and the next ones loaded
+// ahead; 16 lanes have 128 channels of a token side by side, a workgroup 16 runs, of
+// one sequence or several.  Both passes read x (and dy) once, but for the W - 1 rows
+// between two runs, and write once: memory bounds them.
+//
+// Measured: forward of 2 x 16384 x 2048 bf16, W = 4, a slice of wider rows, 62 us for 268
+// MB (4.4 TB/s; a large copy reaches 5.2); its backward 95 us for 403 MB (4.2), with two
+// waves per SIMD (254 registers: taps, their sums, and the rows of x and dz).
 
 #include <hip/hip_runtime.h>
 
@@ -24,7 +28,7 @@ constexpr int kScTile = 128;    // channels of a workgroup
 
 // Tokens loaded ahead, a multiple of W: the last W rows are kept in turn in the same
 // registers, and in a loop of so many tokens each has its place.
-constexpr int sc_ahead(int W) { return W == 2 ? 4 : W == 3 ? 6 : W; }
+constexpr int sc_ahead(int W) { return W == 2 ? 4 : W; }
 int sc_run(int W) { return sc_ahead(W); }
 
 __device__ __forceinline__ float sc_sigmoid(float z) {
@@ -76,16 +80,15 @@ __global__ __launch_bounds__(kScThreads) void sc_fwd_kernel(ScArgs a) {
     constexpr int U = sc_ahead(W);
     const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
     const unsigned nct = ((unsigned)a.C + kScTile - 1) / kScTile;
-    const unsigned per = (unsigned)(((int64_t)a.L + 16 * a.run - 1) / (16 * a.run));   // tiles of a sequence
+    const unsigned per = ((unsigned)a.L + a.run - 1) / a.run;   // runs of a sequence
     const int xs = a.x_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2;
     for (size_t item = blockIdx.x; item < (size_t)a.tiles * nct; item += gridDim.x) {
-        const unsigned ct = (unsigned)(item % nct), tile = (unsigned)(item / nct);
-        const unsigned b = tile / per, k = tile - b * per;
+        const unsigned ct = (unsigned)(item % nct), run = (unsigned)(item / nct) * 16 + sub;
+        const unsigned b = run / per, t0 = (run - b * per) * a.run;
         const OctPlace pl = oct_place(ct * 16 + lane, a.C);
-        const int64_t from = ((int64_t)k * 16 + sub) * a.run;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
-        if (from < a.L) {
-            const int t0 = (int)from, n = (int)min((int64_t)a.run, a.L - from);
+        if (b < (unsigned)a.B) {
+            const int n = min(a.run, a.L - (int)t0);
             float w[W][8], bias[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -96,7 +99,7 @@ __global__ __launch_bounds__(kScThreads) void sc_fwd_kernel(ScArgs a) {
             }
             float past[W][8];   // row t in past[(t - t0) % W]
 #pragma unroll
-            for (int j = 1; j < W; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - W + j, pl.at, past[j]);
+            for (int j = 1; j < W; ++j) sc_row<FX, SMALL>(a, xb, b, (int)t0 - W + j, pl.at, past[j]);
             ScRows<FX, SMALL> rows{xb + t0 * a.sx.t * xs, a.sx.t * xs, n - 1};
             char* y = (char*)a.y + (b * a.sy.b + t0 * a.sy.t) * ys;
             Oct<FX> x[U];
@@ -120,18 +123,16 @@ __global__ __launch_bounds__(kScThreads) void sc_fwd_kernel(ScArgs a) {
                 }
             }
         }
-        if (k == 0 && a.state_out) {
-            // the last W - 1 rows; the only workgroup that reads the state writes it,
-            // so that both may be one tensor
-            __syncthreads();
-            for (int j0 = 0; j0 < W - 1; j0 += 16) {
-                const int j = j0 + sub, t = a.L - (W - 1) + j;
-                float s[8];
-                if (j < W - 1) sc_row<FX, SMALL>(a, xb, b, t, pl.at, s);
-                __syncthreads();
-                if (j < W - 1 && pl.own)
-                    oct_store<SMALL>((char*)a.state_out + ((size_t)b * (W - 1) + j) * a.C * xs, a.x_f32, pl, s);
-            }
+        if (b < (unsigned)a.B && t0 == 0 && a.state_out) {
+            // the last W - 1 rows; the only thread that reads the state writes it, so that
+            // both may be one tensor
+            float s[W - 1][8];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) sc_row<FX, SMALL>(a, xb, b, a.L - (W - 1) + j, pl.at, s[j]);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                if (pl.own)
+                    oct_store<SMALL>((char*)a.state_out + ((size_t)b * (W - 1) + j) * a.C * xs, a.x_f32, pl, s[j]);
         }
     }
 }
@@ -171,13 +172,16 @@ __global__ __launch_bounds__(kScThreads) void sc_step_kernel(ScArgs a) {
 // dz of the run's tokens and of the W - 1 behind it (made again by the next run);
 // dx_t = sum_j w_j dz_{t+W-1-j} is whole once dz_{t+W-1} is in.  Rows behind the last
 // token have no gradient: their dy counts as 0.
+//
+// Two waves per SIMD (256 registers) where a few spilled registers buy them: bf16 up to
+// W = 4 (95 us, one wave 118); fp32, which would spill more, does not gain (109, 105).
 template <bool FX, bool FD, int W, bool SMALL>
-__global__ __launch_bounds__(kScThreads) void sc_bwd_kernel(ScArgs a) {
+__global__ __launch_bounds__(kScThreads, W <= 4 && !FX ? 2 : 1) void sc_bwd_kernel(ScArgs a) {
     constexpr int U = sc_ahead(W);
     __shared__ float red[16][kScTile];
     const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
     const unsigned nct = ((unsigned)a.C + kScTile - 1) / kScTile;
-    const unsigned per = (unsigned)(((int64_t)a.L + 16 * a.run - 1) / (16 * a.run));
+    const unsigned per = ((unsigned)a.L + a.run - 1) / a.run;
     const unsigned ct = blockIdx.x % nct, blk = blockIdx.x / nct;
     const int xs = a.x_f32 ? 4 : 2, ds = a.dy_f32 ? 4 : 2, ys = a.y_f32 ? 4 : 2;
     const OctPlace pl = oct_place(ct * 16 + lane, a.C);
@@ -194,11 +198,10 @@ __global__ __launch_bounds__(kScThreads) void sc_bwd_kernel(ScArgs a) {
         db[e] = 0.f;
     }
     for (unsigned tile = blk; tile < a.tiles; tile += a.blocks) {
-        const unsigned b = tile / per, k = tile - b * per;
-        const int64_t from = ((int64_t)k * 16 + sub) * a.run;
-        if (from >= a.L) continue;
+        const unsigned run = tile * 16 + sub, b = run / per;
+        if (b >= (unsigned)a.B) continue;
         const char* xb = (const char*)a.x + b * a.sx.b * xs;
-        const int t0 = (int)from, rest = a.L - t0, n = min(a.run, rest);
+        const int t0 = (int)((run - b * per) * a.run), rest = a.L - t0, n = min(a.run, rest);
         float past[W][8], dz[W][8];   // rows t of x and dz in [(t - t0) % W]
 #pragma unroll
         for (int j = 1; j < W; ++j) sc_row<FX, SMALL>(a, xb, b, t0 - W + j, pl.at, past[j]);

@@ -133,17 +133,19 @@ struct GsLds {
     float* start;            // [waves][64], a wave's own: what it starts with
     float* waves;            // twice [3][waves][64]: the waves' maps, used in turn
     float2* back;            // [waves][64]: maps of earlier tiles
+    int n;                   // waves
 };
-constexpr int kGsRuns = 32, kGsWaves = 4;   // of a full workgroup
-constexpr unsigned kGsLdsBytes = (3 * kGsRuns + kGsWaves + 6 * kGsWaves + 2 * kGsWaves) * kGsTile * 4;
+constexpr int kGsWaves = 4;   // of a full workgroup
+inline unsigned gs_lds_bytes(int runs) { return (3 * runs + 9 * (runs / 8)) * kGsTile * 4; }
 __device__ __forceinline__ GsLds gs_lds(float* p) {
     GsLds l;
+    l.n = blockDim.x >> 6;
     l.one = p;
-    l.part = l.one + kGsRuns * kGsTile;
-    l.b = l.part + kGsRuns * kGsTile;
-    l.start = l.b + kGsRuns * kGsTile;
-    l.waves = l.start + kGsWaves * kGsTile;
-    l.back = reinterpret_cast<float2*>(l.waves + 6 * kGsWaves * kGsTile);
+    l.part = l.one + 8 * l.n * kGsTile;
+    l.b = l.part + 8 * l.n * kGsTile;
+    l.start = l.b + 8 * l.n * kGsTile;
+    l.waves = l.start + l.n * kGsTile;
+    l.back = reinterpret_cast<float2*>(l.waves + 6 * l.n * kGsTile);
     return l;
 }
 
@@ -193,28 +195,27 @@ __device__ __forceinline__ void gs_join(const GsLds& l, int turn, float (&one)[8
         l.b[k] = all.b;
         all = gs_then(all, m);
     }
-    float* w = l.waves + (turn * 3 * kGsWaves + wave) * kGsTile + c;
+    float* w = l.waves + (turn * 3 * l.n + wave) * kGsTile + c;
     w[0] = all.one;
-    w[kGsWaves * kGsTile] = all.part;
-    w[2 * kGsWaves * kGsTile] = all.b;
+    w[l.n * kGsTile] = all.part;
+    w[2 * l.n * kGsTile] = all.b;
 }
 // Behind the barrier: wave `i`'s map, in the order that the state passes them.
 template <bool FWD>
 __device__ __forceinline__ GsMap gs_wave_map(const GsLds& l, int turn, int i, int c) {
-    const int waves = blockDim.x >> 6;
-    const float* w = l.waves + (turn * 3 * kGsWaves + (FWD ? i : waves - 1 - i)) * kGsTile + c;
-    return {w[0], w[kGsWaves * kGsTile], w[2 * kGsWaves * kGsTile]};
+    const float* w = l.waves + (turn * 3 * l.n + (FWD ? i : l.n - 1 - i)) * kGsTile + c;
+    return {w[0], w[l.n * kGsTile], w[2 * l.n * kGsTile]};
 }
 // The states that a thread's run starts with, in s, from what the tile starts with (h, of
 // the lane's channel).  Returns what it ends with.
 template <bool FWD>
 __device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, float (&s)[8]) {
-    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, waves = blockDim.x >> 6;
+    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63;
     float mine = h;
 #pragma unroll
     for (int i = 0; i < kGsWaves; ++i) {
-        if (i >= waves) break;
-        if ((FWD ? i : waves - 1 - i) == wave) mine = h;
+        if (i >= l.n) break;
+        if ((FWD ? i : l.n - 1 - i) == wave) mine = h;
         h = gs_apply(gs_wave_map<FWD>(l, turn, i, c), h);
     }
     l.start[wave * kGsTile + c] = mine;

@@ -15,7 +15,7 @@ int gs_run(bool) { return kRun; }
 template <bool FX, bool FG, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(256, 4) void gs_fwd_kernel(GsArgs a) {
     constexpr int T = kRun;
-    __shared__ __align__(16) float lds[kGsLdsBytes / 4];
+    extern __shared__ __align__(16) float lds[];
     __shared__ unsigned drawn;
     const int tid = threadIdx.x, lane = tid & 7, tg = tid >> 3, span = a.groups * T;
     const GsLds l = gs_lds(lds);
@@ -153,9 +153,11 @@ static hipError_t gs_launch(const GsArgs& a, bool step, int slot, hipStream_t st
     if (a.maps) {
         const hipError_t e = launch_gs_clear(a, slot, st);
         if (e != hipSuccess) return e;
-        return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, true>, dim3(a.padded * a.nseg), dim3(256), 0, st, a);
+        return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, true>, dim3(a.padded * a.nseg), dim3(256),
+                        gs_lds_bytes(32), st, a);
     }
-    return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups), 0, st, a);
+    return launch_k(slot, gs_fwd_kernel<FX, FG, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups),
+                    gs_lds_bytes(a.groups), st, a);
 }
 
 template <int DEC, int INP>

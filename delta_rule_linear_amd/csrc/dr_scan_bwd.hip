@@ -16,7 +16,7 @@ constexpr int kRunBwd = 4;
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
     constexpr int T = kRunBwd;
-    __shared__ __align__(16) float lds[kGsLdsBytes / 4];
+    extern __shared__ __align__(16) float lds[];
     __shared__ unsigned drawn;
     const int tid = threadIdx.x, lane = tid & 7, tg = tid >> 3, span = a.groups * T;
     const GsLds l = gs_lds(lds);
@@ -152,9 +152,11 @@ static hipError_t gs_launch(const GsArgs& a, int slot, hipStream_t st) {
     if (a.maps) {
         const hipError_t e = launch_gs_clear(a, slot, st);
         if (e != hipSuccess) return e;
-        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.padded * a.nseg), dim3(256), 0, st, a);
+        return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, true>, dim3(a.padded * a.nseg), dim3(256),
+                        gs_lds_bytes(32), st, a);
     }
-    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups), 0, st, a);
+    return launch_k(slot, gs_bwd_kernel<FX, FG, FH, FD, DEC, INP, SMALL, false>, dim3(a.columns < 65536 ? a.columns : 65536), dim3(8 * a.groups),
+                    gs_lds_bytes(a.groups), st, a);
 }
 
 template <bool FX, bool FG, int DEC, int INP>

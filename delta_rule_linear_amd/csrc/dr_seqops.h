@@ -61,7 +61,7 @@ struct ScArgs {
     int B, L, C, W;
     int silu;
     int run;              // tokens of a thread
-    unsigned tiles;       // tiles of 16 runs, over all sequences
+    unsigned tiles;       // 16 runs each, over all sequences
     unsigned blocks;      // backward: workgroups that share a channel tile's tiles
     int x_f32, y_f32, dy_f32;
 };

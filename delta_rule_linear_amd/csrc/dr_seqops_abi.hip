@@ -287,14 +287,15 @@ void sc_split(const dr_short_conv_desc& d, dr::ScArgs& a) {
     const int64_t nct = channel_tiles(d.C);
     const int step = dr::sc_run(d.W);
     a.run = 16 * step;
-    auto tiles = [&] { return (int64_t)d.B * (((int64_t)d.L + 16 * a.run - 1) / (16 * a.run)); };
+    auto tiles = [&] { return (d.B * (((int64_t)d.L + a.run - 1) / a.run) + 15) / 16; };
     while (a.run > step && tiles() * nct < 1024) a.run /= 2;
     a.tiles = (unsigned)std::min<int64_t>(tiles(), kMaxSeqRows);
     a.blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.tiles, (1024 + nct - 1) / nct));
 }
 
 dr_status check_sc_tiles(const dr_short_conv_desc& d) {
-    if ((double)d.B * (((double)d.L + 1023) / 1024) > (double)kMaxSeqRows)
+    // runs are counted in 32 bits
+    if ((double)d.B * (((double)d.L + 63) / 64) > (double)kMaxSeqRows)
         return fail(DR_ERR_UNSUPPORTED, "B*L=%.0f too large", (double)d.B * d.L);
     return DR_OK;
 }
