@@ -2,6 +2,14 @@
 //
 // Memory bounds it: x and the gate are read once, and what is made of them stays in
 // registers until the state that a tile starts with is known (dr_scan.h).
+//
+// Measured: 2 x 16384 x 2048 bf16, sigmoid gates, unit inputs, 92 us for 403 MB (4.35
+// TB/s; a large copy reaches 5.2), the vector units busy for 76% of it; 1 x 65536 x 200
+// fp32 68 us for 157 MB, with two rounds of tiles that wait for each other; one token
+// for 256 x 2048 states 4 us.
+//
+// kRun is 4 by count, not by a timing of this form: 8 tokens do not fit the registers of
+// four waves per SIMD, 2 double the joining.
 
 #include "dr_scan.h"
 
