@@ -260,7 +260,7 @@ dr_status check_seq_dims(int B, int L, int C) {
     if (C < 1) return fail(DR_ERR_SHAPE, "C=%d: at least one channel is needed", C);
     if (C > (1 << 23)) return fail(DR_ERR_UNSUPPORTED, "C=%d: at most 2^23 channels are supported", C);
     if (L > 2147483647 - 4096) return fail(DR_ERR_UNSUPPORTED, "L=%d too large", L);
-    if (B * 2 * channel_tiles(C) > kMaxSeqRows)
+    if ((int64_t)B * 2 * channel_tiles(C) > kMaxSeqRows)
         return fail(DR_ERR_UNSUPPORTED, "B*C=%.0f too large", (double)B * C);
     return DR_OK;
 }
