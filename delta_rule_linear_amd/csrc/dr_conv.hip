@@ -11,8 +11,8 @@
 // between two runs, and write once: memory bounds them.
 //
 // Measured: forward of 2 x 16384 x 2048 bf16, W = 4, a slice of wider rows, 62 us for 268
-// MB (4.4 TB/s; a large copy reaches 5.2); its backward 95 us for 403 MB (4.2), with two
-// waves per SIMD (254 registers: taps, their sums, and the rows of x and dz).
+// MB (4.4 TB/s; a large copy reaches 5.2); its backward 93 us for 403 MB (4.3), with two
+// waves per SIMD (243 registers: taps, their sums, and the rows of x and dz).
 
 #include <hip/hip_runtime.h>
 
@@ -170,11 +170,12 @@ __global__ __launch_bounds__(kScThreads) void sc_step_kernel(ScArgs a) {
 }
 
 // dz of the run's tokens and of the W - 1 behind it (made again by the next run);
-// dx_t = sum_j w_j dz_{t+W-1-j} is whole once dz_{t+W-1} is in.  Rows behind the last
-// token have no gradient: their dy counts as 0.
+// dx_t = sum_j w_j dz_{t+W-1-j} is whole once dz_{t+W-1} is in.  Places behind the last
+// token, which stand for its row again, have dz = 0 and are no part of the sums: a product
+// with 0 would make NaN of an infinity that is in their windows.
 //
-// Two waves per SIMD (256 registers) where a few spilled registers buy them: bf16 up to
-// W = 4 (95 us, one wave 118); fp32, which would spill more, does not gain (109, 105).
+// Two waves per SIMD (256 registers) for bf16 up to W = 4 (an earlier form 95 us, with one
+// wave 118; now 93); fp32, which would spill, does not gain (109, 105).
 template <bool FX, bool FD, int W, bool SMALL>
 __global__ __launch_bounds__(kScThreads, W <= 4 && !FX ? 2 : 1) void sc_bwd_kernel(ScArgs a) {
     constexpr int U = sc_ahead(W);
@@ -223,10 +224,7 @@ __global__ __launch_bounds__(kScThreads, W <= 4 && !FX ? 2 : 1) void sc_bwd_kern
         }
         // token t0 + i, at place u of the U
         auto token = [&](int u, int i, bool sums) {
-            if (i >= rest) {
-#pragma unroll
-                for (int q = 0; q < (FD ? 8 : 4); ++q) y[u].w[q] = 0u;
-            }
+            const bool in = i < rest;
             float s[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -238,15 +236,20 @@ __global__ __launch_bounds__(kScThreads, W <= 4 && !FX ? 2 : 1) void sc_bwd_kern
                     for (int j = 0; j < W; ++j) z = __builtin_fmaf(w[j][e], past[(u + 1 + j) % W][e], z);
                     g *= sc_slope(z);
                 }
+                g = in ? g : 0.f;
                 dz[u % W][e] = g;
-                if (sums) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][e] = __builtin_fmaf(g, past[(u + 1 + j) % W][e], dw[j][e]);
-                    db[e] += g;
-                }
                 s[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < W; ++j) s[e] = __builtin_fmaf(w[j][e], dz[(u + W - j) % W][e], s[e]);
+            }
+            if (sums && in) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        dw[j][e] = __builtin_fmaf(dz[u % W][e], past[(u + 1 + j) % W][e], dw[j][e]);
+                    db[e] += dz[u % W][e];
+                }
             }
             const int r = i - (W - 1);   // of the run
             if ((r >= 0 || t0 == 0) && r < n && pl.own) {
