@@ -33,14 +33,26 @@ __device__ __forceinline__ float gs_select(int mask, float x, float y) {
     return __int_as_float((mask & __float_as_int(x)) | (~mask & __float_as_int(y)));
 }
 
+// e^x within 3 + |x| / 20 units of 2^-24 of itself (one of the exponential's last place, one
+// rounding, and ln 2 in 24 bits): the product with log2 e is rounded, which alone would be
+// 64 units at x = 87; what that left out, x - p ln 2, is added (2 x 16384 x 2048 92.4 -> 94.6
+// us, backward 174.0 -> 174.6).  GROWS: x may be positive.
+template <bool GROWS>
+__device__ __forceinline__ float gs_exp(float x) {
+    if (!GROWS) x = __builtin_elementwise_maximum(x, -104.f);   // e^x is 0 there; NaN stays
+    const float p = x * 1.44269504088896340736f, e = __builtin_amdgcn_exp2f(p);
+    const float r = __builtin_fmaf(-p, 0.69314718055994530942f, x);
+    // where e is 0 or infinite it stays
+    return __builtin_fmaf(e, !GROWS || __builtin_fabsf(p) < 128.f ? r : 0.f, e);
+}
+
 template <int DEC>
 __device__ __forceinline__ GsFactor gs_factor(float g) {
-    constexpr float kLog2e = 1.44269504088896340736f;
     GsFactor o;
     if constexpr (DEC == kGsLog) {
         // expm1 by its series for -0.4 < g <= -0 (the next term, g^9 / 9!, is below
         // 2^-28 of g), e^g elsewhere
-        const float e = __builtin_amdgcn_exp2f(g * kLog2e);
+        const float e = gs_exp<true>(g);
         float q = 1.f / 40320.f;
         q = __builtin_fmaf(q, g, 1.f / 5040.f);
         q = __builtin_fmaf(q, g, 1.f / 720.f);
@@ -54,7 +66,7 @@ __device__ __forceinline__ GsFactor gs_factor(float g) {
         o.part = __float_as_int(g) < __float_as_int(-0.4f) ? -__builtin_fabsf(q) : e;
         o.rest = gs_masked(~gs_near(o.part), 1.f) - o.part;
     } else {
-        const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
+        const float e = gs_exp<false>(-__builtin_fabsf(g));
         const float big = __builtin_amdgcn_rcpf(1.f + e), little = e * big;
         o.part = gs_select(0x7fffffff, little, __int_as_float(~__float_as_int(g)));
         o.rest = gs_select(gs_near(o.part), little, big);
