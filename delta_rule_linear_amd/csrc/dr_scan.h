@@ -119,9 +119,19 @@ __device__ __forceinline__ void gs_settle(float& one, float& part) {
     part = strong ? 1.f + part : part;
     one = strong ? 0.f : one;
 }
-// first m, then n
+// first m, then n; settled or, if little follows, not
+__device__ __forceinline__ GsMap gs_pair(const GsMap& m, const GsMap& n) {
+    return {m.one * n.one, __builtin_fmaf(m.part, n.part, __builtin_fmaf(m.one, n.part, m.part * n.one)), gs_apply(n, m.b)};
+}
 __device__ __forceinline__ GsMap gs_then(const GsMap& m, const GsMap& n) {
-    GsMap r{m.one * n.one, __builtin_fmaf(m.part, n.part, __builtin_fmaf(m.one, n.part, m.part * n.one)), gs_apply(n, m.b)};
+    GsMap r = gs_pair(m, n);
+    gs_settle(r.one, r.part);
+    return r;
+}
+// Four, by two.  Of four decays that are near one (over 1/2) 1/16 at least is left, which is
+// early enough for settling.
+__device__ __forceinline__ GsMap gs_four(const GsMap (&m)[4]) {
+    GsMap r = gs_pair(gs_pair(m[0], m[1]), gs_pair(m[2], m[3]));
     gs_settle(r.one, r.part);
     return r;
 }
@@ -131,6 +141,10 @@ __device__ __forceinline__ GsMap gs_then(const GsMap& m, float part, float b) {
     const int near = gs_near(part);
     return {gs_masked(near, m.one), __builtin_fmaf(m.part, part, __builtin_fmaf(m.one, part, gs_masked(near, m.part))),
             gs_step(part, m.b, b)};
+}
+// A map's decay as a token's, in one word.
+__device__ __forceinline__ float gs_word(const GsMap& m) {
+    return __int_as_float(__float_as_int(m.part) | (__float_as_int(m.one) << 2 & (int)0x80000000));   // a bit of 1.0
 }
 
 // ---------------------------------------------------------------- tiles
@@ -144,11 +158,11 @@ struct GsLds {
     float *one, *part, *b;   // [runs][64], a wave's own
     float* start;            // [waves][64], a wave's own: what it starts with
     float* waves;            // twice [3][waves][64]: the waves' maps, used in turn
-    float2* back;            // [waves][64]: maps of earlier tiles
+    float* back;             // [3][waves][64]: maps of earlier tiles
     int n;                   // waves
 };
 constexpr int kGsWaves = 4;   // of a full workgroup
-inline unsigned gs_lds_bytes(int runs) { return (3 * runs + 9 * (runs / 8)) * kGsTile * 4; }
+inline unsigned gs_lds_bytes(int runs) { return (3 * runs + 10 * (runs / 8)) * kGsTile * 4; }
 __device__ __forceinline__ GsLds gs_lds(float* p) {
     GsLds l;
     l.n = blockDim.x >> 6;
@@ -157,7 +171,7 @@ __device__ __forceinline__ GsLds gs_lds(float* p) {
     l.b = l.part + 8 * l.n * kGsTile;
     l.start = l.b + 8 * l.n * kGsTile;
     l.waves = l.start + l.n * kGsTile;
-    l.back = reinterpret_cast<float2*>(l.waves + 6 * l.n * kGsTile);
+    l.back = l.waves + 6 * l.n * kGsTile;
     return l;
 }
 
@@ -189,8 +203,6 @@ __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
 template <bool FWD>
 __device__ __forceinline__ void gs_join(const GsLds& l, int turn, float (&one)[8], float (&part)[8], const float (&b)[8]) {
     const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, at = (tid >> 3) * kGsTile + (tid & 7) * 8;
-    // a run is short enough for this to be late enough: four tokens' decays that are near
-    // one (over 1/2) make 1/16 at least
 #pragma unroll
     for (int e = 0; e < 8; ++e) gs_settle(one[e], part[e]);
     gs_put(l.one + at, one);
@@ -259,10 +271,10 @@ __device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, fl
 // for, once.  (Maps joined over groups of 8 tiles and blocks of 8 groups need fewer
 // words, but three such round trips of 1.5 us and more.)
 //
-// A map is one 64-bit word (A in the low half, B in the high one), a state another,
-// so that a word is whole when it is there at all; until then it is kGsAbsent, which
-// launch_gs_clear writes first.  Between tiles A is rounded to 24 bits, which costs
-// half a rounding of the state per tile.
+// A map is one 64-bit word (A in the low half, held as a token's, B in the high one), a
+// state another, so that a word is whole when it is there at all; until then it is
+// kGsAbsent, which launch_gs_clear writes first.  (A rounded to 24 bits would be off by the
+// same in every tile of an even decay: 7e-5 of the state at a memory of 1e6 tokens.)
 constexpr uint64_t kGsAbsent = ~(uint64_t)0;
 constexpr int kGsBack = 16;
 
@@ -301,16 +313,17 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
     uint64_t* maps = a.maps + (size_t)col * a.nseg * 2 * kGsTile;
     uint64_t* states = maps + (size_t)a.nseg * kGsTile;
     if (wave == 0 && seg + 1 < a.nseg) {
-        GsMap all{1.f, 0.f, 0.f};
+        GsMap w[kGsWaves];
 #pragma unroll
-        for (int i = 0; i < kGsWaves; ++i) all = gs_then(all, gs_wave_map<FWD>(l, 0, i, c));
+        for (int i = 0; i < kGsWaves; ++i) w[i] = gs_wave_map<FWD>(l, 0, i, c);
+        const GsMap all = gs_four(w);
         // what comes in is part of the first tile's map, so that nobody else reads it
-        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? all.one + all.part : 0.f, seg ? all.b : gs_apply(all, first));
+        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? gs_word(all) : 0.f, seg ? all.b : gs_apply(all, first));
     }
     if (seg == 0) return first;
     const int from = seg - kGsBack + wave * N;               // this wave's maps: from .. from + N - 1
     const bool state = wave == 0 && seg > kGsBack;
-    float A = 1.f, B = 0.f;
+    GsMap all{1.f, 0.f, 0.f};
     if (from + N > 0) {
         // one lane looks for the word that comes last, as a rule
         const uint64_t* at = maps + (int64_t)from * kGsTile;
@@ -318,31 +331,32 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
             while (gs_peek(at + (N - 1) * kGsTile) == kGsAbsent) __builtin_amdgcn_s_sleep(2);
         uint64_t m[N], h = 0;
         for (;;) {
-            bool all = true;
+            bool there = true;
 #pragma unroll
             for (int i = 0; i < N; ++i) m[i] = gs_peek(at + (from + i < 0 ? N - 1 : i) * kGsTile + c);
             if (state) h = gs_peek(states + (size_t)(seg - kGsBack) * kGsTile + c);
 #pragma unroll
-            for (int i = 0; i < N; ++i) all = all && m[i] != kGsAbsent;
-            if (all && h != kGsAbsent) break;
+            for (int i = 0; i < N; ++i) there = there && m[i] != kGsAbsent;
+            if (there && h != kGsAbsent) break;
             __builtin_amdgcn_s_sleep(2);
         }
-        if (wave == 0) B = gs_low(h);   // the first of all starts with 0: its map holds what came in
+        GsMap t[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (from + i < 0) continue;
-            A *= gs_low(m[i]);
-            B = __builtin_fmaf(gs_low(m[i]), B, gs_high(m[i]));
-        }
+        for (int i = 0; i < N; ++i) t[i] = from + i < 0 ? all : gs_token(gs_low(m[i]), gs_high(m[i]));
+        all = gs_four(t);
+        // the first of all starts with 0: its map holds what came in
+        if (wave == 0) all.b = gs_apply(all, gs_low(h));
     }
-    if (wave == 0) A = 0.f;
-    l.back[wave * kGsTile + c] = make_float2(A, B);
+    float* back = l.back + wave * kGsTile + c;
+    back[0] = all.b;
+    back[kGsWaves * kGsTile] = all.one;
+    back[2 * kGsWaves * kGsTile] = all.part;
     __syncthreads();
-    float s = 0.f;
+    float s = l.back[c];   // the first wave's, which begins with the state
 #pragma unroll
-    for (int i = 0; i < kGsWaves; ++i) {
-        const float2 m = l.back[i * kGsTile + c];
-        s = __builtin_fmaf(m.x, s, m.y);
+    for (int i = 1; i < kGsWaves; ++i) {
+        const float* m = l.back + i * kGsTile + c;
+        s = gs_apply({m[kGsWaves * kGsTile], m[2 * kGsWaves * kGsTile], m[0]}, s);
     }
     if (wave == 0 && seg + kGsBack < a.nseg) gs_publish(states + (size_t)seg * kGsTile + c, s, 0.f);
     return s;

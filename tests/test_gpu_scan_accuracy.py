@@ -75,3 +75,30 @@ def test_strong_decays_over_tokens():
     assert torch.equal(last[0], h[0, 3])
     back = drl.dr_gated_scan_bwd(x, g, one, h, x, one, decay="log")
     assert (units(back["dh0"][0], d(g)[0].sum(0).exp()) <= 5.2 * 4).all()
+
+
+@pytest.mark.parametrize("gate,B,L,C", [(-1e-6, 1, 2 ** 20, 8), (-1.3e-7, 1, 2 ** 20, 72), (-1e-6, 3, 2 ** 20 - 77, 5),
+                                        (-2.0 ** -14, 1, 200000, 8)])
+@pytest.mark.parametrize("inputs", ["plain", "blend"])
+def test_memories_of_very_many_tokens(gate, B, L, C, inputs):
+    """The same decay and input for 2^20 tokens, 8192 tiles: a decay rounded to 24 bits anywhere on
+    the way would be the same error in every tile, a part in 14000 of the state at -1e-6.  The state itself is
+    rounded a few times in each tile, at random, and forgets 8192 tiles over 1e6 tokens: about the root of 3 x 8192 of
+    2^-24, below 1e-5."""
+    import delta_rule_linear_amd as drl
+    announce("memories of very many tokens", gate, B, L, C, inputs)
+    g, x = torch.full((B, L, C), gate, device="cuda"), torch.ones((B, L, C), device="cuda")
+    m = dict(decay="log", inputs=inputs)
+    h, last = drl.dr_gated_scan_fwd(x, g, None, **m)
+    rest = -torch.expm1(g[0, 0, 0].double().cpu())
+    t = torch.tensor([L, L // 2, L // 3, 4097, 128, 1], dtype=torch.float64)
+    geometric = -torch.expm1(t * g[0, 0, 0].double().cpu()) / rest    # the sum of a^k over t tokens
+    want = geometric * (1 if inputs == "plain" else rest)
+    for k, w in zip(t.long().tolist(), want):
+        assert float((d(h[:, k - 1]) / w - 1).abs().max()) <= 1e-5, k
+    assert torch.equal(last, h[:, -1])
+    # the gradient runs through the same maps, backwards
+    one = torch.ones_like(h)
+    back = drl.dr_gated_scan_bwd(x, g, None, h, one, decay="log")
+    for k, w in zip(t.long().tolist(), geometric):
+        assert float((d(back["dx"][:, L - k]) / w - 1).abs().max()) <= 1e-5, k
