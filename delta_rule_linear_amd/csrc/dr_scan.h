@@ -7,6 +7,13 @@
 // (-expm1(g), sigmoid(-g)): a rounded to 24 bits would be off by 2^-25, and a memory
 // of 1 / (1 - a) tokens multiplies that.  Elsewhere a itself is used, so that strong
 // decays are exact relative to themselves.
+//
+// An infinite h stays infinite under every decay, of 0 too: what a tile does to it must not
+// depend on how its tokens' decays multiply.  The forms above make NaN of it (infinity
+// minus infinity, or 0 times it), and NaN stays.  So the forward looks at what comes out, in
+// the places where few values show it, and where that is odd goes through it once more in
+// forms that take any h (`all` in their names).  The backward does not: its gradients are
+// infinite or NaN from there on (looking cost it up to a tenth of its time).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -105,12 +112,33 @@ __device__ __forceinline__ float gs_step(float part, float h, float b) {
     return gs_masked(gs_near(part), h) + __builtin_fmaf(part, h, b);
 }
 
+// What a step makes of any h; s is what gs_step makes of it.
+__device__ __forceinline__ float gs_stay_infinite(float part, float h, float b, float s) {
+    return __builtin_isinf(h) ? h + __builtin_fmaf(part, 0.f, b) : s;   // NaN of a NaN decay
+}
+
+// The same value, of which the compiler knows nothing: what it made of it elsewhere is made
+// again here instead of kept in registers.
+__device__ __forceinline__ float gs_fresh(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Whether the wave has a value that is infinite or NaN, or from 2^100 on, whose sums with
+// others could be.
+__device__ __forceinline__ bool gs_odd(float x) {
+    return __builtin_expect(__builtin_amdgcn_ballot_w64(!(__builtin_fabsf(x) < 0x1p100f)) != 0, 0);
+}
+
 // The map of several tokens, h -> (one + part) h + b, one again 0 or 1.
 struct GsMap {
     float one, part, b;
 };
 __device__ __forceinline__ float gs_apply(const GsMap& m, float h) {
     return __builtin_fmaf(m.one, h, __builtin_fmaf(m.part, h, m.b));
+}
+__device__ __forceinline__ float gs_apply_all(const GsMap& m, float h) {
+    return gs_stay_infinite(m.part, h, m.b, gs_apply(m, h));
 }
 // A decay that has become strong over several tokens is held as it is, so that it is
 // exact relative to itself (1 + part is exact from -1 to -1/2).
@@ -127,6 +155,11 @@ __device__ __forceinline__ GsMap gs_then(const GsMap& m, const GsMap& n) {
     GsMap r = gs_pair(m, n);
     gs_settle(r.one, r.part);
     return r;
+}
+__device__ __forceinline__ float gs_four_all(const GsMap (&m)[4], float h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h = gs_apply_all(m[i], h);
+    return h;
 }
 // Four, by two.  Of four decays that are near one (over 1/2) 1/16 at least is left, which is
 // early enough for settling.
@@ -181,9 +214,8 @@ __device__ __forceinline__ void gs_wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ void gs_put(float* to, const float (&x)[8]) {
-    reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void gs_put4(float* to, float x, float y, float z, float w) {
+    *reinterpret_cast<float4*>(to) = make_float4(x, y, z, w);
 }
 __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
     const float4 a = reinterpret_cast<const float4*>(from)[0], b = reinterpret_cast<const float4*>(from)[1];
@@ -197,17 +229,28 @@ __device__ __forceinline__ void gs_get(const float* from, float (&x)[8]) {
     x[7] = b.w;
 }
 
+// A thread's runs, put where its wave joins them.
+__device__ __forceinline__ int gs_own() { return (threadIdx.x >> 3) * kGsTile + (threadIdx.x & 7) * 8; }
+__device__ __forceinline__ void gs_put_runs(const GsLds& l, GsMap (&run)[8]) {
+    // a run is short enough for this to be late enough: four tokens' decays that are near
+    // one (over 1/2) make 1/16 at least
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gs_settle(run[e].one, run[e].part);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+        gs_put4(l.one + gs_own() + e, run[e].one, run[e + 1].one, run[e + 2].one, run[e + 3].one);
+        gs_put4(l.part + gs_own() + e, run[e].part, run[e + 1].part, run[e + 2].part, run[e + 3].part);
+        gs_put4(l.b + gs_own() + e, run[e].b, run[e + 1].b, run[e + 2].b, run[e + 3].b);
+    }
+}
+
 // A wave's runs joined, channel `c` = the lane: each run's map becomes that of the runs
 // before it in the wave, and the wave's map goes to the others.  FWD: runs, and waves,
-// from the first to the last.
-template <bool FWD>
-__device__ __forceinline__ void gs_join(const GsLds& l, int turn, float (&one)[8], float (&part)[8], const float (&b)[8]) {
-    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63, at = (tid >> 3) * kGsTile + (tid & 7) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) gs_settle(one[e], part[e]);
-    gs_put(l.one + at, one);
-    gs_put(l.part + at, part);
-    gs_put(l.b + at, b);
+// from the first to the last.  Returns whether the wave's map is odd: then some of them are
+// not as they should be, and the runs, with any b, are joined once more by ALL.
+template <bool FWD, bool ALL = false>
+__device__ __forceinline__ bool gs_join(const GsLds& l, int turn) {
+    const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63;
     gs_wave_fence();
     GsMap all{1.f, 0.f, 0.f};
 #pragma unroll
@@ -217,12 +260,15 @@ __device__ __forceinline__ void gs_join(const GsLds& l, int turn, float (&one)[8
         l.one[k] = all.one;
         l.part[k] = all.part;
         l.b[k] = all.b;
+        const float before = all.b;
         all = gs_then(all, m);
+        if (ALL) all.b = gs_apply_all(m, before);
     }
     float* w = l.waves + (turn * 3 * l.n + wave) * kGsTile + c;
     w[0] = all.one;
     w[l.n * kGsTile] = all.part;
     w[2 * l.n * kGsTile] = all.b;
+    return gs_odd(all.b);
 }
 // Behind the barrier: wave `i`'s map, in the order that the state passes them.
 template <bool FWD>
@@ -231,10 +277,11 @@ __device__ __forceinline__ GsMap gs_wave_map(const GsLds& l, int turn, int i, in
     return {w[0], w[l.n * kGsTile], w[2 * l.n * kGsTile]};
 }
 // The states that a thread's run starts with, in s, from what the tile starts with (h, of
-// the lane's channel).  Returns what it ends with.
+// the lane's channel).  Returns what it ends with; odd is set if the wave has odd states.
 template <bool FWD>
-__device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, float (&s)[8]) {
+__device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, float (&s)[8], bool* odd = nullptr) {
     const int tid = threadIdx.x, wave = tid >> 6, c = tid & 63;
+    const float start = h;
     float mine = h;
 #pragma unroll
     for (int i = 0; i < kGsWaves; ++i) {
@@ -242,16 +289,28 @@ __device__ __forceinline__ float gs_starts(const GsLds& l, int turn, float h, fl
         if ((FWD ? i : l.n - 1 - i) == wave) mine = h;
         h = gs_apply(gs_wave_map<FWD>(l, turn, i, c), h);
     }
+    const bool all = FWD && gs_odd(h);
+    if (all) {
+        *odd = true;
+        h = start;
+        for (int i = 0; i < l.n; ++i) {
+            if ((FWD ? i : l.n - 1 - i) == wave) mine = h;
+            h = gs_apply_all(gs_wave_map<FWD>(l, turn, i, c), h);
+        }
+    }
     l.start[wave * kGsTile + c] = mine;
     gs_wave_fence();
     float one[8], part[8], b[8];
-    const int at = (tid >> 3) * kGsTile + (tid & 7) * 8;
+    const int at = gs_own();
     gs_get(l.one + at, one);
     gs_get(l.part + at, part);
     gs_get(l.b + at, b);
     gs_get(l.start + wave * kGsTile + (tid & 7) * 8, s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = gs_apply({one[e], part[e], b[e]}, s[e]);
+    for (int e = 0; e < 8; ++e) {
+        const GsMap m{one[e], part[e], b[e]};
+        s[e] = all ? gs_apply_all(m, s[e]) : gs_apply(m, s[e]);
+    }
     return h;
 }
 
@@ -318,7 +377,8 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
         for (int i = 0; i < kGsWaves; ++i) w[i] = gs_wave_map<FWD>(l, 0, i, c);
         const GsMap all = gs_four(w);
         // what comes in is part of the first tile's map, so that nobody else reads it
-        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? gs_word(all) : 0.f, seg ? all.b : gs_apply(all, first));
+        const bool whole = seg == 0 || (FWD && gs_odd(all.b));
+        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? gs_word(all) : 0.f, whole ? gs_four_all(w, seg ? 0.f : first) : all.b);
     }
     if (seg == 0) return first;
     const int from = seg - kGsBack + wave * N;               // this wave's maps: from .. from + N - 1
@@ -357,6 +417,14 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
     for (int i = 1; i < kGsWaves; ++i) {
         const float* m = l.back + i * kGsTile + c;
         s = gs_apply({m[kGsWaves * kGsTile], m[2 * kGsWaves * kGsTile], m[0]}, s);
+    }
+    if (FWD && gs_odd(s)) {
+        // the words are all there
+        s = seg > kGsBack ? gs_low(gs_peek(states + (size_t)(seg - kGsBack) * kGsTile + c)) : 0.f;
+        for (int i = max(0, seg - kGsBack); i < seg; ++i) {
+            const uint64_t m = gs_peek(maps + (size_t)i * kGsTile + c);
+            s = gs_apply_all(gs_token(gs_low(m), gs_high(m)), s);
+        }
     }
     if (wave == 0 && seg + kGsBack < a.nseg) gs_publish(states + (size_t)seg * kGsTile + c, s, 0.f);
     return s;

@@ -3,10 +3,11 @@
 // Memory bounds it: x and the gate are read once, and what is made of them stays in
 // registers until the state that a tile starts with is known (dr_scan.h).
 //
-// Measured: 2 x 16384 x 2048 bf16, sigmoid gates, unit inputs, 92 us for 403 MB (4.35
-// TB/s; a large copy reaches 5.2), the vector units busy for 76% of it; 1 x 65536 x 200
-// fp32 68 us for 157 MB, with two rounds of tiles that wait for each other; one token
-// for 256 x 2048 states 4 us.
+// Measured: 2 x 16384 x 2048 bf16, sigmoid gates, unit inputs, 95 us for 403 MB (4.25
+// TB/s; a large copy reaches 5.2), the vector units busy for most of it; 1 x 65536 x 200
+// fp32 69.5 us for 157 MB, with two rounds of tiles that wait for each other; 33 x 992 x
+// 2048, where a workgroup walks each column, 116 us for 402 MB; one token for 256 x 2048
+// states 4 us.
 //
 // kRun is 4 by count, not by a timing of this form: 8 tokens do not fit the registers of
 // four waves per SIMD, 2 double the joining.
@@ -19,9 +20,11 @@ constexpr int kRun = 4;
 
 int gs_run(bool) { return kRun; }
 
-// FAR: one tile of a long sequence, drawn; else whole sequences, tile by tile.
+// FAR: one tile of a long sequence, drawn; else whole sequences, tile by tile.  The latter
+// does not fit the 128 registers of four waves per SIMD: 33 x 992 x 2048 took 147 to 180 us
+// with some of them spilled, at three waves 116.
 template <bool FX, bool FG, int DEC, int INP, bool SMALL, bool FAR>
-__global__ __launch_bounds__(256, 4) void gs_fwd_kernel(GsArgs a) {
+__global__ __launch_bounds__(256, FAR ? 4 : 3) void gs_fwd_kernel(GsArgs a) {
     constexpr int T = kRun;
     extern __shared__ __align__(16) float lds[];
     __shared__ unsigned drawn;
@@ -31,19 +34,20 @@ __global__ __launch_bounds__(256, 4) void gs_fwd_kernel(GsArgs a) {
     const unsigned xt = (unsigned)a.sx.t * xs, gt = (unsigned)a.sg.t * gs, ot = (unsigned)a.so.t * os;
     Oct<FX> x[T];
     Oct<FG> g[T];
-    auto load = [&](unsigned col, int seg) {
+    auto load_row = [&](unsigned col, int seg, int i, Oct<FX>& x, Oct<FG>& g) {
         const unsigned b = gs_divide(col, a.by_tiles), ct = col - b * a.tiles;
         const OctPlace pl = oct_place(ct * 8 + lane, a.C);
         const int t0 = seg * span, last = a.L - 1 - t0;
         // rows of the tile by 32-bit offsets from its first
         const char* xb = (const char*)a.x + (b * a.sx.b + t0 * a.sx.t) * xs;
         const char* gb = (const char*)a.g + (b * a.sg.b + t0 * a.sg.t) * gs;
+        const unsigned r = min(tg * T + i, last);
+        oct_load<FX, SMALL>(xb + r * xt, a.x_f32, pl.at, a.C, x);
+        oct_load<FG, SMALL>(gb + r * gt, a.g_f32, pl.at, a.C, g);
+    };
+    auto load = [&](unsigned col, int seg) {
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            const unsigned r = min(tg * T + i, last);
-            oct_load<FX, SMALL>(xb + r * xt, a.x_f32, pl.at, a.C, x[i]);
-            oct_load<FG, SMALL>(gb + r * gt, a.g_f32, pl.at, a.C, g[i]);
-        }
+        for (int i = 0; i < T; ++i) load_row(col, seg, i, x[i], g[i]);
     };
     unsigned first = blockIdx.x, seg0 = 0;
     if constexpr (FAR) {
@@ -78,32 +82,70 @@ __global__ __launch_bounds__(256, 4) void gs_fwd_kernel(GsArgs a) {
                         gs_zero(x[i]);
                     }
             }
-            float part[T][8], in[T][8], one[8], all[8], B[8];
+            float part[T][8], in[T][8];
+            GsMap run[8];
 #pragma unroll
             for (int i = 0; i < T; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
                     part[i][e] = f.part;
-                    in[i][e] = gs_input<INP>(f) * oct_value(x[i], e);
-                    const GsMap run = i == 0 ? gs_token(f.part, in[i][e]) : gs_then({one[e], all[e], B[e]}, f.part, in[i][e]);
-                    one[e] = run.one;
-                    all[e] = run.part;
-                    B[e] = run.b;
+                    in[i][e] = gs_fresh(gs_input<INP>(f) * oct_value(x[i], e));
+                    run[e] = i == 0 ? gs_token(f.part, in[i][e]) : gs_then(run[e], f.part, in[i][e]);
                 }
-            gs_join<true>(l, turn, one, all, B);
+            gs_put_runs(l, run);
+            bool odd = gs_join<true>(l, turn);
+            if (odd) {
+                // b is infinite as the sum of the inputs is, under any decay but NaN
+                GsMap again[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < T; ++i) {
+                        const float p = gs_fresh(part[i][e]);
+                        again[e] = i == 0 ? gs_token(p, in[i][e]) : gs_then(again[e], p, in[i][e]);
+                        sum += in[i][e];
+                    }
+                    again[e].b = __builtin_isfinite(again[e].b) ? again[e].b : __builtin_fmaf(again[e].part, 0.f, sum);
+                }
+                gs_put_runs(l, again);
+                gs_join<true, true>(l, turn);
+            }
             asm volatile("" : "+v"(h));   // what comes in is read before anything goes out: both may be one tensor
             __syncthreads();
             if constexpr (FAR) h = gs_far<true>(a, l, col, seg, h);
             float s[8];
-            h = gs_starts<true>(l, turn, h, s);
+            h = gs_starts<true>(l, turn, h, s, &odd);
             char* ob = (char*)a.out + (b * a.so.b + t0 * a.so.t) * os;
-#pragma unroll
-            for (int i = 0; i < T; ++i) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = gs_step(part[i][e], s[e], in[i][e]);
+            auto store = [&](int i) {
                 if (tg * T + i <= last && pl.own) oct_store<SMALL>(ob + (tg * T + i) * ot, a.out_f32, pl, s);
                 if (tg * T + i == last && pl.own && a.last) oct_store<SMALL>(a.last + (size_t)b * a.C, true, pl, s);
+            };
+            if (!odd) {
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = gs_step(gs_fresh(part[i][e]), s[e], in[i][e]);
+                    store(i);
+                }
+            } else {
+                // token by token from their rows again: few instructions, and no registers, for
+                // what hardly ever runs
+                Oct<FX> xi;
+                Oct<FG> gi;
+#pragma unroll 1
+                for (int i = 0; i < T; ++i) {
+                    if (tg * T + i > last) break;
+                    load_row(col, seg, i, xi, gi);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const GsFactor f = gs_factor<DEC>(oct_value(gi, e));
+                        const float before = s[e], bi = gs_input<INP>(f) * oct_value(xi, e);
+                        s[e] = gs_stay_infinite(f.part, before, bi, gs_step(f.part, before, bi));
+                    }
+                    store(i);
+                }
             }
             if constexpr (FAR) break;
         }
@@ -144,7 +186,8 @@ __global__ __launch_bounds__(256) void gs_step_kernel(GsArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const GsFactor f = gs_factor<DEC>(oct_value(g, e));
-            h[e] = gs_step(f.part, oct_value(s, e), gs_input<INP>(f) * oct_value(x, e));
+            const float before = oct_value(s, e), in = gs_input<INP>(f) * oct_value(x, e);
+            h[e] = gs_stay_infinite(f.part, before, in, gs_step(f.part, before, in));
         }
         oct_store<SMALL>(a.last + row, true, pl, h);
         oct_store<SMALL>((char*)a.out + row * os, a.out_f32, pl, h);

@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
                         gs_zero(d[i]);
                     }
             }
-            float one[8], all[8], B[8];
+            GsMap run[8];
 #pragma unroll
             for (int i = T - 1; i >= 0; --i)
 #pragma unroll
@@ -95,12 +95,10 @@ __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
                     // e -> a (e + dh)
                     const GsFactor f = gs_factor<DEC>(oct_value(g[i], e));
                     const float in = gs_step(f.part, oct_value(d[i], e), 0.f);
-                    const GsMap run = i == T - 1 ? gs_token(f.part, in) : gs_then({one[e], all[e], B[e]}, f.part, in);
-                    one[e] = run.one;
-                    all[e] = run.part;
-                    B[e] = run.b;
+                    run[e] = i == T - 1 ? gs_token(f.part, in) : gs_then(run[e], f.part, in);
                 }
-            gs_join<false>(l, turn, one, all, B);
+            gs_put_runs(l, run);
+            gs_join<false>(l, turn);
             asm volatile("" : "+v"(h));   // what comes in is read before anything goes out: both may be one tensor
             __syncthreads();
             if constexpr (FAR) h = gs_far<false>(a, l, col, seg, h);

@@ -801,9 +801,12 @@ dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const f
  * of the state, from its own roundings); strong decays, also over many tokens, are
  * exact relative to themselves: e^gate below 2/3 is within 3 + |gate| / 20 units of
  * 2^-24 of itself, the sigmoid and its 1 - a within one and a half times that and 4
- * (below 2^-126 they are 0).  A NaN or Inf reaches the later tokens of its channel, also through a
- * zero decay, and no other channel.  Gradients, from the forward's h as it was
- * written (rounded where that is bf16):
+ * (below 2^-126 they are 0).  An infinite h stays infinite under every decay, of 0 too
+ * (an infinite input of the other sign, or a NaN, makes it NaN), and a NaN stays; neither
+ * reaches another channel.  (Inputs from 2^127 on may make the sums of several tokens
+ * infinite where h is not.)  In the gradients an infinity or NaN reaches the tokens before
+ * as one of the two.  Gradients, from the forward's h as it was written (rounded where
+ * that is bf16):
  *
  *   d_t = dh_t + a_{t+1} d_{t+1} (the last: dh_L + dh_final),   dx = c d,   dh0 = a_1 d_1
  *   dgate = d (h_{t-1} + c'(a) x) da/dgate,   c' = 0, -1 or -a / c

@@ -1,5 +1,6 @@
-"""Infinities and NaN in the short convolution's backward on the GPU: they reach the
-gradients that they are a part of, and no others."""
+"""Infinities and NaN on the GPU.  In the short convolution's backward they reach the
+gradients that they are a part of, and no others.  In the gated recurrence an infinite state
+stays infinite under every decay, wherever the sequence is cut into tiles."""
 import pytest
 
 from gpu_common import announce
@@ -74,3 +75,134 @@ def test_convolution_backward(W, L, act, dtype, C):
     agree(g["dstate"], dx[:, :W - 1], mag[:, :W - 1], "dstate")
     agree(g["dweight"], dw, bw, "dweight")
     agree(g["dbias"], dz.sum((0, 1)), (dz_err + n * U * dz.abs()).sum((0, 1)), "dbias")
+
+
+def decays(a, h):
+    """a h, an infinite h kept under a decay of 0 as well; a NaN decay makes NaN of all."""
+    return torch.where(torch.isinf(h) & ~torch.isnan(a), h, a * h)
+
+
+def scan_forward(x, g, h0, decay, inputs):
+    a, _, c = ref.scan_factors(g, decay, inputs)
+    h, out = h0, []
+    for t in range(x.shape[1]):
+        h = decays(a[:, t], h) + c[:, t] * x[:, t]
+        out.append(h)
+    return torch.stack(out, 1), h
+
+
+def finite(*ts):
+    return [torch.nan_to_num(t, nan=0.0, posinf=0.0, neginf=0.0) for t in ts]
+
+
+def scan_case(B, L, C, decay, dtype, seed):
+    """Gates of every strength, from none to resets, a memory of its own for each channel."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    x, dh = r(B, L, C).to(dtype), r(B, L, C).to(dtype)
+    strength = torch.exp(torch.empty((B, 1, C)).uniform_(-9.0, 4.0, generator=gen))
+    if decay == "log":
+        g = -strength * torch.rand((B, L, C), generator=gen)
+    else:
+        g = -strength.log() + r(B, L, C)
+    return x, g.to(dtype), r(B, C), dh, r(B, C), gen
+
+
+def spoil(t, tokens, gen, values=(INF, -INF, NAN)):
+    """Infinities and NaN at random places of a third of the channels, some channels with several."""
+    B, L, C = t.shape
+    for b in range(B):
+        for c in range(0, C, 3):
+            for _ in range(int(torch.randint(1, 4, (1,), generator=gen))):
+                k = int(torch.randint(len(tokens), (1,), generator=gen))
+                v = values[int(torch.randint(len(values), (1,), generator=gen))]
+                t[b, min(tokens[k], L - 1), c] = v
+
+
+# one token, runs of four, waves of 32, tiles of 128; many columns, which a workgroup walks, and few
+SHAPES = [(1, 1, 9), (3, 3, 5), (2, 5, 64), (1, 33, 20), (2, 127, 16), (1, 130, 70), (2, 700, 33), (1, 3000, 65), (1100, 140, 7),
+          (40, 300, 1700)]
+TOKENS = [0, 1, 2, 3, 4, 5, 7, 8, 30, 31, 32, 33, 63, 95, 126, 127, 128, 129, 255, 256, 257, 500, 699, 1500, 2047, 2048, 2999]
+
+
+@pytest.mark.parametrize("decay,inputs", [("log", "plain"), ("log", "blend"), ("logit", "unit"), ("logit", "plain")])
+@pytest.mark.parametrize("B,L,C", SHAPES)
+def test_recurrence(B, L, C, decay, inputs):
+    import delta_rule_linear_amd as drl
+    announce("recurrence, infinities", B, L, C, decay, inputs)
+    x, g, h0, dh, dlast, gen = scan_case(B, L, C, decay, torch.float32, L + C)
+    at = [t for t in TOKENS if t < L]
+    some = slice(0, min(B, 2))   # what the reference sees of a batch: its first two sequences
+    xs, h0s = x[some], h0[some]
+    spoil(xs, at, gen)
+    if C > 4:
+        h0s[0, 1], h0s[0, 4] = INF, -INF
+    if L > 2 and decay == "log":
+        g[0, L // 2:, min(4, C - 1)] = -INF            # resets, and a long time of them
+        g[0, L // 3, 0] = NAN
+    m = dict(decay=decay, inputs=inputs)
+    h, last = drl.dr_gated_scan_fwd(x.cuda(), g.cuda(), h0.cuda(), **m)
+    args = d(xs), d(g[some]), d(h0s)
+    want, wlast = scan_forward(*args, decay, inputs)
+    e, elast = ref.scan_errors(*finite(args[0]), torch.nan_to_num(args[1], nan=0.0, neginf=-INF), *finite(args[2]), decay, inputs)
+    agree(h[some], want, e, "h")
+    agree(last[some], wlast, elast, "h_final")
+    # the same token by token
+    state = h0s.cuda()
+    for t in range(min(L, 40)):
+        y = drl.dr_gated_scan_step(state, xs[:, t].cuda().contiguous(), g[some][:, t].cuda().contiguous(), **m)
+        agree(y, want[:, t], e[:, t], "h of a step")
+
+
+@pytest.mark.parametrize("decay,inputs", [("log", "plain"), ("log", "blend"), ("logit", "unit"), ("logit", "plain")])
+@pytest.mark.parametrize("B,L,C", SHAPES)
+def test_recurrence_backward(B, L, C, decay, inputs):
+    """Infinite and NaN gradients of h and of the last state: all that they are a part of is
+    infinite or NaN, and the rest is as without them.  (Gates are below the strengths where
+    products would be subnormal.)"""
+    import delta_rule_linear_amd as drl
+    announce("recurrence backward, infinities", B, L, C, decay, inputs)
+    x, g, h0, dh, dlast, gen = scan_case(B, L, C, decay, torch.float32, L + C + 1)
+    g = g.clamp(-30, 8)
+    some = slice(0, min(B, 2))
+    at = [L - 1 - t for t in TOKENS if t < L] + [t for t in TOKENS if t < L]
+    dhs, dls = dh[some], dlast[some]
+    spoil(dhs, at, gen)
+    if C > 4:
+        dls[0, 1], dls[0, 4] = INF, -INF
+    m = dict(decay=decay, inputs=inputs)
+    dev = [t.cuda() for t in (x, g, h0)]
+    h, _ = drl.dr_gated_scan_fwd(*dev, **m)
+    got = drl.dr_gated_scan_bwd(*dev, h, dh.cuda(), dlast.cuda(), **m)
+    args = d(x[some]), d(g[some]), d(h0[some]), d(h[some])
+    a, _, _ = ref.scan_factors(args[1], decay, inputs)
+    e, D = d(dls), torch.empty_like(args[0])
+    for t in range(L - 1, -1, -1):
+        D[:, t] = d(dhs)[:, t] + e
+        e = decays(a[:, t], D[:, t])
+    clean = finite(d(dhs), d(dls))
+    f = ref.scan_backward(*args, *clean, decay, inputs)
+    ex, eg, e0 = ref.scan_back_errors(args[0], args[1], f, *clean, decay, inputs)
+    for n, want, err in (("dx", f["c"] * D, ex), ("dgate", D * f["full"] * f["slope"], eg), ("dh0", e, e0)):
+        v, ok = d(got[n][some]), torch.isfinite(want)
+        assert torch.equal(torch.isfinite(v), ok), n
+        near(got[n][some].cpu()[ok], want[ok], err[ok], n)
+
+
+@pytest.mark.parametrize("L,C", [(200, 8), (5000, 8)])
+def test_states_that_grow_out_of_range(L, C):
+    """Sums that pass 2^128 become infinite and stay it; a forward that is cut in two agrees."""
+    import delta_rule_linear_amd as drl
+    x = torch.full((1, L, C), 2.0 ** 126, device="cuda")
+    g = torch.zeros((1, L, C), device="cuda")
+    g[0, :, 1] = -1.0                                        # stays below 2^127
+    x[0, :, 2] *= -1
+    h, last = drl.dr_gated_scan_fwd(x, g, None, decay="log")
+    want, _ = scan_forward(d(x), d(g), torch.zeros(1, C, dtype=torch.float64), "log", "plain")
+    want = torch.where(want.abs() >= 2.0 ** 128, want.sign() * INF, want)
+    e, _ = ref.scan_errors(d(x), d(g), None, "log", "plain")
+    agree(h, want, e, "h")
+    assert torch.equal(last, h[:, -1])
+    h1, s = drl.dr_gated_scan_fwd(x[:, :L // 3].contiguous(), g[:, :L // 3].contiguous(), None, decay="log")
+    h2, _ = drl.dr_gated_scan_fwd(x[:, L // 3:].contiguous(), g[:, L // 3:].contiguous(), s, decay="log")
+    agree(torch.cat([h1, h2], 1), want, e, "h in two parts")
