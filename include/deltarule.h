@@ -656,8 +656,9 @@ dr_status dr_layernorm_bwd(const dr_layernorm_desc* d, const void* x, const floa
  *
  *   dx = ds + rstd (t - n mean(t n)),  n = s rstd,  t = dy weight,  dweight = sum of dy n
  *
- * dx is the gradient of x and of the residual.  Squares are fp32: rows with values
- * beyond 2^63 have rstd 0.
+ * dx is the gradient of x and of the residual.  Squares and their sum are fp32: a row
+ * whose squares sum to 2^128 or more (16384 values of 2^57, or one of 2^64) has rstd
+ * 0, and y is 0 where s is finite.
  *
  *   B, H, L, D, per_head, eps  as in dr_layernorm_desc; D in [1, 16384]
  *   x_dtype    of x
