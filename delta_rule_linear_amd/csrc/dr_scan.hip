@@ -9,23 +9,19 @@
 // 2048, where a workgroup walks each column, 116 us for 402 MB; one token for 256 x 2048
 // states 4 us.
 //
-// kRun is 4 by count, not by a timing of this form: 8 tokens do not fit the registers of
+// kGsRun is 4 by count, not by a timing of this form: 8 tokens do not fit the registers of
 // four waves per SIMD, 2 double the joining.
 
 #include "dr_scan.h"
 
 namespace dr {
 
-constexpr int kRun = 4;
-
-int gs_run(bool) { return kRun; }
-
 // FAR: one tile of a long sequence, drawn; else whole sequences, tile by tile.  The latter
 // does not fit the 128 registers of four waves per SIMD: 33 x 992 x 2048 took 147 to 180 us
 // with some of them spilled, at three waves 116.
 template <bool FX, bool FG, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(256, FAR ? 4 : 3) void gs_fwd_kernel(GsArgs a) {
-    constexpr int T = kRun;
+    constexpr int T = kGsRun;
     extern __shared__ __align__(16) float lds[];
     __shared__ unsigned drawn;
     const int tid = threadIdx.x, lane = tid & 7, tg = tid >> 3, span = a.groups * T;

@@ -14,11 +14,9 @@
 
 namespace dr {
 
-constexpr int kRunBwd = 4;
-
 template <bool FX, bool FG, bool FH, bool FD, int DEC, int INP, bool SMALL, bool FAR>
 __global__ __launch_bounds__(256) void gs_bwd_kernel(GsArgs a) {
-    constexpr int T = kRunBwd;
+    constexpr int T = kGsRun;
     extern __shared__ __align__(16) float lds[];
     __shared__ unsigned drawn;
     const int tid = threadIdx.x, lane = tid & 7, tg = tid >> 3, span = a.groups * T;

@@ -111,7 +111,7 @@ struct GsArgs {
     int inputs;           // 0 plain, 1 blend, 2 unit
 };
 constexpr int kGsTile = 64;    // channels of a workgroup
-int gs_run(bool bwd);          // tokens of a thread
+constexpr int kGsRun = 4;      // tokens of a thread, forward and backward
 hipError_t launch_gs_fwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_bwd(const GsArgs& a, int slot, hipStream_t st);
 hipError_t launch_gs_clear(const GsArgs& a, int slot, hipStream_t st);

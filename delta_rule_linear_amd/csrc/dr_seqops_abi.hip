@@ -477,9 +477,9 @@ struct GsLayout {
     size_t maps, total;   // bytes; the counters stand first
 };
 
-GsLayout gs_layout(const dr_gated_scan_desc& d, bool bwd) {
+GsLayout gs_layout(const dr_gated_scan_desc& d) {
     GsLayout w{};
-    const int run = dr::gs_run(bwd);
+    constexpr int run = dr::kGsRun;
     w.groups = 8;
     while (w.groups < 32 && (int64_t)w.groups * run < d.L) w.groups *= 2;
     const int64_t columns = d.B * gs_tiles(d.C), span = (int64_t)w.groups * run, tiles = (d.L + span - 1) / span;
@@ -538,13 +538,13 @@ extern "C" {
 
 size_t dr_gated_scan_fwd_workspace_bytes(const dr_gated_scan_desc* d) {
     if (check_gs_desc(d) != DR_OK || d->B == 0 || d->L == 0) return 0;
-    const GsLayout w = gs_layout(*d, false);
+    const GsLayout w = gs_layout(*d);
     return check_gs_tiles(*d, w) == DR_OK ? w.total : 0;
 }
 
 size_t dr_gated_scan_bwd_workspace_bytes(const dr_gated_scan_desc* d) {
     if (check_gs_desc(d) != DR_OK || d->B == 0 || d->L == 0) return 0;
-    const GsLayout w = gs_layout(*d, true);
+    const GsLayout w = gs_layout(*d);
     return check_gs_tiles(*d, w) == DR_OK ? w.total : 0;
 }
 
@@ -561,7 +561,7 @@ dr_status dr_gated_scan_fwd(const dr_gated_scan_desc* d, const void* x, const vo
                rg = seq_tensor("gate", gate, d->B, d->L, d->C, d->gate, d->gate_dtype),
                rh = seq_tensor("h", h, d->B, d->L, d->C, d->h, d->h_dtype);
     if ((s = check_gs_rows({&rx, &rg}, {&rh})) != DR_OK) return s;
-    const GsLayout w = d->L ? gs_layout(*d, false) : GsLayout{};
+    const GsLayout w = d->L ? gs_layout(*d) : GsLayout{};
     if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
     const size_t need = w.total;
     const Span ins[] = {rows_span(rx), rows_span(rg), {h0, state, "h0"}};
@@ -605,7 +605,7 @@ dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const vo
                rdx = seq_tensor("dx", dx, d->B, d->L, d->C, d->dx, d->grad_dtype),
                rdg = seq_tensor("dgate", dgate, d->B, d->L, d->C, d->dgate, d->grad_dtype);
     if ((s = check_gs_rows({&rx, &rg, &rh, &rdh}, {&rdx, &rdg})) != DR_OK) return s;
-    const GsLayout w = d->L ? gs_layout(*d, true) : GsLayout{};
+    const GsLayout w = d->L ? gs_layout(*d) : GsLayout{};
     if ((s = check_gs_tiles(*d, w)) != DR_OK) return s;
     const size_t need = w.total;
     const Span ins[] = {rows_span(rx), rows_span(rg), {h0, state, "h0"}, rows_span(rh), rows_span(rdh),

@@ -735,7 +735,8 @@ dr_status dr_rmsnorm_bwd(const dr_rmsnorm_desc* d, const void* x, const float* w
  * Tokens before the first come from a state of W - 1 rows, oldest first (zeros
  * without one); the final state is the last W - 1 rows, as the next call takes it.
  *
- *   B, L >= 0; C in [1, 2^23] channels; W in [2, 8]
+ *   B, L >= 0; C in [1, 2^23] channels; W in [2, 8]; B ceil(C / 128) below 2^30,
+ *   B ceil(L / 64) below 2^31, L below 2^31 - 4096
  *   x_dtype of x and the state, y_dtype of y or dx, dy_dtype of dy (backward)
  *   x, y, dy strides (y: of y or dx)
  */
@@ -779,7 +780,7 @@ dr_status dr_short_conv_bwd(const dr_short_conv_desc* d, const void* x, const fl
 
 /*
  * dr_short_conv_step -- one token for d->B states, in place: y [B][C] of x [B][C]
- * (dense; L and the strides are ignored), state [B][W-1][C] x_dtype moved on by a row.
+ * (dense; L, if a valid one, and the strides are ignored), state [B][W-1][C] x_dtype moved on by a row.
  * The same as dr_short_conv_fwd with L == 1 and state_out == state.
  */
 dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const float* weight, const float* bias,
@@ -813,7 +814,8 @@ dr_status dr_short_conv_step(const dr_short_conv_desc* d, const void* x, const f
  *   dgate = d (h_{t-1} + c'(a) x) da/dgate,   c' = 0, -1 or -a / c
  * (where c = 0, at a = 1, the unit form's last term is left out).
  *
- *   B, L >= 0; C in [1, 2^23]; tokens at most 2^23 elements apart
+ *   B, L >= 0; C in [1, 2^23]; tokens at most 2^23 elements apart; B ceil(C / 128)
+ *   below 2^30, L below 2^31 - 4096
  *   x_dtype of x; gate_dtype x_dtype or DR_F32; h_dtype of h; dh_dtype of dh;
  *   grad_dtype of dx and dgate (the last two: backward only)
  */
@@ -859,8 +861,8 @@ dr_status dr_gated_scan_bwd(const dr_gated_scan_desc* d, const void* x, const vo
 
 /*
  * dr_gated_scan_step -- one token for d->B states, in place: state [B][C] fp32 is
- * moved on and written to h [B][C] in h_dtype; x and gate [B][C].  Dense; L and the
- * strides are ignored.
+ * moved on and written to h [B][C] in h_dtype; x and gate [B][C].  Dense; L, if a
+ * valid one, and the strides are ignored.
  */
 dr_status dr_gated_scan_step(const dr_gated_scan_desc* d, const void* x, const void* gate, float* state, void* h,
                              void* stream);

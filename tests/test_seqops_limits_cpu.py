@@ -25,3 +25,16 @@ def test_the_largest_batch_is_taken():
     # with many columns a workgroup walks whole sequences: no workspace, and no complaint
     assert drl.dr_gated_scan_fwd_workspace_bytes(gs(B=2 ** 30 - 1, C=8, L=1)) == 0
     assert gf(gs(B=2 ** 30 - 1, C=8, L=1), x=None) == drl.DR_ERR_NULL
+
+
+def test_scan_workspaces_are_needed_and_checked():
+    """Long sequences of few columns need one, forward and backward alike (both cut them into
+    the same tiles)."""
+    need = drl.dr_gated_scan_fwd_workspace_bytes(gs())
+    assert need > 0 and need == drl.dr_gated_scan_bwd_workspace_bytes(gs())
+    for f in (gf, gb):
+        assert f(gs(), wbytes=need - 1) == f(gs(), ws=None) == drl.DR_ERR_WORKSPACE
+    # one tile, or columns enough
+    for kw in (dict(L=128), dict(B=1024, L=129, C=8)):
+        assert drl.dr_gated_scan_fwd_workspace_bytes(gs(**kw)) == drl.dr_gated_scan_bwd_workspace_bytes(gs(**kw)) == 0
+    assert drl.dr_gated_scan_fwd_workspace_bytes(gs(L=129)) > 0
