@@ -206,3 +206,42 @@ def test_states_that_grow_out_of_range(L, C):
     h1, s = drl.dr_gated_scan_fwd(x[:, :L // 3].contiguous(), g[:, :L // 3].contiguous(), None, decay="log")
     h2, _ = drl.dr_gated_scan_fwd(x[:, L // 3:].contiguous(), g[:, L // 3:].contiguous(), s, decay="log")
     agree(torch.cat([h1, h2], 1), want, e, "h in two parts")
+
+
+@pytest.mark.parametrize("decay", ["log", "logit"])
+@pytest.mark.parametrize("C", [6, 8, 200])
+def test_recurrence_of_sixteen_bits_in_place_and_replayed(decay, C):
+    """bf16 rows, NaN and infinite gates, the state carried in place, and a captured call
+    whose inputs change between replays from clean to spoiled and back."""
+    import delta_rule_linear_amd as drl
+    L = 1300
+    x, g, h0, _, _, gen = scan_case(1, L, C, decay, torch.bfloat16, C)
+    clean = x.clone(), g.clone(), h0.clone()
+    spoil(x, TOKENS, gen)
+    g[0, 400, 1], g[0, 900, 2] = NAN, -INF
+    if decay == "logit":
+        g[0, 901:905, 2] = INF                       # a = 1
+        g[0, 30, 4] = NAN
+    h0[0, 5] = -INF
+    m = dict(decay=decay, inputs="plain")
+    dev = [t.cuda() for t in clean]
+    graph = torch.cuda.CUDAGraph()
+    drl.dr_gated_scan_fwd(*dev, **m)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        h, last = drl.dr_gated_scan_fwd(*dev, **m)
+    for case in (clean, (x, g, h0), clean, (x, g, h0)):
+        for t, v in zip(dev, case):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        args = tuple(d(v) for v in case)
+        want, wlast = scan_forward(*args, decay, "plain")
+        e, elast = ref.scan_errors(*finite(args[0]), torch.nan_to_num(args[1], nan=0.0, posinf=200.0, neginf=-INF if decay == "log" else -200.0),
+                                   *finite(args[2]), decay, "plain")
+        agree(h, want, e, "h")
+        agree(last, wlast, elast, "h_final")
+        s = dev[2].clone()
+        h2, got = drl.dr_gated_scan_fwd(dev[0], dev[1], s, h_final=s, **m)
+        assert got is s and torch.equal(torch.nan_to_num(h2, nan=7.0), torch.nan_to_num(h, nan=7.0))
+        assert torch.equal(torch.nan_to_num(s, nan=7.0), torch.nan_to_num(last, nan=7.0))
