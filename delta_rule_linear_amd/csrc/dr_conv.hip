@@ -44,7 +44,7 @@ __device__ __forceinline__ float sc_slope(float z) {
 
 // The rows of a run, one after the other; behind the last one that one again.  They are
 // loaded as read once: the outputs stay in the last-level cache instead, for who comes
-// next (2 x 16384 x 2048 67 -> 60 us, backward 101 -> 93).
+// next (2 x 16384 x 2048 67 -> 62 us, backward 101 -> 95, then 93).
 template <bool F32, bool SMALL>
 struct ScRows {
     const char* p;

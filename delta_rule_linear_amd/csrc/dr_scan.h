@@ -356,7 +356,7 @@ __device__ __forceinline__ unsigned gs_draw(const GsArgs& a, unsigned col) {
 
 // The column of the i-th workgroup of a row of tiles.  Workgroups go to the eight dies in
 // turn; neighbouring columns, whose channels lie side by side in memory, go to the same
-// one where the row is a multiple of eight (2 x 16384 x 2048 103 -> 93 us, backward 193
+// one where the row is a multiple of eight (2 x 16384 x 2048 103 -> 91 us, backward 193
 // -> 171).
 __device__ __forceinline__ unsigned gs_column(const GsArgs& a, unsigned i) {
     return a.padded % 8 ? i : i % 8 * (a.padded / 8) + i / 8;

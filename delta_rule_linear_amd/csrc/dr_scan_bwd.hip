@@ -7,8 +7,10 @@
 // The same walk as the forward's, over the tokens backwards, with e as the state.
 // h is the forward's output as it was kept: nothing is run forwards again.
 //
-// Measured: 2 x 16384 x 2048 bf16, sigmoid gates, blended inputs, 172 us for 805 MB (4.7
-// TB/s), the vector units busy for 59% of it.
+// Measured: 2 x 16384 x 2048 bf16, sigmoid gates, blended inputs, 174 us for 805 MB (4.65
+// TB/s), the vector units busy for 67% of it; 33 x 992 x 2048 bf16, unit inputs, where a
+// workgroup walks each column, 232 us for 802 MB, two waves per SIMD (up to 237
+// registers).
 
 #include "dr_scan.h"
 

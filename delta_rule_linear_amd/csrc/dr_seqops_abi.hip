@@ -469,7 +469,17 @@ int64_t gs_tiles(int C) { return ((int64_t)C + dr::kGsTile - 1) / dr::kGsTile; }
 
 // Runs side by side in a workgroup: 8 (a wave), 16 or 32, the least that cover the
 // tokens.  Sequences of several such tiles whose columns (64 channels of one) are too
-// few to fill the chip have a workgroup for each tile.
+// few to fill the chip have a workgroup for each tile; else a workgroup walks a column.
+// Both, forward and backward in us, bf16, sigmoid gates, unit inputs:
+//              256 tokens                 1024 tokens                4096 tokens
+//   columns    walked        by tile      walked        by tile      walked        by tile
+//     256      14,  21       17,  22       37,  60       31,  52     150, 245       94, 182
+//     768      22,  43       26,  40       74, 158       69, 133     287, 612      270, 486
+//    1024      27,  51       29,  49      100, 202       94, 179     394, 810      354, 646
+//    2048      47, 107       51,  94      186, 388      171, 336
+//    4096      88, 198       90, 175      360, 751      354, 673
+// So walking gains a few percent forward at two tiles, and costs the backward up to a
+// fifth; the border was set before the walked form was timed.
 constexpr int64_t kGsColumns = 1024;
 
 struct GsLayout {
