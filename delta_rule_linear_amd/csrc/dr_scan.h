@@ -126,8 +126,9 @@ __device__ __forceinline__ float gs_fresh(float x) {
 
 // Whether the wave has a value that is infinite or NaN, or from 2^100 on, whose sums with
 // others could be.
+__device__ __forceinline__ bool gs_odd_here(float x) { return !(__builtin_fabsf(x) < 0x1p100f); }
 __device__ __forceinline__ bool gs_odd(float x) {
-    return __builtin_expect(__builtin_amdgcn_ballot_w64(!(__builtin_fabsf(x) < 0x1p100f)) != 0, 0);
+    return __builtin_expect(__builtin_amdgcn_ballot_w64(gs_odd_here(x)) != 0, 0);
 }
 
 // The map of several tokens, h -> (one + part) h + b, one again 0 or 1.
@@ -377,8 +378,13 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
         for (int i = 0; i < kGsWaves; ++i) w[i] = gs_wave_map<FWD>(l, 0, i, c);
         const GsMap all = gs_four(w);
         // what comes in is part of the first tile's map, so that nobody else reads it
-        const bool whole = seg == 0 || (FWD && gs_odd(all.b));
-        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? gs_word(all) : 0.f, whole ? gs_four_all(w, seg ? 0.f : first) : all.b);
+        float b = all.b;
+        if (seg == 0 || (FWD && gs_odd(b))) {
+            // one after the other: for the channels that need it, so that others keep their bits
+            const float whole = gs_four_all(w, seg ? 0.f : first);
+            b = seg == 0 || gs_odd_here(b) ? whole : b;
+        }
+        gs_publish(maps + (size_t)seg * kGsTile + c, seg ? gs_word(all) : 0.f, b);
     }
     if (seg == 0) return first;
     const int from = seg - kGsBack + wave * N;               // this wave's maps: from .. from + N - 1
@@ -420,11 +426,12 @@ __device__ __forceinline__ float gs_far(const GsArgs& a, const GsLds& l, unsigne
     }
     if (FWD && gs_odd(s)) {
         // the words are all there
-        s = seg > kGsBack ? gs_low(gs_peek(states + (size_t)(seg - kGsBack) * kGsTile + c)) : 0.f;
+        float whole = seg > kGsBack ? gs_low(gs_peek(states + (size_t)(seg - kGsBack) * kGsTile + c)) : 0.f;
         for (int i = max(0, seg - kGsBack); i < seg; ++i) {
             const uint64_t m = gs_peek(maps + (size_t)i * kGsTile + c);
-            s = gs_apply_all(gs_token(gs_low(m), gs_high(m)), s);
+            whole = gs_apply_all(gs_token(gs_low(m), gs_high(m)), whole);
         }
+        s = gs_odd_here(s) ? whole : s;
     }
     if (wave == 0 && seg + kGsBack < a.nseg) gs_publish(states + (size_t)seg * kGsTile + c, s, 0.f);
     return s;

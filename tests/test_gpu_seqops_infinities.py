@@ -245,3 +245,29 @@ def test_recurrence_of_sixteen_bits_in_place_and_replayed(decay, C):
         h2, got = drl.dr_gated_scan_fwd(dev[0], dev[1], s, h_final=s, **m)
         assert got is s and torch.equal(torch.nan_to_num(h2, nan=7.0), torch.nan_to_num(h, nan=7.0))
         assert torch.equal(torch.nan_to_num(s, nan=7.0), torch.nan_to_num(last, nan=7.0))
+
+
+@pytest.mark.parametrize("B,L,C", [(1, 9000, 130), (1, 700, 64), (600, 300, 70)])
+@pytest.mark.parametrize("decay", ["log", "logit"])
+def test_other_channels_keep_their_bits(B, L, C, decay):
+    """Channels beside an infinite or NaN one, forward and backward, with memories that reach
+    over many tiles."""
+    import delta_rule_linear_amd as drl
+    gen = torch.Generator().manual_seed(L)
+    x, dh = torch.randn((B, L, C), generator=gen).cuda(), torch.randn((B, L, C), generator=gen).cuda()
+    g = (-0.002 * torch.rand((B, L, C), generator=gen) if decay == "log" else 6 + torch.rand((B, L, C), generator=gen)).cuda()
+    m = dict(decay=decay, inputs="blend")
+    h, last = drl.dr_gated_scan_fwd(x, g, None, **m)
+    base = drl.dr_gated_scan_bwd(x, g, None, h, dh, **m)
+    y, dy = x.clone(), dh.clone()
+    for c, v in ((3, INF), (20, NAN), (C - 1, -INF)):
+        y[:, L // 3, c], dy[:, L // 2, c] = v, v
+    h2, last2 = drl.dr_gated_scan_fwd(y, g, None, **m)
+    back = drl.dr_gated_scan_bwd(x, g, None, h, dy, **m)
+    keep = torch.ones(C, dtype=torch.bool, device="cuda")
+    keep[[3, 20, C - 1]] = False
+    assert torch.equal(h2[..., keep], h[..., keep]) and torch.equal(last2[:, keep], last[:, keep])
+    assert torch.equal(h2[:, :L // 3], h[:, :L // 3]) and not torch.isfinite(h2[:, L // 3:, ~keep]).any()
+    for n in ("dx", "dgate"):
+        assert torch.equal(back[n][..., keep], base[n][..., keep]) and torch.equal(back[n][:, L // 2 + 1:], base[n][:, L // 2 + 1:])
+    assert torch.equal(back["dh0"][:, keep], base["dh0"][:, keep])
